@@ -6,8 +6,10 @@
 #include <cmath>
 #include <cstring>
 
+#include "check.h"
 #include "common.h"
 #include "dispatch.h"
+#include "mx.h"
 
 namespace lq {
 
@@ -29,14 +31,6 @@ int hip_fail(hipError_t e, const char* where) {
 }  // namespace lq
 
 using namespace lq;
-
-#define REQUIRE(cond, code, ...)   \
-  do {                             \
-    if (!(cond)) {                 \
-      set_error(__VA_ARGS__);      \
-      return (code);               \
-    }                              \
-  } while (0)
 
 namespace {
 
@@ -568,6 +562,52 @@ int lq_lora_bwd(const void* dY, const void* X, int64_t M, const lq_weight* W0, c
   if (big && ws_bytes >= align256(need) + big) big_ws = (char*)ws + align256(need);
   return dispatch::bf16_bwd(dY, X, M, *W0, A, B, r, scale, T_saved, dX, dA, dB, accumulate, ws,
                             big_ws, stream);
+}
+
+int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq_weight* W0,
+                     const void* A, const void* B, int64_t r, float scale, const float* T_saved,
+                     void* dX, float* dA, float* dB, int32_t accumulate, void* ws,
+                     size_t ws_bytes, hipStream_t stream) {
+  int rc = check_weight(W0, LQ_BF16);
+  if (rc) return rc;
+  REQUIRE(M >= 0, LQ_ERR_INVALID_ARG, "M = %lld", (long long)M);
+  REQUIRE(r >= 1 && r <= kMaxRank, LQ_ERR_UNSUPPORTED, "rank %lld outside [1, %lld]",
+          (long long)r, (long long)kMaxRank);
+  REQUIRE(A && B, LQ_ERR_INVALID_ARG, "A or B is NULL");
+  REQUIRE((dA == nullptr) == (dB == nullptr), LQ_ERR_INVALID_ARG,
+          "dA and dB must both be given or both be NULL");
+  REQUIRE(dA || dX, LQ_ERR_INVALID_ARG, "nothing to compute: dX, dA and dB are NULL");
+  REQUIRE(M == 0 || dY, LQ_ERR_INVALID_ARG, "dY is NULL");
+  if ((rc = check_bf16_shape(W0)) || (rc = check_bf16_rows(M, W0))) return rc;
+  const int64_t N = W0->N, K = W0->K;
+  if (M == 0) {
+    if (accumulate || !dA) return LQ_OK;
+    if ((rc = launch_zero_f32(dA, r * K, stream))) return rc;
+    return launch_zero_f32(dB, N * r, stream);
+  }
+  if (dA && (rc = mx_check_tensor(Xq, "Xq", LQ_MX_FP4 | LQ_MX_FP8, M, K))) return rc;
+  if ((rc = mx_check_aligned(dY, "dY")) || (rc = mx_check_aligned(dX, "dX")) ||
+      (rc = mx_check_aligned(A, "A")) || (rc = mx_check_aligned(ws, "ws")) ||
+      (rc = mx_check_aligned(T_saved, "T_saved")))
+    return rc;
+  const size_t need = lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT, M, N, K, r);
+  REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
+          ws_bytes, need);
+  const MxBwdWs w = mx_bwd_ws(M, N, K, r);
+  char* base = (char*)ws;
+  float* U = (float*)(base + w.u);
+  void* big_ws = dX && bwd_big_bytes(M, N, K) ? base + w.rest : nullptr;
+  rc = dX ? dispatch::bf16_dx_any(dY, M, *W0, A, B, r, scale, dX, U, dA ? U : nullptr, big_ws,
+                                  stream)
+          : dispatch::u_only(dY, M, N, B, r, U, stream, nullptr, 0);
+  if (rc || !dA) return rc;
+  const float* T = T_saved;
+  if (!T) {
+    float* Tw = (float*)(base + w.t);
+    if ((rc = dispatch::mx_shrink(*Xq, A, r, Tw, stream))) return rc;
+    T = Tw;
+  }
+  return dispatch::mx_grads(*Xq, U, dY, T, N, r, scale, accumulate, dA, dB, base + w.part, stream);
 }
 
 int lq_lora_fwd_dropout(const void* X, int64_t M, const lq_weight* W0, const void* A,

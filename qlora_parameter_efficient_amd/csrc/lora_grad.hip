@@ -18,6 +18,7 @@
 // accumulate flag.
 #include "device_util.h"
 #include "dispatch.h"
+#include "mx.h"
 
 namespace lq {
 namespace {
@@ -382,6 +383,22 @@ size_t grad_partial_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
   return (size_t)(sa * r * K + sb * r * N) * 4 + 512;
 }
 
+// dX (and U = dY B on the way): for an NF4 weight at large M by the
+// product that dequantises in its K loop (no workspace), unless the
+// large-tile path has its workspace and would run 256 x 256 tiles; by the
+// large-tile path when it has its workspace (for an NF4 weight and at most
+// 64 rows, by the weight-streaming kernel, its partial sums in that
+// workspace), else by the fused kernel
+int bf16_dx_any(const void* dY, int64_t M, const lq_weight& W, const void* A, const void* B,
+                int64_t r, float s, void* dX, float* U, float* U_out, void* big_ws,
+                hipStream_t st) {
+  if (big_ws && small_dx_eligible(W, M, r)) return small_dx(dY, M, W, A, B, r, s, U, dX, big_ws, st);
+  if (inloop_dx_eligible(W, M, r) && !(big_ws && big_wide_tiles(M, W.K)))
+    return inloop_dx(dY, M, W, A, B, r, s, dX, U_out, st);
+  return big_ws ? big_dx(dY, M, W, A, B, r, s, dX, U, big_ws, st)
+                : bf16_dx(dY, M, W, A, B, r, s, dX, U_out, st);
+}
+
 int bf16_bwd(const void* dY, const void* X, int64_t M, const lq_weight& W, const void* A,
              const void* B, int64_t r, float s, const float* T_saved, void* dX, float* dA,
              float* dB, int accumulate, void* ws, void* big_ws, hipStream_t st) {
@@ -398,18 +415,8 @@ int bf16_bwd(const void* dY, const void* X, int64_t M, const lq_weight& W, const
     if ((e = launch_zero_f32(dA, r * K, st))) return e;
     return launch_zero_f32(dB, N * r, st);
   }
-  // dX (and U = dY B on the way): for an NF4 weight at large M by the
-  // product that dequantises in its K loop (no workspace), unless the
-  // large-tile path has its workspace and would run 256 x 256 tiles; by the
-  // large-tile path when it has its workspace (for an NF4 weight and at most
-  // 64 rows, by the weight-streaming kernel, its partial sums in that
-  // workspace), else by the fused kernel
   auto run_dx = [&](float* Uo) {
-    if (big_ws && small_dx_eligible(W, M, r)) return small_dx(dY, M, W, A, B, r, s, U, dX, big_ws, st);
-    if (inloop_dx_eligible(W, M, r) && !(big_ws && big_wide_tiles(M, W.K)))
-      return inloop_dx(dY, M, W, A, B, r, s, dX, Uo, st);
-    return big_ws ? big_dx(dY, M, W, A, B, r, s, dX, U, big_ws, st)
-                  : bf16_dx(dY, M, W, A, B, r, s, dX, Uo, st);
+    return bf16_dx_any(dY, M, W, A, B, r, s, dX, U, Uo, big_ws, st);
   };
   if (!grads) return run_dx(nullptr);
   const float* T = T_saved;

@@ -1,0 +1,511 @@
+// Forward product of the MXFP4 layer on the scaled matrix instructions:
+//
+//   Y = X W^T + (s T) B^T      X MXFP8 or MXFP4 (M x K), W MXFP4 (N x K),
+//                              T = X A^T (M x r float32)
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies the codes and applies both
+// operands' block scales, so nothing is dequantised.  MFMA-bound: 4-bit codes
+// on both sides run at twice the rate of an 8-bit side.
+//
+// Operand layout of the instruction (lane l: row l % 32, half h = l / 32; the
+// 64 reduction elements are two scale blocks 0 and 1):
+//   4-bit codes: 16 bytes per lane, block h
+//   8-bit codes: 32 bytes per lane, 16-byte half h of block 0, then of block 1
+//   scale: one byte of the lane's scale register (picked by opsel), block h
+// Any relabelling of the reduction that is the same on both operands leaves
+// the product unchanged; the kernel uses it to make a lane's scale bytes
+// adjacent: in a step of KB blocks per row, instruction kk's block h is block
+// h KB / 2 + kk of the step, so a lane's scales for all instructions of the
+// step are one LDS word.
+//
+// Tiles.  Four waves own a (64 IM) x (64 JM) output tile, i (weight rows n) by
+// j (activation rows m), wave (wi, wj) a (32 IM) x (32 JM) block of 32 x 32
+// accumulators.  The output is computed transposed (n = MFMA rows), so a lane
+// holds four consecutive outputs of one row.  Steps of 256 (FP4 X) or 128
+// (FP8 X) columns; both operands' codes go straight from global memory into
+// LDS (global_load_lds_dwordx4), 16-byte chunks swizzled by row through the
+// lanes' global addresses so that operand reads are conflict-free; the scale
+// bytes come through registers.  Two LDS stages, one barrier per step.
+//
+// Split K (few tiles): workgroups of one tile take ranges of the steps and
+// leave float32 partial sums, which mxg_reduce_kernel adds in order.
+//
+// Epilogue: the expand adds (s T) B^T on the finished accumulators with bf16
+// MFMAs (T rounded to bf16 after the multiply by s: the same rounding as the
+// output's, on one term of it), then the tile goes through LDS and leaves as
+// 16-byte stores covering whole output lines.
+#include <type_traits>
+
+#include "dispatch.h"
+#include "mx_tile.h"
+
+namespace lq {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct MxgParams {
+  const uint8_t* X;   // M x K codes
+  const uint8_t* Xs;  // M x K / 32
+  const uint8_t* W;   // N x K codes (FP4)
+  const uint8_t* Ws;
+  const float* T;     // M x r
+  const uint16_t* B;  // N x r
+  uint16_t* Y;        // M x N
+  float* part;        // splits x M x N (splits > 1)
+  int64_t M, N, K;
+  int32_t r;
+  float s;
+  int32_t ti, tj, splits, ksteps;
+};
+
+template <int FX, int IM, int JM>
+struct MxgShape {
+  static constexpr int BK = FX == LQ_MX_FP4 ? 256 : 128;  // columns per step
+  static constexpr int KB = BK / 32;                       // blocks per row and step
+  static constexpr int TI = 64 * IM, TJ = 64 * JM;
+  static constexpr int WRow = BK / 2, XRow = 128;          // bytes per row and step
+  static constexpr int WBytes = TI * WRow, XBytes = TJ * XRow, SBytes = (TI + TJ) * KB;
+  static constexpr int Stage = WBytes + XBytes + SBytes;
+  static constexpr int Out = TJ * TI * 2;                  // bf16 output tile
+  static constexpr int Smem = 2 * Stage > Out ? 2 * Stage : Out;
+  static constexpr int SR = (TI + TJ + kThreads - 1) / kThreads;  // scale rows per thread
+};
+
+__device__ __forceinline__ i32x8 widen(const u32x4& v) {
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  return __builtin_shufflevector(__builtin_bit_cast(i32x4, v), __builtin_bit_cast(i32x4, v), 0, 1,
+                                 2, 3, -1, -1, -1, -1);
+}
+
+__device__ __forceinline__ i32x8 join(const u32x4& a, const u32x4& b) {
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  return __builtin_shufflevector(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), 0, 1,
+                                 2, 3, 4, 5, 6, 7);
+}
+
+// TAIL: K is not a multiple of BK; the last step's missing blocks are read
+// from the row's first block of the step and zeroed on the weight side, with
+// scale 1 (127) on both, and scales are read in pairs (K / 32 is even).
+// SPLIT: several workgroups per tile, float32 partial sums out.
+template <int FX, int IM, int JM, bool TAIL, bool SPLIT>
+__global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
+  using S = MxgShape<FX, IM, JM>;
+  constexpr int KB = S::KB, MK = KB / 2;
+  __shared__ __attribute__((aligned(1024))) char smem[S::Smem];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave & 1, wj = wave >> 1;
+  const int h = lane >> 5, l32 = lane & 31;
+
+  // tile: each XCD a contiguous range, in groups of four activation tiles
+  const int t = xcd_tile(blockIdx.x, p.ti * p.tj);
+  constexpr int GJ = 4;
+  const int grp = t / (GJ * p.ti);
+  const int in = t - grp * GJ * p.ti;
+  const int gj = (p.tj - grp * GJ) < GJ ? (p.tj - grp * GJ) : GJ;
+  const int tile_j = grp * GJ + in % gj;
+  const int tile_i = in / gj;
+  const int64_t i0 = (int64_t)tile_i * S::TI, j0 = (int64_t)tile_j * S::TJ;
+  const int64_t M = p.M, N = p.N, K = p.K;
+  const int64_t wpitch = K / 2, xpitch = K * FX / 8, spitch = K / 32;
+  const int KT = (int)cdiv(K, S::BK);
+  const int ka = blockIdx.y * p.ksteps;
+  const int kb = ka + p.ksteps < KT ? ka + p.ksteps : KT;
+  const uint32_t sbase = mx_lds_addr(smem);
+
+  // ---- per-thread load offsets, relative to the step's base pointers
+  constexpr int WU = S::WBytes / 4096, XU = S::XBytes / 4096;  // loads per wave and step
+  uint32_t woff[WU], xoff[XU];
+  int wch[WU], xch[XU];
+#pragma unroll
+  for (int u = 0; u < WU; ++u) {
+    const int row = S::WRow == 128 ? 8 * (wave * WU + u) + (lane >> 3)
+                                   : 16 * (wave * WU + u) + (lane >> 2);
+    wch[u] = S::WRow == 128 ? (lane & 7) ^ mx_swz128(row) : (lane & 3) ^ mx_swz64(row);
+    int64_t n = i0 + row;
+    n = n < N ? n : N - 1;
+    woff[u] = (uint32_t)(n * wpitch + 16 * wch[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < XU; ++u) {
+    const int row = 8 * (wave * XU + u) + (lane >> 3);
+    xch[u] = (lane & 7) ^ mx_swz128(row);
+    int64_t m = j0 + row;
+    m = m < M ? m : M - 1;
+    xoff[u] = (uint32_t)(m * xpitch + 16 * xch[u]);
+  }
+  const char* wb0 = reinterpret_cast<const char*>(p.W);
+  const char* xb0 = reinterpret_cast<const char*>(p.X);
+  auto issue = [&](int kt, int b, int go) {
+    const uint32_t st = sbase + b * S::Stage;
+    const char* wb = wb0 + (int64_t)kt * S::WRow;
+    const char* xb = xb0 + (int64_t)kt * S::XRow;
+    const int nb = (int)(spitch - (int64_t)kt * KB);  // blocks left in the rows
+    const bool cut = TAIL && nb < KB;
+#pragma unroll
+    for (int u = 0; u < WU; ++u) {
+      const uint32_t o = cut && wch[u] >= nb ? woff[u] - 16 * wch[u] : woff[u];
+      mx_dma16(wb, o, st + (wave * WU + u) * 1024, go);
+    }
+#pragma unroll
+    for (int u = 0; u < XU; ++u) {
+      const bool past = xch[u] >= (FX == LQ_MX_FP4 ? nb : 2 * nb);
+      const uint32_t o = cut && past ? xoff[u] - 16 * xch[u] : xoff[u];
+      mx_dma16(xb, o, st + S::WBytes + (wave * XU + u) * 1024, go);
+    }
+  };
+
+  // ---- scale bytes: thread t carries rows t, t + 256 of (weight, activation)
+  const uint8_t* srow[S::SR];
+#pragma unroll
+  for (int i = 0; i < S::SR; ++i) {
+    int R = tid + kThreads * i;
+    R = R < S::TI + S::TJ ? R : S::TI + S::TJ - 1;
+    if (R < S::TI) {
+      const int64_t n = i0 + R;
+      srow[i] = p.Ws + (n < N ? n : N - 1) * spitch;
+    } else {
+      const int64_t m = j0 + R - S::TI;
+      srow[i] = p.Xs + (m < M ? m : M - 1) * spitch;
+    }
+  }
+  uint32_t sv[S::SR][KB / 4];
+  auto load_scales = [&](int kt) {
+    const int nb = (int)(spitch - (int64_t)kt * KB);
+#pragma unroll
+    for (int i = 0; i < S::SR; ++i) {
+      const uint8_t* a = srow[i] + (int64_t)kt * KB;
+      if (TAIL) {
+        uint32_t v[KB / 2];
+#pragma unroll
+        for (int e = 0; e < KB / 2; ++e) {
+          const bool in = 2 * e < nb;
+          const uint32_t w = *reinterpret_cast<const uint16_t*>(a + (in ? 2 * e : 0));
+          v[e] = in ? w : 0x7F7Fu;
+        }
+#pragma unroll
+        for (int e = 0; e < KB / 4; ++e) sv[i][e] = v[2 * e] | (v[2 * e + 1] << 16);
+      } else if (KB == 8) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(a);
+        sv[i][0] = v[0];
+        sv[i][KB / 4 - 1] = v[1];
+      } else {
+        sv[i][0] = *reinterpret_cast<const uint32_t*>(a);
+      }
+    }
+  };
+  // (a thread past the last row stores that row's bytes again: no branch)
+  auto store_scales = [&](int b) {
+    char* st = smem + b * S::Stage + S::WBytes + S::XBytes;
+#pragma unroll
+    for (int i = 0; i < S::SR; ++i) {
+      int R = tid + kThreads * i;
+      R = R < S::TI + S::TJ ? R : S::TI + S::TJ - 1;
+#pragma unroll
+      for (int e = 0; e < KB / 4; ++e)
+        *reinterpret_cast<uint32_t*>(st + R * KB + 4 * e) = sv[i][e];
+    }
+  };
+
+  // ---- per-lane LDS read offsets
+  const int wrow0 = 32 * IM * wi + l32, xrow0 = 32 * JM * wj + l32;
+  // row offsets by multiples of 32 leave both swizzles unchanged
+  auto read_w = [&](uint32_t st, int ns, int kk) {
+    const int c = h * (KB / 2) + kk;
+    const int sw = S::WRow == 128 ? mx_swz128(l32) : mx_swz64(l32);
+    return mx_read16(st + (uint32_t)((wrow0 + 32 * ns) * S::WRow + ((c ^ sw) << 4)));
+  };
+  auto read_x = [&](uint32_t st, int ms, int kk) {
+    const uint32_t row = st + S::WBytes + (uint32_t)((xrow0 + 32 * ms) * S::XRow);
+    const int sw = mx_swz128(l32);
+    if (FX == LQ_MX_FP4) {
+      const int c = h * (KB / 2) + kk;
+      return widen(mx_read16(row + (uint32_t)((c ^ sw) << 4)));
+    }
+    const int c0 = 2 * kk + h, c1 = 2 * (KB / 2 + kk) + h;
+    return join(mx_read16(row + (uint32_t)((c0 ^ sw) << 4)),
+                mx_read16(row + (uint32_t)((c1 ^ sw) << 4)));
+  };
+  auto read_scale = [&](int b, int row) -> int {
+    const char* a = smem + b * S::Stage + S::WBytes + S::XBytes + row * KB + h * (KB / 2);
+    if (KB == 8) return *reinterpret_cast<const int*>(a);
+    return (int)*reinterpret_cast<const uint16_t*>(a);
+  };
+
+  f32x16 acc[IM][JM];
+#pragma unroll
+  for (int a = 0; a < IM; ++a)
+#pragma unroll
+    for (int b = 0; b < JM; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
+
+  // One step on LDS stage b.  The loop body has no branch: one between the
+  // products and the barrier would let the compiler sink products past it, so
+  // the last step skips its loads inside mx_dma16 and loads its own scales
+  // again.
+  load_scales(ka);
+  issue(ka, 0, 1);
+  store_scales(0);
+  mx_wait_loads();
+  __syncthreads();
+  int b = 0, kt = ka;
+  do {  // every split has at least one step
+    const int more = __builtin_amdgcn_readfirstlane(kt + 1 < kb ? 1 : 0);
+    load_scales(kt + more);
+    issue(kt + more, b ^ 1, more);
+    const uint32_t st = sbase + b * S::Stage;
+    int ws[IM], xs[JM];
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns) ws[ns] = read_scale(b, wrow0 + 32 * ns);
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) xs[ms] = read_scale(b, S::TI + xrow0 + 32 * ms);
+    const int nb = (int)(spitch - (int64_t)kt * KB);
+    u32x4 wf[2][IM];
+    i32x8 xf[2][JM];
+    auto frags = [&](int kk, int c) {
+#pragma unroll
+      for (int ns = 0; ns < IM; ++ns) {
+        wf[c][ns] = read_w(st, ns, kk);
+        if (TAIL) wf[c][ns] = sel4(h * (KB / 2) + kk < nb, wf[c][ns]);
+      }
+#pragma unroll
+      for (int ms = 0; ms < JM; ++ms) xf[c][ms] = read_x(st, ms, kk);
+    };
+    frags(0, 0);
+    auto sub = [&](auto k) {
+      constexpr int kk = decltype(k)::value, c = kk & 1;
+      if (kk + 1 < MK) frags(kk + 1, c ^ 1);
+      __builtin_amdgcn_sched_barrier(0);  // the next reads before these products
+#pragma unroll
+      for (int ns = 0; ns < IM; ++ns)
+#pragma unroll
+        for (int ms = 0; ms < JM; ++ms)
+          acc[ns][ms] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              widen(wf[c][ns]), xf[c][ms], acc[ns][ms], 4, FX == LQ_MX_FP4 ? 4 : 0, kk, ws[ns],
+              kk, xs[ms]);
+    };
+    sub(std::integral_constant<int, 0>{});
+    sub(std::integral_constant<int, 1>{});
+    if constexpr (MK > 2) {
+      sub(std::integral_constant<int, 2>{});
+      sub(std::integral_constant<int, 3>{});
+    }
+    store_scales(b ^ 1);
+    mx_wait_loads();
+    __syncthreads();
+    b ^= 1;
+  } while (++kt < kb);
+
+  if constexpr (SPLIT) {  // float32 partial sums; lane: rows n = .. + 8 q + 4 h + 0..3, column m
+    float* part = p.part + (int64_t)blockIdx.y * M * N;
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) {
+      const int64_t m = j0 + xrow0 + 32 * ms;
+#pragma unroll
+      for (int ns = 0; ns < IM; ++ns)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t n = i0 + 32 * IM * wi + 32 * ns + 8 * q + 4 * h;
+          if (m < M && n < N)
+            *reinterpret_cast<f32x4*>(part + m * N + n) =
+                f32x4{acc[ns][ms][4 * q], acc[ns][ms][4 * q + 1], acc[ns][ms][4 * q + 2],
+                      acc[ns][ms][4 * q + 3]};
+        }
+    }
+    return;
+  }
+
+  // ---- expand: acc += B-operand x (s T)-operand over rank chunks of 16
+  const int r = p.r;
+  for (int c = 0; c < r; c += 16) {
+    const int jr = c + 8 * h;
+    u32x4 ef[IM], vf[JM];
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns) {
+      int64_t n = i0 + wrow0 + 32 * ns;
+      n = n < N ? n : N - 1;
+      ef[ns] = mx_e_row(p.B + n * r, jr, r);
+    }
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) {
+      int64_t m = j0 + xrow0 + 32 * ms;
+      m = m < M ? m : M - 1;
+      vf[ms] = mx_v_operand(p.T + m * r, jr, r, p.s);
+    }
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns)
+#pragma unroll
+      for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(ef[ns], vf[ms], acc[ns][ms]);
+  }
+
+  // ---- store: bf16 tile in LDS (row j of 2 TI bytes, chunk c at c ^ (j & 15)),
+  // then 16-byte stores of whole output rows.  The last step's barrier has
+  // every wave done with the stages.
+  constexpr int ORow = 2 * S::TI, OC = ORow / 16;  // bytes, chunks per output row
+#pragma unroll
+  for (int ms = 0; ms < JM; ++ms) {
+    const int j = xrow0 + 32 * ms;
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = 32 * IM * wi + 32 * ns + 8 * q + 4 * h;
+        const int chunk = (i >> 3) ^ (j & 15);
+        *reinterpret_cast<u32x2*>(smem + j * ORow + chunk * 16 + (i & 7) * 2) =
+            u32x2{pack_bf16x2(acc[ns][ms][4 * q], acc[ns][ms][4 * q + 1]),
+                  pack_bf16x2(acc[ns][ms][4 * q + 2], acc[ns][ms][4 * q + 3])};
+      }
+  }
+  __syncthreads();
+  const int cl = tid % OC;
+  const int64_t n = i0 + 8 * cl;
+#pragma unroll 4
+  for (int it = 0; it < S::TJ * OC / kThreads; ++it) {
+    const int j = it * (kThreads / OC) + tid / OC;
+    const int64_t m = j0 + j;
+    const u32x4 v = mx_read16(sbase + (uint32_t)(j * ORow + ((cl ^ (j & 15)) << 4)));
+    if (m < M && n < N) *reinterpret_cast<u32x4*>(p.Y + m * N + n) = v;
+  }
+}
+
+// Y = bf16(sum over splits + s T B^T): four outputs of one row per thread,
+// the splits added in order
+struct MxgReduceParams {
+  const float* part;
+  const float* T;
+  const uint16_t* B;
+  uint16_t* Y;
+  int64_t M, N;
+  int32_t splits, r;
+  float s;
+};
+
+__global__ __launch_bounds__(256) void mxg_reduce_kernel(MxgReduceParams p) {
+  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t per = p.N / 4;
+  const int64_t m = idx / per, n = 4 * (idx - m * per);
+  if (m >= p.M) return;
+  f32x4 a = *reinterpret_cast<const f32x4*>(p.part + m * p.N + n);
+  for (int t = 1; t < p.splits; ++t) {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(p.part + ((int64_t)t * p.M + m) * p.N + n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] += b[i];
+  }
+  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < p.r; ++j) {
+    const float t = p.T[m * p.r + j];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = fmaf(t, bf16_to_f32(p.B[(n + i) * p.r + j]), d[i]);
+  }
+  if (p.r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] += p.s * d[i];
+  *reinterpret_cast<u32x2*>(p.Y + m * p.N + n) =
+      u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+}
+
+// Tile and split choice.  256 x 256 tiles read the least per product; where
+// they would leave compute units idle, smaller ones; below 128 tiles of the
+// smallest the reduction is split.
+struct Plan {
+  int im, jm, ti, tj, splits;
+};
+
+Plan plan(int64_t M, int64_t N, int64_t K) {
+  static const int shapes[3][2] = {{4, 4}, {4, 2}, {2, 2}};
+  Plan q{};
+  for (int c = 0; c < 3; ++c) {
+    q.im = shapes[c][0];
+    q.jm = shapes[c][1];
+    q.ti = (int)cdiv(N, 64 * q.im);
+    q.tj = (int)cdiv(M, 64 * q.jm);
+    if ((int64_t)q.ti * q.tj >= 192) break;
+  }
+  const int64_t tiles = (int64_t)q.ti * q.tj;  // fewer than 192 only at 128 x 128
+  int64_t sp = tiles < 128 ? cdiv(256, tiles) : 1;
+  const int64_t most = K / 512;  // at least 512 columns a split
+  if (sp > most) sp = most;
+  if (sp > 8) sp = 8;
+  q.splits = sp < 1 ? 1 : (int)sp;
+  return q;
+}
+
+template <int FX, int IM, int JM, bool SPLIT>
+void launch(const MxgParams& p, hipStream_t st) {
+  const dim3 grid((unsigned)(p.ti * p.tj), (unsigned)p.splits), block(kThreads);
+  if (p.K % MxgShape<FX, IM, JM>::BK)
+    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, true, SPLIT>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, false, SPLIT>), grid, block, 0, st, p);
+}
+
+// p.splits and p.ksteps are set so that every split has a step
+template <int FX>
+void launch_shape(MxgParams& p, const Plan& q, hipStream_t st) {
+  const int64_t steps = cdiv(p.K, FX == LQ_MX_FP4 ? 256 : 128);
+  p.ksteps = (int32_t)cdiv(steps, q.splits);
+  p.splits = (int32_t)cdiv(steps, p.ksteps);
+  if (q.im == 4 && q.jm == 4)
+    launch<FX, 4, 4, false>(p, st);
+  else if (q.im == 4)
+    launch<FX, 4, 2, false>(p, st);
+  else if (q.splits == 1)
+    launch<FX, 2, 2, false>(p, st);
+  else
+    launch<FX, 2, 2, true>(p, st);
+}
+
+}  // namespace
+
+namespace dispatch {
+
+size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  const Plan q = plan(M, N, K);
+  return q.splits > 1 ? (size_t)q.splits * M * N * 4 : 0;
+}
+
+int mx_gemm(const lq_mx_tensor& X, const lq_mx_tensor& W, const float* T, const void* B,
+            int64_t r, float s, void* Y, void* part, hipStream_t st) {
+  MxgParams p;
+  p.X = X.codes;
+  p.Xs = X.scales;
+  p.W = W.codes;
+  p.Ws = W.scales;
+  p.T = T;
+  p.B = (const uint16_t*)B;
+  p.Y = (uint16_t*)Y;
+  p.part = (float*)part;
+  p.M = X.rows;
+  p.N = W.rows;
+  p.K = X.cols;
+  p.r = (int32_t)r;
+  p.s = s;
+  const Plan q = plan(p.M, p.N, p.K);
+  p.ti = q.ti;
+  p.tj = q.tj;
+  p.splits = q.splits;
+  if (X.format == LQ_MX_FP8)
+    launch_shape<LQ_MX_FP8>(p, q, st);
+  else
+    launch_shape<LQ_MX_FP4>(p, q, st);
+  int e = hip_fail(hipGetLastError(), "mx_gemm launch");
+  if (e || q.splits == 1) return e;
+  MxgReduceParams d;
+  d.part = p.part;
+  d.T = T;
+  d.B = p.B;
+  d.Y = p.Y;
+  d.M = p.M;
+  d.N = p.N;
+  d.splits = p.splits;
+  d.r = p.r;
+  d.s = s;
+  hipLaunchKernelGGL(mxg_reduce_kernel, dim3((unsigned)cdiv(p.M * (p.N / 4), 256)), dim3(256), 0,
+                     st, d);
+  return hip_fail(hipGetLastError(), "mx_gemm reduce launch");
+}
+
+}  // namespace dispatch
+}  // namespace lq

@@ -1,0 +1,88 @@
+"""Inputs, float64 references and error bounds of the MX layer tests.
+
+Bounds, per element and worst case.  A rounding to bf16 is off by at most 2^-8
+of the value, one to float32 by 2^-24 (2^-23 where an instruction may
+truncate).  A float32 sum of n terms formed by matrix instructions of p
+products has a chain of n / p additions and at most p + 16 more inside the
+instruction and across waves: its error is at most (n / p + p + 16) 2^-23 of
+the sum of magnitudes.  The scaled instructions align the 64 products of one
+instruction to the largest and keep at least 13 bits below it (512 128-product
+probes kept 14.6), so a group's sum is off by at most 2^-13 of its largest
+product, which is at most 2^-13 of its sum of magnitudes.
+"""
+import torch
+
+from qlora_parameter_efficient_amd import mx
+from tests.gpu_helpers import DEV
+
+BF16 = 2.0**-8
+
+
+def gamma(n, p=16, parts=1):
+    return (parts * n / p + p + 16) * 2.0**-23
+
+
+GAMMA_SCALED = 2.0**-13
+
+
+def values(q):
+    """Element values of an MxTensor, float64, by the oracle's tables."""
+    from oracle import mx as omx
+    v = omx.mx_dequantize(q.codes.cpu().numpy().reshape(q.rows, -1),
+                          q.scales.cpu().numpy().reshape(q.rows, -1), q.format, q.cols)
+    return torch.from_numpy(v).to(DEV)
+
+
+def make(M, N, K, r, fmt, seed=0, bf16_x=False):
+    """(X or its MxTensor, W, A, B, dY, s) with wide-ranging block scales."""
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    X = rnd(M, K) * torch.exp2(torch.randint(-3, 4, (M, K // 32, 1), generator=g).expand(
+        M, K // 32, 32).reshape(M, K).float())
+    W = rnd(N, K) * 0.02 * torch.exp2(torch.randint(-2, 3, (N, K // 32, 1), generator=g).expand(
+        N, K // 32, 32).reshape(N, K).float())
+    A = (rnd(r, K) / max(r, 1) ** 0.5).to(torch.bfloat16).to(DEV)
+    B = (rnd(N, r) * 0.02).to(torch.bfloat16).to(DEV)
+    dY = rnd(M, N).to(torch.bfloat16).to(DEV)
+    X = X.to(torch.bfloat16).to(DEV)
+    Wq = mx.lq_mx_quantize(W.to(DEV), "fp4")
+    return (X if bf16_x else mx.lq_mx_quantize(X, fmt)), Wq, A, B, dY, 1.5
+
+
+def ref_forward(x, w, A, B, s, scaled):
+    """(Y, bound of Y, T, bound of T) in float64."""
+    K = x.shape[1]
+    A, B = A.double(), B.double()
+    T = x @ A.t()
+    Y = x @ w.t() + s * (T @ B.t())
+    gk = gamma(K) + (GAMMA_SCALED if scaled else 0.0)
+    bT = gamma(K) * (x.abs() @ A.abs().t())
+    bY = (BF16 * Y.abs() + gk * (x.abs() @ w.abs().t())
+          + abs(s) * (2 * BF16 * T.abs() + bT) @ B.abs().t())
+    return Y, bY + 1e-37, T, bT + 1e-37
+
+
+def ref_backward(dY, x, T, w, A, B, s):
+    """dX, dA, dB in float64, each with its bound (T as given, float64)."""
+    M, N = dY.shape
+    d, A, B = dY.double(), A.double(), B.double()
+    U = d @ B
+    eU = gamma(N) * (d.abs() @ B.abs())
+    dX = d @ w + s * (U @ A)
+    bX = (BF16 * dX.abs() + gamma(N) * (d.abs() @ w.abs())
+          + abs(s) * (2 * BF16 * U.abs() + eU) @ A.abs())
+    gm = gamma(M, parts=3)
+    dA = s * (U.t() @ x)
+    bA = abs(s) * (gm * (U.abs().t() @ x.abs()) + eU.t() @ x.abs()) + 2.0**-23 * dA.abs()
+    dB = s * (d.t() @ T)
+    bB = abs(s) * gm * (d.abs().t() @ T.abs()) + 2.0**-23 * dB.abs()
+    return (dX, bX + 1e-37), (dA, bA + 1e-37), (dB, bB + 1e-37)
+
+
+def assert_within(got, want, bound, what):
+    err = (got.double() - want).abs()
+    bad = ~(err <= bound)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} elements off, first at "
+                           f"{bad.nonzero()[0].tolist()}: got {got[tuple(bad.nonzero()[0])].item()} "
+                           f"want {want[tuple(bad.nonzero()[0])].item()} "
+                           f"bound {bound[tuple(bad.nonzero()[0])].item()}")

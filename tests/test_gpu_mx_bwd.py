@@ -1,0 +1,206 @@
+"""Backward from MX checkpoints against float64: the MXFP4 layer and the dense
+and NF4 layers, with bounds derived in mx_helpers; a whole step; gradients
+against differences; streams, graphs and shared leaves."""
+import pytest
+import torch
+
+from qlora_parameter_efficient_amd import lq, mx
+from tests.gpu_helpers import DEV, announce
+from tests.mx_helpers import assert_within, make, ref_backward, ref_forward, values
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(1, 64, 64, 1), (3, 128, 192, 5), (64, 256, 320, 8), (65, 320, 128, 64), (130, 64, 1088, 16),
+          (300, 1088, 832, 33), (777, 512, 1920, 24), (1000, 2048, 2048, 16), (2048, 4096, 512, 11)]
+
+
+def out_buffers(M, N, K, r):
+    """dX, dA, dB as views with guard rows on both sides."""
+    X = torch.full((M + 2, K), 5.0, dtype=torch.bfloat16, device=DEV)
+    a = torch.full((r + 2, K), 5.0, device=DEV)
+    b = torch.full((N + 2, r), 5.0, device=DEV)
+    return (X, a, b), (X[1:-1], a[1:-1], b[1:-1])
+
+
+def compare(got, refs, names=("dX", "dA", "dB")):
+    for g, (w, b), n in zip(got, refs, names):
+        assert_within(g, w, b, n)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("saved", [True, False])
+@pytest.mark.parametrize("M,N,K,r", SHAPES)
+def test_mx_layer(M, N, K, r, fmt, saved):
+    announce(f"mx bwd {fmt} M={M} N={N} K={K} r={r} saved={saved}")
+    X, W, A, B, dY, s = make(M, N, K, r, fmt)
+    x = values(X)
+    T = (x @ A.double().t()).float() if saved else None
+    whole, (dX, dA, dB) = out_buffers(M, N, K, r)
+    got = mx.lq_mx_lora_bwd(dY, X, W, A, B, s, T_saved=T, dX=dX, dA=dA, dB=dB)
+    torch.cuda.synchronize()
+    Tr = T.double() if saved else x @ A.double().t()
+    refs = ref_backward(dY, x, Tr, values(W), A, B, s)
+    if not saved:  # T's own error
+        _, _, _, bT = ref_forward(x, values(W), A, B, s, False)
+        w, b = refs[2]
+        refs = refs[:2] + ((w, b + abs(s) * (dY.double().abs().t() @ bT)),)
+    compare(got, refs)
+    for t in whole:
+        assert (t[0] == 5.0).all() and (t[-1] == 5.0).all()
+
+
+@pytest.mark.parametrize("base", ["dense", "nf4", "nf4_single"])
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,N,K,r", SHAPES)
+def test_checkpoint_of_dense_and_nf4_layers(M, N, K, r, fmt, base):
+    announce(f"ckpt bwd {base} {fmt} M={M} N={N} K={K} r={r}")
+    X, _, A, B, dY, s = make(M, N, K, r, fmt)
+    g = torch.Generator().manual_seed(9)
+    Wd = (torch.randn((N, K), generator=g) * 0.02).to(torch.bfloat16).to(DEV)
+    W = Wd
+    if base != "dense":
+        W = lq.lq_nf4_quantize(Wd, double_quant=base == "nf4")
+        Wd = lq.lq_nf4_dequantize(W).view(N, K)
+    x = values(X)
+    T = (x @ A.double().t()).float()
+    got = mx.lq_lora_bwd_ckpt(dY, X, W, A, B, s, T_saved=T)
+    torch.cuda.synchronize()
+    compare(got, ref_backward(dY, x, T.double(), Wd.double(), A, B, s))
+
+
+def test_parts_and_accumulation():
+    M, N, K, r = 200, 256, 320, 12
+    X, W, A, B, dY, s = make(M, N, K, r, "fp8")
+    Wd = mx.lq_mx_dequantize(W)
+    for fn, w in ((mx.lq_mx_lora_bwd, W), (mx.lq_lora_bwd_ckpt, Wd)):
+        announce(f"bwd parts {fn.__name__}")
+        dX, dA, dB = fn(dY, X, w, A, B, s)
+        only, na, nb = fn(dY, None, w, A, B, s, need_grads=False)
+        assert na is None and nb is None and torch.equal(only, dX)
+        nx, ga, gb = fn(dY, X, w, A, B, s, need_dx=False)
+        assert nx is None
+        # without dX, U = dY B comes from another kernel: equal up to its sum's rounding
+        assert torch.allclose(ga, dA, rtol=0, atol=float(dA.abs().max()) * 1e-5)
+        assert torch.equal(gb, dB)
+        a0, b0 = torch.randn_like(dA), torch.randn_like(dB)
+        a1, b1 = a0.clone(), b0.clone()
+        fn(dY, X, w, A, B, s, dA=a1, dB=b1, accumulate=True)
+        assert torch.equal(a1, a0 + dA) and torch.equal(b1, b0 + dB)
+        # the same call again gives the same bits
+        again = fn(dY, X, w, A, B, s)
+        assert all(torch.equal(p, q) for p, q in zip(again, (dX, dA, dB)))
+
+
+def test_no_rows():
+    _, W, A, B, _, s = make(1, 128, 64, 4, "fp8")
+    X = mx.MxTensor(torch.empty((0, 64), dtype=torch.uint8, device=DEV),
+                    torch.empty((0, 2), dtype=torch.uint8, device=DEV), 0, 64, "fp8")
+    dY = torch.empty((0, 128), dtype=torch.bfloat16, device=DEV)
+    for fn, w in ((mx.lq_mx_lora_bwd, W), (mx.lq_lora_bwd_ckpt, mx.lq_mx_dequantize(W))):
+        dX, dA, dB = fn(dY, X, w, A, B, s)
+        assert dX.shape == (0, 64) and not dA.any() and not dB.any()
+        a, b = torch.ones_like(dA), torch.ones_like(dB)
+        fn(dY, X, w, A, B, s, dA=a, dB=b, accumulate=True)
+        assert (a == 1).all() and (b == 1).all()
+
+
+def test_gradients_against_differences():
+    """L = sum(Y G): dA and dB of the step against float64 central differences
+    of the formula (L is linear in A and in B alone), and dX against its own."""
+    M, N, K, r = 48, 64, 128, 4
+    X, W, A, B, G, s = make(M, N, K, r, "fp8")
+    x, w = values(X), values(W)
+
+    def loss(x, A, B):
+        return ((x @ w.t() + s * (x @ A.t()) @ B.t()) * G.double()).sum()
+
+    dX, dA, dB = mx.lq_mx_lora_bwd(G, X, W, A, B, s)
+    (_, bX), (_, bA), (_, bB) = ref_backward(G, x, x @ A.double().t(), w, A, B, s)
+    g = torch.Generator().manual_seed(2)
+    for _ in range(6):
+        for t, grad, bound, at in ((A.double(), dA, bA, 1), (B.double(), dB, bB, 2), (x, dX, bX, 0)):
+            v = torch.randn(t.shape, generator=g, dtype=torch.float64).to(DEV)
+            args = [x, A.double(), B.double()]
+            hi, lo = list(args), list(args)
+            hi[at], lo[at] = t + 0.5 * v, t - 0.5 * v
+            diff = loss(*hi) - loss(*lo)
+            slack = (bound * v.abs()).sum() * 1.01 + 1e-9 * diff.abs()
+            if at == 2:  # T recomputed in float32
+                slack = slack + (abs(s) * v.abs().t() @ (G.double().abs().t() @ (
+                    (K / 16 + 32) * 2.0**-23 * (x.abs() @ A.double().abs().t())))).diagonal().sum()
+            assert (diff - (grad.double() * v).sum()).abs() <= slack
+
+
+def step(X, W, A, B, dY, s, fmt):
+    q = mx.lq_mx_quantize(X, fmt)
+    T = torch.empty((X.shape[0], A.shape[0]), device=DEV)
+    Y = mx.lq_mx_lora_fwd(q, W, A, B, s, T_out=T)
+    return (Y,) + tuple(mx.lq_mx_lora_bwd(dY, q, W, A, B, s, T_saved=T))
+
+
+@pytest.mark.parametrize("M,N,K,r", [(5, 128, 256, 8), (333, 512, 832, 16), (1100, 1024, 512, 64)])
+def test_training_step_captured_and_replayed(M, N, K, r):
+    """Quantise, forward and backward captured into a graph: every replay on
+    new inputs equals the eager step bit for bit, with eager work between."""
+    announce(f"mx step graph M={M}")
+    X, W, A, B, dY, s = make(M, N, K, r, "fp8", bf16_x=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(X, W, A, B, dY, s, "fp8")
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(X, W, A, B, dY, s, "fp8")
+    for k in range(4):
+        X.copy_(torch.randn(X.shape, generator=torch.Generator().manual_seed(k)))
+        dY.copy_(torch.randn(dY.shape, generator=torch.Generator().manual_seed(50 + k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = step(X, W, A, B, dY, s, "fp8")
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(outs, eager))
+
+
+def test_two_streams_at_once():
+    M, N, K, r = 256, 512, 512, 16
+    sets = [make(M, N, K, r, "fp8", seed=i, bf16_x=True) for i in range(2)]
+    want = [step(*c[:5], c[5], "fp8") for c in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for c, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(step(*c[:5], c[5], "fp8"))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(g, w))
+
+
+def test_decode_follows_training():
+    """The trained layer served: one bf16 row through the streaming forward is
+    within the rounding of the quantised forward of the same row's values."""
+    M, N, K, r = 40, 256, 512, 8
+    X, W, A, B, _, s = make(M, N, K, r, "fp8")
+    xb = mx.lq_mx_dequantize(X)  # exact in bf16
+    Y = mx.lq_mx_lora_fwd(X, W, A, B, s)
+    Z = mx.lq_mx_lora_fwd(xb, W, A, B, s)
+    _, bY, _, _ = ref_forward(values(X), values(W), A, B, s, scaled=True)
+    assert ((Y.double() - Z.double()).abs() <= 2 * bY).all()
+
+
+def test_binding_refuses_wrong_operands():
+    X, W, A, B, dY, s = make(8, 128, 192, 4, "fp8")
+    T = torch.empty((8, 4), device=DEV)
+    bad = [dict(dY=dY.float()), dict(dY=dY[:, :64].contiguous()), dict(A=A[:, :64].contiguous()),
+           dict(T_saved=T[:4]), dict(dA=torch.empty(3, 192, device=DEV)), dict(A=None, B=None),
+           dict(dX=torch.empty(8, 128, dtype=torch.bfloat16, device=DEV)), dict(accumulate=True),
+           dict(need_grads=False, dA=torch.empty(4, 192, device=DEV)),
+           dict(Xq=mx.lq_mx_quantize(torch.zeros(9, 192, device=DEV), "fp8"))]
+    for fn, w in ((mx.lq_mx_lora_bwd, W), (mx.lq_lora_bwd_ckpt, mx.lq_mx_dequantize(W))):
+        for b in bad:
+            kw = dict(dY=dY, Xq=X, W0=w, A=A, B=B, scale=s)
+            kw.update(b)
+            with pytest.raises(ValueError):
+                fn(**kw)
