@@ -15,17 +15,21 @@
 // Any relabelling of the reduction that is the same on both operands leaves
 // the product unchanged; the kernel uses it to make a lane's scale bytes
 // adjacent: in a step of KB blocks per row, instruction kk's block h is block
-// h KB / 2 + kk of the step, so a lane's scales for all instructions of the
-// step are one LDS word.
+// h KB / 2 + kk of the step, so a lane's scale bytes for all instructions of
+// the step are one LDS word or half word.
 //
 // Tiles.  Four waves own a (64 IM) x (64 JM) output tile, i (weight rows n) by
 // j (activation rows m), wave (wi, wj) a (32 IM) x (32 JM) block of 32 x 32
 // accumulators.  The output is computed transposed (n = MFMA rows), so a lane
-// holds four consecutive outputs of one row.  Steps of 256 (FP4 X) or 128
-// (FP8 X) columns; both operands' codes go straight from global memory into
-// LDS (global_load_lds_dwordx4), 16-byte chunks swizzled by row through the
-// lanes' global addresses so that operand reads are conflict-free; the scale
-// bytes come through registers.  Two LDS stages, one barrier per step.
+// holds four consecutive outputs of one row.  Codes and scales of a step go
+// straight from global memory into LDS (global_load_lds_dwordx4 and _dword),
+// 16-byte chunks of the codes swizzled by row through the lanes' global
+// addresses so that operand reads are conflict-free.  Steps of 256 columns
+// with an FP4 X, so that every row piece is a whole 128-byte line (with 128
+// columns the lines are fetched twice: 4096^3 48 -> 56 us although twice the
+// stages fit), and of 128 columns with an FP8 X.  Two to four LDS stages (what
+// fits), one barrier per step, placed before the step's last substep of
+// products (see the loop).
 //
 // Split K (few tiles): workgroups of one tile take ranges of the steps and
 // leave float32 partial sums, which mxg_reduce_kernel adds in order.
@@ -61,15 +65,24 @@ struct MxgParams {
 
 template <int FX, int IM, int JM>
 struct MxgShape {
-  static constexpr int BK = FX == LQ_MX_FP4 ? 256 : 128;  // columns per step
+  static constexpr int BK = FX == LQ_MX_FP4 ? 256 : 128;   // columns per step
   static constexpr int KB = BK / 32;                       // blocks per row and step
   static constexpr int TI = 64 * IM, TJ = 64 * JM;
   static constexpr int WRow = BK / 2, XRow = 128;          // bytes per row and step
   static constexpr int WBytes = TI * WRow, XBytes = TJ * XRow, SBytes = (TI + TJ) * KB;
   static constexpr int Stage = WBytes + XBytes + SBytes;
+  // stages: as many as one workgroup per compute unit allows (256-row tiles:
+  // their accumulators leave room for one), two workgroups for 128 x 128
+  static constexpr int Room = (IM == 4 ? 160 : 80) * 1024;
+  static constexpr int NST = Room / Stage < 4 ? Room / Stage : 4;
   static constexpr int Out = TJ * TI * 2;                  // bf16 output tile
-  static constexpr int Smem = 2 * Stage > Out ? 2 * Stage : Out;
-  static constexpr int SR = (TI + TJ + kThreads - 1) / kThreads;  // scale rows per thread
+  static constexpr int Smem = NST * Stage > Out ? NST * Stage : Out;
+  static constexpr int WU = WBytes / 4096, XU = XBytes / 4096;   // code loads per wave
+  static constexpr int SRows = 256 / KB;                         // rows of a scale load
+  static constexpr int SG = (TI + TJ) / SRows;                   // scale loads per step ...
+  static constexpr int SU = (SG + 3) / 4;                        // ... and per wave
+  static constexpr int Loads = WU + XU + SU;
+  static constexpr int SR = (TI + TJ + kThreads - 1) / kThreads; // scale rows per thread (TAIL)
 };
 
 __device__ __forceinline__ i32x8 widen(const u32x4& v) {
@@ -84,14 +97,15 @@ __device__ __forceinline__ i32x8 join(const u32x4& a, const u32x4& b) {
                                  2, 3, 4, 5, 6, 7);
 }
 
-// TAIL: K is not a multiple of BK; the last step's missing blocks are read
-// from the row's first block of the step and zeroed on the weight side, with
-// scale 1 (127) on both, and scales are read in pairs (K / 32 is even).
+// TAIL: K is not a multiple of the step; the last step's missing blocks (an
+// even number) are read from the row's first blocks of the step and zeroed on
+// the weight side, with scale 1 (byte 127) on both, and the scales, whose rows
+// may then start at any even address, go through registers.
 // SPLIT: several workgroups per tile, float32 partial sums out.
 template <int FX, int IM, int JM, bool TAIL, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   using S = MxgShape<FX, IM, JM>;
-  constexpr int KB = S::KB, MK = KB / 2;
+  constexpr int KB = S::KB, MK = KB / 2;  // blocks and instructions (64 wide) per step
   __shared__ __attribute__((aligned(1024))) char smem[S::Smem];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -110,12 +124,13 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   const int64_t M = p.M, N = p.N, K = p.K;
   const int64_t wpitch = K / 2, xpitch = K * FX / 8, spitch = K / 32;
   const int KT = (int)cdiv(K, S::BK);
+  const int last_nb = (int)(K / 32) - (KT - 1) * KB;  // blocks of the last step
   const int ka = blockIdx.y * p.ksteps;
   const int kb = ka + p.ksteps < KT ? ka + p.ksteps : KT;
   const uint32_t sbase = mx_lds_addr(smem);
 
   // ---- per-thread load offsets, relative to the step's base pointers
-  constexpr int WU = S::WBytes / 4096, XU = S::XBytes / 4096;  // loads per wave and step
+  constexpr int WU = S::WU, XU = S::XU, SU = S::SU;
   uint32_t woff[WU], xoff[XU];
   int wch[WU], xch[XU];
 #pragma unroll
@@ -135,97 +150,119 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     m = m < M ? m : M - 1;
     xoff[u] = (uint32_t)(m * xpitch + 16 * xch[u]);
   }
+  // scale rows of this wave's SU loads: group g of SRows rows (weight rows
+  // first), a word per lane; a group past the last is loaded again, to the
+  // same place
+  uint32_t soff[SU];
+  bool sw_[SU];
+  int sgrp[SU];
+#pragma unroll
+  for (int u = 0; u < SU; ++u) {
+    int g = wave * SU + u;
+    g = g < S::SG ? g : S::SG - 1;
+    sgrp[u] = g;
+    const int R = g * S::SRows + lane / (KB / 4);
+    sw_[u] = g * S::SRows < S::TI;
+    const int64_t row = sw_[u] ? i0 + R : j0 + R - S::TI;
+    const int64_t last = (sw_[u] ? N : M) - 1;
+    soff[u] = (uint32_t)((row < last ? row : last) * spitch + 4 * (lane % (KB / 4)));
+  }
   const char* wb0 = reinterpret_cast<const char*>(p.W);
   const char* xb0 = reinterpret_cast<const char*>(p.X);
-  auto issue = [&](int kt, int b, int go) {
+  // load u of this wave's Loads of step kt into stage b
+  auto issue_one = [&](int kt, int b, int go, int u) {
     const uint32_t st = sbase + b * S::Stage;
-    const char* wb = wb0 + (int64_t)kt * S::WRow;
-    const char* xb = xb0 + (int64_t)kt * S::XRow;
-    const int nb = (int)(spitch - (int64_t)kt * KB);  // blocks left in the rows
-    const bool cut = TAIL && nb < KB;
-#pragma unroll
-    for (int u = 0; u < WU; ++u) {
-      const uint32_t o = cut && wch[u] >= nb ? woff[u] - 16 * wch[u] : woff[u];
-      mx_dma16(wb, o, st + (wave * WU + u) * 1024, go);
+    const bool cut = TAIL && kt == KT - 1;
+    if (u < WU) {
+      const uint32_t o = cut && wch[u] >= last_nb ? woff[u] - 16 * wch[u] : woff[u];
+      mx_dma16(wb0 + (int64_t)kt * S::WRow, o, st + (wave * WU + u) * 1024, go);
+    } else if (u < WU + XU) {
+      const int v = u - WU;
+      const bool past = xch[v] >= (FX == LQ_MX_FP4 ? last_nb : 2 * last_nb);
+      const uint32_t o = cut && past ? xoff[v] - 16 * xch[v] : xoff[v];
+      mx_dma16(xb0 + (int64_t)kt * S::XRow, o, st + S::WBytes + (wave * XU + v) * 1024, go);
+    } else if (!TAIL) {
+      const int v = u - WU - XU;
+      mx_dma4((sw_[v] ? p.Ws : p.Xs) + (int64_t)kt * KB, soff[v],
+              st + S::WBytes + S::XBytes + sgrp[v] * 256, go);
     }
+  };
+  auto issue = [&](int kt, int b, int go) {
 #pragma unroll
-    for (int u = 0; u < XU; ++u) {
-      const bool past = xch[u] >= (FX == LQ_MX_FP4 ? nb : 2 * nb);
-      const uint32_t o = cut && past ? xoff[u] - 16 * xch[u] : xoff[u];
-      mx_dma16(xb, o, st + S::WBytes + (wave * XU + u) * 1024, go);
-    }
+    for (int u = 0; u < S::Loads; ++u) issue_one(kt, b, go, u);
+  };
+  // the loads dealt over the IM JM products of a substep: part i of IM JM
+  auto issue_part = [&](int kt, int b, int go, int i) {
+    constexpr int parts = IM * JM;
+#pragma unroll
+    for (int u = 0; u < S::Loads; ++u)
+      if (u * parts / S::Loads == i) issue_one(kt, b, go, u);
   };
 
-  // ---- scale bytes: thread t carries rows t, t + 256 of (weight, activation)
+  // ---- TAIL: thread t carries the scale bytes of rows t, t + 256 of (weight,
+  // activation); a thread past the last row stores that row's bytes again
   const uint8_t* srow[S::SR];
-#pragma unroll
-  for (int i = 0; i < S::SR; ++i) {
-    int R = tid + kThreads * i;
-    R = R < S::TI + S::TJ ? R : S::TI + S::TJ - 1;
-    if (R < S::TI) {
-      const int64_t n = i0 + R;
-      srow[i] = p.Ws + (n < N ? n : N - 1) * spitch;
-    } else {
-      const int64_t m = j0 + R - S::TI;
-      srow[i] = p.Xs + (m < M ? m : M - 1) * spitch;
-    }
-  }
   uint32_t sv[S::SR][KB / 4];
-  auto load_scales = [&](int kt) {
-    const int nb = (int)(spitch - (int64_t)kt * KB);
-#pragma unroll
-    for (int i = 0; i < S::SR; ++i) {
-      const uint8_t* a = srow[i] + (int64_t)kt * KB;
-      if (TAIL) {
-        uint32_t v[KB / 2];
-#pragma unroll
-        for (int e = 0; e < KB / 2; ++e) {
-          const bool in = 2 * e < nb;
-          const uint32_t w = *reinterpret_cast<const uint16_t*>(a + (in ? 2 * e : 0));
-          v[e] = in ? w : 0x7F7Fu;
-        }
-#pragma unroll
-        for (int e = 0; e < KB / 4; ++e) sv[i][e] = v[2 * e] | (v[2 * e + 1] << 16);
-      } else if (KB == 8) {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(a);
-        sv[i][0] = v[0];
-        sv[i][KB / 4 - 1] = v[1];
-      } else {
-        sv[i][0] = *reinterpret_cast<const uint32_t*>(a);
-      }
-    }
-  };
-  // (a thread past the last row stores that row's bytes again: no branch)
-  auto store_scales = [&](int b) {
-    char* st = smem + b * S::Stage + S::WBytes + S::XBytes;
+  if constexpr (TAIL) {
 #pragma unroll
     for (int i = 0; i < S::SR; ++i) {
       int R = tid + kThreads * i;
       R = R < S::TI + S::TJ ? R : S::TI + S::TJ - 1;
+      const int64_t row = R < S::TI ? i0 + R : j0 + R - S::TI;
+      const int64_t last = (R < S::TI ? N : M) - 1;
+      srow[i] = (R < S::TI ? p.Ws : p.Xs) + (row < last ? row : last) * spitch;
+    }
+  }
+  auto load_scales = [&](int kt) {
+    if constexpr (TAIL) {
+      const int nb = kt == KT - 1 ? last_nb : KB;
 #pragma unroll
-      for (int e = 0; e < KB / 4; ++e)
-        *reinterpret_cast<uint32_t*>(st + R * KB + 4 * e) = sv[i][e];
+      for (int i = 0; i < S::SR; ++i) {
+        const uint16_t* a = reinterpret_cast<const uint16_t*>(srow[i] + (int64_t)kt * KB);
+        uint32_t v[KB / 2];
+#pragma unroll
+        for (int e = 0; e < KB / 2; ++e) {
+          const bool in = 2 * e < nb;
+          const uint32_t w = a[in ? e : 0];
+          v[e] = in ? w : 0x7F7Fu;
+        }
+#pragma unroll
+        for (int e = 0; e < KB / 4; ++e) sv[i][e] = v[2 * e] | (v[2 * e + 1] << 16);
+      }
+    }
+  };
+  auto store_scales = [&](int b) {
+    if constexpr (TAIL) {
+#pragma unroll
+      for (int i = 0; i < S::SR; ++i) {
+        int R = tid + kThreads * i;
+        R = R < S::TI + S::TJ ? R : S::TI + S::TJ - 1;
+#pragma unroll
+        for (int e = 0; e < KB / 4; ++e)
+          *reinterpret_cast<uint32_t*>(smem + b * S::Stage + S::WBytes + S::XBytes + R * KB +
+                                       4 * e) = sv[i][e];
+      }
     }
   };
 
   // ---- per-lane LDS read offsets
   const int wrow0 = 32 * IM * wi + l32, xrow0 = 32 * JM * wj + l32;
   // row offsets by multiples of 32 leave both swizzles unchanged
+  const int xsw = mx_swz128(l32), wsw = S::WRow == 128 ? mx_swz128(l32) : mx_swz64(l32);
   auto read_w = [&](uint32_t st, int ns, int kk) {
     const int c = h * (KB / 2) + kk;
-    const int sw = S::WRow == 128 ? mx_swz128(l32) : mx_swz64(l32);
-    return mx_read16(st + (uint32_t)((wrow0 + 32 * ns) * S::WRow + ((c ^ sw) << 4)));
+    return mx_read16(st + (uint32_t)((wrow0 + 32 * ns) * S::WRow + ((c ^ wsw) << 4)));
   };
   auto read_x = [&](uint32_t st, int ms, int kk) {
     const uint32_t row = st + S::WBytes + (uint32_t)((xrow0 + 32 * ms) * S::XRow);
-    const int sw = mx_swz128(l32);
     if (FX == LQ_MX_FP4) {
       const int c = h * (KB / 2) + kk;
-      return widen(mx_read16(row + (uint32_t)((c ^ sw) << 4)));
+      return widen(mx_read16(row + (uint32_t)((c ^ xsw) << 4)));
     }
-    const int c0 = 2 * kk + h, c1 = 2 * (KB / 2 + kk) + h;
-    return join(mx_read16(row + (uint32_t)((c0 ^ sw) << 4)),
-                mx_read16(row + (uint32_t)((c1 ^ sw) << 4)));
+    // half h of block kk (the instruction's block 0) and of block KB / 2 + kk
+    const int c0 = 2 * kk + h, c1 = KB + 2 * kk + h;
+    return join(mx_read16(row + (uint32_t)((c0 ^ xsw) << 4)),
+                mx_read16(row + (uint32_t)((c1 ^ xsw) << 4)));
   };
   auto read_scale = [&](int b, int row) -> int {
     const char* a = smem + b * S::Stage + S::WBytes + S::XBytes + row * KB + h * (KB / 2);
@@ -241,62 +278,107 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
 
-  // One step on LDS stage b.  The loop body has no branch: one between the
-  // products and the barrier would let the compiler sink products past it, so
-  // the last step skips its loads inside mx_dma16 and loads its own scales
-  // again.
+  // The loop, pipelined across the barrier: a substep's LDS reads go out before
+  // the previous substep's products, and the last substep's products run after
+  // the barrier, covering the first reads of the next step and the issue of
+  // the loads NST steps ahead (into the stage the barrier has just freed), so
+  // those loads have NST - 1 steps to land.  The body has no branch: one
+  // between the products and the barrier would let the compiler sink products
+  // past it, so loads past the last step are skipped inside mx_dma16.
+  u32x4 wf[2][IM];
+  i32x8 xf[2][JM];
+  int ws[2][IM], xs[2][JM];
+  auto frags = [&](uint32_t st, int kt, int kk, int c) {
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns) {
+      wf[c][ns] = read_w(st, ns, kk);
+      if (TAIL) wf[c][ns] = sel4(kt < KT - 1 || h * (KB / 2) + kk < last_nb, wf[c][ns]);
+    }
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) xf[c][ms] = read_x(st, ms, kk);
+  };
+  auto read_scales = [&](int b, int q) {
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns) ws[q][ns] = read_scale(b, wrow0 + 32 * ns);
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) xs[q][ms] = read_scale(b, S::TI + xrow0 + 32 * ms);
+  };
+  constexpr int NST = S::NST;
+  auto uni = [](bool c) { return __builtin_amdgcn_readfirstlane(c ? 1 : 0); };
+  // loads of the first NST steps; every split has at least one step
+#pragma unroll
+  for (int q = 0; q < NST; ++q) {
+    const int go = uni(ka + q < kb);
+    issue(go ? ka + q : ka, q, go);
+  }
   load_scales(ka);
-  issue(ka, 0, 1);
   store_scales(0);
-  mx_wait_loads();
+  if constexpr (TAIL)
+    mx_wait_loads();
+  else
+    mx_wait_loads<(NST - 1) * S::Loads>(uni(ka + NST <= kb));
   __syncthreads();
-  int b = 0, kt = ka;
-  do {  // every split has at least one step
-    const int more = __builtin_amdgcn_readfirstlane(kt + 1 < kb ? 1 : 0);
-    load_scales(kt + more);
-    issue(kt + more, b ^ 1, more);
+  int kt = ka, b = 0;
+  load_scales(uni(ka + 1 < kb) ? ka + 1 : ka);
+  read_scales(0, 0);
+  frags(sbase, ka, 0, 0);
+  do {
     const uint32_t st = sbase + b * S::Stage;
-    int ws[IM], xs[JM];
-#pragma unroll
-    for (int ns = 0; ns < IM; ++ns) ws[ns] = read_scale(b, wrow0 + 32 * ns);
-#pragma unroll
-    for (int ms = 0; ms < JM; ++ms) xs[ms] = read_scale(b, S::TI + xrow0 + 32 * ms);
-    const int nb = (int)(spitch - (int64_t)kt * KB);
-    u32x4 wf[2][IM];
-    i32x8 xf[2][JM];
-    auto frags = [&](int kk, int c) {
-#pragma unroll
-      for (int ns = 0; ns < IM; ++ns) {
-        wf[c][ns] = read_w(st, ns, kk);
-        if (TAIL) wf[c][ns] = sel4(h * (KB / 2) + kk < nb, wf[c][ns]);
-      }
-#pragma unroll
-      for (int ms = 0; ms < JM; ++ms) xf[c][ms] = read_x(st, ms, kk);
-    };
-    frags(0, 0);
-    auto sub = [&](auto k) {
+    const int bn = b + 1 == NST ? 0 : b + 1;
+    auto products = [&](auto k, int ns, int ms) {
       constexpr int kk = decltype(k)::value, c = kk & 1;
-      if (kk + 1 < MK) frags(kk + 1, c ^ 1);
+      acc[ns][ms] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          widen(wf[c][ns]), xf[c][ms], acc[ns][ms], 4, FX == LQ_MX_FP4 ? 4 : 0, kk, ws[0][ns], kk,
+          xs[0][ms]);
+    };
+    auto sub = [&](auto k) {
+      constexpr int kk = decltype(k)::value;
+      frags(st, kt, kk + 1, (kk + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);  // the next reads before these products
 #pragma unroll
       for (int ns = 0; ns < IM; ++ns)
 #pragma unroll
-        for (int ms = 0; ms < JM; ++ms)
-          acc[ns][ms] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              widen(wf[c][ns]), xf[c][ms], acc[ns][ms], 4, FX == LQ_MX_FP4 ? 4 : 0, kk, ws[ns],
-              kk, xs[ms]);
+        for (int ms = 0; ms < JM; ++ms) products(k, ns, ms);
+      __builtin_amdgcn_sched_barrier(0);
     };
     sub(std::integral_constant<int, 0>{});
-    sub(std::integral_constant<int, 1>{});
     if constexpr (MK > 2) {
+      sub(std::integral_constant<int, 1>{});
       sub(std::integral_constant<int, 2>{});
-      sub(std::integral_constant<int, 3>{});
     }
-    store_scales(b ^ 1);
-    mx_wait_loads();
+    // this step's operands are in registers; wait for the next step's loads
+    // (those of later steps stay in flight)
+    store_scales(bn);
+    if constexpr (TAIL)
+      mx_wait_loads();
+    else
+      mx_wait_loads<(NST - 2) * S::Loads>(uni(kt + NST <= kb));
     __syncthreads();
-    b ^= 1;
+    __builtin_amdgcn_sched_barrier(0);
+    const int k1 = uni(kt + 1 < kb) ? kt + 1 : kt;
+    const int go = uni(kt + NST < kb);
+    const int kn = go ? kt + NST : kt;
+    read_scales(bn, 1);
+    frags(sbase + bn * S::Stage, k1, 0, 0);
+    load_scales(uni(kt + 2 < kb) ? kt + 2 : k1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns) {
+#pragma unroll
+      for (int ms = 0; ms < JM; ++ms) {
+        products(std::integral_constant<int, MK - 1>{}, ns, ms);
+        __builtin_amdgcn_sched_barrier(0);
+        issue_part(kn, b, go, ns * JM + ms);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int ns = 0; ns < IM; ++ns) ws[0][ns] = ws[1][ns];
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) xs[0][ms] = xs[1][ms];
+    b = bn;
   } while (++kt < kb);
+  __syncthreads();  // the output tile overwrites the stages
 
   if constexpr (SPLIT) {  // float32 partial sums; lane: rows n = .. + 8 q + 4 h + 0..3, column m
     float* part = p.part + (int64_t)blockIdx.y * M * N;
@@ -341,8 +423,7 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   }
 
   // ---- store: bf16 tile in LDS (row j of 2 TI bytes, chunk c at c ^ (j & 15)),
-  // then 16-byte stores of whole output rows.  The last step's barrier has
-  // every wave done with the stages.
+  // then 16-byte stores of whole output rows
   constexpr int ORow = 2 * S::TI, OC = ORow / 16;  // bytes, chunks per output row
 #pragma unroll
   for (int ms = 0; ms < JM; ++ms) {

@@ -29,6 +29,36 @@ __device__ __forceinline__ void mx_dma16(const char* base, uint32_t off, uint32_
       : "memory", "scc");
 }
 
+// The same, 4 bytes per lane to LDS at lds + 4 lane.
+__device__ __forceinline__ void mx_dma4(const void* base, uint32_t off, uint32_t lds, int go) {
+  asm volatile(
+      "s_cmp_eq_u32 %3, 0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_cbranch_scc1 1f\n\t"
+      "global_load_lds_dword %0, %1\n"
+      "1:"
+      :
+      : "v"(off), "s"(base), "s"(lds), "s"(go)
+      : "memory", "scc");
+}
+
+// Wait for this wave's loads: all but the newest N if ``some`` (uniform) is
+// nonzero, else all of them.
+template <int N>
+__device__ __forceinline__ void mx_wait_loads(int some) {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile(
+      "s_cmp_eq_u32 %0, 0\n\t"
+      "s_cbranch_scc1 1f\n\t"
+      "s_waitcnt vmcnt(%1)\n\t"
+      "s_branch 2f\n"
+      "1:\n\t"
+      "s_waitcnt vmcnt(0)\n"
+      "2:"
+      :
+      : "s"(some), "n"(N)
+      : "memory", "scc");
+}
 __device__ __forceinline__ void mx_wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ u32x4 mx_read16(uint32_t addr) {
