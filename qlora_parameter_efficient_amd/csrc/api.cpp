@@ -587,8 +587,8 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
   }
   if (dA && (rc = mx_check_tensor(Xq, "Xq", LQ_MX_FP4 | LQ_MX_FP8, M, K))) return rc;
   if ((rc = mx_check_aligned(dY, "dY")) || (rc = mx_check_aligned(dX, "dX")) ||
-      (rc = mx_check_aligned(A, "A")) || (rc = mx_check_aligned(ws, "ws")) ||
-      (rc = mx_check_aligned(T_saved, "T_saved")))
+      (rc = mx_check_aligned(A, "A")) || (rc = mx_check_aligned(B, "B")) ||
+      (rc = mx_check_aligned(ws, "ws")) || (rc = mx_check_aligned(T_saved, "T_saved")))
     return rc;
   const size_t need = lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT, M, N, K, r);
   REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
@@ -599,7 +599,7 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
   void* big_ws = dX && bwd_big_bytes(M, N, K) ? base + w.rest : nullptr;
   rc = dX ? dispatch::bf16_dx_any(dY, M, *W0, A, B, r, scale, dX, U, dA ? U : nullptr, big_ws,
                                   stream)
-          : dispatch::u_only(dY, M, N, B, r, U, stream, nullptr, 0);
+          : dispatch::mx_u(dY, M, N, B, r, base + w.bt, U, stream);
   if (rc || !dA) return rc;
   const float* T = T_saved;
   if (!T) {

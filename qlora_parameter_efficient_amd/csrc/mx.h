@@ -72,12 +72,21 @@ int mx_dequantize(const lq_mx_tensor& q, void* out, lq_dtype odt, hipStream_t st
 
 // T = X A^T (M x r float32) from an MX tensor.
 int mx_shrink(const lq_mx_tensor& X, const void* A, int64_t r, float* T, hipStream_t st);
+// U = dY B (M x r float32) from bf16 dY and B (N x r); Bt: N r bf16 of scratch.
+int mx_u(const void* dY, int64_t M, int64_t N, const void* B, int64_t r, void* Bt, float* U,
+         hipStream_t st);
 
 // Y = X W^T + s T B^T, X and W MX tensors (W MXFP4); T M x r float32 or r = 0.
 // part: mx_gemm_ws_bytes bytes.
 size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 int mx_gemm(const lq_mx_tensor& X, const lq_mx_tensor& W, const float* T, const void* B,
             int64_t r, float s, void* Y, void* part, hipStream_t st);
+
+// dX = dY W + s U A (bf16, M x K; W MXFP4, U = dY B M x r float32); part:
+// mx_dx_ws_bytes bytes.
+size_t mx_dx_ws_bytes(int64_t M, int64_t N, int64_t K);
+int mx_dx(const void* dY, int64_t M, const lq_mx_tensor& W, const float* U, const void* A,
+          int64_t r, float s, void* dX, void* part, hipStream_t st);
 
 // Few rows (M <= LQ_MX_ROWS_BF16), X bf16: Y = X W^T + s (X A^T) B^T, W
 // streamed once per 16 rows.  Tp: mx_stream_ws_bytes bytes of partial sums.
@@ -102,17 +111,18 @@ int bf16_dx_any(const void* dY, int64_t M, const lq_weight& W, const void* A, co
 
 }  // namespace dispatch
 
-// Workspace of the backward from an MX checkpoint: [U][T][gradient partials],
-// then the dX path's own part.
+// Workspace of the backward from an MX checkpoint: [U][T][B transposed]
+// [gradient partials], then the dX path's own part.
 struct MxBwdWs {
-  size_t u, t, part, rest;  // byte offsets; rest: the end
+  size_t u, t, bt, part, rest;  // byte offsets; rest: the end
 };
 inline MxBwdWs mx_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   MxBwdWs w;
   w.u = 0;
   w.t = up((size_t)(M * r) * 4);
-  w.part = w.t + up((size_t)(M * r) * 4);
+  w.bt = w.t + up((size_t)(M * r) * 4);
+  w.part = w.bt + up((size_t)(N * r) * 2);
   w.rest = w.part + up(dispatch::mx_grad_bytes(M, N, K, r));
   return w;
 }

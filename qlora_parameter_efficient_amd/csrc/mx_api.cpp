@@ -66,16 +66,6 @@ size_t fwd_part_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
   return g > s ? g : s;
 }
 
-lq_weight dense_weight(const void* W, int64_t N, int64_t K) {
-  lq_weight v{};
-  v.kind = LQ_WEIGHT_DENSE;
-  v.dtype = LQ_BF16;
-  v.N = N;
-  v.K = K;
-  v.dense = W;
-  return v;
-}
-
 size_t big_dx_bytes(int64_t M, int64_t N, int64_t K) {
   return dispatch::big_dx_eligible(M, N, K) ? dispatch::big_dx_ws_bytes(M, N, K) : 0;
 }
@@ -133,7 +123,7 @@ size_t lq_mx_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t
     case LQ_MX_OP_FWD:
       return up256((size_t)(M * r) * 4) + fwd_part_bytes(M, N, K, r);
     case LQ_MX_OP_BWD:
-      return mx_bwd_ws(M, N, K, r).rest + up256((size_t)(N * K) * 2) + big_dx_bytes(M, N, K);
+      return mx_bwd_ws(M, N, K, r).rest + dispatch::mx_dx_ws_bytes(M, N, K);
     case LQ_MX_OP_BWD_CKPT:
       return mx_bwd_ws(M, N, K, r).rest + big_dx_bytes(M, N, K);
     default:
@@ -200,15 +190,8 @@ int lq_mx_lora_bwd(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq_m
   const MxBwdWs w = mx_bwd_ws(M, N, K, r);
   char* base = (char*)ws;
   float* U = (float*)(base + w.u);
-  if (dX) {
-    void* Wd = base + w.rest;
-    void* big = big_dx_bytes(M, N, K) ? base + w.rest + up256((size_t)(N * K) * 2) : nullptr;
-    if ((rc = dispatch::mx_dequantize(*W0, Wd, LQ_BF16, stream))) return rc;
-    rc = dispatch::bf16_dx_any(dY, M, dense_weight(Wd, N, K), A, B, r, scale, dX, U,
-                               dA ? U : nullptr, big, stream);
-  } else {
-    rc = dispatch::u_only(dY, M, N, B, r, U, stream, nullptr, 0);
-  }
+  if ((rc = dispatch::mx_u(dY, M, N, B, r, base + w.bt, U, stream))) return rc;
+  if (dX) rc = dispatch::mx_dx(dY, M, *W0, U, A, r, scale, dX, base + w.rest, stream);
   if (rc || !dA) return rc;
   const float* T = T_saved;
   if (!T) {

@@ -304,11 +304,10 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     for (int ms = 0; ms < JM; ++ms) xs[q][ms] = read_scale(b, S::TI + xrow0 + 32 * ms);
   };
   constexpr int NST = S::NST;
-  auto uni = [](bool c) { return __builtin_amdgcn_readfirstlane(c ? 1 : 0); };
   // loads of the first NST steps; every split has at least one step
 #pragma unroll
   for (int q = 0; q < NST; ++q) {
-    const int go = uni(ka + q < kb);
+    const int go = mx_less(ka + q, kb);
     issue(go ? ka + q : ka, q, go);
   }
   load_scales(ka);
@@ -316,10 +315,10 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   if constexpr (TAIL)
     mx_wait_loads();
   else
-    mx_wait_loads<(NST - 1) * S::Loads>(uni(ka + NST <= kb));
+    mx_wait_loads<(NST - 1) * S::Loads>(mx_less(ka + NST, kb + 1));
   __syncthreads();
   int kt = ka, b = 0;
-  load_scales(uni(ka + 1 < kb) ? ka + 1 : ka);
+  load_scales(mx_less(ka + 1, kb) ? ka + 1 : ka);
   read_scales(0, 0);
   frags(sbase, ka, 0, 0);
   do {
@@ -352,15 +351,15 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     if constexpr (TAIL)
       mx_wait_loads();
     else
-      mx_wait_loads<(NST - 2) * S::Loads>(uni(kt + NST <= kb));
+      mx_wait_loads<(NST - 2) * S::Loads>(mx_less(kt + NST, kb + 1));
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-    const int k1 = uni(kt + 1 < kb) ? kt + 1 : kt;
-    const int go = uni(kt + NST < kb);
+    const int k1 = mx_less(kt + 1, kb) ? kt + 1 : kt;
+    const int go = mx_less(kt + NST, kb);
     const int kn = go ? kt + NST : kt;
     read_scales(bn, 1);
     frags(sbase + bn * S::Stage, k1, 0, 0);
-    load_scales(uni(kt + 2 < kb) ? kt + 2 : k1);
+    load_scales(mx_less(kt + 2, kb) ? kt + 2 : k1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int ns = 0; ns < IM; ++ns) {

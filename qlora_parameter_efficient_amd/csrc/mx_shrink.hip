@@ -1,0 +1,374 @@
+// Rank-r shrinks of the MX layer, in float32: T = X A^T of an MX tensor X
+// (M x K) and U = dY B of a bf16 dY (M x N).
+//
+// Both are out[m][j] = sum_k Z[m][k] G[j][k] with G r x K row-major; for U, G
+// is B's transpose, written to the workspace by a small kernel first (B is a
+// few hundred kilobytes), so that both operands are read along k.
+//
+// Bound by the load path (Z from HBM once, r K bf16 of G from L2 per
+// workgroup); the products are a few percent of the matrix units' time.  Two
+// kernels:
+//
+// mx_shrink_tile_kernel (K % 256 == 0).  A workgroup of eight waves owns 16 H
+// rows and walks the reduction in steps of 256 columns.  The step's Z rows
+// (and scales) and G rows go straight from global memory into LDS in whole
+// lines, NST - 1 steps ahead; wave w multiplies columns 32 w .. of the step, one
+// v_mfma_f32_16x16x32_bf16 per 16 x 16 block of the output (a lane's 8 columns
+// of an MX row are converted as they are read).  16-byte chunks are swizzled by
+// row so that the 16 rows of a read fall on distinct banks.  Loads that give a
+// lane its whole block of a row touch 32 lines per instruction; the kernel
+// below, which does that, takes 12.5 us for T at M = 2048, K = 4096, r = 16
+// and 34 us for U at M = 8192, N = 4096, r = 64.
+//
+// mx_shrink_kernel (other K).  A workgroup owns 16 H rows and deals the
+// 128-column steps of the reduction to its waves; lane (q, l16) of a wave takes
+// one block of 32 columns of row l16 of each 16-row group (an MX block with
+// its scale, or 64 bytes of bf16) and the same columns of row l16 of each
+// 16-rank group of G, the 32 columns of a lane relabelled so that they are
+// contiguous.  The next step's loads are issued before this step's products.
+//
+// In both the waves' sums are added in order through LDS.
+#include "dispatch.h"
+#include "mx_tile.h"
+
+namespace lq {
+namespace {
+
+// 32 bf16 values of a lane, with MxBlock's interface
+struct BfBlock {
+  u32x4 w[4];
+  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t*) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
+  }
+  __device__ __forceinline__ u32x4 part(int d) const { return w[d]; }
+};
+template <int FZ>
+struct ZBlock {
+  typedef MxBlock<FZ> type;
+};
+template <>
+struct ZBlock<16> {
+  typedef BfBlock type;
+};
+
+template <int FZ, int JT, int H, int NW>
+__global__ __launch_bounds__(64 * NW) void mx_shrink_kernel(const uint8_t* __restrict__ Z,
+                                                            const uint8_t* __restrict__ Zs,
+                                                            int64_t M, int64_t K,
+                                                            const uint16_t* __restrict__ G, int r,
+                                                            float* __restrict__ out) {
+  __shared__ f32x4 part[NW][H * JT][64];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int l16 = lane & 15, q = lane >> 4;
+  const int64_t m0 = 16 * H * (int64_t)blockIdx.x;
+  const int blocks = (int)(K / 32), steps = (blocks + 3) / 4;
+  const int64_t pitch = K * FZ / 8;
+  const uint8_t *zr[H], *sr[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    int64_t m = m0 + 16 * h + l16;
+    m = m < M ? m : M - 1;
+    zr[h] = Z + m * pitch;
+    sr[h] = FZ == 16 ? nullptr : Zs + m * blocks;
+  }
+  const uint16_t* gr[JT];
+#pragma unroll
+  for (int j = 0; j < JT; ++j) {
+    const int row = 16 * j + l16 < r ? 16 * j + l16 : r - 1;
+    gr[j] = G + (int64_t)row * K;
+  }
+  struct In {
+    typename ZBlock<FZ>::type z[H];
+    u32x4 g[JT][4];
+  };
+  // a lane whose block is past the row reads block 0 and is masked below
+  auto load = [&](int t, In& in) {
+    int b = 4 * t + q;
+    b = b < blocks ? b : 0;
+#pragma unroll
+    for (int h = 0; h < H; ++h) in.z[h].load(zr[h] + (int64_t)b * (4 * FZ), FZ == 16 ? nullptr : sr[h] + b);
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        in.g[j][d] = *reinterpret_cast<const u32x4*>(gr[j] + 32 * b + 8 * d);
+  };
+  f32x4 acc[H][JT];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc[h][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto products = [&](int t, const In& in) {
+    const bool ok = 4 * t + q < blocks;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const u32x4 zf = sel4(ok, in.z[h].part(d));
+#pragma unroll
+        for (int j = 0; j < JT; ++j) acc[h][j] = mfma16(zf, sel4(ok, in.g[j][d]), acc[h][j]);
+      }
+  };
+  if (wave < steps) {  // uniform
+    In in[2];
+    load(wave, in[0]);
+    for (int t = wave;; t += 2 * NW) {
+      const int t1 = t + NW, t2 = t + 2 * NW;
+      load(t1 < steps ? t1 : t, in[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      products(t, in[0]);
+      if (t1 >= steps) break;
+      load(t2 < steps ? t2 : t1, in[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      products(t1, in[1]);
+      if (t2 >= steps) break;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) part[wave][h * JT + j][lane] = acc[h][j];
+  __syncthreads();
+  for (int c = wave; c < H * JT; c += NW) {
+    f32x4 s = part[0][c][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const f32x4 o = part[w][c][lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += o[i];
+    }
+    const int h = c / JT, j = 16 * (c - h * JT) + l16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + 16 * h + 4 * q + i;
+      if (m < M && j < r) out[m * r + j] = s[i];
+    }
+  }
+}
+
+// -------------------------------------------------------------- K % 256 == 0
+template <int FZ, int JT, int H>
+struct TileShape {
+  static constexpr int NW = 8;
+  static constexpr int ZRow = 256 * FZ / 8, ZBytes = 16 * H * ZRow;
+  static constexpr int GBytes = 16 * JT * 512;
+  static constexpr int SBytes = FZ == 16 ? 0 : 256;       // 8 scale bytes a row, 32 rows
+  static constexpr int Stage = ZBytes + GBytes + SBytes;
+  static constexpr int NST = 4 * Stage <= 80 * 1024 ? 4 : 3;
+  static constexpr int Red = NW * H * JT * 64 * 16;       // the waves' sums
+  static constexpr int Used = NST * Stage + 1024;         // and a place for spare loads
+  static constexpr int Smem = Used > Red ? Used : Red;
+  static constexpr int ZI = ZBytes / 1024, ZU = (ZI + NW - 1) / NW;  // loads per step, per wave
+  static constexpr int Loads = ZU + JT + (FZ == 16 ? 0 : 1);
+};
+
+template <int FZ, int JT, int H>
+__global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __restrict__ Z,
+                                                             const uint8_t* __restrict__ Zs,
+                                                             int64_t M, int64_t K,
+                                                             const uint16_t* __restrict__ G, int r,
+                                                             float* __restrict__ out) {
+  using S = TileShape<FZ, JT, H>;
+  constexpr int NST = S::NST, ZC = S::ZRow / 16;  // chunks per Z row
+  __shared__ __attribute__((aligned(1024))) char smem[S::Smem];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int64_t m0 = 16 * H * (int64_t)blockIdx.x;
+  const int64_t zpitch = K * FZ / 8;
+  const int steps = (int)(K / 256);
+  const uint32_t sbase = mx_lds_addr(smem);
+  auto zswz = [](int row) { return ZC == 8 ? mx_swz128(row) : row & 15; };
+
+  // load offsets relative to the step; Z load i covers 1024 / ZRow rows, G load
+  // i rows 2 i and 2 i + 1, and wave 0 loads the scales.  Every wave makes the
+  // same number of loads (its waits count them); a spare one reads one address
+  // with all its lanes, into a place of its own.
+  uint32_t goff[JT];
+  int64_t zoff[S::ZU];
+  int zi[S::ZU];
+#pragma unroll
+  for (int u = 0; u < S::ZU; ++u) {
+    zi[u] = wave * S::ZU + u;
+    const int row = zi[u] * (1024 / S::ZRow) + lane / ZC;
+    int64_t m = m0 + row;
+    m = m < M ? m : M - 1;
+    zoff[u] = zi[u] < S::ZI ? m * zpitch + 16 * ((lane % ZC) ^ zswz(row)) : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < JT; ++u) {
+    const int row = 2 * (wave * JT + u) + (lane >> 5);
+    const int j = row < r ? row : r - 1;
+    goff[u] = (uint32_t)((int64_t)j * K * 2 + 16 * ((lane & 31) ^ (row & 15)));
+  }
+  uint32_t soff = 0;
+  if (FZ != 16) {
+    int64_t m = m0 + (lane >> 1) % (16 * H);
+    m = m < M ? m : M - 1;
+    soff = wave == 0 ? (uint32_t)(m * (K / 32) + 4 * (lane & 1)) : 0u;
+  }
+  const uint32_t spare = sbase + NST * S::Stage;
+  auto issue = [&](int t, int b, int go) {
+    const uint32_t st = sbase + b * S::Stage;
+#pragma unroll
+    for (int u = 0; u < S::ZU; ++u)
+      mx_dma16(reinterpret_cast<const char*>(Z) + (int64_t)t * S::ZRow, (uint32_t)zoff[u],
+               zi[u] < S::ZI ? st + zi[u] * 1024 : spare, go);
+#pragma unroll
+    for (int u = 0; u < JT; ++u)
+      mx_dma16(reinterpret_cast<const char*>(G) + (int64_t)t * 512, goff[u],
+               st + S::ZBytes + (wave * JT + u) * 1024, go);
+    if (FZ != 16)
+      mx_dma4(Zs + (int64_t)t * 8, soff, wave == 0 ? st + S::ZBytes + S::GBytes : spare, go);
+  };
+
+  f32x4 acc[H][JT];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc[h][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int t = 0; t < NST - 1; ++t) {
+    const int go = mx_less(t, steps);
+    issue(go ? t : 0, t, go);
+  }
+  int b = 0;
+  for (int t = 0; t < steps; ++t) {
+    // step t has landed (those after it may be on their way), and every wave
+    // has read step t - 1, whose stage the next loads take
+    mx_wait_loads<(NST - 2) * S::Loads>(mx_less(t + NST - 1, steps + 1));
+    __syncthreads();
+    {
+      const int go = mx_less(t + NST - 1, steps);
+      issue(go ? t + NST - 1 : t, b == 0 ? NST - 1 : b - 1, go);
+    }
+    const char* st = smem + b * S::Stage;
+    u32x4 zf[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int row = 16 * h + l16;
+      const char* zr = st + row * S::ZRow;
+      if (FZ == 16) {
+        zf[h] = *reinterpret_cast<const u32x4*>(zr + 16 * ((4 * wave + q) ^ zswz(row)));
+      } else {
+        const float sc =
+            mx_scale(*reinterpret_cast<const uint8_t*>(st + S::ZBytes + S::GBytes + 8 * row + wave));
+        if (FZ == LQ_MX_FP8) {
+          const u32x2 w = *reinterpret_cast<const u32x2*>(
+              zr + 16 * ((2 * wave + (q >> 1)) ^ zswz(row)) + 8 * (q & 1));
+          zf[h] = mx8_bf16(w[0], w[1], sc);
+        } else {
+          zf[h] = mx4_bf16(*reinterpret_cast<const uint32_t*>(zr + 16 * (wave ^ zswz(row)) + 4 * q),
+                           sc);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+      const u32x4 gf = *reinterpret_cast<const u32x4*>(
+          st + S::ZBytes + (16 * j + l16) * 512 + 16 * ((4 * wave + q) ^ l16));
+#pragma unroll
+      for (int h = 0; h < H; ++h) acc[h][j] = mfma16(zf[h], gf, acc[h][j]);
+    }
+    b = b + 1 == NST ? 0 : b + 1;
+  }
+  __syncthreads();  // the sums overwrite the stages
+  f32x4(*part)[H * JT][64] = reinterpret_cast<f32x4(*)[H * JT][64]>(smem);
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) part[wave][h * JT + j][lane] = acc[h][j];
+  __syncthreads();
+  for (int c = wave; c < H * JT; c += S::NW) {
+    f32x4 s = part[0][c][lane];
+#pragma unroll
+    for (int w = 1; w < S::NW; ++w) {
+      const f32x4 o = part[w][c][lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += o[i];
+    }
+    const int h = c / JT, j = 16 * (c - h * JT) + l16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + 16 * h + 4 * q + i;
+      if (m < M && j < r) out[m * r + j] = s[i];
+    }
+  }
+}
+
+// Bt[j][n] = B[n][j]: 64 rows of B per workgroup through LDS
+__global__ __launch_bounds__(256) void mx_transpose_kernel(const uint16_t* __restrict__ B,
+                                                           int64_t N, int r,
+                                                           uint16_t* __restrict__ Bt) {
+  __shared__ uint16_t t[64 * 65];
+  const int64_t n0 = 64 * (int64_t)blockIdx.x;  // N % 64 == 0
+  for (int e = threadIdx.x; e < 64 * r; e += 256) {
+    const int n = e / r, j = e - n * r;
+    t[j * 65 + n] = B[n0 * r + e];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < 64 * r; e += 256) Bt[(int64_t)(e >> 6) * N + n0 + (e & 63)] = t[(e >> 6) * 65 + (e & 63)];
+}
+
+// Rows per workgroup: 16 while that fills the chip, 32 beyond (G is read half
+// as often)
+template <int FZ, int JT, int NW>
+void launch_rows(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const uint16_t* G, int r,
+                 float* out, hipStream_t st) {
+  const uint8_t* z = (const uint8_t*)Z;
+  const bool wide = M > 4096;
+  const dim3 grid((unsigned)cdiv(M, wide ? 32 : 16));
+  if (K % 256 == 0) {
+    if (wide)
+      hipLaunchKernelGGL((mx_shrink_tile_kernel<FZ, JT, 2>), grid, dim3(512), 0, st, z, Zs, M, K,
+                         G, r, out);
+    else
+      hipLaunchKernelGGL((mx_shrink_tile_kernel<FZ, JT, 1>), grid, dim3(512), 0, st, z, Zs, M, K,
+                         G, r, out);
+  } else if (wide) {
+    hipLaunchKernelGGL((mx_shrink_kernel<FZ, JT, 2, NW>), grid, dim3(64 * NW), 0, st, z, Zs, M, K,
+                       G, r, out);
+  } else {
+    hipLaunchKernelGGL((mx_shrink_kernel<FZ, JT, 1, NW>), grid, dim3(64 * NW), 0, st, z, Zs, M, K,
+                       G, r, out);
+  }
+}
+
+template <int FZ>
+int launch_z(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const uint16_t* G, int64_t r,
+             float* out, hipStream_t st) {
+  if (r <= 16)
+    launch_rows<FZ, 1, 16>(Z, Zs, M, K, G, (int)r, out, st);
+  else if (r <= 32)
+    launch_rows<FZ, 2, 8>(Z, Zs, M, K, G, (int)r, out, st);
+  else
+    launch_rows<FZ, 4, 8>(Z, Zs, M, K, G, (int)r, out, st);
+  return hip_fail(hipGetLastError(), "mx_shrink launch");
+}
+
+}  // namespace
+
+namespace dispatch {
+
+int mx_shrink(const lq_mx_tensor& X, const void* A, int64_t r, float* T, hipStream_t st) {
+  return X.format == LQ_MX_FP8
+             ? launch_z<LQ_MX_FP8>(X.codes, X.scales, X.rows, X.cols, (const uint16_t*)A, r, T, st)
+             : launch_z<LQ_MX_FP4>(X.codes, X.scales, X.rows, X.cols, (const uint16_t*)A, r, T, st);
+}
+
+int mx_u(const void* dY, int64_t M, int64_t N, const void* B, int64_t r, void* Bt, float* U,
+         hipStream_t st) {
+  const void* G = B;
+  if (r > 1) {  // one rank: B is its own transpose
+    hipLaunchKernelGGL(mx_transpose_kernel, dim3((unsigned)(N / 64)), dim3(256), 0, st,
+                       (const uint16_t*)B, N, (int)r, (uint16_t*)Bt);
+    const int e = hip_fail(hipGetLastError(), "mx_transpose launch");
+    if (e) return e;
+    G = Bt;
+  }
+  return launch_z<16>(dY, nullptr, M, N, (const uint16_t*)G, r, U, st);
+}
+
+}  // namespace dispatch
+}  // namespace lq

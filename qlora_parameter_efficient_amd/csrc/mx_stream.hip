@@ -1,5 +1,4 @@
-// Forward of few rows (M <= 64, bf16 activations) on an MXFP4 base, and the
-// rank-r shrink of an MX tensor.
+// Forward of few rows (M <= 64, bf16 activations) on an MXFP4 base.
 //
 //   Y = X W^T + s T B^T,  T = X A^T
 //
@@ -181,106 +180,9 @@ __global__ __launch_bounds__(64 * kWaves) void mx_stream_kernel(StreamParams p) 
       u32x2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 }
 
-// ----------------------------------------------------- T of an MX tensor
-// A workgroup of eight waves owns 32 rows m; lane (q, l16) takes rows l16 and
-// 16 + l16 and block 4 t + q, t = wave, wave + 8, ...; the waves' sums are
-// added in order through LDS.  HBM-bound on X (A comes from L2).
-template <int FMT, int JT>
-__global__ __launch_bounds__(512) void mx_shrink_kernel(const uint8_t* __restrict__ codes,
-                                                        const uint8_t* __restrict__ scales,
-                                                        int64_t M, int64_t K,
-                                                        const uint16_t* __restrict__ A, int r,
-                                                        float* __restrict__ T) {
-  __shared__ f32x4 part[8][2 * JT][64];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int l16 = lane & 15, q = lane >> 4;
-  const int64_t m0 = 32 * (int64_t)blockIdx.x;
-  const int64_t G = K / 32, steps = (G + 3) / 4;
-  const int64_t pitch = K * FMT / 8;
-  const uint8_t *cr[2], *sr[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    int64_t m = m0 + 16 * h + l16;
-    m = m < M ? m : M - 1;
-    cr[h] = codes + m * pitch;
-    sr[h] = scales + m * G;
-  }
-  f32x4 acc[2][JT];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) acc[h][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t t = wave; t < steps; t += 8) {
-    const int64_t g = 4 * t + q;
-    const bool ok = g < G;
-    const int64_t gb = ok ? g : 0;
-    MxBlock<FMT> x[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) x[h].load(cr[h] + gb * (4 * FMT), sr[h] + gb);
-    u32x4 af[JT][4];
-#pragma unroll
-    for (int j = 0; j < JT; ++j) {
-      const int row = 16 * j + l16 < r ? 16 * j + l16 : r - 1;
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        af[j][d] = sel4(ok, *reinterpret_cast<const u32x4*>(A + (int64_t)row * K + 32 * gb + 8 * d));
-    }
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x4 xf = sel4(ok, x[h].part(d));
-#pragma unroll
-        for (int j = 0; j < JT; ++j) acc[h][j] = mfma16(xf, af[j][d], acc[h][j]);
-      }
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < JT; ++j) part[wave][h * JT + j][lane] = acc[h][j];
-  __syncthreads();
-  for (int c = wave; c < 2 * JT; c += 8) {
-    f32x4 s = part[0][c][lane];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) {
-      const f32x4 o = part[w][c][lane];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += o[i];
-    }
-    const int h = c / JT, j = 16 * (c - h * JT) + l16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + 16 * h + 4 * q + i;
-      if (m < M && j < r) T[m * r + j] = s[i];
-    }
-  }
-}
-
-template <int FMT>
-void launch_mx_shrink(const lq_mx_tensor& X, const uint16_t* A, int r, float* T, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(X.rows, 32)), block(512);
-  if (r <= 16)
-    hipLaunchKernelGGL((mx_shrink_kernel<FMT, 1>), grid, block, 0, st, X.codes, X.scales, X.rows,
-                       X.cols, A, r, T);
-  else if (r <= 32)
-    hipLaunchKernelGGL((mx_shrink_kernel<FMT, 2>), grid, block, 0, st, X.codes, X.scales, X.rows,
-                       X.cols, A, r, T);
-  else
-    hipLaunchKernelGGL((mx_shrink_kernel<FMT, 4>), grid, block, 0, st, X.codes, X.scales, X.rows,
-                       X.cols, A, r, T);
-}
-
 }  // namespace
 
 namespace dispatch {
-
-int mx_shrink(const lq_mx_tensor& X, const void* A, int64_t r, float* T, hipStream_t st) {
-  if (X.format == LQ_MX_FP8)
-    launch_mx_shrink<LQ_MX_FP8>(X, (const uint16_t*)A, (int)r, T, st);
-  else
-    launch_mx_shrink<LQ_MX_FP4>(X, (const uint16_t*)A, (int)r, T, st);
-  return hip_fail(hipGetLastError(), "mx_shrink launch");
-}
 
 size_t mx_stream_ws_bytes(int64_t M, int64_t K, int64_t r) {
   (void)K;

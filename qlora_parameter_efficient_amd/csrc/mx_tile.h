@@ -11,6 +11,15 @@ __device__ __forceinline__ uint32_t mx_lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
+// 1 if a < b, else 0, for uniform a and b less than 2^31 apart, in a scalar
+// register: a comparison the compiler sees may end up in a vector register,
+// which the scalar operands of the asm below do not take.
+__device__ __forceinline__ int mx_less(int a, int b) {
+  int o;
+  asm("s_sub_i32 %0, %1, %2\n\ts_lshr_b32 %0, %0, 31" : "=&s"(o) : "s"(a), "s"(b) : "scc");
+  return o;
+}
+
 // 16 bytes per lane from global memory (base + off) to LDS at lds + 16 lane.
 // Issued from asm so that the compiler does not make later LDS reads of the
 // other stage wait for it; the kernel waits itself (mx_wait_loads) before the
