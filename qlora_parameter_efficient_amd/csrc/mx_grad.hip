@@ -13,13 +13,18 @@
 // of two, but for values below 2^-126), so every product is exact and only
 // the float32 sums round.  (The parts of an infinite or NaN v are v, 0, 0.)
 //
-// HBM-bound on Z (1.03 bytes per element of X in MXFP8, 2 of dY).  A workgroup
-// takes 128 columns of Z and a range of rows in steps of 64: the rows' codes
-// (one block of 32 per thread) or bf16 values are loaded several steps ahead,
-// converted to bf16 and stored in LDS in storage order with the step's V
-// parts beside them, and read back as MFMA operands with the row as the
-// reduction index by the transposing ds_read_b64_tr_b16.  Ranges of rows leave
-// partial sums that mx_grad_reduce_kernel adds in a fixed order: no atomics.
+// A workgroup takes TC columns of Z (256, or 128 where r <= 32) and a range of
+// rows in steps of 64.  A step's rows (MX blocks, one or two per thread, or
+// bf16 values) and its rows of V are loaded into registers two to four steps ahead,
+// converted (V into its parts) and stored in LDS in storage order during the
+// previous step's products, and read back as MFMA operands with the row as the
+// reduction index by the transposing ds_read_b64_tr_b16; two LDS buffers, one
+// barrier per step.  Small r is HBM-bound on Z (1.03 bytes per element of X in
+// MXFP8, 2 of dY); at r = 64 the three parts make 6 products per 32 x 32 block
+// and their LDS traffic is the limit, which is why the tile is 256 columns wide
+// there (the V part of a step is read once per 64 columns of a wave, not per
+// 32).  Ranges of rows leave partial sums that mx_grad_reduce_kernel adds in a
+// fixed order: no atomics.
 #include "dispatch.h"
 #include "mx.h"
 
@@ -27,7 +32,6 @@ namespace lq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileC = 128;
 
 struct MxGradJob {
   const void* Z;          // MX codes, or bf16 values
@@ -46,14 +50,17 @@ struct MxGradParams {
   int32_t blocks0;  // workgroups of job 0
 };
 
-// LDS row of one m: Z[m][c0 .. c0 + 127], then the h, m and l parts of
+// LDS row of one m: Z[m][c0 .. c0 + TC - 1], then the h, m and l parts of
 // V[m][0 .. RP - 1]; 16-byte chunk q at q ^ (m & 3).  Pitches are 64 or 192
 // bytes off a multiple of 256, so four consecutive rows of a transposing read
 // fall on distinct banks.
-template <int RP>
-struct MxGradPitch {
-  static constexpr int P = RP == 32 ? 224 : 352;  // bf16 elements
+template <int TC, int RP>
+struct MxGradShape {
+  static constexpr int Pitch = TC + 3 * RP + (RP == 64 ? 32 : 0);  // bf16 elements
+  static constexpr int Buf = 64 * Pitch;
 };
+static_assert((MxGradShape<128, 32>::Pitch * 2) % 256 == 192, "bank spread");
+static_assert((MxGradShape<256, 64>::Pitch * 2) % 256 == 192, "bank spread");
 
 typedef short s16x4g __attribute__((ext_vector_type(4)));
 
@@ -71,73 +78,84 @@ __device__ __forceinline__ void split3(float v, float& h, float& m, float& l) {
   l = fin ? (float)(__bf16)(d - m) : 0.0f;
 }
 
-// one step's share of Z per thread.  MX: thread (row = tid / 4, block =
-// tid % 4) one block of 32; bf16: chunk tid & 15 of rows tid / 16 + 16 i.
-template <int FZ>
-struct Stage;
-template <>
-struct Stage<16> {
-  u32x4 z[4];
+// one step's share of Z per thread, NS = TC / 128.  MX: blocks q + 4 i of row
+// tid / 4 (q = tid % 4); bf16: chunk tid % 16 + 16 i' of rows tid / 16 + 16 i.
+template <int FZ, int NS>
+struct Stage {
+  MxBlock<FZ> b[NS];
 };
-template <>
-struct Stage<LQ_MX_FP8> {
-  MxBlock<LQ_MX_FP8> b;
-};
-template <>
-struct Stage<LQ_MX_FP4> {
-  MxBlock<LQ_MX_FP4> b;
+template <int NS>
+struct Stage<16, NS> {
+  u32x4 z[4 * NS];
 };
 
-template <int FZ, int RP, bool V4>
+template <int FZ, int TC, int RP, bool V4>
 __device__ __forceinline__ void grad_body(const MxGradParams& p, const MxGradJob& jb, int bid,
-                                          uint16_t* tiles) {
+                                          bool by_col, uint16_t* tiles) {
+  constexpr int NS = TC / 128;
   constexpr int JT = RP / 32;
-  constexpr int PT = MxGradPitch<RP>::P;
+  constexpr int PT = MxGradShape<TC, RP>::Pitch;
   constexpr int NV = RP / 16;  // float4 chunks of V per thread and step
-  constexpr int kAhead = 4;    // steps whose loads are in flight together
+  constexpr int NZ = 4 * NS;   // 16-byte chunks of Z per thread and step
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int h = lane >> 5, l32 = lane & 31;
   const int tl = xcd_tile(bid, jb.c_tiles * jb.splits);
   const int tc = tl % jb.c_tiles, split = tl / jb.c_tiles;
   const int64_t C = jb.C, M = p.M;
-  const int64_t c0 = (int64_t)tc * kTileC;
+  const int64_t c0 = (int64_t)tc * TC;
   const int64_t mbeg = (int64_t)split * jb.rows_per_split;
   int64_t mend = mbeg + jb.rows_per_split;
   mend = mend < M ? mend : M;
   const int steps = mend > mbeg ? (int)cdiv(mend - mbeg, 64) : 0;
   const int r = p.r;
 
-  f32x16 acc[JT];
+  f32x16 acc[NS][JT];
 #pragma unroll
-  for (int jt = 0; jt < JT; ++jt)
+  for (int n = 0; n < NS; ++n)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) acc[jt][v] = 0.0f;
+    for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[n][jt][v] = 0.0f;
 
-  const int zc = tid & 15, zr = tid >> 4;   // bf16 staging
-  const int vr = tid >> 2, vq = tid & 3;    // MX staging and V staging
-  int64_t zcol = FZ == 16 ? c0 + 8 * zc : c0 + 32 * vq;
-  const bool zok = zcol < C;
-  zcol = zok ? zcol : C - (FZ == 16 ? 8 : 32);
+  const int zc = tid & 15, zr = tid >> 4;  // bf16 staging
+  const int vr = tid >> 2, vq = tid & 3;   // MX staging and V staging
+  // columns past C read the tile's first ones and are zeroed when stored
+  const char* Zb[NS];
+  const uint8_t* Sb[NS];
+  bool zok[NS];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    int64_t col = FZ == 16 ? c0 + 8 * zc + 128 * n : c0 + 32 * (vq + 4 * n);
+    zok[n] = col < C;
+    col = zok[n] ? col : c0;
+    Zb[n] = (const char*)jb.Z + col * FZ / 8;
+    Sb[n] = FZ == 16 ? nullptr : jb.Zs + col / 32;
+  }
   const int64_t zpitch = C * FZ / 8, spitch = C / 32;
-  const char* Zb = (const char*)jb.Z + zcol * FZ / 8;
-  const uint8_t* Sb = jb.Zs + zcol / 32;
 
   struct In {
-    Stage<FZ> z;
+    Stage<FZ, NS> z;
     f32x4 v[NV];
   };
-  auto load = [&](int64_t m0r, In& st) {
+  auto load = [&](int step, In& st) {
+    const int64_t m0r = mbeg + 64 * (int64_t)(step < steps ? step : steps - 1);
     if constexpr (FZ == 16) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         int64_t m = m0r + zr + 16 * i;
         m = m < mend ? m : mend - 1;
-        st.z.z[i] = *reinterpret_cast<const u32x4*>(Zb + m * zpitch);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+          st.z.z[4 * n + i] = *reinterpret_cast<const u32x4*>(Zb[n] + m * zpitch);
       }
     }
     int64_t m = m0r + vr;
     m = m < mend ? m : mend - 1;
-    if constexpr (FZ != 16) st.z.b.load((const uint8_t*)Zb + m * zpitch, Sb + m * spitch);
+    if constexpr (FZ != 16) {
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+        st.z.b[n].load((const uint8_t*)Zb[n] + m * zpitch, Sb[n] + m * spitch);
+    }
     const float* row = jb.V + m * r;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -150,35 +168,35 @@ __device__ __forceinline__ void grad_body(const MxGradParams& p, const MxGradJob
       }
     }
   };
-  auto store = [&](int64_t m0r, const In& st, uint16_t* t) {
+  // piece i of a step's stores: NZ chunks of Z, then NV chunks of V in parts
+  auto store = [&](int step, const In& st, uint16_t* t, int i) {
+    const int64_t m0r = mbeg + 64 * (int64_t)step;
     const bool vok = m0r + vr < mend;
-    if constexpr (FZ == 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int m = zr + 16 * i;
-        const bool ok = zok && m0r + m < mend;
-        *reinterpret_cast<u32x4*>(t + m * PT + 8 * (zc ^ (m & 3))) = sel4(ok, st.z.z[i]);
+    if (i < NZ) {
+      if constexpr (FZ == 16) {
+        const int m = zr + 16 * (i & 3), n = i >> 2;
+        const bool ok = zok[n] && m0r + m < mend;
+        *reinterpret_cast<u32x4*>(t + m * PT + 8 * ((zc + 16 * n) ^ (m & 3))) = sel4(ok, st.z.z[i]);
+      } else {
+        const int n = i >> 2, d = i & 3;
+        *reinterpret_cast<u32x4*>(t + vr * PT + 8 * ((4 * (vq + 4 * n) + d) ^ (vr & 3))) =
+            sel4(vok && zok[n], st.z.b[n].part(d));
       }
     } else {
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        *reinterpret_cast<u32x4*>(t + vr * PT + 8 * ((4 * vq + d) ^ (vr & 3))) =
-            sel4(vok && zok, st.z.b.part(d));
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int vc = vq + 4 * i, j0 = 4 * vc;
+      const int vc = vq + 4 * (i - NZ), j0 = 4 * vc;
       float a[3][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        split3(vok && j0 + e < r ? st.v[i][e] : 0.0f, a[0][e], a[1][e], a[2][e]);
+        split3(vok && j0 + e < r ? st.v[i - NZ][e] : 0.0f, a[0][e], a[1][e], a[2][e]);
 #pragma unroll
       for (int q = 0; q < 3; ++q)
-        *reinterpret_cast<u32x2*>(t + vr * PT + 8 * ((16 + q * (RP / 8) + (vc >> 1)) ^ (vr & 3)) +
+        *reinterpret_cast<u32x2*>(t + vr * PT +
+                                  8 * ((TC / 8 + q * (RP / 8) + (vc >> 1)) ^ (vr & 3)) +
                                   4 * (vc & 1)) =
             u32x2{pack_bf16x2(a[q][0], a[q][1]), pack_bf16x2(a[q][2], a[q][3])};
     }
   };
+  constexpr int NP = NZ + NV;
   // transposing reads: lane group g = lane / 16 of lane c = lane % 16
   const int c = lane & 15, g = lane >> 4;
   const int rbase = (32 * h + (c >> 2)) * PT + 8 * ((2 * (g & 1) + ((c >> 1) & 1)) ^ (c >> 2)) +
@@ -188,56 +206,83 @@ __device__ __forceinline__ void grad_body(const MxGradParams& p, const MxGradJob
     const u32x2 lo = lds_tr(q), hi = lds_tr(q + 4 * PT);
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
-
-  for (int s0 = 0; s0 < steps; s0 += kAhead) {
-    In st[kAhead];
+  // products of a step, the next step's stores among them
+  auto body = [&](int step, const In& nxt, int b) {
+    const uint16_t* t = tiles + b * 64 * PT;
+    uint16_t* tn = tiles + (b ^ 1) * 64 * PT;
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int sq = s0 + q < steps ? s0 + q : steps - 1;
-      load(mbeg + (int64_t)sq * 64, st[q]);
+    for (int s = 0; s < 4; ++s) {
+      u32x4 zf[NS];
+#pragma unroll
+      for (int n = 0; n < NS; ++n) zf[n] = frag(t, NS * wave + n, s);
+#pragma unroll
+      for (int jt = 0; jt < JT; ++jt)
+#pragma unroll
+        for (int part = 2; part >= 0; --part) {  // smallest first
+          const u32x4 vf = frag(t, TC / 32 + part * JT + jt, s);
+#pragma unroll
+          for (int n = 0; n < NS; ++n) acc[n][jt] = mfma32(zf[n], vf, acc[n][jt]);
+        }
+#pragma unroll
+      for (int i = NP * s / 4; i < NP * (s + 1) / 4; ++i) store(step + 1, nxt, tn, i);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    __syncthreads();
+  };
+
+  if (steps > 0) {  // uniform
+    constexpr int D = RP == 32 ? 4 : 2;  // steps loaded ahead (what the registers hold)
+    In in[D];
 #pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      if (s0 + q < steps) {  // uniform
-        uint16_t* t = tiles + (q & 1) * 64 * PT;
-        store(mbeg + (int64_t)(s0 + q) * 64, st[q], t);
-        __syncthreads();
+    for (int q = 0; q < D; ++q) load(q, in[q]);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const u32x4 zf = frag(t, wave, s);
+    for (int i = 0; i < NP; ++i) store(0, in[0], tiles, i);
+    __syncthreads();
+    for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
-          for (int jt = 0; jt < JT; ++jt)
+      for (int q = 0; q < D; ++q) {
+        if (s0 + q >= steps) break;
+        // past the last step: nothing at small r, where a range is a few steps
+        // (11 us against 12 at M = 2048, r = 16); the last step again at r >
+        // 32, where the branch costs the schedule more (79 us against 71 at M =
+        // 8192, K = 11008, N = 4096, r = 64)
+        if (RP == 64 || s0 + q + D < steps) load(s0 + q + D, in[q]);
+        body(s0 + q, in[(q + 1) % D], q & 1);
+      }
+    }
+  }
+  // acc lane l: columns c0 + 32 (NS wave + n) + 8 q + 4 h + i, rank 32 jt + l32;
+  // partial sums as [rank][column], or [column][rank] (by_col: dB's layout)
+  float* P = jb.P + (int64_t)split * r * C;
 #pragma unroll
-            for (int part = 2; part >= 0; --part)  // smallest first
-              acc[jt] = mfma32(zf, frag(t, 4 + part * JT + jt, s), acc[jt]);
+  for (int n = 0; n < NS; ++n)
+#pragma unroll
+    for (int jt = 0; jt < JT; ++jt) {
+      const int j = 32 * jt + l32;
+      if (j >= r) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t cc = c0 + 32 * (NS * wave + n) + 8 * q + 4 * h;
+        if (cc >= C) continue;  // C is a multiple of 64
+        if (by_col) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) P[(cc + i) * r + j] = acc[n][jt][4 * q + i];
+        } else {
+          *reinterpret_cast<f32x4*>(P + (int64_t)j * C + cc) =
+              f32x4{acc[n][jt][4 * q], acc[n][jt][4 * q + 1], acc[n][jt][4 * q + 2],
+                    acc[n][jt][4 * q + 3]};
         }
       }
     }
-    __syncthreads();
-  }
-  // acc[jt] lane l: columns c0 + 32 wave + 8 q + 4 h + i, rank j = 32 jt + l32
-  float* P = jb.P + (int64_t)split * r * C;
-#pragma unroll
-  for (int jt = 0; jt < JT; ++jt) {
-    const int j = 32 * jt + l32;
-    if (j >= r) continue;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t cc = c0 + 32 * wave + 8 * q + 4 * h;
-      if (cc < C)  // C is a multiple of 64
-        *reinterpret_cast<f32x4*>(P + (int64_t)j * C + cc) =
-            f32x4{acc[jt][4 * q], acc[jt][4 * q + 1], acc[jt][4 * q + 2], acc[jt][4 * q + 3]};
-    }
-  }
 }
 
-template <int FX, int RP, bool V4>
+template <int FX, int TC, int RP, bool V4>
 __global__ __launch_bounds__(kThreads) void mx_grad_kernel(MxGradParams p) {
-  __shared__ __attribute__((aligned(16))) uint16_t tiles[2 * 64 * MxGradPitch<RP>::P];
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[2 * MxGradShape<TC, RP>::Buf];
   if ((int)blockIdx.x < p.blocks0)
-    grad_body<FX, RP, V4>(p, p.job[0], blockIdx.x, tiles);
+    grad_body<FX, TC, RP, V4>(p, p.job[0], blockIdx.x, false, tiles);
   else
-    grad_body<16, RP, V4>(p, p.job[1], blockIdx.x - p.blocks0, tiles);
+    grad_body<16, TC, RP, V4>(p, p.job[1], blockIdx.x - p.blocks0, true, tiles);
 }
 
 struct MxReduceParams {
@@ -250,56 +295,63 @@ struct MxReduceParams {
   int32_t accumulate;
 };
 
-// out = s sum_split P[split] (+ out): dA (out[j][c]) then dB (out[c][j]), the
-// splits in four interleaved chains (split t in chain t % 4), then pairwise
+// out = s sum_split P[split] (+ out), dA's elements then dB's, four per thread
+// (both counts are multiples of 64); the splits in two interleaved chains
 __global__ __launch_bounds__(256) void mx_grad_reduce_kernel(MxReduceParams p) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t idx = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   const int64_t t0 = (int64_t)p.r * p.C[0];
   const int jb = idx < t0 ? 0 : 1;
   const int64_t total = (int64_t)p.r * p.C[jb];
   const int64_t i = jb ? idx - t0 : idx;
   if (i >= total) return;
-  int64_t src = i;
-  if (jb) {
-    const int64_t c = i / p.r;
-    src = (i - c * p.r) * p.C[1] + c;
-  }
-  const float* P = p.P[jb] + src;
+  const float* P = p.P[jb] + i;
   const int ns = p.splits[jb];
-  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 a[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
   int t = 0;
   for (; t + 4 <= ns; t += 4) {
-    float v[4];
+    f32x4 v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = P[(int64_t)(t + u) * total];
+    for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const f32x4*>(P + (int64_t)(t + u) * total);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) a[u] += v[u];
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[u & 1][e] += v[u][e];
   }
+  for (; t < ns; ++t) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(P + (int64_t)t * total);
 #pragma unroll
-  for (int u = 0; u < 3; ++u)
-    if (t + u < ns) a[u] += P[(int64_t)(t + u) * total];
-  float v = p.s * ((a[0] + a[1]) + (a[2] + a[3]));
-  if (p.accumulate) v += p.out[jb][i];
-  p.out[jb][i] = v;
+    for (int e = 0; e < 4; ++e) a[t & 1][e] += v[e];
+  }
+  float* o = p.out[jb] + i;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float v = p.s * (a[0][e] + a[1][e]);
+    if (p.accumulate) v += o[e];
+    o[e] = v;
+  }
 }
 
-// ranges of rows: about 512 workgroups per output, at least 256 rows each
-int pick_splits(int64_t M, int64_t C) {
-  int64_t want = cdiv(512, cdiv(C, kTileC));
+int tile_cols(int64_t r) { return r <= 32 ? 128 : 256; }
+
+// Ranges of rows: at most 512 (r <= 32: two workgroups fit a compute unit) or
+// 256 workgroups per output, so that no partly filled round follows, and at
+// least 256 rows each.
+int pick_splits(int64_t M, int64_t C, int64_t r) {
+  int64_t want = (r <= 32 ? 512 : 256) / cdiv(C, tile_cols(r));
   const int64_t most = cdiv(M, 256);
   if (want > most) want = most;
   return want < 1 ? 1 : (int)want;
 }
 
 void set_job(MxGradJob& j, const void* Z, const uint8_t* Zs, const float* V, int64_t M, int64_t C,
-             float* P) {
+             int64_t r, float* P) {
   j.Z = Z;
   j.Zs = Zs;
   j.V = V;
   j.P = P;
   j.C = C;
-  j.c_tiles = (int32_t)cdiv(C, kTileC);
-  j.splits = pick_splits(M, C);
+  j.c_tiles = (int32_t)cdiv(C, tile_cols(r));
+  j.splits = pick_splits(M, C, r);
   j.rows_per_split = cdiv(cdiv(M, j.splits), 64) * 64;
 }
 
@@ -309,14 +361,14 @@ void launch_grads(const MxGradParams& p, unsigned blocks, hipStream_t st) {
   const bool v4 = p.r % 4 == 0;
   if (p.r <= 32) {
     if (v4)
-      hipLaunchKernelGGL((mx_grad_kernel<FX, 32, true>), grid, block, 0, st, p);
+      hipLaunchKernelGGL((mx_grad_kernel<FX, 128, 32, true>), grid, block, 0, st, p);
     else
-      hipLaunchKernelGGL((mx_grad_kernel<FX, 32, false>), grid, block, 0, st, p);
+      hipLaunchKernelGGL((mx_grad_kernel<FX, 128, 32, false>), grid, block, 0, st, p);
   } else {
     if (v4)
-      hipLaunchKernelGGL((mx_grad_kernel<FX, 64, true>), grid, block, 0, st, p);
+      hipLaunchKernelGGL((mx_grad_kernel<FX, 256, 64, true>), grid, block, 0, st, p);
     else
-      hipLaunchKernelGGL((mx_grad_kernel<FX, 64, false>), grid, block, 0, st, p);
+      hipLaunchKernelGGL((mx_grad_kernel<FX, 256, 64, false>), grid, block, 0, st, p);
   }
 }
 
@@ -325,7 +377,7 @@ void launch_grads(const MxGradParams& p, unsigned blocks, hipStream_t st) {
 namespace dispatch {
 
 size_t mx_grad_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
-  return (size_t)(pick_splits(M, K) * r * K + pick_splits(M, N) * r * N) * 4;
+  return (size_t)(pick_splits(M, K, r) * r * K + pick_splits(M, N, r) * r * N) * 4;
 }
 
 int mx_grads(const lq_mx_tensor& X, const float* U, const void* dY, const float* T, int64_t N,
@@ -334,9 +386,9 @@ int mx_grads(const lq_mx_tensor& X, const float* U, const void* dY, const float*
   const int64_t M = X.rows, K = X.cols;
   MxGradParams p;
   float* PA = (float*)part;
-  float* PB = PA + (int64_t)pick_splits(M, K) * r * K;
-  set_job(p.job[0], X.codes, X.scales, U, M, K, PA);
-  set_job(p.job[1], dY, nullptr, T, M, N, PB);
+  float* PB = PA + (int64_t)pick_splits(M, K, r) * r * K;
+  set_job(p.job[0], X.codes, X.scales, U, M, K, r, PA);
+  set_job(p.job[1], dY, nullptr, T, M, N, r, PB);
   p.M = M;
   p.r = (int32_t)r;
   p.blocks0 = p.job[0].c_tiles * p.job[0].splits;
@@ -359,7 +411,7 @@ int mx_grads(const lq_mx_tensor& X, const float* U, const void* dY, const float*
   q.r = (int32_t)r;
   q.s = s;
   q.accumulate = accumulate;
-  hipLaunchKernelGGL(mx_grad_reduce_kernel, dim3((unsigned)cdiv(r * (K + N), 256)), dim3(256), 0,
+  hipLaunchKernelGGL(mx_grad_reduce_kernel, dim3((unsigned)cdiv(r * (K + N), 1024)), dim3(256), 0,
                      st, q);
   return hip_fail(hipGetLastError(), "mx_grad_reduce launch");
 }
