@@ -7,7 +7,6 @@ and raises LqError on a negative status.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -85,26 +84,21 @@ def _want(cond, msg):
         raise ValueError(msg)
 
 
-def _same_device(dev, *ts):
-    for t in ts:
-        if t is not None:
-            if not t.is_cuda or t.device != dev:
-                raise ValueError("tensors must be on one GPU")
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous")
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_DT = {_BF16: lq.LQ_BF16, _F32: lq.LQ_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else lambda i: torch.cuda.current_stream(i).cuda_stream
 
 
-def _tensor(t, dtype, shape, what):
-    if t is not None and (t.dtype != dtype or t.shape != shape):
-        raise ValueError(f"{what}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-
-
-def _on(dev):
-    """Context that makes dev the current device (nothing when it already is)."""
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _is(t, dtype, shape, dev, what):
+    """Checks an operand (decode calls are a few microseconds: no helper calls
+    on the way that passes)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{what}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        raise ValueError(f"{what}: tensors must be contiguous and on one GPU")
+    return t.data_ptr()
 
 
 @functools.lru_cache(maxsize=512)
@@ -117,129 +111,146 @@ def lq_mx_workspace_size(op, M, N, K, r):
     return int(lib().lq_mx_workspace_size(op, M, N, K, r))
 
 
-def mx_struct(q: MxTensor, dev):
-    _same_device(dev, q.codes, q.scales)
-    fmt = FORMATS[q.format]
-    if q.codes.dtype != torch.uint8 or q.scales.dtype != torch.uint8:
-        raise ValueError("MX codes and scales are uint8 tensors")
-    if (q.codes.numel(), q.scales.numel()) != _buffer_bytes(fmt, q.rows, q.cols):
-        raise ValueError(f"MX buffers do not hold a {q.rows} x {q.cols} {q.format} tensor")
-    return LqMxStruct(fmt, 0, q.rows, q.cols, q.codes.data_ptr(), q.scales.data_ptr())
+def mx_struct(q: MxTensor, dev: int):
+    """C descriptor of q after checking its buffers (dev: the GPU's index)."""
+    fmt, rows, cols = FORMATS[q.format], q.rows, q.cols
+    codes, scales = q.codes, q.scales
+    if (codes.dtype is not _U8 or scales.dtype is not _U8 or codes.get_device() != dev
+            or scales.get_device() != dev or not codes.is_contiguous()
+            or not scales.is_contiguous()):
+        raise ValueError("MX codes and scales are contiguous uint8 tensors on one GPU")
+    if (codes.numel(), scales.numel()) != _buffer_bytes(fmt, rows, cols):
+        raise ValueError(f"MX buffers do not hold a {rows} x {cols} {q.format} tensor")
+    return LqMxStruct(fmt, 0, rows, cols, codes.data_ptr(), scales.data_ptr())
 
 
-def _workspace(ws, op, M, N, K, r, dev):
+def _workspace(ws, op, M, N, K, r, like, dev):
     """(tensor that keeps it alive, pointer, bytes); ``ws`` is the caller's, or None."""
     if ws is None:
         need = lq_mx_workspace_size(op, M, N, K, r)
         if need == 0:
             return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
-        _same_device(dev, ws)
+        ws = like.new_empty(need, dtype=_U8)
+        return ws, ws.data_ptr(), need
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: tensors must be contiguous and on one GPU")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(dev, fn, *args):
+    """fn(*args) with dev, the GPU its tensors are on, as the current device."""
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 # ------------------------------------------------------------------ calls
 
 def lq_mx_quantize(X: torch.Tensor, format: str = "fp8") -> MxTensor:
-    dev = X.device
-    _same_device(dev, X)
-    _want(X.dim() == 2, "X must be a matrix")
+    dev = X.get_device()
+    if dev != _current():
+        return _elsewhere(dev, lq_mx_quantize, X, format)
+    if X.dim() != 2 or X.dtype not in _DT or not X.is_contiguous():
+        raise ValueError("X must be a contiguous bf16 or float32 matrix")
     rows, cols = X.shape
     kb = -(-cols // LQ_MX_BLOCK)
     fmt = FORMATS[format]
-    with _on(dev):
-        codes = torch.empty((rows, kb * 4 * fmt), dtype=torch.uint8, device=dev)
-        scales = torch.empty((rows, kb), dtype=torch.uint8, device=dev)
-        _check(lib().lq_mx_quantize(X.data_ptr(), lq._dt(X), rows, cols, fmt, codes.data_ptr(),
-                                    scales.data_ptr(), lq._stream()))
+    codes = X.new_empty((rows, kb * 4 * fmt), dtype=_U8)
+    scales = X.new_empty((rows, kb), dtype=_U8)
+    _check(lib().lq_mx_quantize(X.data_ptr(), _DT[X.dtype], rows, cols, fmt, codes.data_ptr(),
+                                scales.data_ptr(), _raw_stream(dev)))
     return MxTensor(codes, scales, rows, cols, format)
 
 
 def lq_mx_dequantize(q: MxTensor, dtype=torch.bfloat16) -> torch.Tensor:
-    dev = q.codes.device
+    dev = q.codes.get_device()
+    if dev != _current():
+        return _elsewhere(dev, lq_mx_dequantize, q, dtype)
     s = mx_struct(q, dev)
-    _want(dtype in (torch.bfloat16, torch.float32), f"unsupported dtype {dtype}")
-    with _on(dev):
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=dev)
-        _check(lib().lq_mx_dequantize(ctypes.byref(s), out.data_ptr(), lq._dt(out), lq._stream()))
+    _want(dtype in _DT, f"unsupported dtype {dtype}")
+    out = q.codes.new_empty((q.rows, q.cols), dtype=dtype)
+    _check(lib().lq_mx_dequantize(ctypes.byref(s), out.data_ptr(), _DT[dtype], _raw_stream(dev)))
     return out
 
 
-def _adapter(A, B, N, K):
-    r = 0 if A is None else A.shape[0]
-    _tensor(A, torch.bfloat16, (r, K), "A")
-    if (A is None) != (B is None):
-        raise ValueError("A and B must both be given or both be None")
-    _tensor(B, torch.bfloat16, (N, r), "B")
-    return r
+def _adapter(A, B, N, K, dev):
+    """(rank, pointers of A and B)"""
+    if A is None or B is None:
+        _want(A is None and B is None, "A and B must both be given or both be None")
+        return 0, None, None
+    r = A.shape[0]
+    return r, _is(A, _BF16, (r, K), dev, "A"), _is(B, _BF16, (N, r), dev, "B")
 
 
 def lq_mx_lora_fwd(X, W0: MxTensor, A=None, B=None, scale=0.0, T_out=None, ws=None, Y=None):
     """X: a bf16 matrix (at most LQ_MX_ROWS_BF16 rows) or an MxTensor; A and B
     None: no adapter."""
-    dev = W0.codes.device
+    dev = W0.codes.get_device()
+    if dev != _current():
+        return _elsewhere(dev, lq_mx_lora_fwd, X, W0, A, B, scale, T_out, ws, Y)
     w = mx_struct(W0, dev)
     N, K = W0.rows, W0.cols
     if isinstance(X, MxTensor):
-        M = X.rows
+        M, like = X.rows, X.codes
         xq, xp = ctypes.byref(mx_struct(X, dev)), None
         _want(X.cols == K, f"X has {X.cols} columns, W0 {K}")
     else:
-        M = X.shape[0]
-        _same_device(dev, X)
-        _tensor(X, torch.bfloat16, (M, K), "X")
-        xq, xp = None, X.data_ptr()
-    r = _adapter(A, B, N, K)
-    _same_device(dev, A, B, T_out, Y)
-    _tensor(T_out, torch.float32, (M, r), "T_out")
-    _tensor(Y, torch.bfloat16, (M, N), "Y")
-    with _on(dev):
-        if Y is None:
-            Y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        ws, wp, wn = _workspace(ws, LQ_MX_OP_FWD, M, N, K, r, dev)
-        _check(lib().lq_mx_lora_fwd(xp, xq, M, ctypes.byref(w), lq._ptr(A), lq._ptr(B), r, scale,
-                                    Y.data_ptr(), lq._ptr(T_out), wp, wn, lq._stream()))
+        M, like = X.shape[0], X
+        xq, xp = None, _is(X, _BF16, (M, K), dev, "X")
+    r, ap, bp = _adapter(A, B, N, K, dev)
+    tp = None if T_out is None else _is(T_out, _F32, (M, r), dev, "T_out")
+    if Y is None:
+        Y = like.new_empty((M, N), dtype=_BF16)
+        yp = Y.data_ptr()
+    else:
+        yp = _is(Y, _BF16, (M, N), dev, "Y")
+    ws, wp, wn = _workspace(ws, LQ_MX_OP_FWD, M, N, K, r, like, dev)
+    _check(lib().lq_mx_lora_fwd(xp, xq, M, ctypes.byref(w), ap, bp, r, scale, yp, tp, wp, wn,
+                                _raw_stream(dev)))
     return Y
 
 
 def _backward(fn, op, w, N, K, dev, dY, Xq, A, B, scale, T_saved, need_dx, need_grads, dX, dA, dB,
               accumulate, ws):
     M = dY.shape[0]
-    _same_device(dev, dY, A, B, T_saved, dX, dA, dB)
-    _tensor(dY, torch.bfloat16, (M, N), "dY")
-    r = _adapter(A, B, N, K)
+    yp = _is(dY, _BF16, (M, N), dev, "dY")
+    r, ap, bp = _adapter(A, B, N, K, dev)
     _want(r > 0, "the backward needs an adapter")
-    _tensor(T_saved, torch.float32, (M, r), "T_saved")
-    _tensor(dX, torch.bfloat16, (M, K), "dX")
-    _tensor(dA, torch.float32, (r, K), "dA")
-    _tensor(dB, torch.float32, (N, r), "dB")
+    tp = None if T_saved is None else _is(T_saved, _F32, (M, r), dev, "T_saved")
     _want(not accumulate or not need_grads or (dA is not None and dB is not None),
           "accumulate needs dA and dB")
     xq = None
     if need_grads:
         _want((Xq.rows, Xq.cols) == (M, K), f"Xq is {Xq.rows} x {Xq.cols}, expected {M} x {K}")
         xq = ctypes.byref(mx_struct(Xq, dev))
+        if dA is None:
+            dA = dY.new_empty((r, K), dtype=_F32)
+        if dB is None:
+            dB = dY.new_empty((N, r), dtype=_F32)
     else:
         _want(dA is None and dB is None, "dA and dB given with need_grads=False")
-    with _on(dev):
-        if dX is None and need_dx:
-            dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-        if need_grads and dA is None:
-            dA = torch.empty((r, K), dtype=torch.float32, device=dev)
-        if need_grads and dB is None:
-            dB = torch.empty((N, r), dtype=torch.float32, device=dev)
-        ws, wp, wn = _workspace(ws, op, M, N, K, r, dev)
-        _check(fn(dY.data_ptr(), xq, M, ctypes.byref(w), A.data_ptr(), B.data_ptr(), r, scale,
-                  lq._ptr(T_saved), lq._ptr(dX), lq._ptr(dA), lq._ptr(dB), int(accumulate), wp, wn,
-                  lq._stream()))
+    if dX is None and need_dx:
+        dX = dY.new_empty((M, K), dtype=_BF16)
+    xp = None if dX is None else _is(dX, _BF16, (M, K), dev, "dX")
+    gap = None if dA is None else _is(dA, _F32, (r, K), dev, "dA")
+    gbp = None if dB is None else _is(dB, _F32, (N, r), dev, "dB")
+    ws, wp, wn = _workspace(ws, op, M, N, K, r, dY, dev)
+    _check(fn(yp, xq, M, ctypes.byref(w), ap, bp, r, scale, tp, xp, gap, gbp, int(accumulate), wp,
+              wn, _raw_stream(dev)))
     return dX, dA, dB
 
 
-def lq_mx_lora_bwd(dY, Xq, W0: MxTensor, A, B, scale, T_saved=None, need_dx=True, need_grads=True,
-                   dX=None, dA=None, dB=None, accumulate=False, ws=None):
+def lq_mx_lora_bwd(dY, Xq, W0: MxTensor, A, B, scale, T_saved=None, need_dx=True,
+                   need_grads=True, dX=None, dA=None, dB=None, accumulate=False, ws=None):
     """Xq: the MxTensor the forward multiplied (None with need_grads=False)."""
-    dev = W0.codes.device
+    dev = dY.get_device()
+    if dev != _current():
+        return _elsewhere(dev, lq_mx_lora_bwd, dY, Xq, W0, A, B, scale, T_saved, need_dx,
+                          need_grads, dX, dA, dB, accumulate, ws)
     return _backward(lib().lq_mx_lora_bwd, LQ_MX_OP_BWD, mx_struct(W0, dev), W0.rows, W0.cols, dev,
                      dY, Xq, A, B, scale, T_saved, need_dx, need_grads, dX, dA, dB, accumulate, ws)
 
@@ -248,11 +259,14 @@ def lq_lora_bwd_ckpt(dY, Xq, W0, A, B, scale, T_saved=None, need_dx=True, need_g
                      dX=None, dA=None, dB=None, accumulate=False, ws=None):
     """W0: a dense bf16 matrix or an NF4Weight; Xq: the MxTensor of the layer's
     input (None with need_grads=False)."""
-    dev = dY.device
+    dev = dY.get_device()
+    if dev != _current():
+        return _elsewhere(dev, lq_lora_bwd_ckpt, dY, Xq, W0, A, B, scale, T_saved, need_dx,
+                          need_grads, dX, dA, dB, accumulate, ws)
+    nf4 = isinstance(W0, NF4Weight)
+    for t in (W0.codes, W0.q8, W0.c2, W0.absmax) if nf4 else (W0,):
+        _want(t is None or t.get_device() == dev, "W0: tensors must be on one GPU")
+    _want(nf4 or W0.dtype is _BF16, "a dense W0 is bf16")
     w = lq.weight_struct(W0, lq.LQ_BF16)
-    for t in ((W0.codes, W0.q8, W0.c2, W0.absmax) if isinstance(W0, NF4Weight) else (W0,)):
-        _same_device(dev, t)
-    if not isinstance(W0, NF4Weight):
-        _want(W0.dtype == torch.bfloat16, "a dense W0 is bf16")
     return _backward(lib().lq_lora_bwd_ckpt, LQ_MX_OP_BWD_CKPT, w, w.N, w.K, dev, dY, Xq, A, B,
                      scale, T_saved, need_dx, need_grads, dX, dA, dB, accumulate, ws)

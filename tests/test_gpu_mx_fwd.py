@@ -36,6 +36,14 @@ def test_few_bf16_rows(M, N, K, r):
     check(M, N, K, r, "bf16")
 
 
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 128, 1), (1, 192, 4096, 16), (2, 64, 8192, 8), (3, 320, 4096, 5),
+                                     (4, 128, 4096, 16), (1, 64, 16384, 4), (1, 8256, 4736, 13),
+                                     (4, 64, 640, 2), (5, 64, 2048, 16), (1, 128, 4096, 17)])
+def test_single_tokens(M, N, K, r):
+    """T formed in the stream kernel (M <= 4, r <= 16, r K <= 65536), and just past that."""
+    check(M, N, K, r, "bf16")
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("M,N,K,r", [
     (1, 64, 64, 1), (1, 4096, 4096, 16), (7, 128, 320, 8), (33, 64, 256, 0), (64, 192, 576, 11),
