@@ -7,11 +7,14 @@
 // largest = 1.75 2^8 (E4M3) or 1.5 2^2 (E2M1), b = E - 8 (or 2), plus one
 // where the fraction exceeds that of the largest element, never below 0.
 //
-// Both kernels are bound by HBM.  A thread owns half a block (16 columns), so
-// a lane pair shares a block and one DPP move completes its amax; codes leave
-// as one 16-byte (FP8) or 8-byte (FP4) store per thread.  A tensor whose rows
-// hold whole blocks is one flat run of blocks; other widths locate each unit's
-// row and read the row's last block element by element.
+// Both kernels are bound by HBM.  Quantiser: a thread owns half a block (16
+// columns), so a lane pair shares a block and one DPP move completes its amax;
+// codes leave as one 16-byte (FP8) or 8-byte (FP4) store per thread.
+// Dequantiser: a thread owns two 16-byte pieces of the output, consecutive
+// lanes consecutive pieces (with 16 float32 of a row per thread, four stores 64
+// bytes apart, 2049 x 4095 to float32 took 15 us).  A tensor whose rows hold
+// whole blocks is one flat run; other widths locate each piece's row and
+// handle the row's end element by element.
 #include "dispatch.h"
 #include "mx.h"
 
@@ -183,70 +186,78 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void* __res
 
 typedef float f32x2v __attribute__((ext_vector_type(2)));
 
+// Output elements of a piece (16 bytes), pieces of a thread
+template <bool BF16>
+struct Piece {
+  static constexpr int E = BF16 ? 8 : 4;
+  static constexpr int N = 2;
+};
+
+// the E codes of a piece: FP8 8 or 4 bytes, FP4 4 or 2
+template <int BYTES>
+__device__ __forceinline__ u32x2 load_codes(const uint8_t* p) {
+  if (BYTES == 8) return *reinterpret_cast<const u32x2*>(p);
+  return u32x2{BYTES == 4 ? *reinterpret_cast<const uint32_t*>(p)
+                          : (uint32_t)*reinterpret_cast<const uint16_t*>(p), 0u};
+}
+
+// pieces = rows kp / E; FLAT: cols % 32 == 0, so piece u starts at element E u
 template <bool BF16, int FMT, bool FLAT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t units,
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t pieces,
     int64_t cols, int64_t per_row, void* __restrict__ out) {
-  const int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (u >= units) return;
-  uint32_t w[4];
-  if (FMT == LQ_MX_FP8) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(codes + kUnit * u);
+  constexpr int E = Piece<BF16>::E, PN = Piece<BF16>::N, CB = E * FMT / 8;
+  const int64_t u0 = (int64_t)blockIdx.x * (kThreads * PN) + threadIdx.x;
+  u32x2 w[PN];
+  uint32_t b[PN];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = v[i];
-  } else {
-    const u32x2 v = *reinterpret_cast<const u32x2*>(codes + (kUnit / 2) * u);
-    w[0] = v[0];
-    w[1] = v[1];
+  for (int i = 0; i < PN; ++i) {
+    int64_t u = u0 + kThreads * i;
+    u = u < pieces ? u : pieces - 1;
+    w[i] = load_codes<CB>(codes + CB * u);
+    b[i] = scales[u / (32 / E)];
   }
-  const float s = mx_scale(scales[u >> 1]);
-  int64_t e = kUnit * u, left = kUnit;
-  if (!FLAT) {
-    const int64_t row = u / per_row;
-    const int64_t c = (u - row * per_row) * kUnit;
-    e = row * cols + c;
-    left = cols - c;
-  }
-  if (BF16) {
-    u32x4 o[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      o[i] = FMT == LQ_MX_FP8 ? mx8_bf16(w[2 * i], w[2 * i + 1], s) : mx4_bf16(w[i], s);
-    uint16_t* dst = (uint16_t*)out + e;
-    if (FLAT || left >= kUnit) {
-      reinterpret_cast<u32x4_a2*>(dst)[0] = o[0];
-      reinterpret_cast<u32x4_a2*>(dst)[1] = o[1];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < left) dst[i] = (uint16_t)(o[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
+  for (int i = 0; i < PN; ++i) {
+    const int64_t u = u0 + kThreads * i;
+    if (u >= pieces) break;
+    const float s = mx_scale(b[i]);
+    int64_t e = E * u, left = E;
+    if (!FLAT) {
+      // (the division in 32 bits where the tensor allows: a few instructions)
+      const int64_t row = (pieces >> 32) == 0 ? (int64_t)((uint32_t)u / (uint32_t)per_row) : u / per_row;
+      const int64_t c = (u - row * per_row) * E;
+      e = row * cols + c;
+      left = cols - c;
     }
-  } else {
-    f32x4 o[4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f32x2v v;
-      if (FMT == LQ_MX_FP8) {
-        v = (i & 1) ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i >> 1], s, true)
-                    : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i >> 1], s, false);
+    if (BF16) {
+      const u32x4 o = FMT == LQ_MX_FP8 ? mx8_bf16(w[i][0], w[i][1], s) : mx4_bf16(w[i][0], s);
+      uint16_t* dst = (uint16_t*)out + e;
+      if (FLAT || left >= E) {
+        *reinterpret_cast<u32x4_a2*>(dst) = o;
       } else {
-        const int j = i & 3;
-        v = j == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i >> 2], s, 0)
-            : j == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i >> 2], s, 1)
-            : j == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i >> 2], s, 2)
-                     : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i >> 2], s, 3);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < left) dst[k] = (uint16_t)(o[k >> 1] >> (16 * (k & 1)));
       }
-      o[i >> 1][2 * (i & 1)] = v[0];
-      o[i >> 1][2 * (i & 1) + 1] = v[1];
-    }
-    float* dst = (float*)out + e;
-    if (FLAT || left >= kUnit) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) reinterpret_cast<f32x4_a4*>(dst)[i] = o[i];
     } else {
+      f32x2v lo, hi;
+      if (FMT == LQ_MX_FP8) {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i][0], s, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i][0], s, true);
+      } else {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i][0], s, 0);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i][0], s, 1);
+      }
+      const f32x4 o = f32x4{lo[0], lo[1], hi[0], hi[1]};
+      float* dst = (float*)out + e;
+      if (FLAT || left >= E) {
+        *reinterpret_cast<f32x4_a4*>(dst) = o;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < left) dst[i] = o[i >> 2][i & 3];
+        for (int k = 0; k < 4; ++k)
+          if (k < left) dst[k] = o[k];
+      }
     }
   }
 }
@@ -266,14 +277,15 @@ void launch_q(const void* X, int64_t rows, int64_t cols, uint8_t* codes, uint8_t
 
 template <bool BF16, int FMT>
 void launch_d(const lq_mx_tensor& q, void* out, hipStream_t st) {
-  const int64_t per_row = cdiv(q.cols, kMxB) * 2, units = q.rows * per_row;
-  const dim3 grid((unsigned)cdiv(units, kThreads)), block(kThreads);
+  using P = Piece<BF16>;
+  const int64_t per_row = cdiv(q.cols, kMxB) * (kMxB / P::E), pieces = q.rows * per_row;
+  const dim3 grid((unsigned)cdiv(pieces, kThreads * P::N)), block(kThreads);
   if (q.cols % kMxB == 0)
     hipLaunchKernelGGL((mx_dequantize_kernel<BF16, FMT, true>), grid, block, 0, st, q.codes,
-                       q.scales, units, q.cols, per_row, out);
+                       q.scales, pieces, q.cols, per_row, out);
   else
     hipLaunchKernelGGL((mx_dequantize_kernel<BF16, FMT, false>), grid, block, 0, st, q.codes,
-                       q.scales, units, q.cols, per_row, out);
+                       q.scales, pieces, q.cols, per_row, out);
 }
 
 }  // namespace

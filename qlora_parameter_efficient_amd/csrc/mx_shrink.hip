@@ -1,9 +1,11 @@
 // Rank-r shrinks of the MX layer, in float32: T = X A^T of an MX tensor X
 // (M x K) and U = dY B of a bf16 dY (M x N).
 //
-// Both are out[m][j] = sum_k Z[m][k] G[j][k] with G r x K row-major; for U, G
-// is B's transpose, written to the workspace by a small kernel first (B is a
-// few hundred kilobytes), so that both operands are read along k.
+// Both are out[m][j] = sum_k Z[m][k] G[j][k] with G r x K row-major.  For U, G
+// is B's transpose: where r % 4 == 0 and K % 256 == 0 the rows of B (K x r) are
+// staged as they lie and read by the transposing ds_read_b64_tr_b16; otherwise
+// a small kernel writes the transpose to the workspace first (another launch,
+// 4.7 us).
 //
 // Bound by the load path (Z from HBM once, r K bf16 of G from L2 per
 // workgroup); the products are a few percent of the matrix units' time.  Two
@@ -163,7 +165,14 @@ struct TileShape {
   static constexpr int Loads = ZU + JT + (FZ == 16 ? 0 : 1);
 };
 
-template <int FZ, int JT, int H>
+__device__ __forceinline__ u32x2 shrink_tr(const char* p) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
+}
+
+// GT: G is given as K x r (r % 4 == 0)
+template <int FZ, int JT, int H, bool GT>
 __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __restrict__ Z,
                                                              const uint8_t* __restrict__ Zs,
                                                              int64_t M, int64_t K,
@@ -198,9 +207,14 @@ __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __re
   }
 #pragma unroll
   for (int u = 0; u < JT; ++u) {
-    const int row = 2 * (wave * JT + u) + (lane >> 5);
-    const int j = row < r ? row : r - 1;
-    goff[u] = (uint32_t)((int64_t)j * K * 2 + 16 * ((lane & 31) ^ (row & 15)));
+    if (GT) {  // the step's 512 r bytes in order (past them, the first again)
+      const int at = (wave * JT + u) * 1024 + lane * 16;
+      goff[u] = (uint32_t)(at < 512 * r ? at : 0);
+    } else {
+      const int row = 2 * (wave * JT + u) + (lane >> 5);
+      const int j = row < r ? row : r - 1;
+      goff[u] = (uint32_t)((int64_t)j * K * 2 + 16 * ((lane & 31) ^ (row & 15)));
+    }
   }
   uint32_t soff = 0;
   if (FZ != 16) {
@@ -217,7 +231,7 @@ __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __re
                zi[u] < S::ZI ? st + zi[u] * 1024 : spare, go);
 #pragma unroll
     for (int u = 0; u < JT; ++u)
-      mx_dma16(reinterpret_cast<const char*>(G) + (int64_t)t * 512, goff[u],
+      mx_dma16(reinterpret_cast<const char*>(G) + (int64_t)t * 512 * (GT ? r : 1), goff[u],
                st + S::ZBytes + (wave * JT + u) * 1024, go);
     if (FZ != 16)
       mx_dma4(Zs + (int64_t)t * 8, soff, wave == 0 ? st + S::ZBytes + S::GBytes : spare, go);
@@ -266,8 +280,16 @@ __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __re
     }
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
-      const u32x4 gf = *reinterpret_cast<const u32x4*>(
-          st + S::ZBytes + (16 * j + l16) * 512 + 16 * ((4 * wave + q) ^ l16));
+      u32x4 gf;
+      if (GT) {  // lane c of a 16-lane group: row c / 4, columns 4 (c % 4) ..; gets column c
+        const char* a = st + S::ZBytes +
+                        2 * ((32 * wave + 8 * q + (l16 >> 2)) * r + 16 * j + 4 * (l16 & 3));
+        const u32x2 lo = shrink_tr(a), hi = shrink_tr(a + 8 * r);
+        gf = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      } else {
+        gf = *reinterpret_cast<const u32x4*>(st + S::ZBytes + (16 * j + l16) * 512 +
+                                             16 * ((4 * wave + q) ^ l16));
+      }
 #pragma unroll
       for (int h = 0; h < H; ++h) acc[h][j] = mfma16(zf[h], gf, acc[h][j]);
     }
@@ -313,19 +335,23 @@ __global__ __launch_bounds__(256) void mx_transpose_kernel(const uint16_t* __res
 
 // Rows per workgroup: 16 while that fills the chip, 32 beyond (G is read half
 // as often)
+// (gt: G is K x r, see mx_shrink_tile_kernel).
 template <int FZ, int JT, int NW>
 void launch_rows(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const uint16_t* G, int r,
-                 float* out, hipStream_t st) {
+                 bool gt, float* out, hipStream_t st) {
   const uint8_t* z = (const uint8_t*)Z;
   const bool wide = M > 4096;
   const dim3 grid((unsigned)cdiv(M, wide ? 32 : 16));
+  constexpr bool U = FZ == 16;
   if (K % 256 == 0) {
-    if (wide)
-      hipLaunchKernelGGL((mx_shrink_tile_kernel<FZ, JT, 2>), grid, dim3(512), 0, st, z, Zs, M, K,
-                         G, r, out);
+    auto tile = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(512), 0, st, z, Zs, M, K, G, r, out);
+    };
+    if (U && gt)
+      wide ? tile(mx_shrink_tile_kernel<FZ, JT, 2, U>) : tile(mx_shrink_tile_kernel<FZ, JT, 1, U>);
     else
-      hipLaunchKernelGGL((mx_shrink_tile_kernel<FZ, JT, 1>), grid, dim3(512), 0, st, z, Zs, M, K,
-                         G, r, out);
+      wide ? tile(mx_shrink_tile_kernel<FZ, JT, 2, false>)
+           : tile(mx_shrink_tile_kernel<FZ, JT, 1, false>);
   } else if (wide) {
     hipLaunchKernelGGL((mx_shrink_kernel<FZ, JT, 2, NW>), grid, dim3(64 * NW), 0, st, z, Zs, M, K,
                        G, r, out);
@@ -337,13 +363,13 @@ void launch_rows(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const u
 
 template <int FZ>
 int launch_z(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const uint16_t* G, int64_t r,
-             float* out, hipStream_t st) {
+             bool gt, float* out, hipStream_t st) {
   if (r <= 16)
-    launch_rows<FZ, 1, 16>(Z, Zs, M, K, G, (int)r, out, st);
+    launch_rows<FZ, 1, 16>(Z, Zs, M, K, G, (int)r, gt, out, st);
   else if (r <= 32)
-    launch_rows<FZ, 2, 8>(Z, Zs, M, K, G, (int)r, out, st);
+    launch_rows<FZ, 2, 8>(Z, Zs, M, K, G, (int)r, gt, out, st);
   else
-    launch_rows<FZ, 4, 8>(Z, Zs, M, K, G, (int)r, out, st);
+    launch_rows<FZ, 4, 8>(Z, Zs, M, K, G, (int)r, gt, out, st);
   return hip_fail(hipGetLastError(), "mx_shrink launch");
 }
 
@@ -353,21 +379,24 @@ namespace dispatch {
 
 int mx_shrink(const lq_mx_tensor& X, const void* A, int64_t r, float* T, hipStream_t st) {
   return X.format == LQ_MX_FP8
-             ? launch_z<LQ_MX_FP8>(X.codes, X.scales, X.rows, X.cols, (const uint16_t*)A, r, T, st)
-             : launch_z<LQ_MX_FP4>(X.codes, X.scales, X.rows, X.cols, (const uint16_t*)A, r, T, st);
+             ? launch_z<LQ_MX_FP8>(X.codes, X.scales, X.rows, X.cols, (const uint16_t*)A, r, false,
+                                   T, st)
+             : launch_z<LQ_MX_FP4>(X.codes, X.scales, X.rows, X.cols, (const uint16_t*)A, r, false,
+                                   T, st);
 }
 
 int mx_u(const void* dY, int64_t M, int64_t N, const void* B, int64_t r, void* Bt, float* U,
          hipStream_t st) {
   const void* G = B;
-  if (r > 1) {  // one rank: B is its own transpose
+  const bool gt = r % 4 == 0 && N % 256 == 0;
+  if (r > 1 && !gt) {  // one rank: B is its own transpose
     hipLaunchKernelGGL(mx_transpose_kernel, dim3((unsigned)(N / 64)), dim3(256), 0, st,
                        (const uint16_t*)B, N, (int)r, (uint16_t*)Bt);
     const int e = hip_fail(hipGetLastError(), "mx_transpose launch");
     if (e) return e;
     G = Bt;
   }
-  return launch_z<16>(dY, nullptr, M, N, (const uint16_t*)G, r, U, st);
+  return launch_z<16>(dY, nullptr, M, N, (const uint16_t*)G, r, gt, U, st);
 }
 
 }  // namespace dispatch
