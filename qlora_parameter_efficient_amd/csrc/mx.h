@@ -82,6 +82,10 @@ size_t mx_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 int mx_gemm(const lq_mx_tensor& X, const lq_mx_tensor& W, const float* T, const void* B,
             int64_t r, float s, void* Y, void* part, hipStream_t st);
 
+// out (bf16, n values, n % 8 == 0) = the splits' float32 partial sums, each of
+// n values, added in order
+int mx_sum_splits(const float* part, void* out, int64_t n, int splits, hipStream_t st);
+
 // dX = dY W + s U A (bf16, M x K; W MXFP4, U = dY B M x r float32); part:
 // mx_dx_ws_bytes bytes.
 size_t mx_dx_ws_bytes(int64_t M, int64_t N, int64_t K);

@@ -30,8 +30,8 @@
 // KB of operand reads and 48 or 64 KB of writes, which run at less than half
 // the read rate, against 1,024 or 2,048 cycles of products.
 //
-// Split: few tiles leave float32 partial sums of ranges of n, added in order
-// (with the expand) by mxdx_reduce_kernel.
+// Split: few tiles leave float32 partial sums of ranges of n, the
+// first with the expand, added in order by mx_sum_splits_kernel.
 #include <type_traits>
 
 #include "dispatch.h"
@@ -254,29 +254,10 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   } while (++kt < kb);
   __syncthreads();  // the output tile overwrites the stages
 
-  if constexpr (SPLIT) {
-    float* part = p.part + (int64_t)blockIdx.y * M * K;
-#pragma unroll
-    for (int ms = 0; ms < JM; ++ms) {
-      const int64_t m = j0 + 32 * JM * wj + 32 * ms + l32;
-#pragma unroll
-      for (int ns = 0; ns < 4; ++ns)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t k = i0 + 128 * wi + 32 * ns + 8 * q + 4 * h;
-          if (m < M && k < K)
-            *reinterpret_cast<f32x4*>(part + m * K + k) =
-                f32x4{acc[ns][ms][4 * q], acc[ns][ms][4 * q + 1], acc[ns][ms][4 * q + 2],
-                      acc[ns][ms][4 * q + 3]};
-        }
-    }
-    return;
-  }
-
   // ---- expand: acc += A-operand x (s U)-operand over rank chunks of 16; U is
   // rounded to bf16 after the multiply by s (one term of an output that is
   // itself rounded to bf16)
-  const int r = p.r;
+  const int r = SPLIT && blockIdx.y ? 0 : p.r;
   for (int c = 0; c < r; c += 16) {
     const int jr = c + 8 * h;
     u32x4 ef[4], vf[JM];
@@ -296,6 +277,25 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
     for (int ns = 0; ns < 4; ++ns)
 #pragma unroll
       for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(ef[ns], vf[ms], acc[ns][ms]);
+  }
+
+  if constexpr (SPLIT) {
+    float* part = p.part + (int64_t)blockIdx.y * M * K;
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) {
+      const int64_t m = j0 + 32 * JM * wj + 32 * ms + l32;
+#pragma unroll
+      for (int ns = 0; ns < 4; ++ns)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t k = i0 + 128 * wi + 32 * ns + 8 * q + 4 * h;
+          if (m < M && k < K)
+            *reinterpret_cast<f32x4*>(part + m * K + k) =
+                f32x4{acc[ns][ms][4 * q], acc[ns][ms][4 * q + 1], acc[ns][ms][4 * q + 2],
+                      acc[ns][ms][4 * q + 3]};
+        }
+    }
+    return;
   }
 
   // ---- store: bf16 tile in LDS (row j, 512 bytes; chunk c at c ^ (j & 15)),
@@ -325,59 +325,53 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   }
 }
 
-struct MxdxReduceParams {
-  const float* part;
-  const float* U;
-  const uint16_t* A;
-  uint16_t* dX;
-  int64_t M, K;
-  int32_t splits, r;
-  float s;
-};
-
-// dX = bf16(sum over splits + s U A): four outputs of one row per thread
-__global__ __launch_bounds__(256) void mxdx_reduce_kernel(MxdxReduceParams p) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t per = p.K / 4;
-  const int64_t m = idx / per, k = 4 * (idx - m * per);
-  if (m >= p.M) return;
-  f32x4 a = *reinterpret_cast<const f32x4*>(p.part + m * p.K + k);
-  for (int t = 1; t < p.splits; ++t) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p.part + ((int64_t)t * p.M + m) * p.K + k);
+// out = bf16(sum over splits): eight outputs per thread, the splits added in
+// order
+__global__ __launch_bounds__(256) void mx_sum_splits_kernel(const float* part, uint16_t* out,
+                                                            int64_t n, int splits) {
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (i >= n) return;
+  f32x4 a = *reinterpret_cast<const f32x4*>(part + i);
+  f32x4 b = *reinterpret_cast<const f32x4*>(part + i + 4);
+#pragma unroll 4
+  for (int t = 1; t < splits; ++t) {
+    const float* q = part + t * n + i;
+    const f32x4 c = *reinterpret_cast<const f32x4*>(q), d = *reinterpret_cast<const f32x4*>(q + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] += v[i];
+    for (int e = 0; e < 4; ++e) {
+      a[e] += c[e];
+      b[e] += d[e];
+    }
   }
-  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = 0; j < p.r; ++j) {
-    const float u = p.U[m * p.r + j];
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p.A + (int64_t)j * p.K + k);
-    d[0] = fmaf(u, lo_bf16(w[0]), d[0]);
-    d[1] = fmaf(u, hi_bf16(w[0]), d[1]);
-    d[2] = fmaf(u, lo_bf16(w[1]), d[2]);
-    d[3] = fmaf(u, hi_bf16(w[1]), d[3]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a[i] += p.s * d[i];
-  *reinterpret_cast<u32x2*>(p.dX + m * p.K + k) =
-      u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+  *reinterpret_cast<u32x4*>(out + i) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                             pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
 }
 
 struct Plan {
   int jm, ti, tj, splits;
 };
 
-// The widest tile that still gives most compute units one; below 192 tiles of
-// the narrowest the reduction is split.
+// The tile with the least rounds x time of a round, the wider at a tie: at
+// N = 4096 a round of 256 tiles takes 100 us at 256 x 256, 65 to 85 at
+// 256 x 128 and 55 at 256 x 64 (1001 x 4096 x 11008: 118, 137 and 145 us;
+// 2048 x 4096 x 4096: 110, 85 and 103).  Two workgroups of 256 x 64 fit a
+// compute unit; where a third of those places would be filled, the reduction is
+// split (600 x 4096 x 4096, 160 tiles: 58 us whole, 47 in three; 512: 58 and
+// 39 in four; 100: 55 and 22 in eight).
 Plan plan(int64_t M, int64_t N, int64_t K) {
+  static const int shapes[3][2] = {{4, 20}, {2, 14}, {1, 11}};
   Plan q{};
   q.ti = (int)cdiv(K, kTI);
-  for (q.jm = 4; q.jm > 1; q.jm >>= 1) {
-    q.tj = (int)cdiv(M, 64 * q.jm);
-    if ((int64_t)q.ti * q.tj >= 192) break;
+  int64_t best = 0;
+  for (const auto& c : shapes) {
+    const int64_t tj = cdiv(M, 64 * c[0]), cost = c[1] * cdiv(q.ti * tj, 256);
+    if (best && cost >= best) continue;
+    best = cost;
+    q.jm = c[0];
+    q.tj = (int)tj;
   }
-  q.tj = (int)cdiv(M, 64 * q.jm);
   const int64_t tiles = (int64_t)q.ti * q.tj;
-  int64_t sp = tiles < 128 ? 256 / tiles : 1;
+  int64_t sp = q.jm == 1 && tiles <= 170 ? 512 / tiles : 1;
   const int64_t most = N / 256;  // at least four steps a split
   if (sp > most) sp = most;
   if (sp > 8) sp = 8;
@@ -396,6 +390,12 @@ void launch(const MxdxParams& p, hipStream_t st) {
 }  // namespace
 
 namespace dispatch {
+
+int mx_sum_splits(const float* part, void* out, int64_t n, int splits, hipStream_t st) {
+  hipLaunchKernelGGL(mx_sum_splits_kernel, dim3((unsigned)cdiv(n, 2048)), dim3(256), 0, st, part,
+                     (uint16_t*)out, n, splits);
+  return hip_fail(hipGetLastError(), "mx_sum_splits launch");
+}
 
 size_t mx_dx_ws_bytes(int64_t M, int64_t N, int64_t K) {
   const Plan q = plan(M, N, K);
@@ -432,19 +432,7 @@ int mx_dx(const void* dY, int64_t M, const lq_mx_tensor& W, const float* U, cons
     launch<1, false>(p, st);
   const int e = hip_fail(hipGetLastError(), "mx_dx launch");
   if (e || q.splits == 1) return e;
-  MxdxReduceParams d;
-  d.part = p.part;
-  d.U = U;
-  d.A = p.A;
-  d.dX = p.dX;
-  d.M = M;
-  d.K = p.K;
-  d.splits = q.splits;
-  d.r = p.r;
-  d.s = s;
-  hipLaunchKernelGGL(mxdx_reduce_kernel, dim3((unsigned)cdiv(M * (p.K / 4), 256)), dim3(256), 0,
-                     st, d);
-  return hip_fail(hipGetLastError(), "mx_dx reduce launch");
+  return mx_sum_splits(p.part, p.dX, M * p.K, q.splits, st);
 }
 
 }  // namespace dispatch

@@ -32,7 +32,8 @@
 // products (see the loop).
 //
 // Split K (few tiles): workgroups of one tile take ranges of the steps and
-// leave float32 partial sums, which mxg_reduce_kernel adds in order.
+// leave float32 partial sums (the first with the expand), added in order by
+// mx_sum_splits.
 //
 // Epilogue: the expand adds (s T) B^T on the finished accumulators with bf16
 // MFMAs (T rounded to bf16 after the multiply by s: the same rounding as the
@@ -379,27 +380,8 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   } while (++kt < kb);
   __syncthreads();  // the output tile overwrites the stages
 
-  if constexpr (SPLIT) {  // float32 partial sums; lane: rows n = .. + 8 q + 4 h + 0..3, column m
-    float* part = p.part + (int64_t)blockIdx.y * M * N;
-#pragma unroll
-    for (int ms = 0; ms < JM; ++ms) {
-      const int64_t m = j0 + xrow0 + 32 * ms;
-#pragma unroll
-      for (int ns = 0; ns < IM; ++ns)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t n = i0 + 32 * IM * wi + 32 * ns + 8 * q + 4 * h;
-          if (m < M && n < N)
-            *reinterpret_cast<f32x4*>(part + m * N + n) =
-                f32x4{acc[ns][ms][4 * q], acc[ns][ms][4 * q + 1], acc[ns][ms][4 * q + 2],
-                      acc[ns][ms][4 * q + 3]};
-        }
-    }
-    return;
-  }
-
   // ---- expand: acc += B-operand x (s T)-operand over rank chunks of 16
-  const int r = p.r;
+  const int r = SPLIT && blockIdx.y ? 0 : p.r;
   for (int c = 0; c < r; c += 16) {
     const int jr = c + 8 * h;
     u32x4 ef[IM], vf[JM];
@@ -419,6 +401,25 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     for (int ns = 0; ns < IM; ++ns)
 #pragma unroll
       for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(ef[ns], vf[ms], acc[ns][ms]);
+  }
+
+  if constexpr (SPLIT) {  // float32 partial sums; lane: rows n = .. + 8 q + 4 h + 0..3, column m
+    float* part = p.part + (int64_t)blockIdx.y * M * N;
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) {
+      const int64_t m = j0 + xrow0 + 32 * ms;
+#pragma unroll
+      for (int ns = 0; ns < IM; ++ns)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t n = i0 + 32 * IM * wi + 32 * ns + 8 * q + 4 * h;
+          if (m < M && n < N)
+            *reinterpret_cast<f32x4*>(part + m * N + n) =
+                f32x4{acc[ns][ms][4 * q], acc[ns][ms][4 * q + 1], acc[ns][ms][4 * q + 2],
+                      acc[ns][ms][4 * q + 3]};
+        }
+    }
+    return;
   }
 
   // ---- store: bf16 tile in LDS (row j of 2 TI bytes, chunk c at c ^ (j & 15)),
@@ -450,62 +451,32 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   }
 }
 
-// Y = bf16(sum over splits + s T B^T): four outputs of one row per thread,
-// the splits added in order
-struct MxgReduceParams {
-  const float* part;
-  const float* T;
-  const uint16_t* B;
-  uint16_t* Y;
-  int64_t M, N;
-  int32_t splits, r;
-  float s;
-};
-
-__global__ __launch_bounds__(256) void mxg_reduce_kernel(MxgReduceParams p) {
-  const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t per = p.N / 4;
-  const int64_t m = idx / per, n = 4 * (idx - m * per);
-  if (m >= p.M) return;
-  f32x4 a = *reinterpret_cast<const f32x4*>(p.part + m * p.N + n);
-  for (int t = 1; t < p.splits; ++t) {
-    const f32x4 b = *reinterpret_cast<const f32x4*>(p.part + ((int64_t)t * p.M + m) * p.N + n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] += b[i];
-  }
-  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = 0; j < p.r; ++j) {
-    const float t = p.T[m * p.r + j];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = fmaf(t, bf16_to_f32(p.B[(n + i) * p.r + j]), d[i]);
-  }
-  if (p.r)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] += p.s * d[i];
-  *reinterpret_cast<u32x2*>(p.Y + m * p.N + n) =
-      u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
-}
-
-// Tile and split choice.  256 x 256 tiles read the least per product; where
-// they would leave compute units idle, smaller ones; below 128 tiles of the
-// smallest the reduction is split.
+// Tile and split choice: the tile with the least rounds x time of a round, the
+// larger at a tie.  At K = 4096 with an 8-bit X a round of 256 tiles takes 71 us
+// at 256 x 256, 45 us at 256 x 128 and 24 us at 128 x 128 (2048 x 4096 x 4096:
+// 54, 45 and 48 us; 4096 x 4096 x 4096: 71, 88 and 95 us).  Split K fills the
+// chip but costs a second launch and the partial sums: it takes 4096 columns to
+// pay (100 x 4096 x 11008: 45 us whole, 19 in eight; 512 x 4096 x 11008: 50 and
+// 42 in two; 100 x 4096 x 4096: 19 and 15 in four; 512 x 4096 x 4096: 21 and 23
+// in two; 200 x 2048 x 2048: 11 and 12).
 struct Plan {
   int im, jm, ti, tj, splits;
 };
 
 Plan plan(int64_t M, int64_t N, int64_t K) {
-  static const int shapes[3][2] = {{4, 4}, {4, 2}, {2, 2}};
+  static const int shapes[3][3] = {{4, 4, 3}, {4, 2, 2}, {2, 2, 1}};
   Plan q{};
-  for (int c = 0; c < 3; ++c) {
-    q.im = shapes[c][0];
-    q.jm = shapes[c][1];
-    q.ti = (int)cdiv(N, 64 * q.im);
-    q.tj = (int)cdiv(M, 64 * q.jm);
-    if ((int64_t)q.ti * q.tj >= 192) break;
+  int64_t best = 0;
+  for (const auto& c : shapes) {
+    const int64_t ti = cdiv(N, 64 * c[0]), tj = cdiv(M, 64 * c[1]);
+    const int64_t cost = c[2] * cdiv(ti * tj, 256);
+    if (best && cost >= best) continue;
+    best = cost;
+    q = Plan{c[0], c[1], (int)ti, (int)tj, 1};
   }
-  const int64_t tiles = (int64_t)q.ti * q.tj;  // fewer than 192 only at 128 x 128
-  int64_t sp = tiles < 128 ? cdiv(256, tiles) : 1;
-  const int64_t most = K / 512;  // at least 512 columns a split
+  const int64_t tiles = (int64_t)q.ti * q.tj;  // at most 128 only at 128 x 128
+  int64_t sp = tiles <= 128 ? 256 / tiles : 1;
+  const int64_t most = K < 4096 ? 1 : K / (tiles <= 32 ? 1024 : 4096);
   if (sp > most) sp = most;
   if (sp > 8) sp = 8;
   q.splits = sp < 1 ? 1 : (int)sp;
@@ -572,19 +543,7 @@ int mx_gemm(const lq_mx_tensor& X, const lq_mx_tensor& W, const float* T, const 
     launch_shape<LQ_MX_FP4>(p, q, st);
   int e = hip_fail(hipGetLastError(), "mx_gemm launch");
   if (e || q.splits == 1) return e;
-  MxgReduceParams d;
-  d.part = p.part;
-  d.T = T;
-  d.B = p.B;
-  d.Y = p.Y;
-  d.M = p.M;
-  d.N = p.N;
-  d.splits = p.splits;
-  d.r = p.r;
-  d.s = s;
-  hipLaunchKernelGGL(mxg_reduce_kernel, dim3((unsigned)cdiv(p.M * (p.N / 4), 256)), dim3(256), 0,
-                     st, d);
-  return hip_fail(hipGetLastError(), "mx_gemm reduce launch");
+  return mx_sum_splits(p.part, p.Y, p.M * p.N, p.splits, st);
 }
 
 }  // namespace dispatch

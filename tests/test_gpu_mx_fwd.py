@@ -47,6 +47,7 @@ def test_single_tokens(M, N, K, r):
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("M,N,K,r", [
     (1, 64, 64, 1), (1, 4096, 4096, 16), (7, 128, 320, 8), (33, 64, 256, 0), (64, 192, 576, 11),
+    (100, 256, 4160, 24), (70, 512, 8192, 64), (520, 11008, 128, 16), (1030, 11008, 64, 7),
     (65, 320, 128, 64), (100, 256, 512, 32), (129, 448, 1024, 16), (300, 1088, 832, 5),
     (777, 512, 1920, 24), (257, 4096, 448, 16),
 ])
@@ -57,7 +58,8 @@ def test_small_and_ragged(M, N, K, r, fmt):
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("M,N,K,r", [
     (2048, 3200, 512, 16),    # 256 x 128 tiles
-    (2049, 4160, 320, 11),    # the same with a tail and ragged edges
+    (520, 11008, 320, 9),     # the same with a tail
+    (2049, 4160, 320, 11),    # 256 x 256 with a tail and ragged edges
     (4000, 4096, 256, 64),    # 256 x 256 tiles
     (3585, 4160, 576, 9),     # the same with a tail and ragged edges
     (1500, 2048, 384, 16),    # 128 x 128 tiles
