@@ -2,57 +2,43 @@
 // (M x K) and U = dY B of a bf16 dY (M x N).
 //
 // Both are out[m][j] = sum_k Z[m][k] G[j][k] with G r x K row-major.  For U, G
-// is B's transpose: where r % 4 == 0 and K % 256 == 0 the rows of B (K x r) are
-// staged as they lie and read by the transposing ds_read_b64_tr_b16; otherwise
-// a small kernel writes the transpose to the workspace first (another launch,
-// 4.7 us).
+// is B's transpose: where r % 4 == 0 the rows of B (K x r) are staged as they
+// lie and read by the transposing ds_read_b64_tr_b16; otherwise a small kernel
+// writes the transpose to the workspace first (another launch, 4.7 us).
 //
 // Bound by the load path (Z from HBM once, r K bf16 of G from L2 per
 // workgroup); the products are a few percent of the matrix units' time.  Two
 // kernels:
 //
-// mx_shrink_tile_kernel (K % 256 == 0).  A workgroup of eight waves owns 16 H
-// rows and walks the reduction in steps of 256 columns.  The step's Z rows
-// (and scales) and G rows go straight from global memory into LDS in whole
-// lines, NST - 1 steps ahead; wave w multiplies columns 32 w .. of the step, one
+// mx_shrink_tile_kernel (U, and T where K % 128 == 0: a row's scales are then
+// read as 4-byte words).  A workgroup of eight waves owns 16 H rows and walks
+// the reduction in steps of 256 columns.  The step's Z rows (and scales) and G
+// rows go straight from global memory into LDS in whole lines, NST - 1 steps
+// ahead; wave w multiplies columns 32 w .. of the step, one
 // v_mfma_f32_16x16x32_bf16 per 16 x 16 block of the output (a lane's 8 columns
 // of an MX row are converted as they are read).  16-byte chunks are swizzled by
-// row so that the 16 rows of a read fall on distinct banks.  Loads that give a
-// lane its whole block of a row touch 32 lines per instruction; the kernel
-// below, which does that, takes 12.5 us for T at M = 2048, K = 4096, r = 16
-// and 34 us for U at M = 8192, N = 4096, r = 64.
+// row so that the 16 rows of a read fall on distinct banks.  M = 2048,
+// K = 4096, r = 16: T of an 8-bit X 6.1 us (1.4 TB/s, launch and the pipeline's
+// filling included), U 5.8 us (2.9 TB/s); M = 8192, r = 64: U of N = 4096 23.6 us
+// (2.8 TB/s), T of a 4-bit X of K = 4096 15.9.  With few rows a workgroup's steps
+// bound it, 0.28 us each (M = 1001, K = 11008: 12.7 us).
 //
 // mx_shrink_kernel (other K).  A workgroup owns 16 H rows and deals the
 // 128-column steps of the reduction to its waves; lane (q, l16) of a wave takes
-// one block of 32 columns of row l16 of each 16-row group (an MX block with
-// its scale, or 64 bytes of bf16) and the same columns of row l16 of each
-// 16-rank group of G, the 32 columns of a lane relabelled so that they are
-// contiguous.  The next step's loads are issued before this step's products.
+// one block of 32 columns of row l16 of each 16-row group with its scale and
+// the same columns of row l16 of each 16-rank group of G, the 32 columns of a
+// lane relabelled so that they are contiguous.  The next step's loads are
+// issued before this step's products.  Each load touches 32 lines, which costs
+// twice the tile kernel's time (T at M = 2048, K = 4096, r = 16: 12.5 us).
 //
 // In both the waves' sums are added in order through LDS.
+#include <type_traits>
+
 #include "dispatch.h"
 #include "mx_tile.h"
 
 namespace lq {
 namespace {
-
-// 32 bf16 values of a lane, with MxBlock's interface
-struct BfBlock {
-  u32x4 w[4];
-  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t*) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const u32x4*>(p + 16 * i);
-  }
-  __device__ __forceinline__ u32x4 part(int d) const { return w[d]; }
-};
-template <int FZ>
-struct ZBlock {
-  typedef MxBlock<FZ> type;
-};
-template <>
-struct ZBlock<16> {
-  typedef BfBlock type;
-};
 
 template <int FZ, int JT, int H, int NW>
 __global__ __launch_bounds__(64 * NW) void mx_shrink_kernel(const uint8_t* __restrict__ Z,
@@ -72,7 +58,7 @@ __global__ __launch_bounds__(64 * NW) void mx_shrink_kernel(const uint8_t* __res
     int64_t m = m0 + 16 * h + l16;
     m = m < M ? m : M - 1;
     zr[h] = Z + m * pitch;
-    sr[h] = FZ == 16 ? nullptr : Zs + m * blocks;
+    sr[h] = Zs + m * blocks;
   }
   const uint16_t* gr[JT];
 #pragma unroll
@@ -81,7 +67,7 @@ __global__ __launch_bounds__(64 * NW) void mx_shrink_kernel(const uint8_t* __res
     gr[j] = G + (int64_t)row * K;
   }
   struct In {
-    typename ZBlock<FZ>::type z[H];
+    MxBlock<FZ> z[H];
     u32x4 g[JT][4];
   };
   // a lane whose block is past the row reads block 0 and is masked below
@@ -89,7 +75,7 @@ __global__ __launch_bounds__(64 * NW) void mx_shrink_kernel(const uint8_t* __res
     int b = 4 * t + q;
     b = b < blocks ? b : 0;
 #pragma unroll
-    for (int h = 0; h < H; ++h) in.z[h].load(zr[h] + (int64_t)b * (4 * FZ), FZ == 16 ? nullptr : sr[h] + b);
+    for (int h = 0; h < H; ++h) in.z[h].load(zr[h] + (int64_t)b * (4 * FZ), sr[h] + b);
 #pragma unroll
     for (int j = 0; j < JT; ++j)
 #pragma unroll
@@ -149,7 +135,7 @@ __global__ __launch_bounds__(64 * NW) void mx_shrink_kernel(const uint8_t* __res
   }
 }
 
-// -------------------------------------------------------------- K % 256 == 0
+// ------------------------------- K % 64 == 0 of bf16 rows, K % 128 == 0 of MX
 template <int FZ, int JT, int H>
 struct TileShape {
   static constexpr int NW = 8;
@@ -171,8 +157,9 @@ __device__ __forceinline__ u32x2 shrink_tr(const char* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
 }
 
-// GT: G is given as K x r (r % 4 == 0)
-template <int FZ, int JT, int H, bool GT>
+// GT: G is given as K x r (r % 4 == 0).  TAIL: K % 256 != 0, the last step ends
+// inside its columns (apart, because the checks cost 0.1 us per 256 columns).
+template <int FZ, int JT, int H, bool GT, bool TAIL>
 __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __restrict__ Z,
                                                              const uint8_t* __restrict__ Zs,
                                                              int64_t M, int64_t K,
@@ -186,48 +173,53 @@ __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __re
   const int l16 = lane & 15, q = lane >> 4;
   const int64_t m0 = 16 * H * (int64_t)blockIdx.x;
   const int64_t zpitch = K * FZ / 8;
-  const int steps = (int)(K / 256);
+  const int blocks = (int)(K / 32), steps = (blocks + 7) / 8;
   const uint32_t sbase = mx_lds_addr(smem);
   auto zswz = [](int row) { return ZC == 8 ? mx_swz128(row) : row & 15; };
 
   // load offsets relative to the step; Z load i covers 1024 / ZRow rows, G load
   // i rows 2 i and 2 i + 1, and wave 0 loads the scales.  Every wave makes the
   // same number of loads (its waits count them); a spare one reads one address
-  // with all its lanes, into a place of its own.
-  uint32_t goff[JT];
-  int64_t zoff[S::ZU];
+  // with all its lanes, into a place of its own.  cols: the step's columns; a
+  // lane whose chunk lies past them reads the first chunk again.
+  uint32_t goff[JT], zoff[S::ZU], soff = 0;
   int zi[S::ZU];
+  auto offsets = [&](uint32_t cols) {
 #pragma unroll
-  for (int u = 0; u < S::ZU; ++u) {
-    zi[u] = wave * S::ZU + u;
-    const int row = zi[u] * (1024 / S::ZRow) + lane / ZC;
-    int64_t m = m0 + row;
-    m = m < M ? m : M - 1;
-    zoff[u] = zi[u] < S::ZI ? m * zpitch + 16 * ((lane % ZC) ^ zswz(row)) : 0;
-  }
-#pragma unroll
-  for (int u = 0; u < JT; ++u) {
-    if (GT) {  // the step's 512 r bytes in order (past them, the first again)
-      const int at = (wave * JT + u) * 1024 + lane * 16;
-      goff[u] = (uint32_t)(at < 512 * r ? at : 0);
-    } else {
-      const int row = 2 * (wave * JT + u) + (lane >> 5);
-      const int j = row < r ? row : r - 1;
-      goff[u] = (uint32_t)((int64_t)j * K * 2 + 16 * ((lane & 31) ^ (row & 15)));
+    for (int u = 0; u < S::ZU; ++u) {
+      zi[u] = wave * S::ZU + u;
+      const int row = zi[u] * (1024 / S::ZRow) + lane / ZC;
+      int64_t m = m0 + row;
+      m = m < M ? m : M - 1;
+      const uint32_t at = 16u * ((lane % ZC) ^ zswz(row));
+      zoff[u] = zi[u] < S::ZI ? (uint32_t)(m * zpitch) + (at < cols * FZ / 8 ? at : 0u) : 0u;
     }
-  }
-  uint32_t soff = 0;
-  if (FZ != 16) {
-    int64_t m = m0 + (lane >> 1) % (16 * H);
-    m = m < M ? m : M - 1;
-    soff = wave == 0 ? (uint32_t)(m * (K / 32) + 4 * (lane & 1)) : 0u;
-  }
+#pragma unroll
+    for (int u = 0; u < JT; ++u) {
+      if (GT) {  // the step's 2 r cols bytes in order
+        const uint32_t at = (wave * JT + u) * 1024 + lane * 16;
+        goff[u] = at < 2 * r * cols ? at : 0u;
+      } else {
+        const int row = 2 * (wave * JT + u) + (lane >> 5);
+        const int j = row < r ? row : r - 1;
+        const uint32_t at = 16u * ((lane & 31) ^ (row & 15));
+        goff[u] = (uint32_t)((int64_t)j * K * 2) + (at < 2 * cols ? at : 0u);
+      }
+    }
+    if (FZ != 16) {
+      int64_t m = m0 + (lane >> 1) % (16 * H);
+      m = m < M ? m : M - 1;
+      soff = wave == 0 ? (uint32_t)(m * blocks + (cols > 128 ? 4 * (lane & 1) : 0)) : 0u;
+    }
+  };
+  offsets(256);
   const uint32_t spare = sbase + NST * S::Stage;
   auto issue = [&](int t, int b, int go) {
+    if (TAIL && go && 8 * t + 8 > blocks) offsets(32 * (blocks - 8 * t));  // the last step's
     const uint32_t st = sbase + b * S::Stage;
 #pragma unroll
     for (int u = 0; u < S::ZU; ++u)
-      mx_dma16(reinterpret_cast<const char*>(Z) + (int64_t)t * S::ZRow, (uint32_t)zoff[u],
+      mx_dma16(reinterpret_cast<const char*>(Z) + (int64_t)t * S::ZRow, zoff[u],
                zi[u] < S::ZI ? st + zi[u] * 1024 : spare, go);
 #pragma unroll
     for (int u = 0; u < JT; ++u)
@@ -258,6 +250,8 @@ __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __re
       issue(go ? t + NST - 1 : t, b == 0 ? NST - 1 : b - 1, go);
     }
     const char* st = smem + b * S::Stage;
+    b = b + 1 == NST ? 0 : b + 1;
+    if (TAIL && 8 * t + wave >= blocks) break;  // past the last step's columns
     u32x4 zf[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
@@ -293,7 +287,6 @@ __global__ __launch_bounds__(512) void mx_shrink_tile_kernel(const uint8_t* __re
 #pragma unroll
       for (int h = 0; h < H; ++h) acc[h][j] = mfma16(zf[h], gf, acc[h][j]);
     }
-    b = b + 1 == NST ? 0 : b + 1;
   }
   __syncthreads();  // the sums overwrite the stages
   f32x4(*part)[H * JT][64] = reinterpret_cast<f32x4(*)[H * JT][64]>(smem);
@@ -334,30 +327,37 @@ __global__ __launch_bounds__(256) void mx_transpose_kernel(const uint16_t* __res
 }
 
 // Rows per workgroup: 16 while that fills the chip, 32 beyond (G is read half
-// as often)
-// (gt: G is K x r, see mx_shrink_tile_kernel).
-template <int FZ, int JT, int NW>
+// as often).  gt: G is K x r, see mx_shrink_tile_kernel.
+template <int FZ, int JT>
 void launch_rows(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const uint16_t* G, int r,
                  bool gt, float* out, hipStream_t st) {
   const uint8_t* z = (const uint8_t*)Z;
   const bool wide = M > 4096;
   const dim3 grid((unsigned)cdiv(M, wide ? 32 : 16));
   constexpr bool U = FZ == 16;
-  if (K % 256 == 0) {
+  if (U || K % 128 == 0) {  // a row's scales are read as 4-byte words
     auto tile = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(512), 0, st, z, Zs, M, K, G, r, out);
     };
+    auto rows = [&](auto g, auto tail) {
+      constexpr bool GT = decltype(g)::value, TAIL = decltype(tail)::value;
+      wide ? tile(mx_shrink_tile_kernel<FZ, JT, 2, GT, TAIL>)
+           : tile(mx_shrink_tile_kernel<FZ, JT, 1, GT, TAIL>);
+    };
+    const std::false_type no{};
+    const std::true_type yes{};
+    const std::integral_constant<bool, U> u{};
     if (U && gt)
-      wide ? tile(mx_shrink_tile_kernel<FZ, JT, 2, U>) : tile(mx_shrink_tile_kernel<FZ, JT, 1, U>);
+      K % 256 ? rows(u, yes) : rows(u, no);
     else
-      wide ? tile(mx_shrink_tile_kernel<FZ, JT, 2, false>)
-           : tile(mx_shrink_tile_kernel<FZ, JT, 1, false>);
-  } else if (wide) {
-    hipLaunchKernelGGL((mx_shrink_kernel<FZ, JT, 2, NW>), grid, dim3(64 * NW), 0, st, z, Zs, M, K,
-                       G, r, out);
-  } else {
-    hipLaunchKernelGGL((mx_shrink_kernel<FZ, JT, 1, NW>), grid, dim3(64 * NW), 0, st, z, Zs, M, K,
-                       G, r, out);
+      K % 256 ? rows(no, yes) : rows(no, no);
+  } else if constexpr (!U) {
+    // sixteen waves where their registers allow it
+    auto rows = [&](auto kernel, int waves) {
+      hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, z, Zs, M, K, G, r, out);
+    };
+    wide ? rows(mx_shrink_kernel<FZ, JT, 2, JT == 1 ? 16 : 8>, JT == 1 ? 16 : 8)
+         : rows(mx_shrink_kernel<FZ, JT, 1, JT == 4 ? 8 : 16>, JT == 4 ? 8 : 16);
   }
 }
 
@@ -365,11 +365,11 @@ template <int FZ>
 int launch_z(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const uint16_t* G, int64_t r,
              bool gt, float* out, hipStream_t st) {
   if (r <= 16)
-    launch_rows<FZ, 1, 16>(Z, Zs, M, K, G, (int)r, gt, out, st);
+    launch_rows<FZ, 1>(Z, Zs, M, K, G, (int)r, gt, out, st);
   else if (r <= 32)
-    launch_rows<FZ, 2, 8>(Z, Zs, M, K, G, (int)r, gt, out, st);
+    launch_rows<FZ, 2>(Z, Zs, M, K, G, (int)r, gt, out, st);
   else
-    launch_rows<FZ, 4, 8>(Z, Zs, M, K, G, (int)r, gt, out, st);
+    launch_rows<FZ, 4>(Z, Zs, M, K, G, (int)r, gt, out, st);
   return hip_fail(hipGetLastError(), "mx_shrink launch");
 }
 
@@ -388,7 +388,7 @@ int mx_shrink(const lq_mx_tensor& X, const void* A, int64_t r, float* T, hipStre
 int mx_u(const void* dY, int64_t M, int64_t N, const void* B, int64_t r, void* Bt, float* U,
          hipStream_t st) {
   const void* G = B;
-  const bool gt = r % 4 == 0 && N % 256 == 0;
+  const bool gt = r % 4 == 0;
   if (r > 1 && !gt) {  // one rank: B is its own transpose
     hipLaunchKernelGGL(mx_transpose_kernel, dim3((unsigned)(N / 64)), dim3(256), 0, st,
                        (const uint16_t*)B, N, (int)r, (uint16_t*)Bt);

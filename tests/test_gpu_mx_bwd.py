@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 SHAPES = [(1, 64, 64, 1), (3, 128, 192, 5), (64, 256, 320, 8), (65, 320, 128, 64), (130, 64, 1088, 16),
           (300, 1088, 832, 33), (777, 512, 1920, 24), (1000, 2048, 2048, 16), (2048, 4096, 512, 11),
-          (1001, 64, 11008, 8), (50, 512, 256, 28), (4101, 256, 256, 16), (4130, 512, 512, 36)]
+          (1001, 64, 11008, 8), (50, 512, 256, 28), (40, 832, 1152, 20), (4100, 320, 384, 48), (4100, 192, 192, 11), (4101, 256, 256, 16), (4130, 512, 512, 36)]
 
 
 def out_buffers(M, N, K, r):
