@@ -352,12 +352,11 @@ void launch_rows(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const u
     else
       K % 256 ? rows(no, yes) : rows(no, no);
   } else if constexpr (!U) {
-    // sixteen waves where their registers allow it
-    auto rows = [&](auto kernel, int waves) {
-      hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, st, z, Zs, M, K, G, r, out);
+    constexpr int NW = JT == 1 ? 16 : 8;
+    auto rows = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), 0, st, z, Zs, M, K, G, r, out);
     };
-    wide ? rows(mx_shrink_kernel<FZ, JT, 2, JT == 1 ? 16 : 8>, JT == 1 ? 16 : 8)
-         : rows(mx_shrink_kernel<FZ, JT, 1, JT == 4 ? 8 : 16>, JT == 4 ? 8 : 16);
+    wide ? rows(mx_shrink_kernel<FZ, JT, 2, NW>) : rows(mx_shrink_kernel<FZ, JT, 1, NW>);
   }
 }
 
