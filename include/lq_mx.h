@@ -135,6 +135,8 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
                      void* dX, float* dA, float* dB, int32_t accumulate, void* ws,
                      size_t ws_bytes, hipStream_t stream);
 
+/* Workspace of an operator (LQ_MX_OP_*), in bytes; 0 where none is needed and
+ * for sizes that the operator refuses. */
 #define LQ_MX_OP_FWD 0
 #define LQ_MX_OP_BWD 1
 #define LQ_MX_OP_BWD_CKPT 2

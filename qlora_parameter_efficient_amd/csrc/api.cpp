@@ -571,6 +571,7 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
   int rc = check_weight(W0, LQ_BF16);
   if (rc) return rc;
   REQUIRE(M >= 0, LQ_ERR_INVALID_ARG, "M = %lld", (long long)M);
+  REQUIRE(M < (int64_t)1 << 31, LQ_ERR_UNSUPPORTED, "M = %lld: 2^31 rows or more", (long long)M);
   REQUIRE(r >= 1 && r <= kMaxRank, LQ_ERR_UNSUPPORTED, "rank %lld outside [1, %lld]",
           (long long)r, (long long)kMaxRank);
   REQUIRE(A && B, LQ_ERR_INVALID_ARG, "A or B is NULL");

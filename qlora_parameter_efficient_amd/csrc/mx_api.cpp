@@ -118,7 +118,10 @@ int lq_mx_dequantize(const lq_mx_tensor* q, void* out, lq_dtype odt, hipStream_t
 }
 
 size_t lq_mx_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r) {
-  if (M <= 0 || N <= 0 || K <= 0 || r < 0) return 0;
+  // 0 too for the sizes that the operators refuse
+  const int64_t lim = (int64_t)1 << 31;
+  if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > kMaxRank) return 0;
+  if (M >= lim || N >= lim || K >= lim || M * K >= lim || M * N >= lim) return 0;
   switch (op) {
     case LQ_MX_OP_FWD:
       return up256((size_t)(M * r) * 4) + fwd_part_bytes(M, N, K, r);

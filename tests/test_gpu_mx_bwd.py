@@ -6,13 +6,14 @@ import torch
 
 from qlora_parameter_efficient_amd import lq, mx
 from tests.gpu_helpers import DEV, announce
-from tests.mx_helpers import assert_within, make, ref_backward, ref_forward, values
+from tests.mx_helpers import assert_within, gamma, make, ref_backward, ref_forward, values
 
 pytestmark = pytest.mark.gpu
 
 SHAPES = [(1, 64, 64, 1), (3, 128, 192, 5), (64, 256, 320, 8), (65, 320, 128, 64), (130, 64, 1088, 16),
           (300, 1088, 832, 33), (777, 512, 1920, 24), (1000, 2048, 2048, 16), (2048, 4096, 512, 11),
-          (1001, 64, 11008, 8), (50, 512, 256, 28), (40, 832, 1152, 20), (4100, 320, 384, 48), (4100, 192, 192, 11), (4101, 256, 256, 16), (4130, 512, 512, 36)]
+          (1001, 64, 11008, 8), (50, 512, 256, 28), (40, 832, 1152, 20), (4100, 320, 384, 48),
+          (4100, 192, 192, 11), (4101, 256, 256, 16), (4130, 512, 512, 36)]
 
 
 def out_buffers(M, N, K, r):
@@ -205,3 +206,68 @@ def test_binding_refuses_wrong_operands():
             kw.update(b)
             with pytest.raises(ValueError):
                 fn(**kw)
+
+
+@pytest.mark.parametrize("N,K", [(64, 11008), (11008, 64)])
+def test_offsets_past_31_bits(N, K):
+    """M K (or M N) just below 2^31 elements: dX at both ends and around 2^31
+    bytes, dA and dB over all rows."""
+    M, r, fmt = 195000, 4, "fp8"
+    announce(f"mx bwd long N={N} K={K}")
+    g = torch.Generator(device=DEV).manual_seed(0)
+    Xq = mx.lq_mx_quantize(torch.randn(M, K, generator=g, device=DEV, dtype=torch.bfloat16), fmt)
+    dY = torch.randn(M, N, generator=g, device=DEV, dtype=torch.bfloat16)
+    _, W, A, B, _, s = make(1, N, K, r, fmt)
+    T = torch.randn(M, r, generator=g, device=DEV)
+    dX, dA, dB = mx.lq_mx_lora_bwd(dY, Xq, W, A, B, s, T_saved=T)
+    torch.cuda.synchronize()
+    w = values(W)
+    half = 2**31 // (2 * max(N, K))
+    for m0 in (0, half - 50, 2 * half - 50, M - 100):
+        m0 = min(m0, M - 100)
+        rows = slice(m0, m0 + 100)
+        x = values(mx.MxTensor(Xq.codes[rows], Xq.scales[rows], 100, K, fmt))
+        want, bound = ref_backward(dY[rows], x, T[rows].double(), w, A, B, s)[0]
+        assert_within(dX[rows], want, bound, "dX")
+    del dX
+    wA, bA, wB, bB = 0, 0, 0, 0
+    for m0 in range(0, M, 8192):  # the decoded values (tested above): exact in float32
+        n = min(8192, M - m0)
+        q = mx.MxTensor(Xq.codes[m0:m0 + n], Xq.scales[m0:m0 + n], n, K, fmt)
+        x, d, t = mx.lq_mx_dequantize(q, torch.float32).double(), dY[m0:m0 + n].double(), T[m0:m0 + n].double()
+        u, eu = d @ B.double(), gamma(N) * (d.abs() @ B.double().abs())
+        wA, bA = wA + s * (u.t() @ x), bA + s * ((gamma(M, parts=3) * u.abs() + eu).t() @ x.abs())
+        wB, bB = wB + s * (d.t() @ t), bB + s * gamma(M, parts=3) * (d.abs().t() @ t.abs())
+    assert_within(dA, wA, bA + 2.0**-23 * wA.abs(), "dA")
+    assert_within(dB, wB, bB + 2.0**-23 * wB.abs(), "dB")
+
+
+@pytest.mark.parametrize("base", ["dense", "nf4"])
+def test_checkpoint_backward_captured_and_replayed(base):
+    M, N, K, r = 333, 512, 832, 11
+    announce(f"ckpt graph {base}")
+    X, _, A, B, dY, s = make(M, N, K, r, "fp8", bf16_x=True)
+    W = torch.randn(N, K, generator=torch.Generator().manual_seed(7)) * 0.02
+    W = W.to(torch.bfloat16).to(DEV)
+    W = W if base == "dense" else lq.lq_nf4_quantize(W)
+
+    def step():
+        q = mx.lq_mx_quantize(X, "fp8")
+        return mx.lq_lora_bwd_ckpt(dY, q, W, A, B, s)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for k in range(4):
+        X.copy_(torch.randn(X.shape, generator=torch.Generator().manual_seed(k)))
+        dY.copy_(torch.randn(dY.shape, generator=torch.Generator().manual_seed(50 + k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(outs, eager))

@@ -146,3 +146,55 @@ def test_binding_refuses_wrong_operands():
         mx.lq_mx_lora_fwd(torch.zeros(65, 128, dtype=torch.bfloat16, device=DEV), W, A, B, s)
     with pytest.raises(mx.LqError):  # an 8-bit base is not a weight format
         mx.lq_mx_lora_fwd(X, mx.lq_mx_quantize(torch.zeros(128, 128, device=DEV), "fp8"), A, B, s)
+
+
+@pytest.mark.parametrize("M,r", [(1, 16), (4, 16), (13, 64), (64, 8), (3, 0)])
+def test_decode_captured_and_replayed(M, r):
+    """The single-token forward in a graph: every replay on new inputs equals
+    the eager call bit for bit, with eager work between the replays."""
+    announce(f"mx decode graph M={M} r={r}")
+    X, W, A, B, _, s = make(M, 512, 1024, r, "fp8", bf16_x=True)
+    call = lambda: mx.lq_mx_lora_fwd(X, W, A if r else None, B if r else None, s)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for k in range(4):
+        X.copy_(torch.randn(X.shape, generator=torch.Generator().manual_seed(k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("N,K", [(64, 11008), (11008, 64)])
+def test_offsets_past_31_bits(N, K, fmt):
+    """M K (or M N) just below 2^31 elements, 4 GB of bf16: rows at both ends
+    and around 2^31 bytes."""
+    M, r = 195000, 4
+    announce(f"mx long {fmt} N={N} K={K}")
+    g = torch.Generator(device=DEV).manual_seed(0)
+    X = torch.randn(M, K, generator=g, device=DEV, dtype=torch.bfloat16)
+    Xq = mx.lq_mx_quantize(X, fmt)
+    del X
+    _, W, A, B, _, s = make(1, N, K, r, fmt)
+    T = torch.empty(M, r, device=DEV)
+    Y = mx.lq_mx_lora_fwd(Xq, W, A, B, s, T_out=T)
+    back = mx.lq_mx_dequantize(Xq)
+    torch.cuda.synchronize()
+    w = values(W)
+    half = 2**31 // (2 * max(N, K))  # the row at 2^31 bytes of bf16
+    for m0 in (0, half - 50, 2 * half - 50, M - 100):
+        m0 = min(m0, M - 100)
+        rows = slice(m0, m0 + 100)
+        x = values(mx.MxTensor(Xq.codes[rows], Xq.scales[rows], 100, K, fmt))
+        assert torch.equal(back[rows].double(), x)
+        Yr, bY, Tr, bT = ref_forward(x, w, A, B, s, scaled=True)
+        assert_within(T[rows], Tr, bT, "T")
+        assert_within(Y[rows], Yr, bY, "Y")

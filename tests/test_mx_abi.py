@@ -35,6 +35,28 @@ def test_buffer_and_workspace_sizes():
     assert size(99, 2048, 4096, 4096, 16) == 0
 
 
+@pytest.mark.parametrize("op", [mx.LQ_MX_OP_FWD, mx.LQ_MX_OP_BWD, mx.LQ_MX_OP_BWD_CKPT])
+def test_workspace_size_of_refused_sizes_is_zero(op):
+    """Products that pass 64 bits, tile counts that pass 32: an answer, no fault."""
+    size = mx.lib().lq_mx_workspace_size
+    for M, N, K, r in [(1 << 40, 64, 64, 8), (1 << 62, 4096, 4096, 8), (1 << 33, 128, 128, 8),
+                       (64, 1 << 40, 64, 8), (64, 64, 1 << 62, 8), (64, 64, 64, 1 << 62),
+                       (64, 64, 64, 65), (1 << 25, 4096, 64, 8), (64, 64, 64, -1), (-1, 64, 64, 8)]:
+        assert size(op, M, N, K, r) == 0, (M, N, K, r)
+    assert size(op, 1 << 24, 64, 64, 8) > 0
+
+
+def test_row_counts_past_the_limits():
+    W, X = q(4, 64, 64), q(8, 1 << 40, 64)
+    assert fwd(X=None, Xq=X, M=1 << 40, W=W) == UNSUPPORTED
+    assert bwd(Xq=X, M=1 << 40, W=W) == UNSUPPORTED
+    w = lq.LqWeightStruct()
+    w.kind, w.dtype, w.N, w.K, w.dense = 0, lq.LQ_BF16, 64, 64, P
+    for M in (1 << 31, 1 << 40, 1 << 62):
+        assert mx.lib().lq_lora_bwd_ckpt(P, ctypes.byref(X), M, ctypes.byref(w), P, P, 8, 1.0, None,
+                                         P, P, P, 0, P, 1 << 40, None) == UNSUPPORTED
+
+
 def fwd(X=P, Xq=None, M=4, W=None, A=P, B=P, r=8, Y=P, T=None, ws=P, n=1 << 40):
     ref = lambda s: None if s is None else ctypes.byref(s)  # noqa: E731
     return mx.lib().lq_mx_lora_fwd(X, ref(Xq), M, ref(W), A, B, r, 1.0, Y, T, ws, n, None)
