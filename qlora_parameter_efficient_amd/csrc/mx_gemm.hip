@@ -47,8 +47,6 @@
 namespace lq {
 namespace {
 
-constexpr int kThreads = 256;
-
 struct MxgParams {
   const uint8_t* X;   // M x K codes
   const uint8_t* Xs;  // M x K / 32
@@ -64,26 +62,38 @@ struct MxgParams {
   int32_t ti, tj, splits, ksteps;
 };
 
-template <int FX, int IM, int JM>
+// IM, JM: 32 x 32 blocks of a wave; WI x 2 waves.  Scales of a step: WIDE (rows
+// of scales 16-byte aligned, K % 512 == 0) 16 bytes a row for the GS steps that
+// they cover, into two buffers of their own; else 4 or 8 bytes a row with the
+// step's stage.
+template <int FX, int IM, int JM, int WI, bool WIDE>
 struct MxgShape {
+  static constexpr int NW = 2 * WI, NT = 64 * NW;          // waves, threads
   static constexpr int BK = FX == LQ_MX_FP4 ? 256 : 128;   // columns per step
   static constexpr int KB = BK / 32;                       // blocks per row and step
-  static constexpr int TI = 64 * IM, TJ = 64 * JM;
+  static constexpr int GS = 16 / KB;                       // steps of a 16-byte scale load
+  static constexpr int TI = 32 * IM * WI, TJ = 64 * JM;
   static constexpr int WRow = BK / 2, XRow = 128;          // bytes per row and step
-  static constexpr int WBytes = TI * WRow, XBytes = TJ * XRow, SBytes = (TI + TJ) * KB;
-  static constexpr int Stage = WBytes + XBytes + SBytes;
+  static constexpr int WBytes = TI * WRow, XBytes = TJ * XRow;
+  static constexpr int Stage = WBytes + XBytes + (WIDE ? 0 : (TI + TJ) * KB);
+  static constexpr int GBytes = (TI + TJ) * 16;            // a scale buffer (WIDE)
   // stages: as many as one workgroup per compute unit allows (256-row tiles:
   // their accumulators leave room for one), two workgroups for 128 x 128
-  static constexpr int Room = (IM == 4 ? 160 : 80) * 1024;
+  static constexpr int Room = (TI == 256 ? 160 : 80) * 1024 - (WIDE ? 2 * GBytes : 0);
   static constexpr int NST = Room / Stage < 4 ? Room / Stage : 4;
+  static constexpr int SBase = NST * Stage;
+  static constexpr int Used = SBase + (WIDE ? 2 * GBytes : 0);
   static constexpr int Out = TJ * TI * 2;                  // bf16 output tile
-  static constexpr int Smem = NST * Stage > Out ? NST * Stage : Out;
-  static constexpr int WU = WBytes / 4096, XU = XBytes / 4096;   // code loads per wave
-  static constexpr int SRows = 256 / KB;                         // rows of a scale load
-  static constexpr int SG = (TI + TJ) / SRows;                   // scale loads per step ...
-  static constexpr int SU = (SG + 3) / 4;                        // ... and per wave
+  static constexpr int Smem = Used > Out ? Used : Out;
+  static constexpr int WU = WBytes / (1024 * NW), XU = XBytes / (1024 * NW);  // code loads per wave
+  static constexpr int SRows = WIDE ? 64 : 256 / KB;       // rows of a scale load
+  static constexpr int SG = (TI + TJ) / SRows;             // scale loads (WIDE: of GS steps) ...
+  static constexpr int SU = (SG + NW - 1) / NW;            // ... and per wave
   static constexpr int Loads = WU + XU + SU;
-  static constexpr int SR = (TI + TJ + kThreads - 1) / kThreads; // scale rows per thread (TAIL)
+  static constexpr int Counted = WIDE ? WU + XU : Loads;   // those of every step
+  static constexpr int SR = (TI + TJ + NT - 1) / NT;       // scale rows per thread (TAIL)
+  // a group's buffer is free when the loads of the next but one go out
+  static_assert(!WIDE || NST <= GS + 1, "scale buffers");
 };
 
 __device__ __forceinline__ i32x8 widen(const u32x4& v) {
@@ -103,14 +113,16 @@ __device__ __forceinline__ i32x8 join(const u32x4& a, const u32x4& b) {
 // the weight side, with scale 1 (byte 127) on both, and the scales, whose rows
 // may then start at any even address, go through registers.
 // SPLIT: several workgroups per tile, float32 partial sums out.
-template <int FX, int IM, int JM, bool TAIL, bool SPLIT>
-__global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
-  using S = MxgShape<FX, IM, JM>;
+template <int FX, int IM, int JM, int WI, bool TAIL, bool WIDE, bool SPLIT>
+__global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
+  using S = MxgShape<FX, IM, JM, WI, WIDE>;
+  static_assert(!(TAIL && WIDE), "a tail's scales go through registers");
+  constexpr int kThreads = S::NT;
   constexpr int KB = S::KB, MK = KB / 2;  // blocks and instructions (64 wide) per step
   __shared__ __attribute__((aligned(1024))) char smem[S::Smem];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wi = wave & 1, wj = wave >> 1;
+  const int wi = wave % WI, wj = wave / WI;
   const int h = lane >> 5, l32 = lane & 31;
 
   // tile: each XCD a contiguous range, in groups of four activation tiles
@@ -152,8 +164,8 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     xoff[u] = (uint32_t)(m * xpitch + 16 * xch[u]);
   }
   // scale rows of this wave's SU loads: group g of SRows rows (weight rows
-  // first), a word per lane; a group past the last is loaded again, to the
-  // same place
+  // first), a word (WIDE: 16 bytes) per lane; a group past the last is loaded
+  // again, to the same place (WIDE: not loaded)
   uint32_t soff[SU];
   bool sw_[SU];
   int sgrp[SU];
@@ -162,11 +174,11 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     int g = wave * SU + u;
     g = g < S::SG ? g : S::SG - 1;
     sgrp[u] = g;
-    const int R = g * S::SRows + lane / (KB / 4);
+    const int R = g * S::SRows + (WIDE ? lane : lane / (KB / 4));
     sw_[u] = g * S::SRows < S::TI;
     const int64_t row = sw_[u] ? i0 + R : j0 + R - S::TI;
     const int64_t last = (sw_[u] ? N : M) - 1;
-    soff[u] = (uint32_t)((row < last ? row : last) * spitch + 4 * (lane % (KB / 4)));
+    soff[u] = (uint32_t)((row < last ? row : last) * spitch + (WIDE ? 0 : 4 * (lane % (KB / 4))));
   }
   const char* wb0 = reinterpret_cast<const char*>(p.W);
   const char* xb0 = reinterpret_cast<const char*>(p.X);
@@ -182,6 +194,12 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
       const bool past = xch[v] >= (FX == LQ_MX_FP4 ? last_nb : 2 * last_nb);
       const uint32_t o = cut && past ? xoff[v] - 16 * xch[v] : xoff[v];
       mx_dma16(xb0 + (int64_t)kt * S::XRow, o, st + S::WBytes + (wave * XU + v) * 1024, go);
+    } else if (WIDE) {  // the group's first step in this workgroup brings its scales
+      const int v = u - WU - XU;
+      const int first = mx_less(kt & (S::GS - 1), 1) | mx_less(kt, ka + 1);
+      mx_dma16(reinterpret_cast<const char*>(sw_[v] ? p.Ws : p.Xs) + (int64_t)(kt / S::GS) * 16,
+               soff[v], sbase + S::SBase + (kt / S::GS & 1) * S::GBytes + sgrp[v] * 1024,
+               go & first & mx_less(wave * SU + v, S::SG));
     } else if (!TAIL) {
       const int v = u - WU - XU;
       mx_dma4((sw_[v] ? p.Ws : p.Xs) + (int64_t)kt * KB, soff[v],
@@ -265,8 +283,11 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     return join(mx_read16(row + (uint32_t)((c0 ^ xsw) << 4)),
                 mx_read16(row + (uint32_t)((c1 ^ xsw) << 4)));
   };
-  auto read_scale = [&](int b, int row) -> int {
-    const char* a = smem + b * S::Stage + S::WBytes + S::XBytes + row * KB + h * (KB / 2);
+  auto read_scale = [&](int kt, int b, int row) -> int {
+    const char* a = smem + (WIDE ? S::SBase + (kt / S::GS & 1) * S::GBytes + row * 16 +
+                                       (kt & (S::GS - 1)) * KB
+                                 : b * S::Stage + S::WBytes + S::XBytes + row * KB) +
+                    h * (KB / 2);
     if (KB == 8) return *reinterpret_cast<const int*>(a);
     return (int)*reinterpret_cast<const uint16_t*>(a);
   };
@@ -298,11 +319,11 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
 #pragma unroll
     for (int ms = 0; ms < JM; ++ms) xf[c][ms] = read_x(st, ms, kk);
   };
-  auto read_scales = [&](int b, int q) {
+  auto read_scales = [&](int kt, int b, int q) {
 #pragma unroll
-    for (int ns = 0; ns < IM; ++ns) ws[q][ns] = read_scale(b, wrow0 + 32 * ns);
+    for (int ns = 0; ns < IM; ++ns) ws[q][ns] = read_scale(kt, b, wrow0 + 32 * ns);
 #pragma unroll
-    for (int ms = 0; ms < JM; ++ms) xs[q][ms] = read_scale(b, S::TI + xrow0 + 32 * ms);
+    for (int ms = 0; ms < JM; ++ms) xs[q][ms] = read_scale(kt, b, S::TI + xrow0 + 32 * ms);
   };
   constexpr int NST = S::NST;
   // loads of the first NST steps; every split has at least one step
@@ -316,11 +337,11 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
   if constexpr (TAIL)
     mx_wait_loads();
   else
-    mx_wait_loads<(NST - 1) * S::Loads>(mx_less(ka + NST, kb + 1));
+    mx_wait_loads<(NST - 1) * S::Counted>(mx_less(ka + NST, kb + 1));
   __syncthreads();
   int kt = ka, b = 0;
   load_scales(mx_less(ka + 1, kb) ? ka + 1 : ka);
-  read_scales(0, 0);
+  read_scales(ka, 0, 0);
   frags(sbase, ka, 0, 0);
   do {
     const uint32_t st = sbase + b * S::Stage;
@@ -352,13 +373,13 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
     if constexpr (TAIL)
       mx_wait_loads();
     else
-      mx_wait_loads<(NST - 2) * S::Loads>(mx_less(kt + NST, kb + 1));
+      mx_wait_loads<(NST - 2) * S::Counted>(mx_less(kt + NST, kb + 1));
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     const int k1 = mx_less(kt + 1, kb) ? kt + 1 : kt;
     const int go = mx_less(kt + NST, kb);
     const int kn = go ? kt + NST : kt;
-    read_scales(bn, 1);
+    read_scales(k1, bn, 1);
     frags(sbase + bn * S::Stage, k1, 0, 0);
     load_scales(mx_less(kt + 2, kb) ? kt + 2 : k1);
     __builtin_amdgcn_sched_barrier(0);
@@ -460,15 +481,15 @@ __global__ __launch_bounds__(kThreads) void mxg_kernel(MxgParams p) {
 // 42 in two; 100 x 4096 x 4096: 19 and 15 in four; 512 x 4096 x 4096: 21 and 23
 // in two; 200 x 2048 x 2048: 11 and 12).
 struct Plan {
-  int im, jm, ti, tj, splits;
+  int rows_i, rows_j, ti, tj, splits;
 };
 
 Plan plan(int64_t M, int64_t N, int64_t K) {
-  static const int shapes[3][3] = {{4, 4, 3}, {4, 2, 2}, {2, 2, 1}};
+  static const int shapes[3][3] = {{256, 256, 3}, {256, 128, 2}, {128, 128, 1}};
   Plan q{};
   int64_t best = 0;
   for (const auto& c : shapes) {
-    const int64_t ti = cdiv(N, 64 * c[0]), tj = cdiv(M, 64 * c[1]);
+    const int64_t ti = cdiv(N, c[0]), tj = cdiv(M, c[1]);
     const int64_t cost = c[2] * cdiv(ti * tj, 256);
     if (best && cost >= best) continue;
     best = cost;
@@ -483,13 +504,15 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
   return q;
 }
 
-template <int FX, int IM, int JM, bool SPLIT>
+template <int FX, int IM, int JM, int WI, bool SPLIT>
 void launch(const MxgParams& p, hipStream_t st) {
-  const dim3 grid((unsigned)(p.ti * p.tj), (unsigned)p.splits), block(kThreads);
-  if (p.K % MxgShape<FX, IM, JM>::BK)
-    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, true, SPLIT>), grid, block, 0, st, p);
+  const dim3 grid((unsigned)(p.ti * p.tj), (unsigned)p.splits), block(128 * WI);
+  if (p.K % MxgShape<FX, IM, JM, WI, false>::BK)
+    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, WI, true, false, SPLIT>), grid, block, 0, st, p);
+  else if (p.K % 512)
+    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, WI, false, false, SPLIT>), grid, block, 0, st, p);
   else
-    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, false, SPLIT>), grid, block, 0, st, p);
+    hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, WI, false, true, SPLIT>), grid, block, 0, st, p);
 }
 
 // p.splits and p.ksteps are set so that every split has a step
@@ -498,14 +521,14 @@ void launch_shape(MxgParams& p, const Plan& q, hipStream_t st) {
   const int64_t steps = cdiv(p.K, FX == LQ_MX_FP4 ? 256 : 128);
   p.ksteps = (int32_t)cdiv(steps, q.splits);
   p.splits = (int32_t)cdiv(steps, p.ksteps);
-  if (q.im == 4 && q.jm == 4)
-    launch<FX, 4, 4, false>(p, st);
-  else if (q.im == 4)
-    launch<FX, 4, 2, false>(p, st);
+  if (q.rows_j == 256)
+    launch<FX, 2, 4, 4, false>(p, st);
+  else if (q.rows_i == 256)
+    launch<FX, 2, 2, 4, false>(p, st);
   else if (q.splits == 1)
-    launch<FX, 2, 2, false>(p, st);
+    launch<FX, 2, 2, 2, false>(p, st);
   else
-    launch<FX, 2, 2, true>(p, st);
+    launch<FX, 2, 2, 2, true>(p, st);
 }
 
 }  // namespace

@@ -63,6 +63,10 @@ def test_small_and_ragged(M, N, K, r, fmt):
     (4000, 4096, 256, 64),    # 256 x 256 tiles
     (3585, 4160, 576, 9),     # the same with a tail and ragged edges
     (1500, 2048, 384, 16),    # 128 x 128 tiles
+    (1500, 2048, 1024, 16),   # the same, scales of several steps per load
+    (4000, 4096, 512, 20),    # 256 x 256, the same
+    (2048, 3200, 2560, 16),   # 256 x 128, the same
+    (100, 512, 4608, 8),      # split K that starts inside such a load
 ])
 def test_tile_variants(M, N, K, r, fmt):
     check(M, N, K, r, fmt)
