@@ -31,6 +31,7 @@ Modules:
     lora  -- forward, backward, merge, segmented multi-adapter forward
              (uniform or per-adapter ranks and scales), LoRA-input dropout,
              DoRA forward and backward, trainable-parameter counts
+    mx    -- MXFP8 / MXFP4 quantize and dequantize (OCP microscaling formats)
     optim -- AdamW step on the adapter factors (float32 master, m, v)
 
 Parity unpinned: none of the functions here is without a pin; what pins
@@ -40,4 +41,4 @@ second-level constants are readings of the pages (see the ``nf4`` module
 docstring); they are pinned to the pages' properties, not to an external
 NF4 implementation, which none of the pages prints.
 """
-from . import lora, nf4, optim  # noqa: F401
+from . import lora, mx, nf4, optim  # noqa: F401

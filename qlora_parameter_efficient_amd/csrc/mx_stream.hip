@@ -23,6 +23,10 @@
 // costs the device little more than the launch it saves, and a host that
 // issues single decode calls half the time.  (With MFMA operand loads, 16 lines
 // per instruction, the same took 12 us at M = 1, N = K = 4096, r = 16.)
+//
+// Measured: M = 1, N = K = 4096, r = 16 9.4 us (8.9 MB of W: 0.95 TB/s; the launch,
+// T and the one wave of blocks bound it), M = 13, N = 11008, K = 4096, r = 64 14.4
+// us (24 MB: 1.7 TB/s) and 4.1 for T.
 #include "dispatch.h"
 #include "mx.h"
 
