@@ -9,7 +9,9 @@
 //
 // Both kernels are bound by HBM.  Quantiser: a thread owns half a block (16
 // columns), so a lane pair shares a block and one DPP move completes its amax;
-// codes leave as one 16-byte (FP8) or 8-byte (FP4) store per thread.
+// codes leave as one 16-byte (FP8) or 8-byte (FP4) store per thread (with one
+// 16-byte load a thread, consecutive as below, it takes the same 51 us, and
+// float32 8.1 against 7.6).
 // Dequantiser: a thread owns two 16-byte pieces of the output, consecutive
 // lanes consecutive pieces (with 16 float32 of a row per thread, four stores 64
 // bytes apart, 2049 x 4095 to float32 took 15 us).  A tensor whose rows hold

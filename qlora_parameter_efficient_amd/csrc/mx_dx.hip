@@ -26,12 +26,15 @@
 // One barrier per step, before the last substep's products (see mxg_kernel):
 // after it the tiles just read are free, so the last substep converts the W
 // tile two steps ahead, and the next step's first substep issues the loads
-// behind that.  LDS-bound: per step and compute unit about 96 (JM = 2) or 128
-// KB of operand reads and 48 or 64 KB of writes, which run at less than half
-// the read rate, against 1,024 or 2,048 cycles of products.  Measured: 2048 x 4096
+// behind that.  Bound by what LDS moves: per step and compute unit
+// about 96 (JM = 2) or 128 KB of operand reads and 48 or 64 KB of writes, which
+// run at less than half the read rate, against 1,024 or 2,048 cycles of products.  Measured: 2048 x 4096
 // x 4096 79 us (0.87 PFLOP/s), 8192 x 4096 x 11008 707 us (1.04), 1001 x 4096 x
 // 11008 111 us (0.81).  Timed apart at the first shape when it took 88 us: 67
-// without the W tile's writes, 76 without the loads, 58 without both.
+// without the W tile's writes, 76 without the loads, 58 without both.  Eight
+// waves on the tile, with half again the operand reads, take the same time
+// (8192 x 4096 x 11008 at r = 16: 677 us both), so neither the reads nor the
+// waves' latency bound it; the clock falls with the work moved.
 //
 // Split: few tiles leave float32 partial sums of ranges of n, the first with
 // the expand, added in order by mx_sum_splits_kernel.
