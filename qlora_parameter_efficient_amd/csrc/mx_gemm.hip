@@ -40,12 +40,12 @@
 // leave float32 partial sums (the first with the expand), added in order by
 // mx_sum_splits.
 //
-// Measured: 2048 x 4096 x 4096 MXFP8 39 us (1.76 PFLOP/s), 8192 x 11008 x 4096
-// MXFP4 283 us (2.6 PFLOP/s), 1001 x 4096 x 11008 MXFP8 60 us (1.5).  The same
-// instructions alone on random codes run at 3.9 to 4.4 and 7.1 to 7.5 PFLOP/s:
-// the matrix units are busy 44% of the time at the first shape, LDS 30%; the
-// rest are the waits of waves in step at a step's barrier, and a clock that
-// falls under this load (codes of zeros run 20% faster).
+// Measured: 2048 x 4096 x 4096 MXFP8 38 us (1.8 PFLOP/s), 8192 x 11008 x 4096
+// MXFP4 279 us (2.6 PFLOP/s), 1001 x 4096 x 11008 MXFP8 61 us (1.5).
+// The matrix units are busy 62 to 69% of the loop's cycles, and the shader clock
+// falls to 1.4 to 2.0 GHz under it (codes of zeros run 20% faster): power bounds
+// the rest.  The same instructions alone, on random codes in registers, run at
+// 3.9 to 4.4 PFLOP/s with an 8-bit X and 7.1 to 7.5 with a 4-bit one.
 //
 // Epilogue: the expand adds (s T) B^T on the finished accumulators with bf16
 // MFMAs (T rounded to bf16 after the multiply by s: the same rounding as the
@@ -222,9 +222,9 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
 #pragma unroll
     for (int u = 0; u < S::Loads; ++u) issue_one(kt, b, go, u);
   };
-  // the loads dealt over the IM JM products of a substep: part i of IM JM
+  // the loads dealt over the products of two substeps: part i of 2 IM JM
   auto issue_part = [&](int kt, int b, int go, int i) {
-    constexpr int parts = IM * JM;
+    constexpr int parts = 2 * IM * JM;
 #pragma unroll
     for (int u = 0; u < S::Loads; ++u)
       if (u * parts / S::Loads == i) issue_one(kt, b, go, u);
@@ -314,11 +314,13 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
 
   // The loop, pipelined across the barrier: a substep's LDS reads go out before
   // the previous substep's products, and the last substep's products run after
-  // the barrier, covering the first reads of the next step and the issue of
-  // the loads NST steps ahead (into the stage the barrier has just freed), so
-  // those loads have NST - 1 steps to land.  The body has no branch: one
-  // between the products and the barrier would let the compiler sink products
-  // past it, so loads past the last step are skipped inside mx_dma16.
+  // the barrier, covering the first reads of the next step and the first half
+  // of the loads NST steps ahead (into the stage the barrier has just freed);
+  // the second half goes out among the next step's first products (all of them
+  // in one substep: 8192 x 11008 x 4096 MXFP4 249 us against 239).  The body has
+  // no branch: one between the products and the barrier would let the compiler
+  // sink products past it, so loads past the last step are skipped inside
+  // mx_dma16.
   u32x4 wf[2][IM];
   i32x8 xf[2][JM];
   int ws[2][IM], xs[2][JM];
@@ -355,6 +357,7 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
   load_scales(mx_less(ka + 1, kb) ? ka + 1 : ka);
   read_scales(ka, 0, 0);
   frags(sbase, ka, 0, 0);
+  int kp = ka, bp = 0, gp = 0;  // step, stage and go of the loads under way
   do {
     const uint32_t st = sbase + b * S::Stage;
     const int bn = b + 1 == NST ? 0 : b + 1;
@@ -371,7 +374,14 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
 #pragma unroll
       for (int ns = 0; ns < IM; ++ns)
 #pragma unroll
-        for (int ms = 0; ms < JM; ++ms) products(k, ns, ms);
+        for (int ms = 0; ms < JM; ++ms) {
+          products(k, ns, ms);
+          if (kk == 0) {  // the second half of the loads that the last step began
+            __builtin_amdgcn_sched_barrier(0);
+            issue_part(kp, bp, gp, IM * JM + ns * JM + ms);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
       __builtin_amdgcn_sched_barrier(0);
     };
     sub(std::integral_constant<int, 0>{});
@@ -409,6 +419,7 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
     for (int ns = 0; ns < IM; ++ns) ws[0][ns] = ws[1][ns];
 #pragma unroll
     for (int ms = 0; ms < JM; ++ms) xs[0][ms] = xs[1][ms];
+    kp = kn, bp = b, gp = go;
     b = bn;
   } while (++kt < kb);
   __syncthreads();  // the output tile overwrites the stages
