@@ -114,6 +114,23 @@ size_t bwd_big_bytes(int64_t M, int64_t N, int64_t K) {
   return dispatch::big_dx_eligible(M, N, K) ? dispatch::big_dx_ws_bytes(M, N, K) : 0;
 }
 
+// dX of a dense base from an MX checkpoint by mxdx_kernel (U apart) instead of
+// the kernels of lq_lora_bwd, dX and U in us, theirs / this:
+//   off the large-tile product (K % 256 != 0): 66 x 5056 x 320 63 / 22, 300 x 4160 x
+//     4992 56 / 42, 4000 x 4160 x 4992 (r 64) 339 / 241; but where both are launches,
+//     500 x 512 x 448 12 / 16, 8000 x 128 x 192 11 / 13
+//   on it, where this splits the reduction or has tiles of 128 rows: 64 x 4096 x
+//     4096 44 / 26, 512 x 4096 x 4096 47 / 39, 2048 x 4096 x 4096 78 / 75; between,
+//     with 64-row tiles in one round, 777 x 4096 x 4096 50 / 60
+//   and at ranks that U reads element by element there, 1001 x 4096 x 11008 (r 11)
+//     303 / 108
+bool ckpt_dense_dx(int64_t M, const lq_weight& w, int64_t r) {
+  if (w.kind != LQ_WEIGHT_DENSE) return false;
+  if (!dispatch::big_dx_eligible(M, w.N, w.K))
+    return w.N >= 1024 || (double)M * w.N * w.K >= 2147483648.0;
+  return r % 4 != 0 || dispatch::mx_dx_fills(M, w.N, w.K);
+}
+
 size_t multi_big_bytes(int64_t T, int64_t N, int64_t K, int64_t rc) {
   return dispatch::big_fwd_eligible(T, N, K) ? dispatch::big_multi_ws_bytes(T, N, K, rc) : 0;
 }
@@ -589,7 +606,8 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
   if (dA && (rc = mx_check_tensor(Xq, "Xq", LQ_MX_FP4 | LQ_MX_FP8, M, K))) return rc;
   if ((rc = mx_check_aligned(dY, "dY")) || (rc = mx_check_aligned(dX, "dX")) ||
       (rc = mx_check_aligned(A, "A")) || (rc = mx_check_aligned(B, "B")) ||
-      (rc = mx_check_aligned(ws, "ws")) || (rc = mx_check_aligned(T_saved, "T_saved")))
+      (rc = mx_check_aligned(ws, "ws")) || (rc = mx_check_aligned(T_saved, "T_saved")) ||
+      (W0->kind == LQ_WEIGHT_DENSE && (rc = mx_check_aligned(W0->dense, "W0"))))
     return rc;
   const size_t need = lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT, M, N, K, r);
   REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
@@ -598,9 +616,13 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
   char* base = (char*)ws;
   float* U = (float*)(base + w.u);
   void* big_ws = dX && bwd_big_bytes(M, N, K) ? base + w.rest : nullptr;
-  rc = dX ? dispatch::bf16_dx_any(dY, M, *W0, A, B, r, scale, dX, U, dA ? U : nullptr, big_ws,
-                                  stream)
-          : dispatch::mx_u(dY, M, N, B, r, base + w.bt, U, stream);
+  const bool own_dx = dX && ckpt_dense_dx(M, *W0, r);
+  if (!dX || own_dx)
+    rc = dispatch::mx_u(dY, M, N, B, r, base + w.bt, U, stream);
+  else
+    rc = dispatch::bf16_dx_any(dY, M, *W0, A, B, r, scale, dX, U, dA ? U : nullptr, big_ws, stream);
+  if (!rc && own_dx)
+    rc = dispatch::mx_dx_dense(dY, M, *W0, U, A, r, scale, dX, base + w.rest, stream);
   if (rc || !dA) return rc;
   const float* T = T_saved;
   if (!T) {

@@ -92,6 +92,12 @@ size_t mx_dx_ws_bytes(int64_t M, int64_t N, int64_t K);
 int mx_dx(const void* dY, int64_t M, const lq_mx_tensor& W, const float* U, const void* A,
           int64_t r, float s, void* dX, void* part, hipStream_t st);
 
+// The same with a dense bf16 W (N, K <= 65536).  mx_dx_fills: not tiles of 64
+// rows in one round (too many to split, too few to fill the chip).
+bool mx_dx_fills(int64_t M, int64_t N, int64_t K);
+int mx_dx_dense(const void* dY, int64_t M, const lq_weight& W, const float* U, const void* A,
+                int64_t r, float s, void* dX, void* part, hipStream_t st);
+
 // Few rows (M <= LQ_MX_ROWS_BF16), X bf16: Y = X W^T + s (X A^T) B^T, W
 // streamed once per 16 rows.  Tp: mx_stream_ws_bytes bytes of partial sums.
 size_t mx_stream_ws_bytes(int64_t M, int64_t K, int64_t r);

@@ -66,8 +66,13 @@ size_t fwd_part_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
   return g > s ? g : s;
 }
 
+// dX of a dense or NF4 base: the large-tile product's part, or that of the
+// split dX of a dense base (the weight's kind and which of them runs are not
+// known here)
 size_t big_dx_bytes(int64_t M, int64_t N, int64_t K) {
-  return dispatch::big_dx_eligible(M, N, K) ? dispatch::big_dx_ws_bytes(M, N, K) : 0;
+  const size_t a = dispatch::big_dx_eligible(M, N, K) ? dispatch::big_dx_ws_bytes(M, N, K) : 0;
+  const size_t b = dispatch::mx_dx_ws_bytes(M, N, K);
+  return a > b ? a : b;
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
 // Input gradient of the MXFP4 layer:
 //
-//   dX = dY W + (s U) A       dY bf16 (M x N), W MXFP4 (N x K), U = dY B
+//   dX = dY W + (s U) A       dY bf16 (M x N), W MXFP4 or bf16 (N x K), U = dY B
 //                             (M x r float32), A bf16 (r x K)
 //
 // The reduction runs over N while a scale covers 32 columns k of one row n, so
@@ -36,6 +36,9 @@
 // (8192 x 4096 x 11008 at r = 16: 677 us both), so neither the reads nor the
 // waves' latency bound it; the clock falls with the work moved.
 //
+// A dense bf16 W (the backward from an MX checkpoint of a dense layer) takes
+// the same loop with its W tiles loaded straight into LDS.
+//
 // Split: few tiles leave float32 partial sums of ranges of n, the first with
 // the expand, added in order by mx_sum_splits_kernel.
 #include <type_traits>
@@ -52,8 +55,8 @@ constexpr int kStep = 64; // reduction rows n per step
 
 struct MxdxParams {
   const uint16_t* dY;     // M x N
-  const uint8_t* W;       // N x K / 2
-  const uint8_t* Ws;      // N x K / 32
+  const uint8_t* W;       // N x K / 2 codes, or bf16 N x K
+  const uint8_t* Ws;      // N x K / 32 (codes)
   const float* U;         // M x r
   const uint16_t* A;      // r x K
   uint16_t* dX;           // M x K
@@ -73,6 +76,7 @@ struct MxdxShape {
   static constexpr int Out = TJ * kTI * 2;
   static constexpr int Smem = YBase + 2 * YTile > Out ? YBase + 2 * YTile : Out;
   static constexpr int YU = YTile / 4096;        // dY loads per wave and step
+  static constexpr int WU = WTile / 4096;        // W loads per wave and step (bf16 W)
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -88,7 +92,9 @@ __device__ __forceinline__ int wphys(int c, int n) {
   return c ^ (2 * (n & 3)) ^ (8 * ((c >> 1) & 1));
 }
 
-template <int JM, bool SPLIT>
+// FP4: W are MXFP4 codes; else bf16 values, whose tiles come straight from global
+// memory like dY's, at the places where the codes are converted.
+template <bool FP4, int JM, bool SPLIT>
 __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   using S = MxdxShape<JM>;
   __shared__ __attribute__((aligned(1024))) char smem[S::Smem];
@@ -132,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   const int cn = tid >> 2, cq = tid & 3;
   const uint8_t *wp[2], *sp[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; FP4 && i < 2; ++i) {
     const int blk = cq + 4 * i < blocks ? cq + 4 * i : 0;
     wp[i] = p.W + cn * (K / 2) + i0 / 2 + 16 * blk;
     sp[i] = p.Ws + cn * (K / 32) + i0 / 32 + blk;
@@ -142,7 +148,7 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   auto load_codes = [&](int kt) {
     const int64_t row0 = (int64_t)kt * kStep;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; FP4 && i < 2; ++i) {
       cw[i] = *reinterpret_cast<const u32x4*>(wp[i] + row0 * (K / 2));
       cs[i] = sp[i][row0 * (K / 32)];
     }
@@ -151,10 +157,27 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     wst[c] = (uint32_t)(cn * 512 + wphys(4 * (cq + 4 * (c >> 2)) + (c & 3), cn) * 16);
-  auto convert = [&](int b, int c) {
-    *reinterpret_cast<u32x4*>(smem + b * S::WTile + wst[c]) =
-        mx4_bf16(cw[c >> 2][c & 3], mx_scale(cs[c >> 2]));
+  // bf16 W: load u of the wave brings rows n and n + 1, lane i their chunk that
+  // sits at i % 32 (one past K: the row's first)
+  uint32_t wo[S::WU];
+#pragma unroll
+  for (int u = 0; !FP4 && u < S::WU; ++u) {
+    const int n = 2 * (wave * S::WU + u) + (lane >> 5), at = lane & 31;
+    const int c1 = ((at >> 1) ^ n) & 1;  // bit 1 of the chunk at this place
+    const int c = at ^ (2 * (n & 3)) ^ (8 * c1);
+    wo[u] = (uint32_t)(n * K * 2 + 16 * (c < 4 * blocks ? c : 0));
+  }
+  const char* wb0 = reinterpret_cast<const char*>(p.W) + i0 * 2;
+  // piece c of 8 of the W tile of step kt into tile b
+  auto convert = [&](int kt, int b, int go, int c) {
+    if constexpr (FP4)
+      *reinterpret_cast<u32x4*>(smem + b * S::WTile + wst[c]) =
+          mx4_bf16(cw[c >> 2][c & 3], mx_scale(cs[c >> 2]));
+    else
+      mx_dma16(wb0 + (int64_t)kt * kStep * K * 2, wo[c],
+               sbase + b * S::WTile + (wave * S::WU + c) * 1024, go);
   };
+  static_assert(S::WU == 8, "pieces of a W tile");
 
   // ---- per-lane LDS read offsets
   const int sw = mx_swz128(l32);
@@ -203,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
 #pragma unroll
     for (int u = 0; u < S::YU; ++u) issue_y(next(ka, q), q, q == 0 ? 1 : mx_less(ka + 1, kb), u);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) convert(q, c);
+    for (int c = 0; c < 8; ++c) convert(next(ka, q), q, q == 0 ? 1 : mx_less(ka + 1, kb), c);
   }
   load_codes(next(ka, 2));
   mx_wait_loads();
@@ -216,6 +239,7 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   do {
     const int go1 = (mx_less(ka, kt) & mx_less(kt + 1, kb));  // dY of step kt + 1 (the first is there)
     const int k1 = next(kt, 1);
+    const int go2 = FP4 ? 0 : mx_less(kt + 2, kb), k2 = go2 ? kt + 2 : kt;
     auto sub = [&](auto k) {
       constexpr int s = decltype(k)::value, c = s & 1;
       frags(b, s + 1, c ^ 1);
@@ -251,7 +275,7 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          if (c * JM / 2 == ns * JM + ms) convert(b, c);
+          if (c * JM / 2 == ns * JM + ms) convert(k2, b, go2, c);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -387,10 +411,30 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
   return q;
 }
 
-template <int JM, bool SPLIT>
+template <bool FP4, int JM, bool SPLIT>
 void launch(const MxdxParams& p, hipStream_t st) {
-  hipLaunchKernelGGL((mxdx_kernel<JM, SPLIT>), dim3((unsigned)(p.ti * p.tj), (unsigned)p.splits),
+  hipLaunchKernelGGL((mxdx_kernel<FP4, JM, SPLIT>), dim3((unsigned)(p.ti * p.tj), (unsigned)p.splits),
                      dim3(kThreads), 0, st, p);
+}
+
+template <bool FP4>
+int run_dx(MxdxParams& p, hipStream_t st) {
+  const Plan q = plan(p.M, p.N, p.K);
+  p.ti = q.ti;
+  p.tj = q.tj;
+  p.splits = q.splits;
+  p.ksteps = (int32_t)cdiv(p.N / kStep, q.splits);
+  if (q.splits > 1)
+    launch<FP4, 1, true>(p, st);
+  else if (q.jm == 4)
+    launch<FP4, 4, false>(p, st);
+  else if (q.jm == 2)
+    launch<FP4, 2, false>(p, st);
+  else
+    launch<FP4, 1, false>(p, st);
+  const int e = hip_fail(hipGetLastError(), "mx_dx launch");
+  if (e || q.splits == 1) return e;
+  return dispatch::mx_sum_splits(p.part, p.dX, p.M * p.K, q.splits, st);
 }
 
 }  // namespace
@@ -410,35 +454,21 @@ size_t mx_dx_ws_bytes(int64_t M, int64_t N, int64_t K) {
 
 int mx_dx(const void* dY, int64_t M, const lq_mx_tensor& W, const float* U, const void* A,
           int64_t r, float s, void* dX, void* part, hipStream_t st) {
-  MxdxParams p;
-  p.dY = (const uint16_t*)dY;
-  p.W = W.codes;
-  p.Ws = W.scales;
-  p.U = U;
-  p.A = (const uint16_t*)A;
-  p.dX = (uint16_t*)dX;
-  p.part = (float*)part;
-  p.M = M;
-  p.N = W.rows;
-  p.K = W.cols;
-  p.r = (int32_t)r;
-  p.s = s;
-  const Plan q = plan(M, p.N, p.K);
-  p.ti = q.ti;
-  p.tj = q.tj;
-  p.splits = q.splits;
-  p.ksteps = (int32_t)cdiv(p.N / kStep, q.splits);
-  if (q.splits > 1)
-    launch<1, true>(p, st);
-  else if (q.jm == 4)
-    launch<4, false>(p, st);
-  else if (q.jm == 2)
-    launch<2, false>(p, st);
-  else
-    launch<1, false>(p, st);
-  const int e = hip_fail(hipGetLastError(), "mx_dx launch");
-  if (e || q.splits == 1) return e;
-  return mx_sum_splits(p.part, p.dX, M * p.K, q.splits, st);
+  MxdxParams p = {(const uint16_t*)dY, W.codes, W.scales, U, (const uint16_t*)A, (uint16_t*)dX,
+                  (float*)part, M, W.rows, W.cols, (int32_t)r, s, 0, 0, 0, 0};
+  return run_dx<true>(p, st);
+}
+
+bool mx_dx_fills(int64_t M, int64_t N, int64_t K) {
+  const Plan q = plan(M, N, K);
+  return q.jm > 1 || q.splits > 1;
+}
+
+int mx_dx_dense(const void* dY, int64_t M, const lq_weight& W, const float* U, const void* A,
+                int64_t r, float s, void* dX, void* part, hipStream_t st) {
+  MxdxParams p = {(const uint16_t*)dY, (const uint8_t*)W.dense, nullptr, U, (const uint16_t*)A,
+                  (uint16_t*)dX, (float*)part, M, W.N, W.K, (int32_t)r, s, 0, 0, 0, 0};
+  return run_dx<false>(p, st);
 }
 
 }  // namespace dispatch

@@ -70,6 +70,29 @@ def test_checkpoint_of_dense_and_nf4_layers(M, N, K, r, fmt, base):
     compare(got, ref_backward(dY, x, T.double(), Wd.double(), A, B, s))
 
 
+@pytest.mark.parametrize("M,N,K,r", [(2, 3840, 384, 11), (1, 1024, 64, 1), (66, 5056, 320, 16),
+                                     (16, 4096, 512, 8), (300, 1024, 4992, 5), (1001, 1088, 11072, 8),
+                                     (2050, 1024, 4160, 16), (130, 1024, 512, 7), (512, 1024, 1024, 64)])
+def test_dense_base_of_many_shapes(M, N, K, r):
+    """dX of a dense base, alone and with the gradients: split reductions, every
+    tile height, columns that end inside a tile, ranks that are no multiple of 4."""
+    announce(f"ckpt dense M={M} N={N} K={K} r={r}")
+    X, _, A, B, dY, s = make(M, N, K, r, "fp8")
+    W = (torch.randn((N, K), generator=torch.Generator().manual_seed(9)) * 0.02)
+    W = W.to(torch.bfloat16).to(DEV)
+    x = values(X)
+    T = (x @ A.double().t()).float()
+    refs = ref_backward(dY, x, T.double(), W.double(), A, B, s)
+    whole, (dX, dA, dB) = out_buffers(M, N, K, r)
+    got = mx.lq_lora_bwd_ckpt(dY, X, W, A, B, s, T_saved=T, dX=dX, dA=dA, dB=dB)
+    alone, _, _ = mx.lq_lora_bwd_ckpt(dY, None, W, A, B, s, need_grads=False)
+    torch.cuda.synchronize()
+    compare(got, refs)
+    assert torch.equal(alone, dX)
+    for t in whole:
+        assert (t[0] == 5.0).all() and (t[-1] == 5.0).all()
+
+
 def test_parts_and_accumulation():
     M, N, K, r = 200, 256, 320, 12
     X, W, A, B, dY, s = make(M, N, K, r, "fp8")

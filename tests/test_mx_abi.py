@@ -170,6 +170,9 @@ def test_checkpoint_backward_refusals():
     assert call(dY=None) == INVALID and call(A=None) == INVALID
     assert call(n=0) == WORKSPACE and call(ws=None) == WORKSPACE
     assert call(dY=P + 2) == INVALID and call(T=P + 4) == INVALID
+    w.dense = P + 2
+    assert call() == INVALID
+    w.dense = P
     f32 = lq.LqWeightStruct()
     f32.kind, f32.dtype, f32.N, f32.K, f32.dense = 0, lq.LQ_F32, 256, 256, P
     assert call(W=f32) == INVALID
