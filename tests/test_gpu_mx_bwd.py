@@ -93,6 +93,32 @@ def test_dense_base_of_many_shapes(M, N, K, r):
         assert (t[0] == 5.0).all() and (t[-1] == 5.0).all()
 
 
+@pytest.mark.parametrize("base", ["mxfp4", "dense"])
+@pytest.mark.parametrize("M,N,K", [(70, 1024, 320), (300, 1088, 4992)])
+def test_non_finite_rows_stay_in_their_rows(M, N, K, base):
+    """A NaN in row m of dY makes row m of dX NaN, one in a weight its columns
+    (a block of 32, or one of a dense base); nothing else."""
+    announce(f"bwd NaN {base} {M} {N} {K}")
+    X, W, A, B, dY, s = make(M, N, K, 8, "fp8")
+    dY[5, 3] = float("nan")
+    dY[M - 1, N - 1] = float("inf")
+    want = torch.zeros((M, K), dtype=torch.bool, device=DEV)
+    if base == "mxfp4":
+        W.scales[N - 2, K // 32 - 1] = 255
+        want[:, K - 32:] = True
+        dX, _, _ = mx.lq_mx_lora_bwd(dY, None, W, A, B, s, need_grads=False)
+    else:
+        Wd = (torch.randn((N, K), generator=torch.Generator().manual_seed(9)) * 0.02)
+        Wd = Wd.to(torch.bfloat16).to(DEV)
+        Wd[N - 2, K - 1] = float("nan")
+        want[:, K - 1] = True
+        dX, _, _ = mx.lq_lora_bwd_ckpt(dY, None, Wd, A, B, s, need_grads=False)
+    torch.cuda.synchronize()
+    assert not torch.isfinite(dX[M - 1]).any()  # infinities of both signs, or their sums
+    want[5] = True
+    assert torch.equal(torch.isnan(dX[:-1]), want[:-1])
+
+
 def test_parts_and_accumulation():
     M, N, K, r = 200, 256, 320, 12
     X, W, A, B, dY, s = make(M, N, K, r, "fp8")

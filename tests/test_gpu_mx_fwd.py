@@ -102,6 +102,24 @@ def test_non_finite_blocks_stay_in_their_rows():
             assert torch.isnan(T[3]).all() and not torch.isnan(torch.cat([T[:3], T[4:]])).any()
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,N,K", [(70, 128, 1024), (40, 512, 4608), (2000, 3200, 512)])
+def test_non_finite_blocks_under_wide_scale_loads(M, N, K, fmt):
+    """The same where one load brings the scales of several steps (K % 512 == 0),
+    whole and split: first, last and middle blocks."""
+    announce(f"mx fwd NaN wide {fmt} {M} {N} {K}")
+    X, W, A, B, _, s = make(M, N, K, 8, fmt)
+    kb = K // 32
+    X.scales[3, kb - 1], X.scales[17, 0], X.scales[M - 1, kb // 2 + 1] = 255, 255, 255
+    W.scales[5, 7], W.scales[N - 1, kb - 2] = 255, 255
+    Y = mx.lq_mx_lora_fwd(X, W, A, B, s)
+    nan = torch.isnan(Y).cpu().numpy()
+    want = np.zeros((M, N), bool)
+    want[[3, 17, M - 1]] = True
+    want[:, [5, N - 1]] = True
+    assert np.array_equal(nan, want)
+
+
 def test_extreme_scales():
     """Scale bytes far from 127 on both sides: products from 2^-200 up to 2^100."""
     M, N, K = 96, 128, 256
