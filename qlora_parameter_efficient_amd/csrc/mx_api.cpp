@@ -38,7 +38,18 @@ constexpr int64_t kMaxElems = (int64_t)1 << 35;
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// shape rules of the layer's MX entry points
+// The first of the layer's shape rules that the sizes break, or NULL: one place
+// for the calls and for the workspace sizes, which are asked for before a call
+// has checked anything.  M, N and K are positive, or M is 0.
+const char* broken_rule(int64_t M, int64_t N, int64_t K, int64_t r, int64_t rmin) {
+  const int64_t lim = (int64_t)1 << 31;
+  if (K % 64 || N % 64) return "N and K must be multiples of 64";
+  if (K > 65536 || N > 65536) return "N, K <= 65536";
+  if (M >= lim || M * K >= lim || M * N >= lim) return "M*K and M*N must be below 2^31 elements";
+  if (r < rmin || r > kMaxRank) return rmin ? "rank outside [1, 64]" : "rank outside [0, 64]";
+  return nullptr;
+}
+
 int check_layer(const lq_mx_tensor* W0, int64_t M, int64_t r, int64_t rmin) {
   REQUIRE(W0 != nullptr, LQ_ERR_INVALID_ARG, "W0 is NULL");
   const int64_t N = W0->rows, K = W0->cols;
@@ -46,15 +57,9 @@ int check_layer(const lq_mx_tensor* W0, int64_t M, int64_t r, int64_t rmin) {
   REQUIRE(M >= 0, LQ_ERR_INVALID_ARG, "M = %lld", (long long)M);
   int rc = mx_check_tensor(W0, "W0", LQ_MX_FP4, N, K);
   if (rc) return rc;
-  REQUIRE(K % 64 == 0 && N % 64 == 0, LQ_ERR_UNSUPPORTED,
-          "N and K must be multiples of 64 (N=%lld K=%lld)", (long long)N, (long long)K);
-  REQUIRE(K <= 65536 && N <= 65536, LQ_ERR_UNSUPPORTED, "N, K <= 65536 (N=%lld K=%lld)",
-          (long long)N, (long long)K);
-  const int64_t lim = (int64_t)1 << 31;
-  REQUIRE(M < lim && M * K < lim && M * N < lim, LQ_ERR_UNSUPPORTED,
-          "M*K and M*N must be below 2^31 elements (M=%lld)", (long long)M);
-  REQUIRE(r >= rmin && r <= kMaxRank, LQ_ERR_UNSUPPORTED, "rank %lld outside [%lld, %lld]",
-          (long long)r, (long long)rmin, (long long)kMaxRank);
+  const char* rule = broken_rule(M, N, K, r, rmin);
+  REQUIRE(!rule, LQ_ERR_UNSUPPORTED, "%s (M=%lld N=%lld K=%lld r=%lld)", rule, (long long)M,
+          (long long)N, (long long)K, (long long)r);
   return LQ_OK;
 }
 
@@ -124,9 +129,7 @@ int lq_mx_dequantize(const lq_mx_tensor* q, void* out, lq_dtype odt, hipStream_t
 
 size_t lq_mx_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r) {
   // 0 too for the sizes that the operators refuse
-  const int64_t lim = (int64_t)1 << 31;
-  if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > kMaxRank) return 0;
-  if (M >= lim || N >= lim || K >= lim || M * K >= lim || M * N >= lim) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || broken_rule(M, N, K, r, op == LQ_MX_OP_FWD ? 0 : 1)) return 0;
   switch (op) {
     case LQ_MX_OP_FWD:
       return up256((size_t)(M * r) * 4) + fwd_part_bytes(M, N, K, r);

@@ -257,6 +257,17 @@ def test_binding_refuses_wrong_operands():
                 fn(**kw)
 
 
+@pytest.mark.parametrize("N,K", [(32, 64), (63, 128), (96, 100)])
+def test_layers_off_the_shape_rules_raise(N, K):
+    """Also where no tile fits the layer: an error of the call, from both backwards."""
+    announce(f"mx bwd refused shape N={N} K={K}")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    W, X = mx.lq_mx_quantize(bf(N, K), "fp4"), mx.lq_mx_quantize(bf(8, K), "fp8")
+    for fn, w in ((mx.lq_mx_lora_bwd, W), (mx.lq_lora_bwd_ckpt, bf(N, K))):
+        with pytest.raises(mx.LqError, match="64"):
+            fn(bf(8, N), X, w, bf(4, K), bf(N, 4), 1.0)
+
+
 @pytest.mark.parametrize("N,K", [(64, 11008), (11008, 64)])
 def test_offsets_past_31_bits(N, K):
     """M K (or M N) just below 2^31 elements: dX at both ends and around 2^31

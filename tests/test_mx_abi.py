@@ -1,7 +1,10 @@
 """The MX entry points' host side (no GPU): exported symbols, sizes, and the
 refusals that come before any launch."""
 import ctypes
+import json
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -9,6 +12,7 @@ from qlora_parameter_efficient_amd import lq, mx
 
 pytestmark = pytest.mark.skipif(not os.path.exists(lq.LIB_PATH),
                                 reason="liblq.so not built (run __graft_entry__.build())")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 0x10000  # a pointer that is never dereferenced: every call below is refused
 
 
@@ -44,6 +48,35 @@ def test_workspace_size_of_refused_sizes_is_zero(op):
                        (64, 64, 64, 65), (1 << 25, 4096, 64, 8), (64, 64, 64, -1), (-1, 64, 64, 8)]:
         assert size(op, M, N, K, r) == 0, (M, N, K, r)
     assert size(op, 1 << 24, 64, 64, 8) > 0
+
+
+@pytest.mark.parametrize("op", [mx.LQ_MX_OP_FWD, mx.LQ_MX_OP_BWD, mx.LQ_MX_OP_BWD_CKPT])
+def test_workspace_size_is_zero_just_where_the_call_refuses(op):
+    """Widths off 64, below it and past 65536, rank 0 of a backward: in a process
+    of its own, since a size that no tile fits must not end it."""
+    sizes = [(M, N, K, r) for M in (1, 8, 2048, 32767, 32768) for N in (1, 32, 63, 64, 65, 96, 128, 65536, 65600)
+             for K in (1, 32, 64, 100, 128, 65536, 65600) for r in (0, 1, 11, 64, 65)]
+    code = ("import sys, json\nfrom qlora_parameter_efficient_amd import mx\n"
+            f"sizes = {sizes!r}\n"
+            f"print(json.dumps([mx.lib().lq_mx_workspace_size({op}, *s) for s in sizes]))\n")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert run.returncode == 0, (run.returncode, run.stderr)
+    w = lq.LqWeightStruct()
+    w.kind, w.dtype, w.dense = 0, lq.LQ_BF16, P
+    for (M, N, K, r), got in zip(sizes, json.loads(run.stdout)):
+        legal = N % 64 == 0 and K % 64 == 0 and max(N, K) <= 65536 and M * max(N, K) < 2**31
+        legal = legal and r <= 64 and (r > 0 or op == mx.LQ_MX_OP_FWD)
+        if legal and r == 0 and got == 0:
+            continue  # a forward that needs no workspace: the call would go through
+        assert (got > 0) == legal, (M, N, K, r, got)
+        # the same sizes without a workspace: refused either way
+        W, X = q(4, N, K), q(8, M, K)
+        w.N, w.K = N, K
+        rc = (fwd(X=None, Xq=X, M=M, W=W, r=r, ws=None) if op == mx.LQ_MX_OP_FWD else
+              bwd(Xq=X, M=M, W=W, r=r, ws=None) if op == mx.LQ_MX_OP_BWD else
+              mx.lib().lq_lora_bwd_ckpt(P, ctypes.byref(X), M, ctypes.byref(w), P, P, r, 1.0, None,
+                                        P, P, P, 0, None, 0, None))
+        assert rc == (WORKSPACE if legal else UNSUPPORTED), (M, N, K, r, rc)
 
 
 def test_row_counts_past_the_limits():
