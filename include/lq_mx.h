@@ -40,6 +40,9 @@ extern "C" {
  *   scales  rows x kp / 32 bytes, row-major: scale byte b stands for
  *           2^(b - 127), b = 255 for NaN (every element of the block is NaN)
  * Element value = value of its code times its block's scale.
+ * Consecutive rows of a tensor are a tensor: both pointers at their first row.
+ * The layer's calls take codes at multiples of 16 bytes and scales at even
+ * addresses, which every such row has where cols % 64 == 0.
  */
 typedef struct lq_mx_tensor {
   int32_t format;            /* LQ_MX_FP4 / LQ_MX_FP8                            */
@@ -65,7 +68,7 @@ size_t lq_mx_scales_bytes(int64_t rows, int64_t cols);
  * a block; the stored format is the same.)  A block that holds an infinity or
  * a NaN gets b = 255 and zero codes.  Results are bit-exact functions of the
  * input.  rows, cols >= 1; at most 2^35 elements, padding included; X aligned
- * to its element, codes to 16 bytes.
+ * to its element, codes to 16 bytes (scales: any address here).
  */
 int lq_mx_quantize(const void* X, lq_dtype xdt, int64_t rows, int64_t cols, int32_t format,
                    uint8_t* codes, uint8_t* scales, hipStream_t stream);
@@ -93,8 +96,9 @@ int lq_mx_dequantize(const lq_mx_tensor* q, void* out, lq_dtype odt, hipStream_t
  * 14 bits below the largest.  T is formed from the exact element values in
  * float32 and rounded to bf16 (after the multiply by s) for its product with B.
  * Requires K % 64 == 0, N % 64 == 0, N, K <= 65536, M K and M N < 2^31,
- * 0 <= r <= 64, every pointer but W0's and Xq's scales 16-byte aligned
- * (T_out: 4).  M = 0 is a no-op.
+ * 0 <= r <= 64, every pointer 16-byte aligned but T_out (4) and the scales of
+ * W0 and Xq (2; on multiples of 16, K % 512 == 0, they load fastest).  M = 0 is
+ * a no-op.
  */
 #define LQ_MX_ROWS_BF16 64
 int lq_mx_lora_fwd(const void* X, const lq_mx_tensor* Xq, int64_t M, const lq_mx_tensor* W0,

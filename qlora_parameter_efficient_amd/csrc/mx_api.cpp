@@ -24,9 +24,11 @@ int mx_check_tensor(const lq_mx_tensor* q, const char* name, int32_t formats, in
           "%s is %lld x %lld, expected %lld x %lld", name, (long long)q->rows,
           (long long)q->cols, (long long)rows, (long long)cols);
   REQUIRE(q->codes && q->scales, LQ_ERR_INVALID_ARG, "%s has a NULL buffer", name);
-  int rc = mx_check_aligned(q->codes, name);
-  if (!rc) rc = mx_check_aligned(q->scales, name);
-  return rc;
+  // rows of whole 64-column groups start at even addresses, also in a tensor that
+  // begins at a row of another
+  REQUIRE((uintptr_t)q->scales % 2 == 0, LQ_ERR_INVALID_ARG, "%s has scales at an odd address",
+          name);
+  return mx_check_aligned(q->codes, name);
 }
 
 }  // namespace lq

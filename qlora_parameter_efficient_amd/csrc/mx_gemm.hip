@@ -123,7 +123,8 @@ __device__ __forceinline__ i32x8 join(const u32x4& a, const u32x4& b) {
 // TAIL: K is not a multiple of the step; the last step's missing blocks (an
 // even number) are read from the row's first blocks of the step and zeroed on
 // the weight side, with scale 1 (byte 127) on both, and the scales, whose rows
-// may then start at any even address, go through registers.
+// may then start at any even address, go through registers.  It also takes whole
+// steps whose scales start off a word (rows cut from a larger tensor).
 // SPLIT: several workgroups per tile, float32 partial sums out.
 template <int FX, int IM, int JM, int WI, bool TAIL, bool WIDE, bool SPLIT>
 __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
@@ -530,9 +531,10 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
 template <int FX, int IM, int JM, int WI, bool SPLIT>
 void launch(const MxgParams& p, hipStream_t st) {
   const dim3 grid((unsigned)(p.ti * p.tj), (unsigned)p.splits), block(128 * WI);
-  if (p.K % MxgShape<FX, IM, JM, WI, false>::BK)
+  const uintptr_t at = (uintptr_t)p.Xs | (uintptr_t)p.Ws;  // the scale loads' alignment
+  if (p.K % MxgShape<FX, IM, JM, WI, false>::BK || at % 4)
     hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, WI, true, false, SPLIT>), grid, block, 0, st, p);
-  else if (p.K % 512)
+  else if (p.K % 512 || at % 16)
     hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, WI, false, false, SPLIT>), grid, block, 0, st, p);
   else
     hipLaunchKernelGGL((mxg_kernel<FX, IM, JM, WI, false, true, SPLIT>), grid, block, 0, st, p);

@@ -10,8 +10,8 @@
 // workgroup); the products are a few percent of the matrix units' time.  Two
 // kernels:
 //
-// mx_shrink_tile_kernel (U, and T where K % 128 == 0: a row's scales are then
-// read as 4-byte words).  A workgroup of eight waves owns 16 H rows and walks
+// mx_shrink_tile_kernel (U, and T where K % 128 == 0 and the scales lie on
+// words: they are read as 4-byte words).  A workgroup of eight waves owns 16 H rows and walks
 // the reduction in steps of 256 columns.  The step's Z rows (and scales) and G
 // rows go straight from global memory into LDS in whole lines, NST - 1 steps
 // ahead; wave w multiplies columns 32 w .. of the step, one
@@ -23,7 +23,7 @@
 // (2.8 TB/s), T of a 4-bit X of K = 4096 15.9.  With few rows a workgroup's steps
 // bound it, 0.28 us each (M = 1001, K = 11008: 12.7 us).
 //
-// mx_shrink_kernel (other K).  A workgroup owns 16 H rows and deals the
+// mx_shrink_kernel (the rest).  A workgroup owns 16 H rows and deals the
 // 128-column steps of the reduction to its waves; lane (q, l16) of a wave takes
 // one block of 32 columns of row l16 of each 16-row group with its scale and
 // the same columns of row l16 of each 16-rank group of G, the 32 columns of a
@@ -335,7 +335,7 @@ void launch_rows(const void* Z, const uint8_t* Zs, int64_t M, int64_t K, const u
   const bool wide = M > 4096;
   const dim3 grid((unsigned)cdiv(M, wide ? 32 : 16));
   constexpr bool U = FZ == 16;
-  if (U || K % 128 == 0) {  // a row's scales are read as 4-byte words
+  if (U || (K % 128 == 0 && (uintptr_t)Zs % 4 == 0)) {  // scales are read as 4-byte words
     auto tile = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, grid, dim3(512), 0, st, z, Zs, M, K, G, r, out);
     };

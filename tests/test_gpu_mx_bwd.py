@@ -257,6 +257,28 @@ def test_binding_refuses_wrong_operands():
                 fn(**kw)
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("K", [64, 128, 192, 512])
+def test_rows_of_a_larger_tensor(K, fmt):
+    """The backward of a micro-batch whose checkpoint and base are rows of larger
+    tensors, T recomputed."""
+    M, N, r = 45, 128, 8
+    X, W, A, B, dY, s = make(M + 5, N + 64, K, r, fmt)
+    x, w = values(X), values(W)
+    for m0, n0 in ((1, 1), (5, 64)):
+        announce(f"mx bwd rows {m0} / {n0} {fmt} K={K}")
+        cut = lambda q, a, n: mx.MxTensor(q.codes[a:a + n], q.scales[a:a + n], n, K, q.format)  # noqa: E731
+        b, d = B[n0:n0 + N].contiguous(), dY[m0:m0 + M, :N].contiguous()
+        got = mx.lq_mx_lora_bwd(d, cut(X, m0, M), cut(W, n0, N), A, b, s)
+        torch.cuda.synchronize()
+        xs, ws = x[m0:m0 + M], w[n0:n0 + N]
+        Tr = xs @ A.double().t()
+        refs = ref_backward(d, xs, Tr, ws, A, b, s)
+        _, _, _, bT = ref_forward(xs, ws, A, b, s, False)
+        refs = refs[:2] + ((refs[2][0], refs[2][1] + abs(s) * (d.double().abs().t() @ bT)),)
+        compare(got, refs)
+
+
 @pytest.mark.parametrize("N,K", [(32, 64), (63, 128), (96, 100)])
 def test_layers_off_the_shape_rules_raise(N, K):
     """Also where no tile fits the layer: an error of the call, from both backwards."""

@@ -120,6 +120,52 @@ def test_non_finite_blocks_under_wide_scale_loads(M, N, K, fmt):
     assert np.array_equal(nan, want)
 
 
+def moved(q, at):
+    """q with its scales ``at`` bytes past a 16-byte boundary."""
+    flat = torch.full((q.scales.numel() + 32,), 0x5A, dtype=torch.uint8, device=DEV)
+    assert flat.data_ptr() % 16 == 0
+    s = flat[at:at + q.scales.numel()].view(q.scales.shape)
+    s.copy_(q.scales)
+    return mx.MxTensor(q.codes, s, q.rows, q.cols, q.format)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,N,K,r,ax,aw", [
+    (70, 128, 512, 8, 2, 0), (70, 128, 512, 8, 0, 4), (130, 192, 1024, 16, 8, 2),
+    (2000, 3200, 512, 16, 4, 8), (4000, 4096, 256, 5, 2, 6), (100, 512, 4608, 8, 14, 0),
+    (100, 256, 4160, 24, 2, 10), (33, 64, 128, 33, 6, 0), (4100, 128, 384, 64, 2, 4)])
+def test_scales_at_even_addresses(M, N, K, r, ax, aw, fmt):
+    """Scales of X and W off 16 bytes, words or neither; the values beside them
+    are not read into the result."""
+    announce(f"mx fwd scales at +{ax} / +{aw} {fmt} M={M} N={N} K={K} r={r}")
+    X, W, A, B, _, s = make(M, N, K, r, fmt)
+    x, w = values(X), values(W)
+    T = torch.empty((M, r), device=DEV)
+    Y = mx.lq_mx_lora_fwd(moved(X, ax), moved(W, aw), A, B, s, T_out=T)
+    torch.cuda.synchronize()
+    Yr, bY, Tr, bT = ref_forward(x, w, A, B, s, scaled=True)
+    assert_within(Y, Yr, bY, "Y")
+    assert_within(T, Tr, bT, "T")
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("K", [64, 128, 192, 256, 512, 832])
+def test_rows_of_a_larger_tensor(K, fmt):
+    """A micro-batch cut from a checkpoint, and a slice of the layer's outputs:
+    consecutive rows of an MX tensor, each wherever its scales begin."""
+    M, N, r = 41, 192, 8
+    X, W, A, B, _, s = make(M + 7, N + 64, K, r, fmt)
+    x, w = values(X), values(W)
+    for m0, n0 in ((1, 64), (3, 0), (7, 1), (2, 33)):
+        announce(f"mx fwd rows {m0} / {n0} {fmt} K={K}")
+        cut = lambda q, a, n: mx.MxTensor(q.codes[a:a + n], q.scales[a:a + n], n, K, q.format)  # noqa: E731
+        b = B[n0:n0 + N].contiguous()
+        Y = mx.lq_mx_lora_fwd(cut(X, m0, M), cut(W, n0, N), A, b, s)
+        torch.cuda.synchronize()
+        Yr, bY, _, _ = ref_forward(x[m0:m0 + M], w[n0:n0 + N], A, b, s, scaled=True)
+        assert_within(Y, Yr, bY, "Y")
+
+
 def test_extreme_scales():
     """Scale bytes far from 127 on both sides: products from 2^-200 up to 2^100."""
     M, N, K = 96, 128, 256

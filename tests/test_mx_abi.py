@@ -184,6 +184,19 @@ def test_backward_refusals():
     assert bwd(W=q(), M=0, dA=None, dB=None) == 0
 
 
+@pytest.mark.parametrize("at", [2, 4, 6, 8, 14])
+def test_scales_at_even_addresses_are_taken(at):
+    """Rows cut from a larger tensor: past the operands' checks, to the workspace's."""
+    W, X = q(scales=P + at), q(8, 4, 256, scales=P + at)
+    assert fwd(W=W, X=None, Xq=X, ws=None) == WORKSPACE
+    assert bwd(W=W, Xq=X, ws=None) == WORKSPACE
+    assert fwd(W=q(), X=None, Xq=q(8, 4, 256, scales=P + at + 1), ws=None) == INVALID
+    w = lq.LqWeightStruct()
+    w.kind, w.dtype, w.N, w.K, w.dense = 0, lq.LQ_BF16, 256, 256, P
+    assert mx.lib().lq_lora_bwd_ckpt(P, ctypes.byref(X), 4, ctypes.byref(w), P, P, 8, 1.0, None, P,
+                                     P, P, 0, None, 0, None) == WORKSPACE
+
+
 def test_checkpoint_backward_refusals():
     w = lq.LqWeightStruct()
     w.kind, w.dtype, w.N, w.K, w.dense = 0, lq.LQ_BF16, 256, 256, P
