@@ -113,7 +113,8 @@ int lq_mx_lora_fwd(const void* X, const lq_mx_tensor* Xq, int64_t M, const lq_mx
  * dA and dB are given together or both NULL (Xq and T_saved are then not
  * read, and Xq may be NULL); dX, dA and dB all NULL is refused.  accumulate =
  * 1 adds into dA and dB.  T_saved: T_out of the forward, or NULL (recomputed).
- *   ws  lq_mx_workspace_size(LQ_MX_OP_BWD, M, N, K, r) bytes
+ *   ws  lq_mx_workspace_size(LQ_MX_OP_BWD, M, N, K, r) bytes (without dA and dB,
+ *       LQ_MX_OP_BWD + LQ_MX_NO_GRADS)
  * The weight enters as its exact bf16 values; dA and dB are sums in float32
  * of products with float32 T and U = dY B (carried as three bf16 parts, so
  * that nothing of their 24 bits is lost), in a fixed order.  1 <= r <= 64;
@@ -131,7 +132,11 @@ int lq_mx_lora_bwd(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq_m
  * the dense bf16 or NF4 layer with Xq, the MX tensor of X, in the place of X.
  * dX does not depend on X; dA and dB (and T, where T_saved is NULL) are those
  * of the restored input.  dA and dB are summed as in lq_mx_lora_bwd.
- *   ws  lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT, M, N, K, r) bytes
+ *   ws  at least lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT_FUSED, M, N, K, r) bytes
+ *       (without dA and dB, + LQ_MX_NO_GRADS); lq_lora_bwd_ckpt_workspace bytes
+ *       let dX take its fastest path, whose results may differ in their
+ *       rounding.  LQ_MX_OP_BWD_CKPT is enough for that whatever W0 is: it holds
+ *       a bf16 copy of W0, which only some NF4 weights use.
  * Other arguments and rules as lq_lora_bwd with dt = LQ_BF16.
  */
 int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq_weight* W0,
@@ -139,11 +144,20 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
                      void* dX, float* dA, float* dB, int32_t accumulate, void* ws,
                      size_t ws_bytes, hipStream_t stream);
 
+/* Bytes with which lq_lora_bwd_ckpt takes its fastest path: of W0 only kind, N
+ * and K are read; need_dx, need_grads: whether dX, and dA and dB, are given.  0
+ * for sizes that the call refuses. */
+size_t lq_lora_bwd_ckpt_workspace(int64_t M, const lq_weight* W0, int64_t r, int32_t need_dx,
+                                  int32_t need_grads);
+
 /* Workspace of an operator (LQ_MX_OP_*), in bytes; 0 where none is needed and
- * for sizes that the operator refuses. */
+ * for sizes that the operator refuses.  LQ_MX_NO_GRADS added to a backward's op:
+ * its calls without dA and dB. */
 #define LQ_MX_OP_FWD 0
 #define LQ_MX_OP_BWD 1
 #define LQ_MX_OP_BWD_CKPT 2
+#define LQ_MX_OP_BWD_CKPT_FUSED 3
+#define LQ_MX_NO_GRADS 16
 size_t lq_mx_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r);
 
 #ifdef __cplusplus

@@ -131,6 +131,17 @@ bool ckpt_dense_dx(int64_t M, const lq_weight& w, int64_t r) {
   return r % 4 != 0 || dispatch::mx_dx_fills(M, w.N, w.K);
 }
 
+// Workspace of the dX of a checkpoint backward on the path it takes given that
+// workspace; with less it runs the path that needs none.
+size_t ckpt_dx_bytes(int64_t M, const lq_weight& w, int64_t r) {
+  if (ckpt_dense_dx(M, w, r)) return dispatch::mx_dx_ws_bytes(M, w.N, w.K);
+  if (!dispatch::big_dx_eligible(M, w.N, w.K)) return 0;
+  if (w.kind == LQ_WEIGHT_DENSE) return dispatch::big_dx_dense_bytes(M, w.K);
+  if (dispatch::small_dx_eligible(w, M, r)) return dispatch::small_dx_ws_bytes(M, w.N, w.K, r);
+  if (dispatch::inloop_dx_eligible(w, M, r) && !dispatch::big_wide_tiles(M, w.K)) return 0;
+  return dispatch::big_dx_ws_bytes(M, w.N, w.K);
+}
+
 size_t multi_big_bytes(int64_t T, int64_t N, int64_t K, int64_t rc) {
   return dispatch::big_fwd_eligible(T, N, K) ? dispatch::big_multi_ws_bytes(T, N, K, rc) : 0;
 }
@@ -609,14 +620,15 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
       (rc = mx_check_aligned(ws, "ws")) || (rc = mx_check_aligned(T_saved, "T_saved")) ||
       (W0->kind == LQ_WEIGHT_DENSE && (rc = mx_check_aligned(W0->dense, "W0"))))
     return rc;
-  const size_t need = lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT, M, N, K, r);
-  REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
-          ws_bytes, need);
-  const MxBwdWs w = mx_bwd_ws(M, N, K, r);
+  const MxBwdWs w = mx_bwd_ws(M, N, K, r, dA != nullptr);
+  REQUIRE(ws != nullptr && ws_bytes >= w.rest, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
+          ws_bytes, w.rest);
   char* base = (char*)ws;
   float* U = (float*)(base + w.u);
-  void* big_ws = dX && bwd_big_bytes(M, N, K) ? base + w.rest : nullptr;
-  const bool own_dx = dX && ckpt_dense_dx(M, *W0, r);
+  const size_t part = dX ? ckpt_dx_bytes(M, *W0, r) : 0;
+  const bool fits = ws_bytes - w.rest >= part;
+  void* big_ws = part && fits ? base + w.rest : nullptr;
+  const bool own_dx = dX && fits && ckpt_dense_dx(M, *W0, r);
   if (!dX || own_dx)
     rc = dispatch::mx_u(dY, M, N, B, r, base + w.bt, U, stream);
   else
@@ -631,6 +643,14 @@ int lq_lora_bwd_ckpt(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq
     T = Tw;
   }
   return dispatch::mx_grads(*Xq, U, dY, T, N, r, scale, accumulate, dA, dB, base + w.part, stream);
+}
+
+size_t lq_lora_bwd_ckpt_workspace(int64_t M, const lq_weight* W0, int64_t r, int32_t need_dx,
+                                  int32_t need_grads) {
+  if (W0 == nullptr) return 0;
+  const int32_t op = LQ_MX_OP_BWD_CKPT_FUSED + (need_grads ? 0 : LQ_MX_NO_GRADS);
+  const size_t least = lq_mx_workspace_size(op, M, W0->N, W0->K, r);
+  return least && need_dx ? least + ckpt_dx_bytes(M, *W0, r) : least;
 }
 
 int lq_lora_fwd_dropout(const void* X, int64_t M, const lq_weight* W0, const void* A,

@@ -106,6 +106,7 @@ bool big_wide_tiles(int64_t M, int64_t NI);
 bool big_dx_eligible(int64_t M, int64_t N, int64_t K);
 size_t big_fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t r);
 size_t big_dx_ws_bytes(int64_t M, int64_t N, int64_t K);
+size_t big_dx_dense_bytes(int64_t M, int64_t K);  // of it, all that a dense W0 uses
 // Xa: the adapter branch's input when it differs from X (dropout), whose T is
 // then scaled by inv_keep.
 int big_fwd(const void* X, int64_t M, const lq_weight& W, const void* A, const void* B, int64_t r,

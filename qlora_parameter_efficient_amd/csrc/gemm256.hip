@@ -1721,8 +1721,9 @@ size_t big_fwd_ws_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
 
 // [g256: header, flags, split-K slots] [bf16 W0]
 size_t big_dx_ws_bytes(int64_t M, int64_t N, int64_t K) {
-  return align256(g256_ws_bytes(M, K)) + (size_t)(N * K) * 2;
+  return big_dx_dense_bytes(M, K) + (size_t)(N * K) * 2;
 }
+size_t big_dx_dense_bytes(int64_t M, int64_t K) { return align256(g256_ws_bytes(M, K)); }
 
 int big_fwd(const void* X, int64_t M, const lq_weight& W, const void* A, const void* B, int64_t r,
             float s, void* Y, float* T_out, void* ws, hipStream_t st, const void* Xa,

@@ -122,18 +122,19 @@ int bf16_dx_any(const void* dY, int64_t M, const lq_weight& W, const void* A, co
 }  // namespace dispatch
 
 // Workspace of the backward from an MX checkpoint: [U][T][B transposed]
-// [gradient partials], then the dX path's own part.
+// [gradient partials], then the dX path's own part.  Without dA and dB no T and
+// no partials.
 struct MxBwdWs {
   size_t u, t, bt, part, rest;  // byte offsets; rest: the end
 };
-inline MxBwdWs mx_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r) {
+inline MxBwdWs mx_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, bool grads) {
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   MxBwdWs w;
   w.u = 0;
   w.t = up((size_t)(M * r) * 4);
-  w.bt = w.t + up((size_t)(M * r) * 4);
+  w.bt = w.t + (grads ? up((size_t)(M * r) * 4) : 0);
   w.part = w.bt + up((size_t)(N * r) * 2);
-  w.rest = w.part + up(dispatch::mx_grad_bytes(M, N, K, r));
+  w.rest = w.part + (grads ? up(dispatch::mx_grad_bytes(M, N, K, r)) : 0);
   return w;
 }
 

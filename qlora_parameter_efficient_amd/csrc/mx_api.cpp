@@ -73,9 +73,8 @@ size_t fwd_part_bytes(int64_t M, int64_t N, int64_t K, int64_t r) {
   return g > s ? g : s;
 }
 
-// dX of a dense or NF4 base: the large-tile product's part, or that of the
-// split dX of a dense base (the weight's kind and which of them runs are not
-// known here)
+// dX of a dense or NF4 base whose kind is not known: the large-tile product's
+// part, or that of the split dX of a dense base
 size_t big_dx_bytes(int64_t M, int64_t N, int64_t K) {
   const size_t a = dispatch::big_dx_eligible(M, N, K) ? dispatch::big_dx_ws_bytes(M, N, K) : 0;
   const size_t b = dispatch::mx_dx_ws_bytes(M, N, K);
@@ -132,13 +131,18 @@ int lq_mx_dequantize(const lq_mx_tensor* q, void* out, lq_dtype odt, hipStream_t
 size_t lq_mx_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r) {
   // 0 too for the sizes that the operators refuse
   if (M <= 0 || N <= 0 || K <= 0 || broken_rule(M, N, K, r, op == LQ_MX_OP_FWD ? 0 : 1)) return 0;
-  switch (op) {
+  const bool grads = op < LQ_MX_NO_GRADS;
+  const int32_t kind = grads ? op : op - LQ_MX_NO_GRADS;
+  if (!grads && kind == LQ_MX_OP_FWD) return 0;
+  switch (kind) {
     case LQ_MX_OP_FWD:
       return up256((size_t)(M * r) * 4) + fwd_part_bytes(M, N, K, r);
     case LQ_MX_OP_BWD:
-      return mx_bwd_ws(M, N, K, r).rest + dispatch::mx_dx_ws_bytes(M, N, K);
+      return mx_bwd_ws(M, N, K, r, grads).rest + dispatch::mx_dx_ws_bytes(M, N, K);
     case LQ_MX_OP_BWD_CKPT:
-      return mx_bwd_ws(M, N, K, r).rest + big_dx_bytes(M, N, K);
+      return mx_bwd_ws(M, N, K, r, grads).rest + big_dx_bytes(M, N, K);
+    case LQ_MX_OP_BWD_CKPT_FUSED:
+      return mx_bwd_ws(M, N, K, r, grads).rest;
     default:
       return 0;
   }
@@ -197,10 +201,10 @@ int lq_mx_lora_bwd(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq_m
       (rc = mx_check_aligned(A, "A")) || (rc = mx_check_aligned(B, "B")) ||
       (rc = mx_check_aligned(ws, "ws")) || (rc = mx_check_aligned(T_saved, "T_saved")))
     return rc;
-  const size_t need = lq_mx_workspace_size(LQ_MX_OP_BWD, M, N, K, r);
+  const MxBwdWs w = mx_bwd_ws(M, N, K, r, dA != nullptr);
+  const size_t need = w.rest + (dX ? dispatch::mx_dx_ws_bytes(M, N, K) : 0);
   REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
           ws_bytes, need);
-  const MxBwdWs w = mx_bwd_ws(M, N, K, r);
   char* base = (char*)ws;
   float* U = (float*)(base + w.u);
   if ((rc = dispatch::mx_u(dY, M, N, B, r, base + w.bt, U, stream))) return rc;

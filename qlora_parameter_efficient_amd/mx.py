@@ -22,7 +22,8 @@ HEADER = os.path.join(os.path.dirname(lq.HEADER), "lq_mx.h")
 LQ_MX_BLOCK = 32
 LQ_MX_FP4, LQ_MX_FP8 = 4, 8
 LQ_MX_ROWS_BF16 = 64
-LQ_MX_OP_FWD, LQ_MX_OP_BWD, LQ_MX_OP_BWD_CKPT = 0, 1, 2
+LQ_MX_OP_FWD, LQ_MX_OP_BWD, LQ_MX_OP_BWD_CKPT, LQ_MX_OP_BWD_CKPT_FUSED = 0, 1, 2, 3
+LQ_MX_NO_GRADS = 16
 FORMATS = {"fp4": LQ_MX_FP4, "fp8": LQ_MX_FP8}
 
 
@@ -46,6 +47,7 @@ _SIGS = {
                                       _vp, _i32, _vp, _sz, _vp]),
     "lq_lora_bwd_ckpt": (ctypes.c_int, [_vp, _QP, _i64, lq._WP, _vp, _vp, _i64, _f32, _vp, _vp,
                                         _vp, _vp, _i32, _vp, _sz, _vp]),
+    "lq_lora_bwd_ckpt_workspace": (_sz, [_i64, lq._WP, _i64, _i32, _i32]),
     "lq_mx_workspace_size": (_sz, [_i32, _i64, _i64, _i64, _i64]),
 }
 
@@ -111,6 +113,15 @@ def lq_mx_workspace_size(op, M, N, K, r):
     return int(lib().lq_mx_workspace_size(op, M, N, K, r))
 
 
+@functools.lru_cache(maxsize=1024)
+def lq_lora_bwd_ckpt_workspace(M, kind, N, K, r, need_dx=True, need_grads=True):
+    """kind: lq.LQ_WEIGHT_DENSE or lq.LQ_WEIGHT_NF4."""
+    w = LqWeightStruct()
+    w.kind, w.dtype, w.N, w.K = kind, lq.LQ_BF16, N, K
+    return int(lib().lq_lora_bwd_ckpt_workspace(M, ctypes.byref(w), r, int(need_dx),
+                                                int(need_grads)))
+
+
 def mx_struct(q: MxTensor, dev: int):
     """C descriptor of q after checking its buffers (dev: the GPU's index)."""
     fmt, rows, cols = FORMATS[q.format], q.rows, q.cols
@@ -124,10 +135,11 @@ def mx_struct(q: MxTensor, dev: int):
     return LqMxStruct(fmt, 0, rows, cols, codes.data_ptr(), scales.data_ptr())
 
 
-def _workspace(ws, op, M, N, K, r, like, dev):
-    """(tensor that keeps it alive, pointer, bytes); ``ws`` is the caller's, or None."""
+def _workspace(ws, size, args, like, dev):
+    """(tensor that keeps it alive, pointer, bytes); ``ws`` is the caller's, or
+    None for one of size(*args) bytes."""
     if ws is None:
-        need = lq_mx_workspace_size(op, M, N, K, r)
+        need = size(*args)
         if need == 0:
             return None, None, 0
         ws = like.new_empty(need, dtype=_U8)
@@ -208,14 +220,15 @@ def lq_mx_lora_fwd(X, W0: MxTensor, A=None, B=None, scale=0.0, T_out=None, ws=No
         yp = Y.data_ptr()
     else:
         yp = _is(Y, _BF16, (M, N), dev, "Y")
-    ws, wp, wn = _workspace(ws, LQ_MX_OP_FWD, M, N, K, r, like, dev)
+    ws, wp, wn = _workspace(ws, lq_mx_workspace_size, (LQ_MX_OP_FWD, M, N, K, r), like, dev)
     _check(lib().lq_mx_lora_fwd(xp, xq, M, ctypes.byref(w), ap, bp, r, scale, yp, tp, wp, wn,
                                 _raw_stream(dev)))
     return Y
 
 
-def _backward(fn, op, w, N, K, dev, dY, Xq, A, B, scale, T_saved, need_dx, need_grads, dX, dA, dB,
+def _backward(fn, kind, w, N, K, dev, dY, Xq, A, B, scale, T_saved, need_dx, need_grads, dX, dA, dB,
               accumulate, ws):
+    """kind: None on an MXFP4 base, else that of the base."""
     M = dY.shape[0]
     yp = _is(dY, _BF16, (M, N), dev, "dY")
     r, ap, bp = _adapter(A, B, N, K, dev)
@@ -238,7 +251,12 @@ def _backward(fn, op, w, N, K, dev, dY, Xq, A, B, scale, T_saved, need_dx, need_
     xp = None if dX is None else _is(dX, _BF16, (M, K), dev, "dX")
     gap = None if dA is None else _is(dA, _F32, (r, K), dev, "dA")
     gbp = None if dB is None else _is(dB, _F32, (N, r), dev, "dB")
-    ws, wp, wn = _workspace(ws, op, M, N, K, r, dY, dev)
+    if kind is None:
+        size, args = lq_mx_workspace_size, (LQ_MX_OP_BWD + (0 if need_grads else LQ_MX_NO_GRADS),
+                                            M, N, K, r)
+    else:
+        size, args = lq_lora_bwd_ckpt_workspace, (M, kind, N, K, r, dX is not None, need_grads)
+    ws, wp, wn = _workspace(ws, size, args, dY, dev)
     _check(fn(yp, xq, M, ctypes.byref(w), ap, bp, r, scale, tp, xp, gap, gbp, int(accumulate), wp,
               wn, _raw_stream(dev)))
     return dX, dA, dB
@@ -251,7 +269,7 @@ def lq_mx_lora_bwd(dY, Xq, W0: MxTensor, A, B, scale, T_saved=None, need_dx=True
     if dev != _current():
         return _elsewhere(dev, lq_mx_lora_bwd, dY, Xq, W0, A, B, scale, T_saved, need_dx,
                           need_grads, dX, dA, dB, accumulate, ws)
-    return _backward(lib().lq_mx_lora_bwd, LQ_MX_OP_BWD, mx_struct(W0, dev), W0.rows, W0.cols, dev,
+    return _backward(lib().lq_mx_lora_bwd, None, mx_struct(W0, dev), W0.rows, W0.cols, dev,
                      dY, Xq, A, B, scale, T_saved, need_dx, need_grads, dX, dA, dB, accumulate, ws)
 
 
@@ -268,5 +286,5 @@ def lq_lora_bwd_ckpt(dY, Xq, W0, A, B, scale, T_saved=None, need_dx=True, need_g
         _want(t is None or t.get_device() == dev, "W0: tensors must be on one GPU")
     _want(nf4 or W0.dtype is _BF16, "a dense W0 is bf16")
     w = lq.weight_struct(W0, lq.LQ_BF16)
-    return _backward(lib().lq_lora_bwd_ckpt, LQ_MX_OP_BWD_CKPT, w, w.N, w.K, dev, dY, Xq, A, B,
+    return _backward(lib().lq_lora_bwd_ckpt, w.kind, w, w.N, w.K, dev, dY, Xq, A, B,
                      scale, T_saved, need_dx, need_grads, dX, dA, dB, accumulate, ws)

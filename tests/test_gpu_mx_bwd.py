@@ -257,6 +257,56 @@ def test_binding_refuses_wrong_operands():
                 fn(**kw)
 
 
+@pytest.mark.parametrize("base", ["mxfp4", "dense", "nf4"])
+@pytest.mark.parametrize("M,N,K,r", [(40, 512, 512, 8), (64, 4096, 4096, 16), (130, 192, 1088, 11), (777, 2048, 1024, 8),
+                                     (2048, 1024, 4096, 16), (4100, 512, 4096, 64), (300, 1024, 512, 64)])
+def test_exact_workspaces(M, N, K, r, base):
+    """The backwards in workspaces of just the bytes asked for: the bytes behind
+    stay, and with what the fastest path uses the result is that of the size for
+    any weight, bit for bit; the least size is within the bounds too."""
+    announce(f"bwd workspaces {base} M={M} N={N} K={K} r={r}")
+    X, W, A, B, dY, s = make(M, N, K, r, "fp8")
+    x, w, fn = values(X), W, mx.lq_mx_lora_bwd
+    if base == "mxfp4":
+        wd = values(W)
+    else:
+        fn = mx.lq_lora_bwd_ckpt
+        w = wd = (torch.randn((N, K), generator=torch.Generator().manual_seed(9)) * 0.02).to(torch.bfloat16).to(DEV)
+        if base == "nf4":
+            w = lq.lq_nf4_quantize(wd)
+            wd = lq.lq_nf4_dequantize(w).view(N, K)
+    T = (x @ A.double().t()).float()
+    refs = ref_backward(dY, x, T.double(), wd.double(), A, B, s)
+
+    def run(n, **kw):
+        ws = torch.full((n + 4096,), 0x77, dtype=torch.uint8, device=DEV)
+        out = fn(dY, X if kw.get("need_grads", True) else None, w, A, B, s, T_saved=T, ws=ws[:n], **kw)
+        torch.cuda.synchronize()
+        assert (ws[n:] == 0x77).all()
+        return out
+
+    size, no = mx.lq_mx_workspace_size, mx.LQ_MX_NO_GRADS
+    if base == "mxfp4":
+        full, least, dx = (size(mx.LQ_MX_OP_BWD + f, M, N, K, r) for f in (0, 0, no))
+        default, grads = full, full
+    else:
+        default = size(mx.LQ_MX_OP_BWD_CKPT, M, N, K, r)
+        kind = int(base == "nf4")
+        full = mx.lq_lora_bwd_ckpt_workspace(M, kind, N, K, r)
+        grads = least = size(mx.LQ_MX_OP_BWD_CKPT_FUSED, M, N, K, r)
+        dx = mx.lq_lora_bwd_ckpt_workspace(M, kind, N, K, r, True, False)
+        assert mx.lq_lora_bwd_ckpt_workspace(M, kind, N, K, r, False) == least
+        compare(run(size(mx.LQ_MX_OP_BWD_CKPT_FUSED + no, M, N, K, r), need_grads=False)[:1], refs[:1])
+    whole = run(default)
+    compare(whole, refs)
+    assert all(torch.equal(p, q) for p, q in zip(run(full), whole))
+    compare(run(least), refs)
+    compare(run(dx, need_grads=False)[:1], refs[:1])
+    compare(run(grads, need_dx=False)[1:], refs[1:])
+    with pytest.raises(mx.LqError):
+        run(least - 256)
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("K", [64, 128, 192, 512])
 def test_rows_of_a_larger_tensor(K, fmt):

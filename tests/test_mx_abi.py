@@ -79,6 +79,35 @@ def test_workspace_size_is_zero_just_where_the_call_refuses(op):
         assert rc == (WORKSPACE if legal else UNSUPPORTED), (M, N, K, r, rc)
 
 
+CKPT_SIZES = [(M, N, K, r) for M in (1, 40, 64, 300, 777, 2048, 8192) for N in (64, 1024, 4096, 4160)
+              for K in (64, 320, 4096, 11008) for r in (1, 8, 16, 64)]
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_checkpoint_backward_reserves_what_its_path_uses(kind):
+    """By the weight: between the least that the call accepts and the size for any
+    weight; a dense base never has room for a copy of itself, nor a call without dX."""
+    any_ = lambda op, *s: mx.lib().lq_mx_workspace_size(op, *s)  # noqa: E731
+    for M, N, K, r in CKPT_SIZES:
+        for grads in (True, False):
+            flag = 0 if grads else mx.LQ_MX_NO_GRADS
+            least = any_(mx.LQ_MX_OP_BWD_CKPT_FUSED + flag, M, N, K, r)
+            most = any_(mx.LQ_MX_OP_BWD_CKPT + flag, M, N, K, r)
+            full = mx.lq_lora_bwd_ckpt_workspace(M, kind, N, K, r, True, grads)
+            assert 0 < least <= full <= most
+            assert mx.lq_lora_bwd_ckpt_workspace(M, kind, N, K, r, False, grads) == least
+            if not grads:  # U and B's transpose
+                assert least <= 4 * M * r + 2 * N * r + 512
+            # split-K slots or split sums of at most 512 tiles of 64 x 256, and flags
+            if kind == 0:
+                assert full - least <= 512 * 64 * 256 * 4 + 16 * (M // 64 + 1) * (K // 64 + 1) + 1024
+    w = mx.lq_lora_bwd_ckpt_workspace
+    assert w(777, 0, 4096, 4096, 8) < 16 << 20 and w(2048, 1, 4096, 4096, 16) < 16 << 20
+    assert w(8192, 1, 4096, 11008, 64) > 2 * 4096 * 11008  # 256 x 256 tiles: they use the copy
+    assert w(8, 0, 96, 64, 4) == 0 and w(8, 1, 64, 64, 0) == 0 and w(1 << 40, 0, 64, 64, 4) == 0
+    assert any_(mx.LQ_MX_OP_FWD + mx.LQ_MX_NO_GRADS, 64, 64, 64, 4) == 0
+
+
 def test_row_counts_past_the_limits():
     W, X = q(4, 64, 64), q(8, 1 << 40, 64)
     assert fwd(X=None, Xq=X, M=1 << 40, W=W) == UNSUPPORTED
