@@ -35,7 +35,7 @@ __device__ __forceinline__ void mx_dma16(const char* base, uint32_t off, uint32_
       "1:"
       :
       : "v"(off), "s"(base), "s"(lds), "s"(go)
-      : "memory", "scc");
+      : "memory", "scc", "m0");
 }
 
 // The same, 4 bytes per lane to LDS at lds + 4 lane.
@@ -48,7 +48,7 @@ __device__ __forceinline__ void mx_dma4(const void* base, uint32_t off, uint32_t
       "1:"
       :
       : "v"(off), "s"(base), "s"(lds), "s"(go)
-      : "memory", "scc");
+      : "memory", "scc", "m0");
 }
 
 // Wait for this wave's loads: all but the newest N if ``some`` (uniform) is
