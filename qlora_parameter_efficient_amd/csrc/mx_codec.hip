@@ -212,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t pieces,
     int64_t cols, int64_t per_row, void* __restrict__ out) {
   constexpr int E = Piece<BF16>::E, PN = Piece<BF16>::N, CB = E * FMT / 8;
-  const int64_t u0 = (int64_t)blockIdx.x * (kThreads * PN) + threadIdx.x;
+  const int64_t u0 = (blockIdx.x + (int64_t)blockIdx.y * gridDim.x) * (kThreads * PN) + threadIdx.x;
   u32x2 w[PN];
   uint32_t b[PN];
 #pragma unroll
@@ -284,7 +284,11 @@ template <bool BF16, int FMT>
 void launch_d(const lq_mx_tensor& q, void* out, hipStream_t st) {
   using P = Piece<BF16>;
   const int64_t per_row = cdiv(q.cols, kMxB) * (kMxB / P::E), pieces = q.rows * per_row;
-  const dim3 grid((unsigned)cdiv(pieces, kThreads * P::N)), block(kThreads);
+  // 2^35 elements to float32 take 2^32 threads, one more than a launch's first
+  // dimension may hold
+  const int64_t blocks = cdiv(pieces, kThreads * P::N), wide = (int64_t)1 << 22;
+  const dim3 grid((unsigned)(blocks < wide ? blocks : wide), (unsigned)cdiv(blocks, wide));
+  const dim3 block(kThreads);
   if (q.cols % kMxB == 0)
     hipLaunchKernelGGL((mx_dequantize_kernel<BF16, FMT, true>), grid, block, 0, st, q.codes,
                        q.scales, pieces, q.cols, per_row, out);

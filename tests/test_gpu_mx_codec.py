@@ -88,6 +88,35 @@ def test_every_code_at_every_scale_byte(fmt):
                            torch.nan_to_num(want.float().to(d).float(), nan=7.5, posinf=8.5, neginf=9.5))
 
 
+def test_most_elements():
+    """2^35 elements, the codec's limit (128 GiB of float32): every slice of the
+    rows equals the same call on the slice alone."""
+    free, _ = torch.cuda.mem_get_info()
+    free += torch.cuda.memory_reserved() - torch.cuda.memory_allocated()
+    if free < 160 << 30:
+        pytest.skip("needs 160 GiB of free device memory")
+    torch.cuda.empty_cache()
+    rows, cols, n = 1 << 20, 1 << 15, 1 << 16
+    announce("mx codec 2^35 elements")
+    q = mx.MxTensor(torch.empty((rows, cols // 2), dtype=torch.uint8, device=DEV).random_(),
+                    torch.empty((rows, cols // 32), dtype=torch.uint8, device=DEV).random_(100, 150),
+                    rows, cols, "fp4")
+    cut = lambda t, a: mx.MxTensor(t.codes[a:a + n], t.scales[a:a + n], n, cols, "fp4")  # noqa: E731
+    for dt in (torch.float32, torch.bfloat16):
+        out = mx.lq_mx_dequantize(q, dt)
+        for a in range(0, rows, n):
+            assert torch.equal(out[a:a + n], mx.lq_mx_dequantize(cut(q, a), dt)), a
+        if dt is torch.float32:
+            del out
+            torch.cuda.empty_cache()
+    z = mx.lq_mx_quantize(out, "fp4")
+    for a in range(0, rows, n):
+        part, whole = mx.lq_mx_quantize(out[a:a + n], "fp4"), cut(z, a)
+        assert torch.equal(part.codes, whole.codes) and torch.equal(part.scales, whole.scales), a
+    del out, z, q
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("fmt", omx.FORMATS)
 @pytest.mark.parametrize("src", list(SRC))
 def test_misaligned_source_and_bytes_past_the_end(fmt, src):
