@@ -53,7 +53,8 @@ typedef struct lq_mx_tensor {
   const uint8_t* scales;
 } lq_mx_tensor;
 
-/* Bytes of a tensor's two buffers (0 for a bad format or a negative size). */
+/* Bytes of a tensor's two buffers (0 for a bad format, a negative size or more
+ * elements than lq_mx_quantize takes). */
 size_t lq_mx_codes_bytes(int32_t format, int64_t rows, int64_t cols);
 size_t lq_mx_scales_bytes(int64_t rows, int64_t cols);
 

@@ -38,6 +38,11 @@ namespace {
 constexpr int64_t kMaxRank = 64;
 constexpr int64_t kMaxElems = (int64_t)1 << 35;
 
+// No more elements than the codec takes, padding included (sizes not negative)
+bool codec_fits(int64_t rows, int64_t cols) {
+  return cols == 0 || (cols <= kMaxElems && rows <= kMaxElems / (cdiv(cols, kMxB) * kMxB));
+}
+
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // The first of the layer's shape rules that the sizes break, or NULL: one place
@@ -87,11 +92,11 @@ extern "C" {
 
 size_t lq_mx_codes_bytes(int32_t format, int64_t rows, int64_t cols) {
   if ((format != LQ_MX_FP4 && format != LQ_MX_FP8) || rows < 0 || cols < 0) return 0;
-  return (size_t)(rows * mx_pitch(format, cols));
+  return !codec_fits(rows, cols) ? 0 : (size_t)(rows * mx_pitch(format, cols));
 }
 
 size_t lq_mx_scales_bytes(int64_t rows, int64_t cols) {
-  return rows < 0 || cols < 0 ? 0 : (size_t)(rows * mx_spitch(cols));
+  return rows < 0 || cols < 0 || !codec_fits(rows, cols) ? 0 : (size_t)(rows * mx_spitch(cols));
 }
 
 int lq_mx_quantize(const void* X, lq_dtype xdt, int64_t rows, int64_t cols, int32_t format,
@@ -102,9 +107,8 @@ int lq_mx_quantize(const void* X, lq_dtype xdt, int64_t rows, int64_t cols, int3
           "unknown MX format %d", (int)format);
   REQUIRE(rows >= 1 && cols >= 1, LQ_ERR_INVALID_ARG, "%lld x %lld elements", (long long)rows,
           (long long)cols);
-  REQUIRE(cols <= kMaxElems - 31 && rows <= kMaxElems / (cdiv(cols, kMxB) * kMxB),
-          LQ_ERR_UNSUPPORTED, "%lld x %lld elements: more than 2^35", (long long)rows,
-          (long long)cols);
+  REQUIRE(codec_fits(rows, cols), LQ_ERR_UNSUPPORTED, "%lld x %lld elements: more than 2^35",
+          (long long)rows, (long long)cols);
   REQUIRE((uintptr_t)X % (xdt == LQ_F32 ? 4 : 2) == 0, LQ_ERR_INVALID_ARG, "X is misaligned");
   const int rc = mx_check_aligned(codes, "codes");
   if (rc) return rc;
@@ -118,9 +122,8 @@ int lq_mx_dequantize(const lq_mx_tensor* q, void* out, lq_dtype odt, hipStream_t
           "unknown MX format %d", (int)q->format);
   REQUIRE(q->rows >= 1 && q->cols >= 1, LQ_ERR_INVALID_ARG, "%lld x %lld elements",
           (long long)q->rows, (long long)q->cols);
-  REQUIRE(q->cols <= kMaxElems - 31 && q->rows <= kMaxElems / (cdiv(q->cols, kMxB) * kMxB),
-          LQ_ERR_UNSUPPORTED, "%lld x %lld elements: more than 2^35", (long long)q->rows,
-          (long long)q->cols);
+  REQUIRE(codec_fits(q->rows, q->cols), LQ_ERR_UNSUPPORTED, "%lld x %lld elements: more than 2^35",
+          (long long)q->rows, (long long)q->cols);
   REQUIRE(q->codes && q->scales, LQ_ERR_INVALID_ARG, "q has a NULL buffer");
   REQUIRE((uintptr_t)out % (odt == LQ_F32 ? 4 : 2) == 0, LQ_ERR_INVALID_ARG, "out is misaligned");
   const int rc = mx_check_aligned(q->codes, "codes");

@@ -39,6 +39,21 @@ def test_buffer_and_workspace_sizes():
     assert size(99, 2048, 4096, 4096, 16) == 0
 
 
+def test_buffer_sizes_past_the_codecs_limit_are_zero():
+    """2^35 elements, padding included, have buffers; more have none, also where the
+    byte count passes 64 bits."""
+    L = mx.lib()
+    for rows, cols in ((1 << 30, 32), (1 << 20, 1 << 15), (1, (1 << 35) - 31), (1, 1 << 35)):
+        n = rows * (-(-cols // 32) * 32)
+        assert L.lq_mx_codes_bytes(8, rows, cols) == n and L.lq_mx_codes_bytes(4, rows, cols) == n // 2
+        assert L.lq_mx_scales_bytes(rows, cols) == n // 32
+    for rows, cols in (((1 << 58) + 1, 32), ((1 << 30) + 1, 1), (1, (1 << 35) + 1), (1 << 40, 1 << 40),
+                       ((1 << 63) - 1, 1), (1, (1 << 63) - 1), (0, (1 << 63) - 1)):
+        assert L.lq_mx_codes_bytes(8, rows, cols) == 0, (rows, cols)
+        assert L.lq_mx_codes_bytes(4, rows, cols) == 0 and L.lq_mx_scales_bytes(rows, cols) == 0
+    assert L.lq_mx_codes_bytes(8, 0, 64) == 0 and L.lq_mx_scales_bytes(5, 0) == 0
+
+
 @pytest.mark.parametrize("op", [mx.LQ_MX_OP_FWD, mx.LQ_MX_OP_BWD, mx.LQ_MX_OP_BWD_CKPT])
 def test_workspace_size_of_refused_sizes_is_zero(op):
     """Products that pass 64 bits, tile counts that pass 32: an answer, no fault."""
