@@ -173,6 +173,8 @@ def lq_mx_quantize(X: torch.Tensor, format: str = "fp8") -> MxTensor:
     fmt = FORMATS[format]
     codes = X.new_empty((rows, kb * 4 * fmt), dtype=_U8)
     scales = X.new_empty((rows, kb), dtype=_U8)
+    if rows == 0 and cols:  # an empty batch: the layer's calls take it, the codec has no work
+        return MxTensor(codes, scales, rows, cols, format)
     _check(lib().lq_mx_quantize(X.data_ptr(), _DT[X.dtype], rows, cols, fmt, codes.data_ptr(),
                                 scales.data_ptr(), _raw_stream(dev)))
     return MxTensor(codes, scales, rows, cols, format)
@@ -185,6 +187,8 @@ def lq_mx_dequantize(q: MxTensor, dtype=torch.bfloat16) -> torch.Tensor:
     s = mx_struct(q, dev)
     _want(dtype in _DT, f"unsupported dtype {dtype}")
     out = q.codes.new_empty((q.rows, q.cols), dtype=dtype)
+    if q.rows == 0 and q.cols:
+        return out
     _check(lib().lq_mx_dequantize(ctypes.byref(s), out.data_ptr(), _DT[dtype], _raw_stream(dev)))
     return out
 

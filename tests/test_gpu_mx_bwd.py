@@ -155,6 +155,22 @@ def test_no_rows():
         assert (a == 1).all() and (b == 1).all()
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_training_step_of_no_rows(fmt):
+    """The whole recipe on an empty batch: empty outputs, zero gradients."""
+    announce(f"mx step of no rows {fmt}")
+    _, W, A, B, _, s = make(1, 128, 64, 4, fmt)
+    X = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    dY = torch.empty((0, 128), dtype=torch.bfloat16, device=DEV)
+    Y, dX, dA, dB = step(X, W, A, B, dY, s, fmt)
+    assert Y.shape == (0, 128) and dX.shape == (0, 64) and not dA.any() and not dB.any()
+    q = mx.lq_mx_quantize(X, fmt)
+    assert mx.lq_mx_dequantize(q, torch.float32).shape == (0, 64)
+    for x in (torch.empty((4, 0), device=DEV), torch.empty((0, 0), device=DEV)):
+        with pytest.raises(mx.LqError):
+            mx.lq_mx_quantize(x, fmt)
+
+
 def test_gradients_against_differences():
     """L = sum(Y G): dA and dB of the step against float64 central differences
     of the formula (L is linear in A and in B alone), and dX against its own."""
