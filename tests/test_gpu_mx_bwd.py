@@ -119,6 +119,67 @@ def test_non_finite_rows_stay_in_their_rows(M, N, K, base):
     assert torch.equal(torch.isnan(dX[:-1]), want[:-1])
 
 
+@pytest.mark.parametrize("base", ["mxfp4", "dense", "nf4"])
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 64, 4), (40, 512, 512, 8), (200, 256, 320, 12), (333, 192, 512, 40),
+                                     (777, 512, 256, 64)])
+def test_non_finite_gradients(M, N, K, r, fmt, base):
+    """An infinity or NaN in dY, X, T or B makes the sums of dA and dB that it
+    enters non-finite, and no other: in the first row, the last one before a
+    range's end, and the last."""
+    X, W, A, B, dY, s = make(M, N, K, r, fmt)
+    w, fn = W, mx.lq_mx_lora_bwd
+    if base != "mxfp4":
+        fn = mx.lq_lora_bwd_ckpt
+        w = (torch.randn((N, K), generator=torch.Generator().manual_seed(9)) * 0.02).to(torch.bfloat16).to(DEV)
+        w = w if base == "dense" else lq.lq_nf4_quantize(w)
+    T = (values(X) @ A.double().t()).float()
+    inf, nan = float("inf"), float("nan")
+
+    def run(what, need_dx=True, **kw):
+        announce(f"bwd non-finite {what} {base} {fmt} M={M} N={N} K={K} r={r} dx={need_dx}")
+        a = dict(dY=dY, Xq=X, B=B, T_saved=T)
+        a.update(kw)
+        _, dA, dB = fn(a["dY"], a["Xq"], w, A, a["B"], s, T_saved=a["T_saved"], need_dx=need_dx)
+        torch.cuda.synchronize()
+        return ~torch.isfinite(dA), ~torch.isfinite(dB)
+
+    none_a = torch.zeros((r, K), dtype=torch.bool, device=DEV)
+    none_b = torch.zeros((N, r), dtype=torch.bool, device=DEV)
+    for m in sorted({0, min(63, M - 1), M - 1}):
+        for v in (nan, inf, -inf):
+            d = dY.clone()
+            d[m, N - 2] = v
+            for dx in (True, False):
+                bad_a, bad_b = run(f"dY {v} in row {m}", dx, dY=d)
+                assert bad_a.all()  # U's row m, every rank
+                want = none_b.clone()
+                want[N - 2] = True
+                assert torch.equal(bad_b, want)
+            t = T.clone()
+            t[m, r - 1] = v
+            bad_a, bad_b = run(f"T {v} in row {m}", T_saved=t)
+            want = none_b.clone()
+            want[:, r - 1] = True
+            assert torch.equal(bad_a, none_a) and torch.equal(bad_b, want)
+        q = mx.MxTensor(X.codes, X.scales.clone(), M, K, fmt)
+        q.scales[m, K // 32 - 1] = 255
+        want = none_a.clone()
+        want[:, K - 32:] = True
+        bad_a, bad_b = run(f"X NaN in row {m}", Xq=q)
+        assert torch.equal(bad_a, want) and torch.equal(bad_b, none_b)
+        bad_a, bad_b = run(f"X NaN in row {m}, T formed", Xq=q, T_saved=None)
+        assert torch.equal(bad_a, want) and bad_b.all()
+    for v in (nan, inf):
+        b = B.clone()
+        b[N - 1, 0] = v
+        want = none_a.clone()
+        want[0] = True
+        for dx in (True, False):
+            bad_a, bad_b = run(f"B {v}", dx, B=b)
+            assert torch.equal(bad_a, want) and torch.equal(bad_b, none_b)
+
+
 def test_parts_and_accumulation():
     M, N, K, r = 200, 256, 320, 12
     X, W, A, B, dY, s = make(M, N, K, r, "fp8")

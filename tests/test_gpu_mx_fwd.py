@@ -120,6 +120,55 @@ def test_non_finite_blocks_under_wide_scale_loads(M, N, K, fmt):
     assert np.array_equal(nan, want)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 128, 3), (3, 128, 4096, 16), (3, 64, 192, 8), (13, 320, 4096, 64),
+                                     (13, 64, 11008, 33), (17, 128, 512, 16), (64, 192, 320, 5)])
+def test_non_finite_values_of_the_adapter_and_the_rows(M, N, K, r, fmt):
+    """An infinity or NaN in X makes its row of Y and T non-finite, one in W or B a
+    column of Y, one in A everything (its column of T): and nothing else."""
+    X, W, A, B, _, s = make(M, N, K, r, fmt, bf16_x=fmt == "bf16")
+    inf, nan = float("inf"), float("nan")
+
+    def run(what, X=X, W=W, A=A, B=B):
+        announce(f"mx fwd non-finite {what} {fmt} M={M} N={N} K={K} r={r}")
+        T = torch.empty((M, r), device=DEV)
+        Y = mx.lq_mx_lora_fwd(X, W, A, B, s, T_out=T)
+        torch.cuda.synchronize()
+        return ~torch.isfinite(Y), ~torch.isfinite(T)
+
+    none_y = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    none_t = torch.zeros((M, r), dtype=torch.bool, device=DEV)
+
+    def cut(t, at, v):
+        t = t.clone()
+        t[at] = v
+        return t
+
+    for m in sorted({0, M // 2, M - 1}):
+        for v in (nan, inf, -inf) if fmt == "bf16" else (nan,):
+            if fmt == "bf16":
+                x = cut(X, (m, K - 1), v)
+            else:
+                x = mx.MxTensor(X.codes, cut(X.scales, (m, K // 32 - 1), 255), M, K, fmt)
+            y, t = none_y.clone(), none_t.clone()
+            y[m], t[m] = True, True
+            got = run(f"X {v} in row {m}", X=x)
+            assert torch.equal(got[0], y) and torch.equal(got[1], t)
+    for n in (0, N - 1):
+        y = none_y.clone()
+        y[:, n] = True
+        got = run(f"W NaN in row {n}", W=mx.MxTensor(W.codes, cut(W.scales, (n, K // 64), 255), N, K, "fp4"))
+        assert torch.equal(got[0], y) and torch.equal(got[1], none_t)
+        for v in (nan, inf):
+            got = run(f"B {v} in row {n}", B=cut(B, (n, r - 1), v))
+            assert torch.equal(got[0], y) and torch.equal(got[1], none_t)
+    for v in (nan, inf):
+        t = none_t.clone()
+        t[:, r - 1] = True
+        got = run(f"A {v}", A=cut(A, (r - 1, K - 1), v))
+        assert got[0].all() and torch.equal(got[1], t)
+
+
 def moved(q, at):
     """q with its scales ``at`` bytes past a 16-byte boundary."""
     flat = torch.full((q.scales.numel() + 32,), 0x5A, dtype=torch.uint8, device=DEV)
