@@ -284,13 +284,13 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
   } while (++kt < kb);
   __syncthreads();  // the output tile overwrites the stages
 
-  // ---- expand: acc += A-operand x (s U)-operand over rank chunks of 16; U is
-  // rounded to bf16 after the multiply by s (one term of an output that is
-  // itself rounded to bf16)
+  // ---- expand: acc += A-operand x (s U)-operand over rank chunks of 16, s U in
+  // two bf16 parts
   const int r = SPLIT && blockIdx.y ? 0 : p.r;
   for (int c = 0; c < r; c += 16) {
     const int jr = c + 8 * h;
-    u32x4 ef[4], vf[JM];
+    u32x4 ef[4];
+    MxVParts vf[JM];
 #pragma unroll
     for (int ns = 0; ns < 4; ++ns) {
       int64_t k = i0 + 128 * wi + 32 * ns + l32;
@@ -306,7 +306,10 @@ __global__ __launch_bounds__(kThreads) void mxdx_kernel(MxdxParams p) {
 #pragma unroll
     for (int ns = 0; ns < 4; ++ns)
 #pragma unroll
-      for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(ef[ns], vf[ms], acc[ns][ms]);
+      for (int ms = 0; ms < JM; ++ms) {
+        acc[ns][ms] = mfma32(ef[ns], vf[ms].l, acc[ns][ms]);
+        acc[ns][ms] = mfma32(ef[ns], vf[ms].h, acc[ns][ms]);
+      }
   }
 
   if constexpr (SPLIT) {

@@ -48,9 +48,9 @@
 // 3.9 to 4.4 PFLOP/s with an 8-bit X and 7.1 to 7.5 with a 4-bit one.
 //
 // Epilogue: the expand adds (s T) B^T on the finished accumulators with bf16
-// MFMAs (T rounded to bf16 after the multiply by s: the same rounding as the
-// output's, on one term of it), then the tile goes through LDS and leaves as
-// 16-byte stores covering whole output lines.
+// MFMAs (s T in two bf16 parts, off by 2^-16, so that the adapter's term is no
+// coarser here than in the forward of few bf16 rows), then the tile goes through
+// LDS and leaves as 16-byte stores covering whole output lines.
 #include <type_traits>
 
 #include "dispatch.h"
@@ -429,7 +429,8 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
   const int r = SPLIT && blockIdx.y ? 0 : p.r;
   for (int c = 0; c < r; c += 16) {
     const int jr = c + 8 * h;
-    u32x4 ef[IM], vf[JM];
+    u32x4 ef[IM];
+    MxVParts vf[JM];
 #pragma unroll
     for (int ns = 0; ns < IM; ++ns) {
       int64_t n = i0 + wrow0 + 32 * ns;
@@ -445,7 +446,10 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
 #pragma unroll
     for (int ns = 0; ns < IM; ++ns)
 #pragma unroll
-      for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(ef[ns], vf[ms], acc[ns][ms]);
+      for (int ms = 0; ms < JM; ++ms) {
+        acc[ns][ms] = mfma32(ef[ns], vf[ms].l, acc[ns][ms]);
+        acc[ns][ms] = mfma32(ef[ns], vf[ms].h, acc[ns][ms]);
+      }
   }
 
   if constexpr (SPLIT) {  // float32 partial sums; lane: rows n = .. + 8 q + 4 h + 0..3, column m

@@ -81,9 +81,14 @@ __device__ __forceinline__ u32x4 mx_read16(uint32_t addr) {
 __device__ __forceinline__ int mx_swz128(int x) { return (x & 7) ^ ((x >> 3) & 1); }
 __device__ __forceinline__ int mx_swz64(int x) { return (x >> 2) & 3; }
 
-// s v[0..7] rounded to bf16 (nearest even): an operand of the expand; v is a
+// s v[0..7] as an operand of the expand, in two bf16 parts, h = bf16(s v) and
+// l = bf16(s v - h), together off by 2^-16 of the value (one part alone, 2^-8, is
+// as much as the rounding of the output, and more where ranks cancel); v is a
 // float32 row of length r at rank j0, ranks past r are zero
-__device__ __forceinline__ u32x4 mx_v_operand(const float* row, int j0, int r, float s) {
+struct MxVParts {
+  u32x4 h, l;
+};
+__device__ __forceinline__ MxVParts mx_v_operand(const float* row, int j0, int r, float s) {
   float e[8];
   if (j0 + 8 <= r && (reinterpret_cast<uintptr_t>(row + j0) & 15) == 0) {
     const f32x4 a = *reinterpret_cast<const f32x4*>(row + j0);
@@ -97,8 +102,17 @@ __device__ __forceinline__ u32x4 mx_v_operand(const float* row, int j0, int r, f
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = j0 + i < r ? row[j0 + i] : 0.0f;
   }
-  return u32x4{pack_bf16x2(s * e[0], s * e[1]), pack_bf16x2(s * e[2], s * e[3]),
-               pack_bf16x2(s * e[4], s * e[5]), pack_bf16x2(s * e[6], s * e[7])};
+  MxVParts o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = s * e[2 * i], b = s * e[2 * i + 1];
+    o.h[i] = pack_bf16x2(a, b);
+    const float ha = lo_bf16(o.h[i]), hb = hi_bf16(o.h[i]);
+    // (the rest of an infinity or NaN is 0)
+    o.l[i] = pack_bf16x2(fabsf(ha) < __builtin_inff() ? a - ha : 0.0f,
+                         fabsf(hb) < __builtin_inff() ? b - hb : 0.0f);
+  }
+  return o;
 }
 
 __device__ __forceinline__ u32x4 mx_pack8(const uint16_t (&v)[8]) {

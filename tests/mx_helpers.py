@@ -79,6 +79,33 @@ def ref_backward(dY, x, T, w, A, B, s):
     return (dX, bX + 1e-37), (dA, bA + 1e-37), (dB, bB + 1e-37)
 
 
+PARTS2 = 2.0**-16  # two bf16 parts of a value: 2^-8 of the 2^-8 that one part leaves
+
+
+def cancelling(r, K, N, seed):
+    """A and B whose ranks cancel in pairs: the adapter's term is some 2^-7 of its
+    parts' magnitude, so a rounding of T or U to bf16 would show in the output.
+    A's odd ranks are its even ones with one element in eight a step off, B's odd
+    ranks the negative of its even ones; the same for A in B's place."""
+    g = torch.Generator().manual_seed(seed)
+
+    def pairs(n, sign):
+        a = torch.randn((r // 2, n), generator=g).to(torch.bfloat16).float()
+        off = (torch.rand((r // 2, n), generator=g) < 0.125).float() * 2.0**-7
+        return torch.stack((a, sign * a * (1 + off if sign > 0 else 1)), 1).reshape(r, n)
+
+    A, B = pairs(K, 1.0), pairs(N, -1.0).t()
+    return A.to(torch.bfloat16).to(DEV), B.contiguous().to(torch.bfloat16).to(DEV)
+
+
+def expand_bound(Y, V, eV, E, s):
+    """Bound of the output s V E^T where nothing else enters it (V float32 off by
+    eV): its rounding, V's two parts and their product's sum."""
+    r = V.shape[1]
+    return (BF16 * Y.abs() + abs(s) * ((PARTS2 + gamma(r, parts=2)) * V.abs() + eV) @ E.abs().t()
+            + 1e-37)
+
+
 def assert_within(got, want, bound, what):
     err = (got.double() - want).abs()
     bad = ~(err <= bound)

@@ -6,7 +6,8 @@ import torch
 
 from qlora_parameter_efficient_amd import lq, mx
 from tests.gpu_helpers import DEV, announce
-from tests.mx_helpers import assert_within, gamma, make, ref_backward, ref_forward, values
+from tests.mx_helpers import (assert_within, cancelling, expand_bound, gamma, make, ref_backward,
+                              ref_forward, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -178,6 +179,37 @@ def test_non_finite_gradients(M, N, K, r, fmt, base):
         for dx in (True, False):
             bad_a, bad_b = run(f"B {v}", dx, B=b)
             assert torch.equal(bad_a, want) and torch.equal(bad_b, none_b)
+
+
+@pytest.mark.parametrize("base", ["mxfp4", "dense"])
+@pytest.mark.parametrize("M,N,K,r", [(100, 1024, 512, 6), (3, 4096, 320, 16), (600, 1024, 11008, 8),
+                                     (700, 1024, 4096, 6), (1030, 1024, 8192, 11), (4100, 1024, 4096, 61)])
+def test_adapter_term_with_cancelling_ranks(M, N, K, r, base):
+    """On a base of zeros dX is s U A alone, and its ranks cancel: U enters with
+    more than one bf16's bits in every tile variant (a dense base on shapes that
+    take the same kernel).  U's own sum is kept exact: dY is one element a row."""
+    announce(f"bwd cancelling ranks {base} M={M} N={N} K={K} r={r}")
+    even = r - r % 2
+    B, A = cancelling(even, N, K, 5)
+    B, A = B.t().contiguous(), A.t().contiguous()  # A cancels over ranks, B nearly equal in pairs
+    if r % 2:
+        A = torch.cat((A, torch.zeros((1, K), dtype=A.dtype, device=DEV)))
+        B = torch.cat((B, torch.zeros((N, 1), dtype=B.dtype, device=DEV)), 1)
+    g = torch.Generator().manual_seed(1)
+    dY = torch.zeros((M, N))
+    dY[torch.arange(M), torch.randint(0, N, (M,), generator=g)] = torch.randn(M, generator=g)
+    dY = dY.to(torch.bfloat16).to(DEV)
+    s = 1.375
+    if base == "mxfp4":
+        W = mx.lq_mx_quantize(torch.zeros(N, K, device=DEV), "fp4")
+        dX, _, _ = mx.lq_mx_lora_bwd(dY, None, W, A, B.contiguous(), s, need_grads=False)
+    else:
+        W = torch.zeros((N, K), dtype=torch.bfloat16, device=DEV)
+        dX, _, _ = mx.lq_lora_bwd_ckpt(dY, None, W, A, B.contiguous(), s, need_grads=False)
+    torch.cuda.synchronize()
+    U = dY.double() @ B.double()  # one product a row: exact in float32
+    want = s * (U @ A.double())
+    assert_within(dX, want, expand_bound(want, U, 0.0, A.double().t(), s), "dX")
 
 
 def test_parts_and_accumulation():

@@ -6,7 +6,7 @@ import torch
 
 from qlora_parameter_efficient_amd import mx
 from tests.gpu_helpers import DEV, announce
-from tests.mx_helpers import assert_within, make, ref_forward, values
+from tests.mx_helpers import assert_within, cancelling, expand_bound, gamma, make, ref_forward, values
 
 pytestmark = pytest.mark.gpu
 
@@ -167,6 +167,30 @@ def test_non_finite_values_of_the_adapter_and_the_rows(M, N, K, r, fmt):
         t[:, r - 1] = True
         got = run(f"A {v}", A=cut(A, (r - 1, K - 1), v))
         assert got[0].all() and torch.equal(got[1], t)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4", "bf16"])
+@pytest.mark.parametrize("M,N,K,r", [(3, 128, 256, 6), (40, 192, 512, 16), (100, 512, 4608, 8), (520, 11008, 128, 16),
+                                     (2048, 3200, 512, 32), (4000, 4096, 256, 64)])
+def test_adapter_term_with_cancelling_ranks(M, N, K, r, fmt):
+    """On a base of zeros Y is s T B^T alone, and its ranks cancel: T enters with
+    more than one bf16's bits in every tile variant."""
+    if fmt == "bf16" and M > mx.LQ_MX_ROWS_BF16:
+        M = 64
+    announce(f"mx fwd cancelling ranks {fmt} M={M} N={N} K={K} r={r}")
+    X, *_ = make(M, 64, K, r, fmt, bf16_x=fmt == "bf16")
+    A, B = cancelling(r, K, N, 3)
+    s = 1.5
+    W = mx.lq_mx_quantize(torch.zeros(N, K, device=DEV), "fp4")
+    T = torch.empty((M, r), device=DEV)
+    Y = mx.lq_mx_lora_fwd(X, W, A, B, s, T_out=T)
+    torch.cuda.synchronize()
+    x = X.double() if fmt == "bf16" else values(X)
+    Tr = x @ A.double().t()
+    bT = gamma(K) * (x.abs() @ A.double().abs().t()) + 1e-37
+    assert_within(T, Tr, bT, "T")
+    Yr = s * (T.double() @ B.double().t())  # of T as it was formed
+    assert_within(Y, Yr, expand_bound(Yr, T.double(), 0.0, B.double(), s), "Y")
 
 
 def moved(q, at):
