@@ -115,15 +115,16 @@ size_t bwd_big_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 // dX of a dense base from an MX checkpoint by mxdx_kernel (U apart) instead of
-// the kernels of lq_lora_bwd, dX and U in us, theirs / this:
-//   off the large-tile product (K % 256 != 0): 66 x 5056 x 320 63 / 22, 300 x 4160 x
-//     4992 56 / 42, 4000 x 4160 x 4992 (r 64) 339 / 241; but where both are launches,
-//     500 x 512 x 448 12 / 16, 8000 x 128 x 192 11 / 13
+// the kernels of lq_lora_bwd, dX and U in us in a replayed graph, theirs / this:
+//   off the large-tile product (K % 256 != 0): 66 x 5056 x 320 61 / 23, 300 x 4160 x
+//     4992 56 / 37, 4000 x 4160 x 4992 (r 64) 316 / 228; where both are little but
+//     their launches (one / up to three), 500 x 512 x 448 12.0 / 12.9, 8000 x 128 x
+//     192 11.5 / 9.7
 //   on it, where this splits the reduction or has tiles of 128 rows: 64 x 4096 x
-//     4096 44 / 26, 512 x 4096 x 4096 47 / 39, 2048 x 4096 x 4096 78 / 75; between,
-//     with 64-row tiles in one round, 777 x 4096 x 4096 50 / 60
+//     4096 44 / 25, 512 x 4096 x 4096 47 / 39, 2048 x 4096 x 4096 78 / 73; between,
+//     with 64-row tiles in one round, 777 x 4096 x 4096 50 / 61
 //   and at ranks that U reads element by element there, 1001 x 4096 x 11008 (r 11)
-//     303 / 108
+//     341 / 110
 bool ckpt_dense_dx(int64_t M, const lq_weight& w, int64_t r) {
   if (w.kind != LQ_WEIGHT_DENSE) return false;
   if (!dispatch::big_dx_eligible(M, w.N, w.K))

@@ -26,15 +26,16 @@
 // One barrier per step, before the last substep's products (see mxg_kernel):
 // after it the tiles just read are free, so the last substep converts the W
 // tile two steps ahead, and the next step's first substep issues the loads
-// behind that.  Bound by what LDS moves: per step and compute unit
-// about 96 (JM = 2) or 128 KB of operand reads and 48 or 64 KB of writes, which
-// run at less than half the read rate, against 1,024 or 2,048 cycles of products.  Measured: 2048 x 4096
-// x 4096 79 us (0.87 PFLOP/s), 8192 x 4096 x 11008 707 us (1.04), 1001 x 4096 x
-// 11008 111 us (0.81).  Timed apart at the first shape when it took 88 us: 67
-// without the W tile's writes, 76 without the loads, 58 without both.  Eight
-// waves on the tile, with half again the operand reads, take the same time
-// (8192 x 4096 x 11008 at r = 16: 677 us both), so neither the reads nor the
-// waves' latency bound it; the clock falls with the work moved.
+// behind that.  Per step and compute unit LDS moves about 96 (JM = 2) or
+// 128 KB of operand reads and 48 or 64 KB of writes, against 1,024 or 2,048 cycles
+// of products.  Measured: 2048 x 4096 x 4096 76 to 79 us (0.9 PFLOP/s), 8192 x 4096
+// x 11008 722 us (1.02), 1001 x 4096 x 11008 112 us (0.81).  Timed apart, dX and U
+// at the first two shapes: 83 and 726 us, without the W tile's writes 78 and 690,
+// without the loads 70 and 614, without both 69 and 602.  So the products with
+// their operand reads are four fifths of it; the matrix units are busy 43 and 53%
+// of the compute units' cycles, at 2.3 and 2.1 GHz (the instruction alone, on random
+// values in registers, runs at 1.8 PFLOP/s).  Eight waves on the tile, with half
+// again the operand reads, take the same time.
 //
 // A dense bf16 W (the backward from an MX checkpoint of a dense layer) takes
 // the same loop with its W tiles loaded straight into LDS.
@@ -385,12 +386,12 @@ struct Plan {
 };
 
 // The tile with the least rounds x time of a round, the wider at a tie: at
-// N = 4096 a round of 256 tiles takes 100 us at 256 x 256, 65 to 85 at
-// 256 x 128 and 55 at 256 x 64 (1001 x 4096 x 11008: 118, 137 and 145 us;
-// 2048 x 4096 x 4096: 110, 85 and 103).  Two workgroups of 256 x 64 fit a
+// N = 4096 a round of 256 tiles takes 105 us at 256 x 256, 65 to 75 at
+// 256 x 128 and 45 to 60 at 256 x 64 (dX and U, 1001 x 4096 x 11008: 114, 138 and
+// 131 us; 2048 x 4096 x 4096: 110, 79 and 89).  Two workgroups of 256 x 64 fit a
 // compute unit; where a third of those places would be filled, the reduction is
-// split (600 x 4096 x 4096, 160 tiles: 58 us whole, 47 in three; 512: 58 and
-// 39 in four; 100: 55 and 22 in eight).
+// split (600 x 4096 x 4096, 160 tiles: 63 us whole, 48 in three; 512: 62 and
+// 43 in four; 100: 61 and 28 in eight).
 Plan plan(int64_t M, int64_t N, int64_t K) {
   static const int shapes[3][2] = {{4, 20}, {2, 14}, {1, 11}};
   Plan q{};

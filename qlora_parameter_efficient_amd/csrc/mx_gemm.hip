@@ -4,8 +4,8 @@
 //                              T = X A^T (M x r float32)
 //
 // v_mfma_scale_f32_32x32x64_f8f6f4 multiplies the codes and applies both
-// operands' block scales, so nothing is dequantised.  MFMA-bound: 4-bit codes
-// on both sides run at twice the rate of an 8-bit side.
+// operands' block scales, so nothing is dequantised; 4-bit codes on both sides
+// run at twice the rate of an 8-bit side.
 //
 // Operand layout of the instruction (lane l: row l % 32, half h = l / 32; the
 // 64 reduction elements are two scale blocks 0 and 1):
@@ -29,10 +29,10 @@
 // addresses so that operand reads are conflict-free.  A scale load costs the
 // load path a line per row however few bytes it takes, half of a step's lines
 // at 4 or 8 bytes, so where K % 512 == 0 a load brings 16 bytes of each row, the
-// scales of two (FP4) or four steps (with the eight waves: 300 -> 284 us there).  Steps of 256 columns
-// with an FP4 X, so that every row piece is a whole 128-byte line (with 128
-// columns the lines are fetched twice: 4096^3 48 -> 56 us although twice the
-// stages fit), and of 128 columns with an FP8 X.  Two to four LDS stages (what
+// scales of two (FP4) or four steps (with the eight waves 5% off that shape).
+// Steps of 256 columns with an FP4 X, so that every row piece is a whole 128-byte
+// line (with 128 columns the lines are fetched twice: 4096^3 takes 17% longer
+// although twice the stages fit), and of 128 columns with an FP8 X.  Two to four LDS stages (what
 // fits), one barrier per step, placed before the step's last substep of
 // products (see the loop).
 //
@@ -41,11 +41,16 @@
 // mx_sum_splits.
 //
 // Measured: 2048 x 4096 x 4096 MXFP8 38 us (1.8 PFLOP/s), 8192 x 11008 x 4096
-// MXFP4 279 us (2.6 PFLOP/s), 1001 x 4096 x 11008 MXFP8 61 us (1.5).
-// The matrix units are busy 62 to 69% of the loop's cycles, and the shader clock
-// falls to 1.4 to 2.0 GHz under it (codes of zeros run 20% faster): power bounds
-// the rest.  The same instructions alone, on random codes in registers, run at
-// 3.9 to 4.4 PFLOP/s with an 8-bit X and 7.1 to 7.5 with a 4-bit one.
+// MXFP4 282 us (2.6 PFLOP/s), 1001 x 4096 x 11008 MXFP8 60 us (1.5).
+// No one unit is full.  Over these kernels the matrix units are busy 49, 42 and
+// 35% of the compute units' cycles, at a shader clock of 2.4 GHz (2.1 in the
+// second).  At M = N = 4096 and K = 1024, 4096, 16384 a call takes 18, 41 and 136 us
+// with an FP4 X and 24, 59 and 214 with an FP8 one: a further step costs 4.4 and
+// 2.7 PFLOP/s, and 7 to 10 us of a call lie outside the steady loop (a tile's
+// first loads, its expand and its stores leave the matrix units idle, as there
+// is one workgroup per compute unit).  The same instructions alone, on random
+// codes in registers, run at 7.0 to 7.4 PFLOP/s with a 4-bit X, 3.9 to 4.3 with an
+// 8-bit one.
 //
 // Epilogue: the expand adds (s T) B^T on the finished accumulators with bf16
 // MFMAs (s T in two bf16 parts, off by 2^-16, so that the adapter's term is no
@@ -318,7 +323,7 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
   // the barrier, covering the first reads of the next step and the first half
   // of the loads NST steps ahead (into the stage the barrier has just freed);
   // the second half goes out among the next step's first products (all of them
-  // in one substep: 8192 x 11008 x 4096 MXFP4 249 us against 239).  The body has
+  // in one substep: 4% longer at 8192 x 11008 x 4096 MXFP4).  The body has
   // no branch: one between the products and the barrier would let the compiler
   // sink products past it, so loads past the last step are skipped inside
   // mx_dma16.
@@ -501,13 +506,14 @@ __global__ __launch_bounds__(128 * WI) void mxg_kernel(MxgParams p) {
 }
 
 // Tile and split choice: the tile with the least rounds x time of a round, the
-// larger at a tie.  At K = 4096 with an 8-bit X a round of 256 tiles takes 71 us
-// at 256 x 256, 45 us at 256 x 128 and 24 us at 128 x 128 (2048 x 4096 x 4096:
-// 54, 45 and 48 us; 4096 x 4096 x 4096: 71, 88 and 95 us).  Split K fills the
-// chip but costs a second launch and the partial sums: it takes 4096 columns to
-// pay (100 x 4096 x 11008: 45 us whole, 19 in eight; 512 x 4096 x 11008: 50 and
-// 42 in two; 100 x 4096 x 4096: 19 and 15 in four; 512 x 4096 x 4096: 21 and 23
-// in two; 200 x 2048 x 2048: 11 and 12).
+// larger at a tie.  At K = 4096 a round of 256 tiles takes about 3, 2 and 1 parts
+// of 18 us at 256 x 256, 256 x 128 and 128 x 128 with an 8-bit X and of 12 with a
+// 4-bit one (2048 x 4096 x 4096, calls of the three tiles: 51, 35 and 35 us 8-bit,
+// 31, 24 and 25 4-bit; 4096 x 4096 x 4096: 59, 67 and 69 us, 39, 46 and 47).  Split
+// K fills the chip but costs a second launch and the partial sums: it takes 4096
+// columns to pay (8-bit X, 100 x 4096 x 11008: 44 us whole, 18 in eight; 512 x 4096 x
+// 11008: 48 and 37 in two; 100 x 4096 x 4096: 19 and 14 in four; 512 x 4096 x 4096:
+// 20 and 21 in two; 200 x 2048 x 2048: 11.0 and 11.4 in two).
 struct Plan {
   int rows_i, rows_j, ti, tj, splits;
 };

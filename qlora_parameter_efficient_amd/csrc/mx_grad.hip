@@ -26,9 +26,9 @@
 // 32).  Ranges of rows leave partial sums that mx_grad_reduce_kernel adds in a
 // fixed order: no atomics.
 //
-// Measured (gradients + reduction): M = 2048, N = K = 4096, r = 16 11.1 + 4.8 us
-// (25 MB: 2.3 TB/s; short ranges, the fill of the loads ahead bounds it); M =
-// 8192, N = 4096, K = 11008, r = 64 71 + 7.8 us (0.67 PFLOP/s over the three parts).
+// Measured (gradients + reduction): M = 2048, N = K = 4096, r = 16 10.7 + 4.8 us
+// (25 MB: 2.4 TB/s; short ranges, the fill of the loads ahead bounds it); M =
+// 8192, N = 4096, K = 11008, r = 64 71 + 7.6 us (0.67 PFLOP/s over the three parts).
 #include "dispatch.h"
 #include "mx.h"
 

@@ -18,10 +18,10 @@
 // v_mfma_f32_16x16x32_bf16 per 16 x 16 block of the output (a lane's 8 columns
 // of an MX row are converted as they are read).  16-byte chunks are swizzled by
 // row so that the 16 rows of a read fall on distinct banks.  M = 2048,
-// K = 4096, r = 16: T of an 8-bit X 6.1 us (1.4 TB/s, launch and the pipeline's
-// filling included), U 5.8 us (2.9 TB/s); M = 8192, r = 64: U of N = 4096 23.6 us
-// (2.8 TB/s), T of a 4-bit X of K = 4096 15.9.  With few rows a workgroup's steps
-// bound it, 0.28 us each (M = 1001, K = 11008: 12.7 us).
+// K = 4096, r = 16: T of an 8-bit X 7.0 us (1.2 TB/s, launch and the pipeline's
+// filling included), U 6.0 us (2.8 TB/s); M = 8192, r = 64: U of N = 4096 23.7 us
+// (2.8 TB/s), T of a 4-bit X of K = 4096 16.0 (512 KB of A per workgroup from L2).  With few rows a workgroup's steps
+// bound it, 0.28 us each (M = 1001, K = 11008: 13.0 us).
 //
 // mx_shrink_kernel (the rest).  A workgroup owns 16 H rows and deals the
 // 128-column steps of the reduction to its waves; lane (q, l16) of a wave takes

@@ -19,14 +19,18 @@
 //
 // T comes from a small kernel first, as partial sums over ranges of K; but for
 // a few tokens (M <= 4, r <= 16, r K <= 65536) every workgroup forms all of T
-// itself, wave j the products of rank j with A's row read in whole lines: that
-// costs the device little more than the launch it saves, and a host that
-// issues single decode calls half the time.  (With MFMA operand loads, 16 lines
-// per instruction, the same took 12 us at M = 1, N = K = 4096, r = 16.)
+// itself, wave j the products of rank j with A's row read in whole lines.  That
+// spares a launch, which is what a host that issues single calls waits for, and
+// costs the device time that grows with M and with r K.  N = K = 4096, r = 16,
+// this / two launches: calls from the host M = 1 8.7 / 10.9 us, 2 9.7 / 10.8, 4
+// 12.1 / 10.9; in a replayed graph 8.7 to 9.2 / 8.1, 10.1 / 8.2 and 12.5 / 8.3.  So
+// it pays for one or two tokens off a graph.  Past r K = 65536, K = 11008, M = 1:
+// calls 15.3 / 13.0, in a graph 16.1 / 13.6.
 //
-// Measured: M = 1, N = K = 4096, r = 16 9.4 us (8.9 MB of W: 0.95 TB/s; the launch,
-// T and the one wave of blocks bound it), M = 13, N = 11008, K = 4096, r = 64 14.4
-// us (24 MB: 1.7 TB/s) and 4.1 for T.
+// Measured: M = 1, N = K = 4096, r = 16 9.5 us (8.9 MB of W: 0.94 TB/s; without an
+// adapter 5.0), M = 13, N = 11008, K = 4096, r = 64 14.4 us (24 MB: 1.7 TB/s) and
+// 4.1 for T.  Past 16 rows W is read again for every 16: N = K = 4096, r = 16, M = 17,
+// 32, 48 and 64 take 16, 17, 24 and 30 us.
 #include "dispatch.h"
 #include "mx.h"
 
