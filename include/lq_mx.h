@@ -95,7 +95,7 @@ int lq_mx_dequantize(const lq_mx_tensor* q, void* out, lq_dtype odt, hipStream_t
  * Products are summed in float32; with an MX X they are formed by the scaled
  * matrix instructions, whose sums inside one group of 64 products keep about
  * 14 bits below the largest.  T is formed from the exact element values in
- * float32 and rounded to bf16 (after the multiply by s) for its product with B.
+ * float32 and enters its product with B in two bf16 parts, 2^-16 of its value.
  * Requires K % 64 == 0, N % 64 == 0, N, K <= 65536, M K and M N < 2^31,
  * 0 <= r <= 64, every pointer 16-byte aligned but T_out (4) and the scales of
  * W0 and Xq (2; on multiples of 16, K % 512 == 0, they load fastest).  M = 0 is
@@ -116,7 +116,8 @@ int lq_mx_lora_fwd(const void* X, const lq_mx_tensor* Xq, int64_t M, const lq_mx
  * 1 adds into dA and dB.  T_saved: T_out of the forward, or NULL (recomputed).
  *   ws  lq_mx_workspace_size(LQ_MX_OP_BWD, M, N, K, r) bytes (without dA and dB,
  *       LQ_MX_OP_BWD + LQ_MX_NO_GRADS)
- * The weight enters as its exact bf16 values; dA and dB are sums in float32
+ * The weight enters as its exact bf16 values, s U its product with A in two
+ * bf16 parts (2^-16 of its value); dA and dB are sums in float32
  * of products with float32 T and U = dY B (carried as three bf16 parts, so
  * that nothing of their 24 bits is lost), in a fixed order.  1 <= r <= 64;
  * other rules as lq_mx_lora_fwd (T_saved: 16).  A non-finite element of dY or

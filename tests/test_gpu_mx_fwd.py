@@ -263,6 +263,21 @@ def test_widest_layers():
     check(130, 65536, 192, 7, "fp4")
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp4", "bf16"])
+@pytest.mark.parametrize("M,N,K,r", [(2, 128, 256, 16), (40, 192, 512, 8), (64, 128, 192, 5), (33, 64, 128, 64)])
+def test_t_out_at_any_word(M, N, K, r, fmt):
+    """T_out 4 bytes past a 16-byte boundary: the same T and Y, nothing beside it."""
+    announce(f"mx fwd T_out at +4 {fmt} M={M} N={N} K={K} r={r}")
+    X, W, A, B, _, s = make(M, N, K, r, fmt, bf16_x=fmt == "bf16")
+    T = torch.empty((M, r), device=DEV)
+    Y = mx.lq_mx_lora_fwd(X, W, A, B, s, T_out=T)
+    flat = torch.full((M * r + 8,), 3.0, device=DEV)
+    Z = mx.lq_mx_lora_fwd(X, W, A, B, s, T_out=flat[1:1 + M * r].view(M, r))
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Z) and torch.equal(flat[1:1 + M * r].view(M, r), T)
+    assert flat[0] == 3.0 and (flat[1 + M * r:] == 3.0).all()
+
+
 def test_no_rows():
     _, W, A, B, _, s = make(1, 64, 64, 4, "fp8")
     X = mx.MxTensor(torch.empty((0, 64), dtype=torch.uint8, device=DEV),
