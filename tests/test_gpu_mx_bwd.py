@@ -6,8 +6,8 @@ import torch
 
 from qlora_parameter_efficient_amd import lq, mx
 from tests.gpu_helpers import DEV, announce
-from tests.mx_helpers import (assert_within, cancelling, expand_bound, gamma, make, ref_backward,
-                              ref_forward, values)
+from tests.mx_helpers import assert_within, gamma, make, ref_backward, ref_forward, values
+from tests.mx_helpers import cancelling, expand_bound
 
 pytestmark = pytest.mark.gpu
 
