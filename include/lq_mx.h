@@ -132,8 +132,9 @@ int lq_mx_lora_bwd(const void* dY, const lq_mx_tensor* Xq, int64_t M, const lq_m
 /*
  * lq_lora_bwd (lq.h) from a checkpoint of the layer's input: the backward of
  * the dense bf16 or NF4 layer with Xq, the MX tensor of X, in the place of X.
- * dX does not depend on X; dA and dB (and T, where T_saved is NULL) are those
- * of the restored input.  dA and dB are summed as in lq_mx_lora_bwd.
+ * dX does not depend on X: it is formed as lq_lora_bwd forms it, or for a dense
+ * base where that is faster as lq_mx_lora_bwd does.  dA and dB (and T, where
+ * T_saved is NULL) are those of the restored input, summed as in lq_mx_lora_bwd.
  *   ws  at least lq_mx_workspace_size(LQ_MX_OP_BWD_CKPT_FUSED, M, N, K, r) bytes
  *       (without dA and dB, + LQ_MX_NO_GRADS); lq_lora_bwd_ckpt_workspace bytes
  *       let dX take its fastest path, whose results may differ in their
