@@ -1,0 +1,881 @@
+// Low-rank adapters of many requests beside a shared projection
+// (lq_adapters_fwd, lq_adapters_bwd).
+//
+//   Y[i] += s_a (X[i] A_a^T) B_a^T,  a = rows[i]
+//   dX[i] += s_a U[i] A_a,  U[i] = dY[i] B_a
+//   dA_a = s_a sum_i U[i]^T X[i],  dB_a = s_a sum_i dY[i]^T T[i]
+//
+// Rows are taken in tiles of up to 64 that share one adapter.  Up to 64 rows
+// every workgroup finds its tile by itself: workgroup i looks at the row ids
+// (one per lane, one ballot) and goes on only if row i is the first with its
+// adapter.  More rows are sorted by one workgroup first (plan_kernel).
+//
+// Shrink (T = X A^T, U = dY B): no LDS in its loop.  The four waves of a
+// workgroup take turns at 64-column steps of the reduction, each with all the
+// tile's rows and ranks, so that an operand line is read once per workgroup,
+// and are added at the end; further workgroups split the reduction, their
+// partial sums are added in order by the expand.
+// Expand (Y += s T B^T, dX += s U A): the output transposed (B's rows = MFMA
+// rows), with B's rows permuted so that a lane holds 16 consecutive outputs of
+// a row and four lanes a whole 128-byte line.
+#include "block.h"
+#include "device_util.h"
+#include "dispatch.h"
+
+namespace lq {
+namespace {
+
+constexpr int kTM = 64;       // rows per tile
+constexpr int kDirect = 64;   // up to so many rows workgroups find their tiles by themselves
+constexpr int kCnt = 32768;   // counters of the plan
+
+struct RowArgs {
+  const int32_t* rows;
+  const int32_t* ranks;
+  const float* scales;
+  // the plan (NULL: M <= kDirect): first sorted position of each place's rows
+  // (place ``slots``: rows without an adapter; then M), rows in sorted order,
+  // (place, first position) of each tile, of each segment of the gradients, and
+  // the first segment of each place
+  const int32_t* off;
+  const int32_t* perm;
+  const int2* tiles;
+  const int2* segs;
+  const int32_t* seg0;
+  const int32_t* count;  // tiles, segments
+  int32_t M, slots, r;
+};
+
+__device__ __forceinline__ int place_of(int32_t a, int slots) {
+  return a >= 0 && a < slots ? a : slots;
+}
+
+__device__ __forceinline__ int rank_of(const RowArgs& a, int slot) {
+  if (slot >= a.slots) return 0;
+  if (!a.ranks) return a.r;
+  const int k = a.ranks[slot];
+  return k < 0 ? 0 : k > a.r ? a.r : k;
+}
+
+// This workgroup's tile: its place and number of rows (0: none) and their
+// indices in rows_s (ready after the caller's next barrier).
+__device__ __forceinline__ int find_tile(const RowArgs& a, int tile, int32_t* rows_s, int& slot) {
+  const int lane = threadIdx.x & 63;
+  if (!a.tiles) {
+    const int id = lane < a.M ? place_of(a.rows[lane], a.slots) : -1;
+    slot = __builtin_amdgcn_readlane(id, tile);
+    const uint64_t same = __ballot(id == slot);
+    if ((int)__builtin_ctzll(same) != tile) return 0;
+    if (threadIdx.x < 64 && id == slot)
+      rows_s[__builtin_popcountll(same & ((1ull << lane) - 1))] = lane;
+    return __builtin_popcountll(same);
+  }
+  if (tile >= a.count[0]) return 0;
+  const int2 t = a.tiles[tile];
+  slot = t.x;
+  const int left = a.off[slot + 1] - t.y;
+  const int n = left < kTM ? left : kTM;
+  if ((int)threadIdx.x < n) rows_s[threadIdx.x] = a.perm[t.y + threadIdx.x];
+  return n;
+}
+
+// ---------------------------------------------------------------- plan
+// Stable counting sort of the rows by place, in one workgroup of 16 waves: each
+// wave counts its own range of rows into counters of its own (rows of a wave
+// that share a place are found with one ballot per bit of the place), the
+// counters become first positions, and a second walk over the rows places them.
+// A wave's range is walked eight loads at a time, since a step's load is its
+// longest part.
+struct PlanArgs {
+  const int32_t* rows;
+  int32_t* off;
+  int32_t* perm;
+  int2* tiles;
+  int2* segs;
+  int32_t* seg0;
+  int32_t* count;
+  int32_t M, slots, waves, bits, seg_rows;
+};
+
+// the lanes of the wave whose value equals this lane's
+__device__ __forceinline__ uint64_t lanes_like(int v, int bits, bool in) {
+  uint64_t m = __ballot(in);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t k = __ballot((v >> b) & 1);
+    m &= (v >> b) & 1 ? k : ~k;
+  }
+  return m;
+}
+
+// exclusive sums over the workgroup of three values per thread; the totals
+__device__ __forceinline__ void scan3(int (&v)[3], int (&total)[3], int (*sh)[3]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  int x[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    x[k] = v[k];
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(x[k], o);
+      if (lane >= o) x[k] += y;
+    }
+  }
+  if (lane == 63)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sh[wave][k] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int before = 0, all = 0;
+    for (int w = 0; w < nw; ++w) {
+      before += w < wave ? sh[w][k] : 0;
+      all += sh[w][k];
+    }
+    v[k] = before + x[k] - v[k];
+    total[k] = all;
+  }
+}
+
+__global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
+  __shared__ int32_t cnt[kCnt];
+  __shared__ int sh[16][3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int S1 = p.slots + 1, W = p.waves;
+  for (int i = tid; i < W * S1; i += 1024) cnt[i] = 0;
+  __syncthreads();
+  const int per = (int)cdiv(cdiv(p.M, 64), W) * 64;
+  const int64_t lo = (int64_t)wave * per;
+  const int64_t end = lo + per;
+  const int hi = wave < W ? (int)(end < p.M ? end : p.M) : 0;
+  const uint64_t below = (1ull << lane) - 1;
+  auto walk = [&](bool place) {
+    for (int64_t b = lo; b < hi; b += 512) {
+      int id[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t i = b + 64 * k + lane;
+        id[k] = i < hi ? place_of(p.rows[i], p.slots) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t i = b + 64 * k + lane;
+        if (b + 64 * k >= hi) break;
+        const bool in = i < hi;
+        const uint64_t m = lanes_like(id[k], p.bits, in);
+        const int first = in ? (int)__builtin_ctzll(m) : lane;
+        int old = 0;
+        if (in && lane == first) old = atomicAdd(&cnt[wave * S1 + id[k]], __builtin_popcountll(m));
+        if (place) {
+          old = __shfl(old, first);
+          if (in) p.perm[old + __builtin_popcountll(m & below)] = (int32_t)i;
+        }
+      }
+    }
+  };
+  walk(false);
+  __syncthreads();
+  // counts become positions: thread t has places c t .. c t + c - 1
+  const int c = (int)cdiv(S1, 1024);
+  int v[3] = {0, 0, 0}, total[3];
+  for (int k = 0; k < c; ++k) {
+    const int s = tid * c + k;
+    if (s >= S1) break;
+    int n = 0;
+    for (int w = 0; w < W; ++w) {
+      const int x = cnt[w * S1 + s];
+      cnt[w * S1 + s] = n;
+      n += x;
+    }
+    v[0] += n;
+    v[1] += (int)cdiv(n, kTM);
+    v[2] += s < p.slots ? (int)cdiv(n, p.seg_rows) : 0;
+    p.off[s + 1] = n;  // the count, until the positions are known
+  }
+  scan3(v, total, sh);
+  for (int k = 0; k < c; ++k) {
+    const int s = tid * c + k;
+    if (s >= S1) break;
+    const int n = p.off[s + 1];
+    for (int w = 0; w < W; ++w) cnt[w * S1 + s] += v[0];
+    if (s < p.slots) {
+      p.seg0[s] = v[2];
+      for (int i = 0; i < n; i += p.seg_rows) p.segs[v[2]++] = make_int2(s, v[0] + i);
+    }
+    for (int i = 0; i < n; i += kTM) p.tiles[v[1]++] = make_int2(s, v[0] + i);
+    v[0] += n;
+    p.off[s + 1] = v[0];
+  }
+  if (tid == 0) {
+    p.off[0] = 0;
+    p.seg0[p.slots] = total[2];
+    p.count[0] = total[1];
+    p.count[1] = total[2];
+  }
+  __syncthreads();
+  walk(true);
+}
+
+// -------------------------------------------------------------- shrink
+
+struct ShrinkParams {
+  RowArgs a;
+  const uint16_t* X;  // M x C
+  const uint16_t* A;  // slots x r x C
+  float* Tp;          // splits x M x r
+  int32_t C, steps;   // 64-column steps of the reduction, of one split
+};
+
+template <int MB, int JB>
+__device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t* rows_s, int n,
+                                            const uint16_t* A, int rank, int s0, int s1,
+                                            float* red) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, i16 = lane & 15;
+  const uint16_t* xr[MB];
+  const uint16_t* ar[JB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m) {
+    const int i = 16 * m + i16;
+    xr[m] = p.X + (int64_t)rows_s[i < n ? i : n - 1] * p.C + 8 * g;
+  }
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int k = 16 * j + i16;
+    ar[j] = A + (int64_t)(k < rank ? k : rank - 1) * p.C + 8 * g;
+  }
+  f32x4 acc[MB][JB];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int j = 0; j < JB; ++j) acc[m][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 x[2][MB][2], a[2][JB][2];
+  auto load = [&](int s, int b) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+        x[b][m][h] = *reinterpret_cast<const u32x4*>(xr[m] + 64 * s + 32 * h);
+#pragma unroll
+      for (int j = 0; j < JB; ++j)
+        a[b][j][h] = *reinterpret_cast<const u32x4*>(ar[j] + 64 * s + 32 * h);
+    }
+  };
+  auto mul = [&](int b) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[m][j] = mfma16(x[b][m][h], a[b][j][h], acc[m][j]);
+  };
+  int s = s0 + wave;
+  if (s < s1) {
+    load(s, 0);
+    for (; s + 4 < s1; s += 8) {
+      load(s + 4, 1);
+      mul(0);
+      if (s + 8 < s1) load(s + 8, 0);
+      mul(1);
+    }
+    if (s < s1) mul(0);
+  }
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        red[(wave * kTM + 16 * m + 4 * g + v) * (16 * JB) + 16 * j + i16] = acc[m][j][v];
+}
+
+template <int JB>
+__global__ __launch_bounds__(256) void shrink_tiles_kernel(ShrinkParams p) {
+  __shared__ int32_t rows_s[kTM];
+  __shared__ float red[4 * kTM * 16 * JB];
+  int slot;
+  const int n = find_tile(p.a, blockIdx.x, rows_s, slot);
+  if (n == 0) return;
+  const int rank = rank_of(p.a, slot);
+  if (rank == 0) return;
+  __syncthreads();
+  const int s0 = blockIdx.y * p.steps, all = p.C / 64;
+  const int s1 = s0 + p.steps < all ? s0 + p.steps : all;
+  const uint16_t* A = p.A + (int64_t)slot * p.a.r * p.C;
+  if (n <= 16)
+    shrink_tile<1, JB>(p, rows_s, n, A, rank, s0, s1, red);
+  else
+    shrink_tile<4, JB>(p, rows_s, n, A, rank, s0, s1, red);
+  __syncthreads();
+  float* out = p.Tp + (int64_t)blockIdx.y * p.a.M * p.a.r;
+  for (int e = threadIdx.x; e < n * 16 * JB; e += 256) {
+    const int i = e / (16 * JB), j = e % (16 * JB);
+    if (j < rank)
+      out[(int64_t)rows_s[i] * p.a.r + j] =
+          (red[e] + red[kTM * 16 * JB + e]) + (red[2 * kTM * 16 * JB + e] + red[3 * kTM * 16 * JB + e]);
+  }
+}
+
+// -------------------------------------------------------------- expand
+
+struct ExpandParams {
+  RowArgs a;
+  const float* Tp;    // splits x M x r
+  const uint16_t* B;  // slots x N x ldb
+  const uint16_t* Yi;
+  uint16_t* Yo;
+  float* T_out;  // M x r or NULL
+  int32_t splits, N, ldb, passes;
+};
+
+// B[n][j0 .. j0 + 7], zeros from ``rank``; ld: row stride in elements.  WHOLE:
+// ld % 8 == 0, rows 16-byte aligned
+template <bool WHOLE>
+__device__ __forceinline__ u32x4 b_operand(const uint16_t* row, int j0, int rank, int ld) {
+  if (j0 >= rank) return u32x4{0u, 0u, 0u, 0u};
+  if (WHOLE) {
+    u32x4 v = *reinterpret_cast<const u32x4*>(row + j0);
+    const int left = rank - j0;
+    if (left < 8) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        v[d] = 2 * d + 1 < left ? v[d] : 2 * d < left ? v[d] & 0xFFFFu : 0u;
+    }
+    return v;
+  }
+  uint16_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = j0 + i < rank ? row[j0 + i] : (uint16_t)0;
+  return u32x4{(uint32_t)e[0] | ((uint32_t)e[1] << 16), (uint32_t)e[2] | ((uint32_t)e[3] << 16),
+               (uint32_t)e[4] | ((uint32_t)e[5] << 16), (uint32_t)e[6] | ((uint32_t)e[7] << 16)};
+}
+
+// v as two bf16 parts: hi + lo is v to 2^-16 of it (lo 0 where hi is not finite)
+__device__ __forceinline__ void split2(float v, uint16_t& hi, uint16_t& lo) {
+  hi = f32_to_bf16(v);
+  const float h = bf16_to_f32(hi);
+  lo = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0 : f32_to_bf16(v - h);
+}
+
+// JC: 32-rank chunks
+template <int JC, bool WHOLE>
+__global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
+  constexpr int LD = 32 * JC + 8;  // LDS row pitch of T in elements
+  __shared__ int32_t rows_s[kTM];
+  __shared__ __attribute__((aligned(16))) uint16_t t_hi[kTM * LD], t_lo[kTM * LD];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, i16 = lane & 15;
+  int slot;
+  const int n = find_tile(p.a, blockIdx.x, rows_s, slot);
+  if (n == 0) return;
+  const int rank = rank_of(p.a, slot);
+  const bool store_t = p.T_out && blockIdx.y == 0;
+  if (rank == 0 && p.Yi == p.Yo && !store_t) return;
+  __syncthreads();
+  const int r = p.a.r, M = p.a.M, N = p.N;
+  const float s = rank ? p.a.scales[slot] : 0.0f;
+  for (int e = tid; e < 16 * (int)cdiv(n, 16) * 32 * JC; e += 256) {
+    const int i = e / (32 * JC), j = e % (32 * JC);
+    float v = 0.0f;
+    if (i < n && j < rank) {
+      const float* q = p.Tp + (int64_t)rows_s[i] * r + j;
+      for (int k = 0; k < p.splits; ++k) v += q[(int64_t)k * M * r];
+    }
+    if (store_t && i < n && j < r) p.T_out[(int64_t)rows_s[i] * r + j] = v;
+    uint16_t hi, lo;
+    split2(v * s, hi, lo);
+    t_hi[i * LD + j] = hi;
+    t_lo[i * LD + j] = lo;
+  }
+  __syncthreads();
+  if (!p.Yo) return;
+  const uint16_t* B = p.B + (int64_t)slot * N * p.ldb;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int n0 = ((int)blockIdx.y * p.passes + pass) * 256 + 64 * wave;
+    if (n0 >= N) return;
+    u32x4 bf[4][JC];
+    if (rank) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int jc = 0; jc < JC; ++jc)
+          bf[b][jc] = b_operand<WHOLE>(
+              B + (int64_t)(n0 + 16 * (i16 >> 2) + 4 * b + (i16 & 3)) * p.ldb, 32 * jc + 8 * g,
+              rank, p.ldb);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (16 * m >= n) break;
+      const int i = 16 * m + i16;
+      const int64_t at = (int64_t)rows_s[i < n ? i : n - 1] * N + n0 + 16 * g;
+      u32x4 y[2] = {*reinterpret_cast<const u32x4*>(p.Yi + at),
+                    *reinterpret_cast<const u32x4*>(p.Yi + at + 8)};
+      if (rank) {
+        f32x4 acc[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          acc[b] = f32x4{lo_bf16(y[b >> 1][2 * (b & 1)]), hi_bf16(y[b >> 1][2 * (b & 1)]),
+                         lo_bf16(y[b >> 1][2 * (b & 1) + 1]), hi_bf16(y[b >> 1][2 * (b & 1) + 1])};
+#pragma unroll
+        for (int jc = 0; jc < JC; ++jc) {
+          const u32x4 th = *reinterpret_cast<const u32x4*>(t_hi + i * LD + 32 * jc + 8 * g);
+          const u32x4 tl = *reinterpret_cast<const u32x4*>(t_lo + i * LD + 32 * jc + 8 * g);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            acc[b] = mfma16(bf[b][jc], tl, acc[b]);
+            acc[b] = mfma16(bf[b][jc], th, acc[b]);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          y[b >> 1][2 * (b & 1)] = pack_bf16x2(acc[b][0], acc[b][1]);
+          y[b >> 1][2 * (b & 1) + 1] = pack_bf16x2(acc[b][2], acc[b][3]);
+        }
+      }
+      if (i < n) {
+        *reinterpret_cast<u32x4*>(p.Yo + at) = y[0];
+        *reinterpret_cast<u32x4*>(p.Yo + at + 8) = y[1];
+      }
+    }
+  }
+}
+
+// --------------------------------------------- factors turned (backward)
+// Bt[slot][j][n] = B[slot][n][j] and At[slot][k][j] = A[slot][j][k] (rows of ld
+// elements) for the places that have rows: 64 columns n or k per workgroup.
+struct TurnParams {
+  const uint16_t* A;
+  const uint16_t* B;
+  uint16_t* At;
+  uint16_t* Bt;
+  const int32_t* off;
+  int32_t N, K, r, ld;
+};
+
+__global__ __launch_bounds__(256) void turn_kernel(TurnParams p) {
+  __shared__ uint16_t s[64 * 66];
+  const int slot = blockIdx.y, r = p.r;
+  if (p.off[slot + 1] == p.off[slot]) return;
+  const int nb = p.N / 64;
+  const bool is_b = (int)blockIdx.x < nb;
+  const int c0 = (is_b ? blockIdx.x : blockIdx.x - nb) * 64;
+  if (is_b) {
+    const uint16_t* B = p.B + ((int64_t)slot * p.N + c0) * r;
+    for (int e = threadIdx.x; e < 64 * r; e += 256) s[(e % r) * 66 + e / r] = B[e];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 64 * r; e += 256)
+      p.Bt[((int64_t)slot * r + e / 64) * p.N + c0 + e % 64] = s[(e / 64) * 66 + e % 64];
+  } else {
+    for (int e = threadIdx.x; e < 64 * r; e += 256)
+      s[(e / 64) * 66 + e % 64] = p.A[((int64_t)slot * r + e / 64) * p.K + c0 + e % 64];
+    __syncthreads();
+    uint16_t* At = p.At + ((int64_t)slot * p.K + c0) * p.ld;
+    for (int e = threadIdx.x; e < 64 * p.ld; e += 256) {
+      const int j = e % p.ld;
+      At[e] = j < r ? s[j * 66 + e / p.ld] : (uint16_t)0;
+    }
+  }
+}
+
+// ------------------------------------------------------------- gradients
+// dA_a = s_a sum_i U[i]^T X[i] and dB_a = s_a sum_i dY[i]^T T[i] over one
+// segment of the place's rows, 256 columns of X or dY per workgroup, 64 per
+// wave.  Steps of 32 rows: their columns go row by row into LDS (rows 32 bytes
+// off 512, so that the transposing reads of four rows meet different banks), U
+// or T as three bf16 parts, transposed.
+struct GradParams {
+  RowArgs a;
+  const uint16_t* X;   // M x K
+  const uint16_t* dY;  // M x N
+  const float* U;      // M x r
+  const float* T;
+  float* dA;    // slots x r x K
+  float* dB;    // slots x N x r
+  float* part;  // segments x (r K + N r)
+  int32_t N, K, seg_rows, accumulate;
+};
+
+constexpr int kZP = 256 + 16;  // LDS row pitch of a step's columns, in elements
+constexpr int kVP = 32 + 8;    // ... of the parts of U or T
+
+typedef short s16x4g __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 read_turned(uint16_t* p) {
+  typedef __attribute__((address_space(3))) s16x4g* lds_ptr;
+  const s16x4g v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+  return __builtin_bit_cast(u32x2, v);
+}
+
+template <int JB, bool DB>
+__device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, uint16_t* zs,
+                                          uint16_t* vs) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, i16 = lane & 15;
+  const int2 sg = p.a.segs[seg];
+  const int slot = sg.x, r = p.a.r, C = DB ? p.N : p.K;
+  const int rank = rank_of(p.a, slot);
+  const int left = p.a.off[slot + 1] - sg.y;
+  const int n = left < p.seg_rows ? left : p.seg_rows;
+  const int32_t* perm = p.a.perm + sg.y;
+  const uint16_t* Z = DB ? p.dY : p.X;
+  const float* V = DB ? p.T : p.U;
+  constexpr int R = 16 * JB, VE = 32 * R / 256;  // values of U or T per thread
+  f32x4 acc[4][JB];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < JB; ++j) acc[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 z[4];
+  float v[VE];
+  // piece k of a thread: row 8 k + tid / 32, columns 8 (tid % 32)
+  auto load = [&](int b) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = b + 8 * k + (tid >> 5), c = c0 + 8 * (tid & 31);
+      z[k] = u32x4{0u, 0u, 0u, 0u};
+      if (i < n && c < C) z[k] = *reinterpret_cast<const u32x4*>(Z + (int64_t)perm[i] * C + c);
+    }
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      const int e = 256 * k + tid, i = b + e / R, j = e % R;
+      v[k] = 0.0f;
+      if (i < n && j < rank) v[k] = V[(int64_t)perm[i] * r + j];
+    }
+  };
+  if (rank) {
+    load(0);
+    for (int b = 0; b < n; b += 32) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<u32x4*>(zs + (8 * k + (tid >> 5)) * kZP + 8 * (tid & 31)) = z[k];
+#pragma unroll
+      for (int k = 0; k < VE; ++k) {
+        const int e = 256 * k + tid, i = e / R, j = e % R;
+        const uint16_t hi = f32_to_bf16(v[k]);
+        const bool fin = (hi & 0x7F80u) != 0x7F80u;
+        const float r1 = fin ? v[k] - bf16_to_f32(hi) : 0.0f;
+        const uint16_t mid = f32_to_bf16(r1);
+        vs[j * kVP + i] = hi;
+        vs[(R + j) * kVP + i] = mid;
+        vs[(2 * R + j) * kVP + i] = f32_to_bf16(r1 - bf16_to_f32(mid));
+      }
+      __syncthreads();
+      if (b + 32 < n) load(b + 32);
+      u32x4 zf[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint16_t* q = zs + (8 * g + (i16 >> 2)) * kZP + 64 * wave + 16 * c + 4 * (i16 & 3);
+        const u32x2 lo = read_turned(q), hi = read_turned(q + 4 * kZP);
+        zf[c] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+#pragma unroll
+      for (int part = 2; part >= 0; --part)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+          const u32x4 vf =
+              *reinterpret_cast<const u32x4*>(vs + (part * R + 16 * j + i16) * kVP + 8 * g);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc[c][j] = DB ? mfma16(vf, zf[c], acc[c][j]) : mfma16(zf[c], vf, acc[c][j]);
+        }
+    }
+  }
+  const int first = p.a.seg0[slot];
+  const bool whole = p.a.seg0[slot + 1] == first + 1;  // the place's only segment
+  const float s = p.a.scales[slot];
+  const int64_t size = (int64_t)r * p.K + (int64_t)p.N * r;
+  float* out = whole ? (DB ? p.dB + (int64_t)slot * p.N * r : p.dA + (int64_t)slot * r * p.K)
+                     : p.part + seg * size + (DB ? (int64_t)r * p.K : 0);
+  const bool add = whole && p.accumulate;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = c0 + 64 * wave + 16 * c + (DB ? i16 : 4 * g + e);
+        const int k = 16 * j + (DB ? 4 * g + e : i16);
+        if (col >= C || k >= r) continue;
+        float* o = DB ? out + (int64_t)col * r + k : out + (int64_t)k * C + col;
+        if (k < rank) {
+          const float x = s * acc[c][j][e];
+          *o = add ? *o + x : x;
+        } else if (!add) {
+          *o = 0.0f;
+        }
+      }
+}
+
+template <int JB>
+__global__ __launch_bounds__(256) void adapter_grads_kernel(GradParams p) {
+  __shared__ __attribute__((aligned(16))) uint16_t zs[32 * kZP];
+  __shared__ __attribute__((aligned(16))) uint16_t vs[3 * 16 * JB * kVP];
+  if ((int)blockIdx.y >= p.a.count[1]) return;
+  const int ca = (p.K + 255) / 256;
+  if ((int)blockIdx.x < ca)
+    grad_tile<JB, false>(p, blockIdx.y, 256 * blockIdx.x, zs, vs);
+  else
+    grad_tile<JB, true>(p, blockIdx.y, 256 * (blockIdx.x - ca), zs, vs);
+}
+
+// Places of several segments: their sums in order; places without rows: zeros.
+__global__ __launch_bounds__(256) void grads_finish_kernel(GradParams p) {
+  const int slot = blockIdx.y;
+  const int s0 = p.a.seg0[slot], s1 = p.a.seg0[slot + 1];
+  if (s1 == s0 + 1 || (s1 == s0 && p.accumulate)) return;
+  const int64_t na = (int64_t)p.a.r * p.K, size = na + (int64_t)p.N * p.a.r;
+  const int64_t e = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);  // both parts are multiples of 64
+  if (e >= size) return;
+  f32x4* o = reinterpret_cast<f32x4*>(e < na ? p.dA + slot * na + e
+                                             : p.dB + (int64_t)slot * (size - na) + e - na);
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = s0; k < s1; ++k) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(p.part + k * size + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += x[i];
+  }
+  if (p.accumulate) {
+    const f32x4 x = *o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += x[i];
+  }
+  *o = v;
+}
+
+// ---------------------------------------------------------------- host
+
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+int64_t max_tiles(int64_t M, int32_t slots) {
+  if (M <= kDirect) return M;
+  const int64_t t = cdiv(M, kTM) + slots;
+  return t < M ? t : M;
+}
+
+// Splits of the shrink's reduction over C columns: about 512 workgroups where
+// tiles are full, and no wave without a step
+int shrink_splits(int64_t M, int64_t C) {
+  const int64_t most = cdiv(C / 64, 4), want = cdiv(512, cdiv(M, kTM));
+  const int64_t s = want < most ? want : most;
+  return (int)(s < 32 ? s : 32);
+}
+
+// Rows of a segment of the gradients: about 768 workgroups where places have
+// enough rows
+int64_t segment_rows(int64_t M, int64_t N, int64_t K) {
+  const int64_t cols = cdiv(N, 256) + cdiv(K, 256), want = cdiv(768, cols);
+  const int64_t rows = cdiv(cdiv(M, want), 32) * 32;
+  return rows < 128 ? 128 : rows;
+}
+int64_t max_segments(int64_t M, int64_t N, int64_t K, int32_t slots) {
+  const int64_t s = cdiv(M, segment_rows(M, N, K)) + slots;
+  return s < M ? s : M;
+}
+
+struct PlanLayout {
+  size_t off, seg0, count, tiles, segs, perm, end;
+};
+PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
+  PlanLayout l;
+  l.off = 0;
+  l.seg0 = up256((size_t)(slots + 2) * 4);
+  l.count = l.seg0 + up256((size_t)(slots + 2) * 4);
+  l.tiles = l.count + 256;
+  l.segs = l.tiles + up256((size_t)max_tiles(M > kDirect ? M : kDirect + 1, slots) * 8);
+  l.perm = l.segs + up256((size_t)segs * 8);
+  l.end = l.perm + up256((size_t)M * 4);
+  return l;
+}
+
+int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, hipStream_t st) {
+  PlanArgs p;
+  p.rows = a.rows;
+  p.off = (int32_t*)(ws + l.off);
+  p.seg0 = (int32_t*)(ws + l.seg0);
+  p.count = (int32_t*)(ws + l.count);
+  p.tiles = (int2*)(ws + l.tiles);
+  p.segs = (int2*)(ws + l.segs);
+  p.perm = (int32_t*)(ws + l.perm);
+  p.M = a.M;
+  p.slots = a.slots;
+  p.waves = kCnt / (a.slots + 1) < 16 ? kCnt / (a.slots + 1) : 16;
+  p.bits = 32 - __builtin_clz(a.slots);
+  p.seg_rows = (int32_t)seg_rows;
+  a.off = p.off;
+  a.seg0 = p.seg0;
+  a.count = p.count;
+  a.tiles = p.tiles;
+  a.segs = p.segs;
+  a.perm = p.perm;
+  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, st, p);
+  return hip_fail(hipGetLastError(), "adapters plan launch");
+}
+
+int launch_shrink(const RowArgs& a, const void* X, const void* A, int64_t C, float* Tp,
+                  hipStream_t st) {
+  const int splits = shrink_splits(a.M, C);
+  ShrinkParams p;
+  p.a = a;
+  p.X = (const uint16_t*)X;
+  p.A = (const uint16_t*)A;
+  p.Tp = Tp;
+  p.C = (int32_t)C;
+  p.steps = (int32_t)cdiv(C / 64, splits);
+  const dim3 g((unsigned)max_tiles(a.M, a.slots), (unsigned)splits), b(256);
+  switch ((a.r + 15) / 16) {
+    case 1: hipLaunchKernelGGL(shrink_tiles_kernel<1>, g, b, 0, st, p); break;
+    case 2: hipLaunchKernelGGL(shrink_tiles_kernel<2>, g, b, 0, st, p); break;
+    case 3: hipLaunchKernelGGL(shrink_tiles_kernel<3>, g, b, 0, st, p); break;
+    default: hipLaunchKernelGGL(shrink_tiles_kernel<4>, g, b, 0, st, p);
+  }
+  return hip_fail(hipGetLastError(), "adapters shrink launch");
+}
+
+// Yo NULL: only T_out
+int launch_expand(const RowArgs& a, const float* Tp, int splits, const void* B, int64_t N, int ldb,
+                  const void* Yi, void* Yo, float* T_out, hipStream_t st) {
+  ExpandParams p;
+  p.a = a;
+  p.Tp = Tp;
+  p.B = (const uint16_t*)B;
+  p.Yi = (const uint16_t*)Yi;
+  p.Yo = (uint16_t*)Yo;
+  p.T_out = T_out;
+  p.splits = splits;
+  p.N = (int32_t)N;
+  p.ldb = ldb;
+  // 256 columns per workgroup and pass; more than one pass where full tiles
+  // alone are enough workgroups
+  const int64_t chunks = Yo ? cdiv(N, 256) : 1, full = cdiv(a.M, kTM);
+  int64_t passes = full * chunks / 1024;
+  passes = passes < 1 ? 1 : passes > 8 ? 8 : passes;
+  p.passes = (int32_t)passes;
+  const dim3 g((unsigned)max_tiles(a.M, a.slots), (unsigned)cdiv(chunks, passes)), b(256);
+  const auto kernel = a.r <= 32 ? (ldb % 8 ? expand_tiles_kernel<1, false> : expand_tiles_kernel<1, true>)
+                                : (ldb % 8 ? expand_tiles_kernel<2, false> : expand_tiles_kernel<2, true>);
+  hipLaunchKernelGGL(kernel, g, b, 0, st, p);
+  return hip_fail(hipGetLastError(), "adapters expand launch");
+}
+
+RowArgs row_args(int64_t M, const lq_adapter_pool& q, const int32_t* rows) {
+  RowArgs a{};
+  a.rows = rows;
+  a.ranks = q.ranks;
+  a.scales = q.scales;
+  a.M = (int32_t)M;
+  a.slots = q.slots;
+  a.r = q.r;
+  return a;
+}
+
+// Workspace of the backward: [plan][B turned][A turned][U][T][partial sums of the
+// shrinks][partial gradients]
+struct BwdLayout {
+  PlanLayout plan;
+  size_t bt, at, u, t, tp, part, end;
+};
+BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
+  BwdLayout l;
+  const int64_t segs = max_segments(M, N, K, slots), r8 = cdiv(r, 8) * 8;
+  const int64_t sn = shrink_splits(M, N), sk = shrink_splits(M, K);
+  l.plan = plan_layout(M, slots, segs);
+  l.bt = l.plan.end;
+  l.at = l.bt + up256((size_t)slots * r * N * 2);
+  l.u = l.at + up256((size_t)slots * r8 * K * 2);
+  l.t = l.u + up256((size_t)M * r * 4);
+  l.tp = l.t + up256((size_t)M * r * 4);
+  l.part = l.tp + up256((size_t)(sn > sk ? sn : sk) * M * r * 4);
+  l.end = l.part + up256((size_t)segs * r * (N + K) * 4);
+  return l;
+}
+
+}  // namespace
+
+namespace dispatch {
+
+size_t adapters_fwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
+  (void)N;
+  const size_t plan = M <= kDirect ? 0 : plan_layout(M, slots, max_segments(M, N, K, slots)).end;
+  return plan + (size_t)shrink_splits(M, K) * M * r * 4;
+}
+
+size_t adapters_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
+  return bwd_layout(M, N, K, r, slots).end;
+}
+
+int adapters_fwd(const void* X, int64_t M, const lq_adapter_pool& q, const int32_t* rows,
+                 const void* Y_in, void* Y_out, float* T_out, void* ws, hipStream_t st) {
+  RowArgs a = row_args(M, q, rows);
+  char* base = (char*)ws;
+  int rc;
+  if (M > kDirect) {
+    const PlanLayout l = plan_layout(M, q.slots, max_segments(M, q.N, q.K, q.slots));
+    if ((rc = launch_plan(a, l, base, segment_rows(M, q.N, q.K), st))) return rc;
+    base += l.end;
+  }
+  if ((rc = launch_shrink(a, X, q.A, q.K, (float*)base, st))) return rc;
+  return launch_expand(a, (float*)base, shrink_splits(M, q.K), q.B, q.N, q.r, Y_in, Y_out, T_out,
+                       st);
+}
+
+int adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool& q,
+                 const int32_t* rows, const float* T_saved, const void* dX_in, void* dX_out,
+                 float* dA, float* dB, int accumulate, void* ws, hipStream_t st) {
+  const BwdLayout l = bwd_layout(M, q.N, q.K, q.r, q.slots);
+  char* base = (char*)ws;
+  RowArgs a = row_args(M, q, rows);
+  int rc = launch_plan(a, l.plan, base, segment_rows(M, q.N, q.K), st);
+  if (rc) return rc;
+  TurnParams t;
+  t.A = (const uint16_t*)q.A;
+  t.B = (const uint16_t*)q.B;
+  t.At = (uint16_t*)(base + l.at);
+  t.Bt = (uint16_t*)(base + l.bt);
+  t.off = a.off;
+  t.N = (int32_t)q.N;
+  t.K = (int32_t)q.K;
+  t.r = q.r;
+  t.ld = (q.r + 7) / 8 * 8;
+  // without dX only B is turned
+  hipLaunchKernelGGL(turn_kernel, dim3((unsigned)(q.N / 64 + (dX_out ? q.K / 64 : 0)), q.slots),
+                     dim3(256), 0, st, t);
+  if ((rc = hip_fail(hipGetLastError(), "adapters turn launch"))) return rc;
+  float *U = (float*)(base + l.u), *Tp = (float*)(base + l.tp), *T = (float*)(base + l.t);
+  if ((rc = launch_shrink(a, dY, t.Bt, q.N, Tp, st))) return rc;
+  if ((rc = launch_expand(a, Tp, shrink_splits(M, q.N), t.At, q.K, t.ld, dX_in, dX_out,
+                          dA ? U : nullptr, st)))
+    return rc;
+  if (!dA) return LQ_OK;
+  if (!T_saved) {
+    if ((rc = launch_shrink(a, X, q.A, q.K, Tp, st))) return rc;
+    if ((rc = launch_expand(a, Tp, shrink_splits(M, q.K), nullptr, 0, 8, nullptr, nullptr, T, st)))
+      return rc;
+  }
+  GradParams p;
+  p.a = a;
+  p.X = (const uint16_t*)X;
+  p.dY = (const uint16_t*)dY;
+  p.U = U;
+  p.T = T_saved ? T_saved : T;
+  p.dA = dA;
+  p.dB = dB;
+  p.part = (float*)(base + l.part);
+  p.N = (int32_t)q.N;
+  p.K = (int32_t)q.K;
+  p.seg_rows = (int32_t)segment_rows(M, q.N, q.K);
+  p.accumulate = accumulate;
+  const dim3 g((unsigned)(cdiv(q.N, 256) + cdiv(q.K, 256)),
+               (unsigned)max_segments(M, q.N, q.K, q.slots));
+  switch ((q.r + 15) / 16) {
+    case 1: hipLaunchKernelGGL(adapter_grads_kernel<1>, g, dim3(256), 0, st, p); break;
+    case 2: hipLaunchKernelGGL(adapter_grads_kernel<2>, g, dim3(256), 0, st, p); break;
+    case 3: hipLaunchKernelGGL(adapter_grads_kernel<3>, g, dim3(256), 0, st, p); break;
+    default: hipLaunchKernelGGL(adapter_grads_kernel<4>, g, dim3(256), 0, st, p);
+  }
+  if ((rc = hip_fail(hipGetLastError(), "adapters gradient launch"))) return rc;
+  const int64_t size = (int64_t)q.r * (q.N + q.K);
+  hipLaunchKernelGGL(grads_finish_kernel, dim3((unsigned)cdiv(size, 1024), q.slots), dim3(256), 0,
+                     st, p);
+  return hip_fail(hipGetLastError(), "adapters gradient sums launch");
+}
+
+}  // namespace dispatch
+}  // namespace lq

@@ -1,0 +1,176 @@
+"""lq_rmsnorm_fwd / lq_rmsnorm_bwd against the oracle in float64.
+
+Tolerances.  A sum of K non-negative squares in float32 is off by at most its
+longest chain of additions, here under 100, times 2^-24; the root halves that, and
+y takes a handful of further roundings: 64 x 2^-24 of |y| in float32.  A bf16
+output adds one rounding, 2^-8 of the value at most."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as oblock
+from qlora_parameter_efficient_amd import block, mx
+
+from .gpu_helpers import DEV, announce, bits, f64
+
+pytestmark = pytest.mark.gpu
+U32 = 2.0**-24
+DTYPES = {"bf16": (torch.bfloat16, 2.0**-8), "f32": (torch.float32, 0.0)}
+SHAPES = [(1, 1), (3, 15), (5, 16), (2, 31), (4, 33), (9, 64), (7, 1000), (6, 1024), (5, 1025), (16, 4096), (3, 4097),
+          (777, 4095), (3, 5120), (2, 8193), (3, 11008), (2, 16384), (2, 16385), (1, 65536)]
+
+
+def inputs(M, K, dt, seed=0):
+    g = torch.Generator().manual_seed(1000 * M + K + seed)
+    t = lambda s=1.0, c=0.0: (torch.randn((M, K), generator=g) * s + c).to(dt).to(DEV)  # noqa: E731
+    w = (1 + 0.2 * torch.randn(K, generator=g))
+    return t, w
+
+
+def close(got, want, rel, slack, what):
+    err = np.abs(got - want)
+    bad = ~(err <= rel * np.abs(want) + slack)
+    assert not bad.any(), (what, int(bad.sum()), float(err[bad].max()))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_forward(M, K, dt):
+    announce(f"rmsnorm fwd {M}x{K} {dt}")
+    td, half = DTYPES[dt]
+    t, w = inputs(M, K, td)
+    X, R, W = t(), t(3.0, 0.5), w.to(torch.float32).to(DEV)
+    c = torch.empty(M, device=DEV)
+    H, Y, q = block.lq_rmsnorm_fwd(X, W, 1e-5, R=R, rstd_out=c)
+    assert q is None and torch.equal(H, (X.float() + R.float()).to(td))
+    y, c64 = oblock.rmsnorm(f64(H), f64(W), 1e-5)
+    close(f64(c), c64, 64 * U32, 0, "rstd")
+    close(f64(Y), y, half + 64 * U32, 0, "y")
+
+
+@pytest.mark.parametrize("gain", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_forward_arguments(dt, residual, gain):
+    td, half = DTYPES[dt]
+    M, K = 37, 1100
+    t, w = inputs(M, K, td)
+    X, R, W = t(), t() if residual else None, w.to(gain).to(DEV)
+    H, Y, _ = block.lq_rmsnorm_fwd(X, W, 1e-6, R=R)
+    assert (H is X) == (not residual)
+    y, _ = oblock.rmsnorm(f64(H), f64(W), 1e-6)
+    close(f64(Y), y, half + 64 * U32, 0, "y")
+    # in place: the residual stream over R (or a copy of X into H_out), y over X
+    Xi, Ri = X.clone(), (R if residual else X).clone()
+    Hi, Yi, _ = block.lq_rmsnorm_fwd(Xi, W, 1e-6, R=Ri if residual else None, H_out=Ri, Y=Xi)
+    assert Hi is Ri and Yi is Xi and torch.equal(Hi, H) and torch.equal(Yi, Y)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_mx_output_is_the_quantisers_of_float32_y(M, K, fmt):
+    """float32 in and out: y as it was quantised is there to compare with, bit for
+    bit; bf16 inputs of the same values give the same codes."""
+    announce(f"rmsnorm fwd {M}x{K} {fmt}")
+    t, w = inputs(M, K, torch.bfloat16)
+    X, W = t(2.0), w.to(DEV)
+    _, Y, q = block.lq_rmsnorm_fwd(X.float(), W, 1e-5, format=fmt)
+    want = mx.lq_mx_quantize(Y, fmt)
+    assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+    _, Y, q = block.lq_rmsnorm_fwd(X, W, 1e-5, format=fmt, need_y=False)
+    assert Y is None and torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+
+
+def test_rows_of_zeros_infinities_and_nan():
+    M, K = 8, 2050
+    t, w = inputs(M, K, torch.float32)
+    X, W = t(), w.to(DEV)
+    X[1] = 0.0
+    X[2, 7] = float("inf")
+    X[3, 2049] = float("nan")
+    X[4] = 1e-30
+    c = torch.empty(M, device=DEV)
+    _, Y, q = block.lq_rmsnorm_fwd(X, W, 1e-6, format="fp8", rstd_out=c)
+    y, _ = oblock.rmsnorm(f64(X[[0, 1, 4, 5, 6, 7]]), f64(W), 1e-6)
+    close(f64(Y[[0, 1, 4, 5, 6, 7]]), y, 64 * U32, 0, "y")
+    assert torch.isnan(Y[3]).all() and torch.isnan(Y[2, 7]) and (Y[2, :7] == 0).all()
+    d = mx.lq_mx_dequantize(q, torch.float32)
+    assert torch.isnan(d[3]).all() and torch.isnan(d[2, :32]).all() and (d[2, 32:] == 0).all()
+    assert (q.scales[1] == 0).all() and (d[1] == 0).all()
+    # eps = 0 on a row of zeros: 0 / 0
+    _, Y, _ = block.lq_rmsnorm_fwd(X[:2], W, 0.0)
+    assert torch.isnan(Y[1]).all() and torch.isfinite(Y[0]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", SHAPES + [(2500, 96), (5000, 1024), (1100, 4096), (300, 16384)])
+def test_backward(M, K, dt):
+    announce(f"rmsnorm bwd {M}x{K} {dt}")
+    td, half = DTYPES[dt]
+    t, w = inputs(M, K, td)
+    H, dY, G, W = t(2.0, 0.3), t(), t(), w.to(td).to(DEV)
+    _, c = oblock.rmsnorm(f64(H), f64(W), 1e-5)
+    dX, dW = block.lq_rmsnorm_bwd(dY, H, W, 1e-5, dH=G)
+    want, dw = oblock.rmsnorm_backward(f64(dY), f64(H), f64(W), c, f64(G))
+    # every term of dX is off by a chain under 200 roundings of sums of magnitudes
+    g, h = np.abs(f64(dY) * f64(W)), np.abs(f64(H))
+    mag = c[:, None] * g + h * c[:, None]**3 * (g * h).mean(axis=1, keepdims=True) + np.abs(f64(G))
+    close(f64(dX), want, half, 200 * U32 * mag, "dX")
+    close(f64(dW), dw, 0, (M + 200) * U32 * (np.abs(f64(dY)) * h * c[:, None]).sum(axis=0), "dW")
+    # saved rstd, no residual gradient, in place
+    _, _, _ = block.lq_rmsnorm_fwd(H, W, 1e-5, rstd_out=(cs := torch.empty(M, device=DEV)))
+    want, _ = oblock.rmsnorm_backward(f64(dY), f64(H), f64(W), f64(cs))
+    buf = dY.clone()
+    dX2, none = block.lq_rmsnorm_bwd(buf, H, W, 1e-5, rstd=cs, need_dw=False, dX=buf)
+    assert none is None and dX2 is buf
+    close(f64(dX2), want, half, 200 * U32 * mag, "dX in place")
+
+
+def test_backward_accumulates_and_repeats():
+    t, w = inputs(3000, 4096, torch.bfloat16)
+    H, dY, W = t(), t(), w.to(DEV)
+    dX, dW = block.lq_rmsnorm_bwd(dY, H, W)
+    first = dW.clone()
+    none, again = block.lq_rmsnorm_bwd(dY, H, W, need_dx=False, dW=dW, accumulate=True)
+    assert none is None and again is dW
+    assert torch.allclose(dW, 2 * first, rtol=2 * U32, atol=1e-5)
+    _, dW3 = block.lq_rmsnorm_bwd(dY, H, W)
+    assert np.array_equal(bits(dW3), bits(first))
+
+
+def test_backward_is_the_derivative():
+    """Central differences of sum(dY y) in float64 through the oracle's forward."""
+    M, K = 3, 40
+    t, w = inputs(M, K, torch.float32)
+    H, dY, W = t(), t(), w.to(DEV)
+    dX, dW = block.lq_rmsnorm_bwd(dY, H, W, 1e-3)
+    h, d, w64 = f64(H), f64(dY), f64(W)
+    f = lambda h, w: float((d * oblock.rmsnorm(h, w, 1e-3)[0]).sum())  # noqa: E731
+    for i, j in [(0, 0), (1, 17), (2, 39)]:
+        e = np.zeros((M, K))
+        e[i, j] = 1e-5
+        assert abs((f(h + e, w64) - f(h - e, w64)) / 2e-5 - float(dX[i, j])) < 1e-5
+        assert abs((f(h, w64 + e[i]) - f(h, w64 - e[i])) / 2e-5 - float(dW[j])) < 1e-5
+
+
+def test_no_rows():
+    W = torch.ones(64, device=DEV)
+    E = torch.empty((0, 64), device=DEV)
+    H, Y, q = block.lq_rmsnorm_fwd(E, W, R=E, format="fp8")
+    assert Y.shape == (0, 64) and q.codes.shape == (0, 64)
+    dX, dW = block.lq_rmsnorm_bwd(E, E, W)
+    assert dX.shape == (0, 64) and (dW == 0).all()
+    dW += 3
+    block.lq_rmsnorm_bwd(E, E, W, dW=dW, accumulate=True)
+    assert (dW == 3).all()
+
+
+def test_many_rows_past_one_launch():
+    """More rows than the launch has row groups: every workgroup takes several."""
+    M, K = (1 << 22) + 5, 4
+    X = torch.ones((M, K), dtype=torch.bfloat16, device=DEV)
+    X[:, 1] = 3.0
+    X[-1] = 0.0
+    _, Y, _ = block.lq_rmsnorm_fwd(X, torch.ones(K, device=DEV), 0.0 + 1e-12)
+    row = (X[0].float() / np.sqrt(3.0)).to(torch.bfloat16)
+    assert torch.equal(Y[:-1], row.expand(M - 1, K)) and (Y[-1] == 0).all()
