@@ -1,7 +1,7 @@
 /*
  * lq_block.h -- what stands around the adapted projections of a decoder block
- * on AMD Instinct MI355X (gfx950): the norm that feeds them and the adapters
- * of many requests beside one projection.  Part of
+ * on AMD Instinct MI355X (gfx950): the norm that feeds them, the adapters of
+ * many requests beside one projection, and the loss at the end.  Part of
  * liblq.so; the conventions of lq.h (row-major, contiguous device pointers
  * owned by the caller, work enqueued on the caller's stream, no allocation, no
  * synchronisation, negative lq_status on a refused call, lq_last_error()) hold
@@ -141,6 +141,40 @@ int lq_adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_p
 /* Workspace in bytes; 0 for M = 0 and for sizes that the call refuses. */
 size_t lq_adapters_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r,
                                   int32_t slots);
+
+/* ------------------------------------------------- loss of a head */
+
+/*
+ * Softmax cross entropy of a frozen head over a vocabulary of V = W0->N
+ * entries, from its input H, without keeping the logits z = c H W0^T
+ * (c = logit_scale; 1 / temperature for distillation):
+ *   lse[i]  = log sum over v of exp(z[i][v])
+ *   loss[i] = sum over the targets j of row i of p[i][j] (lse[i] - z[i][t[i][j]])
+ *   dH[i]   = d (sum over rows of w[i] loss[i]) / d H[i]
+ *           = w[i] c (P_i softmax(z[i]) - sum over j of p[i][j] e(t[i][j])) W0,
+ *             P_i = sum over j of p[i][j]
+ * One label per row: kt = 1, p NULL (weights 1).  A teacher's top kt entries:
+ * their indices and probabilities; the same index twice counts twice.
+ *   H        M x K bf16;  W0  dense bf16, V x K (no gradient: the base is frozen)
+ *   targets  device int32[M x kt]: a value outside [0, V) is no target; a row
+ *            without any has loss 0 and dH 0 whatever H and w hold there
+ *   p        optional device float[M x kt]
+ *   w        optional device float[M]: the row's share of the total (1 / rows for
+ *            a mean); NULL: 1.  Read for dH only
+ *   loss, lse  optional device float[M];  dH  optional M x K bf16
+ *   ws       lq_head_loss_workspace(M, V, K, kt, dH != NULL) bytes (more is not used)
+ * One of loss, lse and dH at least.  The logits of one piece of rows at a time
+ * are held in ws as float32; the gradient with respect to them enters its
+ * product with W0 as bf16.
+ * Requires K % 64 == 0, 64 <= K <= 16384, 1 <= V <= 2^20, 1 <= kt <= 128,
+ * M K < 2^31 and V K < 2^31; H, W0, dH and ws 16-byte aligned.  M = 0 is a no-op.
+ */
+int lq_head_loss(const void* H, int64_t M, const lq_weight* W0, const int32_t* targets,
+                 const float* p, int32_t kt, const float* w, float logit_scale, float* loss,
+                 float* lse, void* dH, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace in bytes; 0 for M = 0 and for sizes that the call refuses. */
+size_t lq_head_loss_workspace(int64_t M, int64_t V, int64_t K, int32_t kt, int32_t need_dh);
 
 #ifdef __cplusplus
 }

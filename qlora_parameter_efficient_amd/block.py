@@ -45,6 +45,9 @@ _SIGS = {
     "lq_adapters_bwd": (ctypes.c_int, [_vp, _vp, _i64, _PP, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
                                        _sz, _vp]),
     "lq_adapters_workspace_size": (_sz, [_i32, _i64, _i64, _i64, _i64, _i32]),
+    "lq_head_loss": (ctypes.c_int, [_vp, _i64, lq._WP, _vp, _vp, _i32, _vp, _f32, _vp, _vp, _vp, _vp,
+                                    _sz, _vp]),
+    "lq_head_loss_workspace": (_sz, [_i64, _i64, _i64, _i32, _i32]),
 }
 
 _lib = None
@@ -240,3 +243,44 @@ def lq_adapters_bwd(dY, X, pool: AdapterPool, rows, dX=None, T_saved=None, need_
     _check(lib().lq_adapters_bwd(gp, xp, M, ctypes.byref(q), ip, tp, dxp, op, ap, bp, int(accumulate),
                                  wp, wn, _raw_stream(dev)))
     return out, dA, dB
+
+
+# ------------------------------------------------------------------- head
+
+@functools.lru_cache(maxsize=1024)
+def lq_head_loss_workspace(M, V, K, kt, need_dh):
+    return int(lib().lq_head_loss_workspace(M, V, K, kt, int(need_dh)))
+
+
+def lq_head_loss(H, W0, targets, p=None, w=None, logit_scale=1.0, need_dh=True, dH=None, loss=None,
+                 lse=None, ws=None):
+    """(loss, lse, dH) of a frozen bf16 head W0 (V x K): targets int32, M (labels)
+    or M x kt; p: their weights (None: 1); w: the rows' shares of the total whose
+    gradient dH is (None: 1)."""
+    dev = H.get_device()
+    if dev != _current():
+        return _elsewhere(dev, lq_head_loss, H, W0, targets, p, w, logit_scale, need_dh, dH, loss, lse,
+                          ws)
+    if H.dim() != 2 or W0.dim() != 2:
+        raise ValueError("H and W0 are matrices")
+    M, (V, K) = H.shape[0], W0.shape
+    hp = _is(H, _BF16, (M, K), dev, "H")
+    s = LqWeightStruct()
+    s.kind, s.dtype, s.N, s.K = lq.LQ_WEIGHT_DENSE, lq.LQ_BF16, V, K
+    s.dense = _is(W0, _BF16, (V, K), dev, "W0")
+    kt = 1 if targets.dim() == 1 else targets.shape[1]
+    tp = _is(targets, _I32, (M,) if targets.dim() == 1 else (M, kt), dev, "targets")
+    pp = None if p is None else _is(p, _F32, targets.shape, dev, "p")
+    sp = None if w is None else _is(w, _F32, (M,), dev, "w")
+    if loss is None:
+        loss = H.new_empty((M,), dtype=_F32)
+    if lse is None:
+        lse = H.new_empty((M,), dtype=_F32)
+    if dH is None and need_dh:
+        dH = torch.empty_like(H)
+    lp, ep = _is(loss, _F32, (M,), dev, "loss"), _is(lse, _F32, (M,), dev, "lse")
+    dp = None if dH is None else _is(dH, _BF16, (M, K), dev, "dH")
+    ws, wp, wn = _workspace(ws, lq_head_loss_workspace, (M, V, K, kt, dH is not None), H, dev)
+    _check(lib().lq_head_loss(hp, M, ctypes.byref(s), tp, pp, kt, sp, logit_scale, lp, ep, dp, wp, wn,
+                              _raw_stream(dev)))
+    return loss, lse, dH

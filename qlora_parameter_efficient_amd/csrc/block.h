@@ -24,5 +24,10 @@ int adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool
                  const int32_t* rows, const float* T_saved, const void* dX_in, void* dX_out,
                  float* dA, float* dB, int accumulate, void* ws, hipStream_t st);
 
+size_t head_loss_ws(int64_t M, int64_t V, int64_t K, int32_t kt, bool need_dh);
+int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, const int32_t* t,
+              const float* p, int32_t kt, const float* w, float scale, float* loss, float* lse,
+              void* dH, void* ws, hipStream_t st);
+
 }  // namespace dispatch
 }  // namespace lq

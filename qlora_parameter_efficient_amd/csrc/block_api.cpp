@@ -73,6 +73,17 @@ int check_pool(const lq_adapter_pool* q, int64_t M, const int32_t* rows) {
   return rc;
 }
 
+// ------------------------------------------------------------------ head
+
+const char* broken_head_rule(int64_t M, int64_t V, int64_t K, int64_t kt) {
+  if (K % 64 || K < 64 || K > 16384) return "K must be a multiple of 64, at most 16384";
+  if (V < 1 || V > (1 << 20)) return "vocabulary outside [1, 2^20]";
+  if (kt < 1 || kt > 128) return "targets per row outside [1, 128]";
+  if (M < 0 || M >= kLim || M * K >= kLim || V * K >= kLim || M * kt >= kLim)
+    return "M*K, V*K and M*kt must be below 2^31 elements";
+  return nullptr;
+}
+
 }  // namespace
 
 extern "C" {
@@ -182,6 +193,41 @@ int lq_adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_p
           ws_bytes, need);
   return dispatch::adapters_bwd(dY, X, M, *pool, rows, T_saved, dX_in, dX_out, dA, dB, accumulate,
                                 ws, stream);
+}
+
+size_t lq_head_loss_workspace(int64_t M, int64_t V, int64_t K, int32_t kt, int32_t need_dh) {
+  return M <= 0 || broken_head_rule(M, V, K, kt)
+             ? 0
+             : dispatch::head_loss_ws(M, V, K, kt, need_dh != 0);
+}
+
+int lq_head_loss(const void* H, int64_t M, const lq_weight* W0, const int32_t* targets,
+                 const float* p, int32_t kt, const float* w, float logit_scale, float* loss,
+                 float* lse, void* dH, void* ws, size_t ws_bytes, hipStream_t stream) {
+  REQUIRE(W0 != nullptr, LQ_ERR_INVALID_ARG, "W0 is NULL");
+  REQUIRE(W0->kind == LQ_WEIGHT_DENSE && W0->dtype == LQ_BF16, LQ_ERR_UNSUPPORTED,
+          "the head is a dense bf16 weight");
+  const int64_t V = W0->N, K = W0->K;
+  REQUIRE(M >= 0 && V >= 1 && K >= 1, LQ_ERR_INVALID_ARG, "M=%lld V=%lld K=%lld", (long long)M,
+          (long long)V, (long long)K);
+  const char* rule = broken_head_rule(M, V, K, kt);
+  REQUIRE(!rule, LQ_ERR_UNSUPPORTED, "%s (M=%lld V=%lld K=%lld kt=%d)", rule, (long long)M,
+          (long long)V, (long long)K, (int)kt);
+  REQUIRE(std::isfinite(logit_scale), LQ_ERR_INVALID_ARG, "logit_scale = %g", (double)logit_scale);
+  REQUIRE(loss || lse || dH, LQ_ERR_INVALID_ARG, "nothing to compute: loss, lse and dH are NULL");
+  if (M == 0) return LQ_OK;
+  REQUIRE(H && W0->dense && targets, LQ_ERR_INVALID_ARG, "H, W0's data or targets is NULL");
+  int rc;
+  if ((rc = check_to(H, 16, "H")) || (rc = check_to(W0->dense, 16, "W0")) ||
+      (rc = check_to(dH, 16, "dH")) || (rc = check_to(ws, 16, "ws")) ||
+      (rc = check_to(targets, 4, "targets")) || (rc = check_to(p, 4, "p")) ||
+      (rc = check_to(w, 4, "w")) || (rc = check_to(loss, 4, "loss")) || (rc = check_to(lse, 4, "lse")))
+    return rc;
+  const size_t need = dispatch::head_loss_ws(M, V, K, kt, dH != nullptr);
+  REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
+          ws_bytes, need);
+  return dispatch::head_loss(H, M, V, K, W0->dense, targets, p, kt, w, logit_scale, loss, lse, dH,
+                             ws, stream);
 }
 
 }  // extern "C"

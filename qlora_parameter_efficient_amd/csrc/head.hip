@@ -1,0 +1,602 @@
+// Loss of a frozen large-vocabulary head and the gradient of its input
+// (lq_head_loss).
+//
+//   z = c H W^T,  lse_i = log sum_v exp z_iv,  loss_i = sum_j p_ij (lse_i - z_i,t_ij)
+//   D = w_i c (P_i softmax(z_i) - sum_j p_ij e(t_ij)),  P_i = sum_j p_ij,   dH = D W
+//
+// Two products of 2 M V K operations bound it; the softmax between them costs
+// memory traffic only.  A piece of rows at a time: its logits as float32 (a bf16
+// logit of 16 would be off by 0.03, three percent of its probability) and then D as
+// bf16 (2^-8 of each entry, as the outputs are) lie in the workspace.  Kept
+// logits are cheaper than formed ones: 12 bytes of traffic per logit against 2 K
+// operations.
+//
+// Products.  Four waves own a 256 (weight side: v or k) x 64 JM (rows m) tile,
+// wave (wi, wj) its 128 x 32 JM block, in 32 x 32 x 16 products, the weight side
+// being the MFMA rows, so that a lane holds four consecutive outputs of a row.
+// Steps of 64 of the reduction, both operands straight from global memory into
+// one of two LDS stages (chunk swizzles as below), four 16-wide substeps whose
+// operands are read one substep ahead, across the barrier too: it stands before
+// the last substep's products, when every wave holds its last operands and the
+// next stage has landed, and behind it go the next step's first reads and the
+// loads of the step after that.
+//   row tiles (H and D; W in z): rows of 128 bytes, chunk c of row x at
+//     c ^ (x & 7) ^ (x >> 3 & 1)
+//   W in dH: 64 reduction rows v of 512 bytes, chunk c of row v at
+//     c ^ 2 (v & 3) ^ 8 (c >> 1 & 1), operands by the transposing LDS read
+#include <type_traits>
+
+#include "block.h"
+#include "mx_tile.h"
+
+namespace lq {
+namespace {
+
+constexpr int kTI = 256;                    // weight side of a tile
+constexpr int kStep = 64;                   // reduction per step
+constexpr int kWTile = kTI * kStep * 2;     // weight tile of a step
+constexpr int kThreads = 256;
+
+struct ProdParams {
+  const uint16_t* P;  // rows x KR (H or D)
+  const uint16_t* Q;  // z: W, NI x KR.  dH: W, KV x NI (KV <= KR rows)
+  float* Z;           // z: rows x ldz; dH, split: splits x rows x NI
+  uint16_t* Y;        // dH, not split: rows x NI
+  int32_t M, NI, KR, KV, ldz;
+  float scale;
+  int32_t ti, tj, splits, ksteps;
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 read_turned(uint32_t addr) {
+  typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)addr));
+}
+
+// physical chunk of logical chunk c in reduction row v of the turned weight
+// tile, and back
+__device__ __forceinline__ int tphys(int c, int v) { return c ^ (2 * (v & 3)) ^ (8 * ((c >> 1) & 1)); }
+__device__ __forceinline__ int tlogical(int p, int v) {
+  return p ^ (2 * (v & 3)) ^ (8 * (((p >> 1) & 1) ^ (v & 1)));
+}
+
+// 16 bytes per lane from base + off to LDS at lds + 16 lane; the kernel waits
+// for them itself
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1"
+      :
+      : "v"(off), "s"(base), "s"(lds)
+      : "memory", "m0");
+}
+
+// TR: the product dH = D W (W read turned); else z = c H W^T.  JM: 32-row
+// blocks per wave.
+template <bool TR, int JM>
+__global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
+  constexpr int TJ = 64 * JM, kPTile = TJ * kStep * 2, kStage = kWTile + kPTile;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave & 1, wj = wave >> 1;
+  const int h = lane >> 5, l32 = lane & 31;
+
+  // Workgroup b runs on XCD b % 8: each XCD has a contiguous range of the
+  // (split, tile) list, in groups of four row tiles that share weight rows
+  const int ntiles = p.ti * p.tj;
+  const int w = xcd_tile(blockIdx.x, ntiles * p.splits);
+  const int split = w / ntiles, t = w - split * ntiles;
+  constexpr int GJ = 4;
+  const int grp = t / (GJ * p.ti), in = t - grp * GJ * p.ti;
+  const int gj = p.tj - grp * GJ < GJ ? p.tj - grp * GJ : GJ;
+  const int i0 = (in / gj) * kTI, j0 = (grp * GJ + in % gj) * TJ;
+  const int NI = p.NI, KR = p.KR, M = p.M;
+  const int steps = KR / kStep;
+  const int ka = split * p.ksteps;
+  const int kb = ka + p.ksteps < steps ? ka + p.ksteps : steps;
+
+  const uint32_t sbase = mx_lds_addr(smem);
+  uint32_t poff[2 * JM], qoff[8];
+#pragma unroll
+  for (int u = 0; u < 2 * JM; ++u) {
+    const int row = 16 * JM * wave + 8 * u + (lane >> 3);
+    const int m = j0 + row < M ? j0 + row : M - 1;
+    poff[u] = ((uint32_t)m * KR + 8 * ((lane & 7) ^ mx_swz128(row))) * 2;
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    if (!TR) {
+      const int row = 64 * wave + 8 * u + (lane >> 3);
+      const int n = i0 + row < NI ? i0 + row : NI - 1;
+      qoff[u] = ((uint32_t)n * KR + 8 * ((lane & 7) ^ mx_swz128(row))) * 2;
+    } else {
+      const int v = 16 * wave + 2 * u + (lane >> 5);
+      const int c = i0 + 8 * tlogical(lane & 31, v);
+      qoff[u] = ((uint32_t)v * NI + (c < NI ? c : NI - 8)) * 2;
+    }
+  }
+  const char* pbase = reinterpret_cast<const char*>(p.P);
+  const char* qbase = reinterpret_cast<const char*>(p.Q);
+  // load u (0 .. 2 JM + 7) of step kt into stage b
+  auto issue = [&](int kt, int b, int u) {
+    const uint32_t st = sbase + b * kStage;
+    if (u < 8) {
+      if (!TR) {
+        dma16(qbase + (int64_t)kt * kStep * 2, qoff[u], st + (64 * wave + 8 * u) * 128);
+      } else {
+        uint32_t off = qoff[u];
+        const int past = kt * kStep + kStep - p.KV;  // rows of the last step past W's end: its last row
+        if (past > 0) {
+          const int v = 16 * wave + 2 * u + (lane >> 5), over = v + past - (kStep - 1);
+          off -= over > 0 ? (uint32_t)over * NI * 2 : 0u;
+        }
+        dma16(qbase + (int64_t)kt * kStep * NI * 2, off, st + (16 * wave + 2 * u) * 512);
+      }
+    } else {
+      dma16(pbase + (int64_t)kt * kStep * 2, poff[u - 8],
+            st + kWTile + (16 * JM * wave + 8 * (u - 8)) * 128);
+    }
+  };
+
+  const int sw = mx_swz128(l32);
+  const uint32_t prow = (uint32_t)((32 * JM * wj + l32) * 128);
+  const uint32_t qrow = (uint32_t)((128 * wi + l32) * 128);
+  uint32_t cx[4], qtr[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) cx[s] = (uint32_t)(((2 * s + h) ^ sw) << 4);
+  if (TR) {
+    const int gc = l32 & 15, half = l32 >> 4, vlo = gc >> 2;
+#pragma unroll
+    for (int ns = 0; ns < 4; ++ns) {
+      const int col = 128 * wi + 32 * ns + 16 * half + 4 * (gc & 3);
+      qtr[ns] = (uint32_t)((8 * h + vlo) * 512 + tphys(col >> 3, vlo) * 16 + (col & 7) * 2);
+    }
+  }
+  auto load_frags = [&](uint32_t st, int s, u32x4 (&wf)[4], u32x4 (&xf)[JM]) {
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) xf[ms] = mx_read16(st + kWTile + prow + ms * 32 * 128 + cx[s]);
+#pragma unroll
+    for (int ns = 0; ns < 4; ++ns) {
+      if (!TR) {
+        wf[ns] = mx_read16(st + qrow + ns * 32 * 128 + cx[s]);
+      } else {
+        const uint32_t a = st + (uint32_t)(16 * s * 512) + qtr[ns];
+        const u32x2 lo = read_turned(a), hi = read_turned(a + 4 * 512);
+        wf[ns] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+    }
+  };
+
+  f32x16 acc[4][JM];
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < JM; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
+  u32x4 wf[2][4], xf[2][JM];
+  constexpr int kLoads = 8 + 2 * JM;
+
+  auto step = [&](int kt, auto stage) {
+    constexpr int B = decltype(stage)::value;
+    const uint32_t st = sbase + B * kStage;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int c = s & 1;
+      if (s < 3) {
+        load_frags(st, s + 1, wf[c ^ 1], xf[c ^ 1]);
+      } else {
+        // every wave holds its last operands of this stage; the next has landed
+        mx_wait_loads();
+        __syncthreads();
+        load_frags(sbase + (B ^ 1) * kStage, 0, wf[0], xf[0]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const bool more = s == 3 && kt + 2 < kb;
+#pragma unroll
+      for (int ns = 0; ns < 4; ++ns) {
+#pragma unroll
+        for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(wf[c][ns], xf[c][ms], acc[ns][ms]);
+        if (s == 3) {
+          if (more)
+#pragma unroll
+            for (int u = ns * kLoads / 4; u < (ns + 1) * kLoads / 4; ++u) issue(kt + 2, B, u);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  if (ka < kb) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) issue(ka, 0, u);
+    mx_wait_loads();
+    __syncthreads();
+    if (ka + 1 < kb)
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) issue(ka + 1, 1, u);
+    load_frags(sbase, 0, wf[0], xf[0]);
+    int kt = ka;
+    for (; kt + 1 < kb; kt += 2) {
+      step(kt, I0{});
+      step(kt + 1, I1{});
+    }
+    if (kt < kb) step(kt, I0{});
+  }
+
+  if (!TR || p.splits > 1) {
+    // float32: four consecutive outputs per lane and store
+    const int ld = TR ? NI : p.ldz;
+    float* out = p.Z + (TR ? (int64_t)split * M * NI : 0);
+#pragma unroll
+    for (int ms = 0; ms < JM; ++ms) {
+      const int m = j0 + 32 * JM * wj + 32 * ms + l32;
+      if (m >= M) continue;
+      float* row = out + (int64_t)m * ld;
+#pragma unroll
+      for (int ns = 0; ns < 4; ++ns)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int i = i0 + 128 * wi + 32 * ns + 8 * q + 4 * h;
+          const f32x16& x = acc[ns][ms];
+          if (i < ld)  // both are multiples of 4
+            *reinterpret_cast<f32x4*>(row + i) =
+                TR ? f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]}
+                   : f32x4{p.scale * x[4 * q], p.scale * x[4 * q + 1], p.scale * x[4 * q + 2],
+                           p.scale * x[4 * q + 3]};
+        }
+    }
+    return;
+  }
+  // bf16: the tile through LDS (row j of 512 bytes, chunk c at c ^ (j & 15)), whole
+  // output lines from there
+  __syncthreads();
+#pragma unroll
+  for (int ms = 0; ms < JM; ++ms) {
+    const int j = 32 * JM * wj + 32 * ms + l32;
+#pragma unroll
+    for (int ns = 0; ns < 4; ++ns)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = 128 * wi + 32 * ns + 8 * q + 4 * h;
+        const f32x16& x = acc[ns][ms];
+        typedef __attribute__((address_space(3))) u32x2* lds_ptr;
+        *(lds_ptr)(uintptr_t)(sbase + (uint32_t)(j * 512 + (((i >> 3) ^ (j & 15)) * 16) + (i & 7) * 2)) =
+            u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])};
+      }
+  }
+  __syncthreads();
+  const int cl = tid & 31;
+#pragma unroll 4
+  for (int it = 0; it < 8 * JM; ++it) {
+    const int j = 8 * it + (tid >> 5);
+    const u32x4 v = mx_read16(sbase + (uint32_t)(j * 512 + ((cl ^ (j & 15)) << 4)));
+    if (j0 + j < M && i0 + 8 * cl < NI)
+      *reinterpret_cast<u32x4*>(p.Y + (int64_t)(j0 + j) * NI + i0 + 8 * cl) = v;
+  }
+}
+
+// ---------------------------------------------------------------- softmax
+// One workgroup per row: its maximum, its sum of exponentials, the loss, and D.
+// The row stays in registers from its one read to D's store (kKeep values per
+// thread; longer rows are read again).
+
+struct RowParams {
+  const float* Z;     // rows x ldz
+  const int32_t* t;   // rows x kt
+  const float* pt;    // rows x kt or NULL
+  const float* w;     // rows or NULL
+  float* loss;
+  float* lse;
+  uint16_t* D;        // rows x ldd or NULL
+  int32_t V, ldz, ldd, kt;
+  float scale;
+};
+
+constexpr int kRowThreads = 1024;
+constexpr int kMaxTargets = 128;
+
+template <bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* sh) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const float y = __shfl_xor(v, o);
+    v = MAX ? fmaxf(v, y) : v + y;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = sh[0];
+#pragma unroll
+  for (int i = 1; i < kRowThreads / 64; ++i) v = MAX ? fmaxf(v, sh[i]) : v + sh[i];
+  return v;
+}
+
+// Q: groups of four values per thread that stay in registers
+template <int Q>
+__global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
+  __shared__ float sh[kRowThreads / 64];
+  __shared__ int tgt[kMaxTargets];
+  __shared__ float wgt[kMaxTargets], zt[kMaxTargets];
+  const int tid = threadIdx.x, V = p.V;
+  const int64_t row = blockIdx.x;
+  const float* z = p.Z + row * p.ldz;
+  if (tid < p.kt) {
+    const int t = p.t[row * p.kt + tid];
+    const bool ok = t >= 0 && t < V;
+    tgt[tid] = ok ? t : -1;
+    wgt[tid] = ok ? (p.pt ? p.pt[row * p.kt + tid] : 1.0f) : 0.0f;
+    zt[tid] = ok ? z[t] : 0.0f;
+  }
+  const int groups = (V + 3) / 4;
+  const float ninf = -__builtin_inff();
+  f32x4 x[Q];
+  auto load = [&](int g) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(z + 4 * g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = 4 * g + k < V ? v[k] : ninf;
+    return v;
+  };
+  float top = ninf;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int g = tid + kRowThreads * i;
+    x[i] = f32x4{ninf, ninf, ninf, ninf};
+    if (g < groups) x[i] = load(g);
+  }
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, x[i][k]);
+  for (int g = tid + kRowThreads * Q; g < groups; g += kRowThreads) {
+    const f32x4 v = load(g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, v[k]);
+  }
+  top = row_reduce<true>(top, sh);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[i][k] = __expf(x[i][k] - top);
+      sum += x[i][k];
+    }
+  for (int g = tid + kRowThreads * Q; g < groups; g += kRowThreads) {
+    const f32x4 v = load(g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += __expf(v[k] - top);
+  }
+  sum = row_reduce<false>(sum, sh);
+  const float lse = top + logf(sum);
+  // the targets: every thread adds the few of them in order
+  float total = 0.0f, loss = 0.0f;
+  bool any = false;
+  for (int j = 0; j < p.kt; ++j) {
+    const bool ok = tgt[j] >= 0;
+    any |= ok;
+    total += wgt[j];
+    loss += ok ? wgt[j] * (lse - zt[j]) : 0.0f;
+  }
+  if (tid == 0) {
+    if (p.loss) p.loss[row] = loss;
+    if (p.lse) p.lse[row] = lse;
+  }
+  if (!p.D) return;
+  uint16_t* d = p.D + row * p.ldd;
+  const float share = any ? (p.w ? p.w[row] : 1.0f) * p.scale : 0.0f;
+  const float f = share * total / sum;
+  auto store = [&](int g, f32x4 e) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = any ? e[k] * f : 0.0f;
+    *reinterpret_cast<u32x2*>(d + 4 * g) = u32x2{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3])};
+  };
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int g = tid + kRowThreads * i;
+    if (g < p.ldd / 4) store(g, x[i]);
+  }
+  for (int g = tid + kRowThreads * Q; g < p.ldd / 4; g += kRowThreads) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (g < groups) {
+      v = load(g);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __expf(v[k] - top);
+    }
+    store(g, v);
+  }
+  // the targets' entries, from float32: by the first of several with one index
+  __syncthreads();
+  if (tid < p.kt && tgt[tid] >= 0) {
+    float q = 0.0f;
+    bool first = true;
+    for (int j = 0; j < p.kt; ++j) {
+      if (tgt[j] != tgt[tid]) continue;
+      if (j < tid) first = false;
+      q += wgt[j];
+    }
+    if (first) d[tgt[tid]] = f32_to_bf16(share * (total * (__expf(zt[tid] - top) / sum) - q));
+  }
+}
+
+// out (bf16) = the splits' sums in order; n % 8 == 0
+__global__ __launch_bounds__(256) void head_sum_kernel(const float* part, uint16_t* out, int64_t n,
+                                                       int splits) {
+  const int64_t e = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (e >= n) return;
+  f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+  for (int k = 0; k < splits; ++k) {
+    const f32x4* q = reinterpret_cast<const f32x4*>(part + k * n + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] += q[0][i];
+      b[i] += q[1][i];
+    }
+  }
+  *reinterpret_cast<u32x4*>(out + e) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                             pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+}
+
+// ---------------------------------------------------------------- host
+
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+constexpr int kCUs = 256;
+
+// 32-row blocks per wave: tiles of 64, 128 or 256 rows
+int tile_jm(int64_t rows) { return rows <= 64 ? 1 : rows <= 128 ? 2 : 4; }
+
+struct Shape {
+  int jm;
+  int64_t ti, tj, splits, ksteps;
+};
+
+Shape z_shape(int64_t rows, int64_t V, int64_t K) {
+  Shape s;
+  s.jm = tile_jm(rows);
+  s.ti = cdiv(V, kTI);
+  s.tj = cdiv(rows, 64 * s.jm);
+  s.splits = 1;
+  s.ksteps = K / kStep;
+  return s;
+}
+
+// dH: fewer tiles than compute units split the reduction over V
+Shape dh_shape(int64_t rows, int64_t V, int64_t K) {
+  Shape s;
+  s.jm = tile_jm(rows);
+  s.ti = cdiv(K, kTI);
+  s.tj = cdiv(rows, 64 * s.jm);
+  const int64_t steps = cdiv(V, kStep), fill = kCUs / (s.ti * s.tj), most = cdiv(steps, 8);
+  s.splits = fill < 1 ? 1 : fill < most ? fill : most;
+  s.ksteps = cdiv(steps, s.splits);
+  s.splits = cdiv(steps, s.ksteps);
+  return s;
+}
+
+// Rows of a piece: at most 2^28 logits (1 GiB of float32), whole 256-row tiles
+int64_t piece_rows(int64_t M, int64_t V) {
+  const int64_t most = ((int64_t)1 << 28) / V / 256 * 256;
+  const int64_t rows = most < 256 ? 256 : most;
+  return M < rows ? M : rows;
+}
+
+int64_t ld_of(int64_t V) { return cdiv(V, 64) * 64; }
+
+struct Layout {
+  size_t z, d, part, end;
+};
+Layout layout(int64_t M, int64_t V, int64_t K, bool need_dh) {
+  const int64_t rows = piece_rows(M, V);
+  Layout l;
+  l.z = 0;
+  l.d = up256((size_t)rows * ld_of(V) * 4);
+  l.part = l.d + (need_dh ? up256((size_t)rows * ld_of(V) * 2) : 0);
+  l.end = l.part;
+  if (need_dh) {
+    // the last piece may have fewer rows and more splits
+    const int64_t last = M - (cdiv(M, rows) - 1) * rows;
+    size_t most = 0;
+    for (int64_t n : {rows, last}) {
+      const Shape s = dh_shape(n, V, K);
+      const size_t b = s.splits > 1 ? (size_t)s.splits * n * K * 4 : 0;
+      if (b > most) most = b;
+    }
+    l.end += up256(most);
+  }
+  return l;
+}
+
+template <bool TR>
+int launch_product(const ProdParams& p, int jm, hipStream_t st) {
+  const dim3 g((unsigned)(p.ti * p.tj * p.splits)), b(kThreads);
+  const auto kernel = jm == 1   ? head_product_kernel<TR, 1>
+                      : jm == 2 ? head_product_kernel<TR, 2>
+                                : head_product_kernel<TR, 4>;
+  hipLaunchKernelGGL(kernel, g, b, 0, st, p);
+  return hip_fail(hipGetLastError(), TR ? "head dH launch" : "head logits launch");
+}
+
+}  // namespace
+
+namespace dispatch {
+
+size_t head_loss_ws(int64_t M, int64_t V, int64_t K, int32_t kt, bool need_dh) {
+  (void)kt;
+  return layout(M, V, K, need_dh).end;
+}
+
+int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, const int32_t* t,
+              const float* pt, int32_t kt, const float* w, float scale, float* loss, float* lse,
+              void* dH, void* ws, hipStream_t st) {
+  const Layout l = layout(M, V, K, dH != nullptr);
+  const int64_t piece = piece_rows(M, V), ld = ld_of(V);
+  char* base = (char*)ws;
+  for (int64_t m0 = 0; m0 < M; m0 += piece) {
+    const int64_t rows = M - m0 < piece ? M - m0 : piece;
+    ProdParams p{};
+    const Shape z = z_shape(rows, V, K);
+    p.P = (const uint16_t*)H + m0 * K;
+    p.Q = (const uint16_t*)W;
+    p.Z = (float*)(base + l.z);
+    p.M = (int32_t)rows;
+    p.NI = (int32_t)V;
+    p.KR = (int32_t)K;
+    p.KV = (int32_t)K;
+    p.ldz = (int32_t)ld;
+    p.scale = scale;
+    p.ti = (int32_t)z.ti;
+    p.tj = (int32_t)z.tj;
+    p.splits = 1;
+    p.ksteps = (int32_t)z.ksteps;
+    int rc = launch_product<false>(p, z.jm, st);
+    if (rc) return rc;
+    RowParams r;
+    r.Z = p.Z;
+    r.t = t + m0 * kt;
+    r.pt = pt ? pt + m0 * kt : nullptr;
+    r.w = w ? w + m0 : nullptr;
+    r.loss = loss ? loss + m0 : nullptr;
+    r.lse = lse ? lse + m0 : nullptr;
+    r.D = dH ? (uint16_t*)(base + l.d) : nullptr;
+    r.V = (int32_t)V;
+    r.ldz = r.ldd = (int32_t)ld;
+    r.kt = kt;
+    r.scale = scale;
+    const auto kernel = ld <= 4096 * 4    ? head_row_kernel<4>
+                        : ld <= 4096 * 8  ? head_row_kernel<8>
+                        : ld <= 4096 * 13 ? head_row_kernel<13>
+                                          : head_row_kernel<16>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(kRowThreads), 0, st, r);
+    if ((rc = hip_fail(hipGetLastError(), "head softmax launch"))) return rc;
+    if (!dH) continue;
+    const Shape s = dh_shape(rows, V, K);
+    ProdParams q{};
+    q.P = (const uint16_t*)(base + l.d);
+    q.Q = (const uint16_t*)W;
+    q.Z = (float*)(base + l.part);
+    q.Y = (uint16_t*)dH + m0 * K;
+    q.M = (int32_t)rows;
+    q.NI = (int32_t)K;
+    q.KR = (int32_t)ld;
+    q.KV = (int32_t)V;
+    q.ti = (int32_t)s.ti;
+    q.tj = (int32_t)s.tj;
+    q.splits = (int32_t)s.splits;
+    q.ksteps = (int32_t)s.ksteps;
+    if ((rc = launch_product<true>(q, s.jm, st))) return rc;
+    if (s.splits > 1) {
+      const int64_t n = rows * K;
+      hipLaunchKernelGGL(head_sum_kernel, dim3((unsigned)cdiv(n, 2048)), dim3(256), 0, st,
+                         (const float*)q.Z, q.Y, n, (int)s.splits);
+      if ((rc = hip_fail(hipGetLastError(), "head sums launch"))) return rc;
+    }
+  }
+  return LQ_OK;
+}
+
+}  // namespace dispatch
+}  // namespace lq
