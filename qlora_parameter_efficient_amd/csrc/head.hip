@@ -119,25 +119,29 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
   }
   const char* pbase = reinterpret_cast<const char*>(p.P);
   const char* qbase = reinterpret_cast<const char*>(p.Q);
-  // load u (0 .. 2 JM + 7) of step kt into stage b
-  auto issue = [&](int kt, int b, int u) {
+  const int64_t qstep = TR ? (int64_t)kStep * NI * 2 : kStep * 2;  // bytes from step to step
+  // load u (0 .. 2 JM + 7) of a step into stage b; qb, pb: the step's operands;
+  // past: rows of the step beyond W's last (which they read instead)
+  auto issue = [&](const char* qb, const char* pb, int past, int b, int u) {
     const uint32_t st = sbase + b * kStage;
-    if (u < 8) {
-      if (!TR) {
-        dma16(qbase + (int64_t)kt * kStep * 2, qoff[u], st + (64 * wave + 8 * u) * 128);
-      } else {
-        uint32_t off = qoff[u];
-        const int past = kt * kStep + kStep - p.KV;  // rows of the last step past W's end: its last row
-        if (past > 0) {
-          const int v = 16 * wave + 2 * u + (lane >> 5), over = v + past - (kStep - 1);
-          off -= over > 0 ? (uint32_t)over * NI * 2 : 0u;
-        }
-        dma16(qbase + (int64_t)kt * kStep * NI * 2, off, st + (16 * wave + 2 * u) * 512);
-      }
+    if (u >= 8) {
+      dma16(pb, poff[u - 8], st + kWTile + (16 * JM * wave + 8 * (u - 8)) * 128);
+    } else if (!TR) {
+      dma16(qb, qoff[u], st + (64 * wave + 8 * u) * 128);
     } else {
-      dma16(pbase + (int64_t)kt * kStep * 2, poff[u - 8],
-            st + kWTile + (16 * JM * wave + 8 * (u - 8)) * 128);
+      uint32_t off = qoff[u];
+      if (past > 0) {
+        const int over = 16 * wave + 2 * u + (lane >> 5) + past - (kStep - 1);
+        off -= over > 0 ? (uint32_t)over * NI * 2 : 0u;
+      }
+      dma16(qb, off, st + (16 * wave + 2 * u) * 512);
     }
+  };
+  auto issue_all = [&](int kt, int b) {
+#pragma unroll
+    for (int u = 0; u < 8 + 2 * JM; ++u)
+      issue(qbase + kt * qstep, pbase + (int64_t)kt * kStep * 2,
+            TR ? kt * kStep + kStep - p.KV : 0, b, u);
   };
 
   const int sw = mx_swz128(l32);
@@ -154,18 +158,17 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
       qtr[ns] = (uint32_t)((8 * h + vlo) * 512 + tphys(col >> 3, vlo) * 16 + (col & 7) * 2);
     }
   }
-  auto load_frags = [&](uint32_t st, int s, u32x4 (&wf)[4], u32x4 (&xf)[JM]) {
-#pragma unroll
-    for (int ms = 0; ms < JM; ++ms) xf[ms] = mx_read16(st + kWTile + prow + ms * 32 * 128 + cx[s]);
-#pragma unroll
-    for (int ns = 0; ns < 4; ++ns) {
-      if (!TR) {
-        wf[ns] = mx_read16(st + qrow + ns * 32 * 128 + cx[s]);
-      } else {
-        const uint32_t a = st + (uint32_t)(16 * s * 512) + qtr[ns];
-        const u32x2 lo = read_turned(a), hi = read_turned(a + 4 * 512);
-        wf[ns] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-      }
+  // operand read i of substep s (JM + 4: the activation side's, the weight side's)
+  constexpr int kReads = JM + 4;
+  auto load_frag = [&](uint32_t st, int s, int i, u32x4 (&wf)[4], u32x4 (&xf)[JM]) {
+    if (i < JM) {
+      xf[i] = mx_read16(st + kWTile + prow + i * 32 * 128 + cx[s]);
+    } else if (!TR) {
+      wf[i - JM] = mx_read16(st + qrow + (i - JM) * 32 * 128 + cx[s]);
+    } else {
+      const uint32_t a = st + (uint32_t)(16 * s * 512) + qtr[i - JM];
+      const u32x2 lo = read_turned(a), hi = read_turned(a + 4 * 512);
+      wf[i - JM] = u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
   };
 
@@ -178,53 +181,68 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
       for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
   u32x4 wf[2][4], xf[2][JM];
   constexpr int kLoads = 8 + 2 * JM;
+  // products among which a substep's reads go
+  constexpr int kSpread = JM == 1 ? 3 : 2 * JM + JM / 2;
 
-  auto step = [&](int kt, auto stage) {
+  // One step on stage B.  STEADY: step kt + 2 exists and is whole, and no branch
+  // parts the products; else it is loaded at once, if it exists.
+  auto step = [&](int kt, auto stage, auto steady) {
     constexpr int B = decltype(stage)::value;
-    const uint32_t st = sbase + B * kStage;
+    constexpr bool STEADY = decltype(steady)::value;
+    const char* qb = qbase + (kt + 2) * qstep;
+    const char* pb = pbase + (int64_t)(kt + 2) * kStep * 2;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int c = s & 1;
-      if (s < 3) {
-        load_frags(st, s + 1, wf[c ^ 1], xf[c ^ 1]);
-      } else {
+      const uint32_t st = sbase + (s < 3 ? B : B ^ 1) * kStage;
+      if (s == 3) {
         // every wave holds its last operands of this stage; the next has landed
         mx_wait_loads();
         __syncthreads();
-        load_frags(sbase + (B ^ 1) * kStage, 0, wf[0], xf[0]);
+        if (!STEADY && kt + 2 < kb) issue_all(kt + 2, B);
       }
       __builtin_amdgcn_sched_barrier(0);
-      const bool more = s == 3 && kt + 2 < kb;
+      // one read behind each product, from the first on: a burst of reads fills
+      // the LDS queue and holds back the products behind it
 #pragma unroll
-      for (int ns = 0; ns < 4; ++ns) {
+      for (int k = 0; k < 4 * JM; ++k) {
+        acc[k / JM][k % JM] = mfma32(wf[c][k / JM], xf[c][k % JM], acc[k / JM][k % JM]);
 #pragma unroll
-        for (int ms = 0; ms < JM; ++ms) acc[ns][ms] = mfma32(wf[c][ns], xf[c][ms], acc[ns][ms]);
-        if (s == 3) {
-          if (more)
+        for (int i = k * kReads / kSpread; i < (k + 1) * kReads / kSpread && i < kReads; ++i)
+          load_frag(st, (s + 1) & 3, i, wf[c ^ 1], xf[c ^ 1]);
+        if (STEADY && s == 3) {
 #pragma unroll
-            for (int u = ns * kLoads / 4; u < (ns + 1) * kLoads / 4; ++u) issue(kt + 2, B, u);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int u = k * kLoads / (4 * JM); u < (k + 1) * kLoads / (4 * JM); ++u)
+            issue(qb, pb, 0, B, u);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  if (ka < kb) {
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) issue(ka, 0, u);
+  using Yes = std::integral_constant<bool, true>;
+  using No = std::integral_constant<bool, false>;
+  {
+    issue_all(ka, 0);
     mx_wait_loads();
     __syncthreads();
-    if (ka + 1 < kb)
+    if (ka + 1 < kb) issue_all(ka + 1, 1);
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) issue(ka + 1, 1, u);
-    load_frags(sbase, 0, wf[0], xf[0]);
+    for (int i = 0; i < kReads; ++i) load_frag(sbase, 0, i, wf[0], xf[0]);
+    // the last step of W's rows may be short
+    const int whole = TR && kb * kStep > p.KV ? kb - 1 : kb;
     int kt = ka;
-    for (; kt + 1 < kb; kt += 2) {
-      step(kt, I0{});
-      step(kt + 1, I1{});
+    for (; kt + 3 < whole; kt += 2) {
+      step(kt, I0{}, Yes{});
+      step(kt + 1, I1{}, Yes{});
     }
-    if (kt < kb) step(kt, I0{});
+#pragma unroll 1
+    for (; kt + 1 < kb; kt += 2) {
+      step(kt, I0{}, No{});
+      step(kt + 1, I1{}, No{});
+    }
+    if (kt < kb) step(kt, I0{}, No{});
   }
 
   if (!TR || p.splits > 1) {
