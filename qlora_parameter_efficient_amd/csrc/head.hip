@@ -40,11 +40,12 @@ constexpr int kThreads = 256;
 struct ProdParams {
   const uint16_t* P;  // rows x KR (H or D)
   const uint16_t* Q;  // z: W, NI x KR.  dH: W, KV x NI (KV <= KR rows)
-  float* Z;           // z: rows x ldz; dH, split: splits x rows x NI
+  float* Z;           // z: splits x rows x ldz; dH, split: splits x rows x NI
   uint16_t* Y;        // dH, not split: rows x NI
   int32_t M, NI, KR, KV, ldz;
   float scale;
   int32_t ti, tj, splits, ksteps;
+  int32_t i_first;    // first output column
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
   constexpr int GJ = 4;
   const int grp = t / (GJ * p.ti), in = t - grp * GJ * p.ti;
   const int gj = p.tj - grp * GJ < GJ ? p.tj - grp * GJ : GJ;
-  const int i0 = (in / gj) * kTI, j0 = (grp * GJ + in % gj) * TJ;
+  const int i0 = p.i_first + (in / gj) * kTI, j0 = (grp * GJ + in % gj) * TJ;
   const int NI = p.NI, KR = p.KR, M = p.M;
   const int steps = KR / kStep;
   const int ka = split * p.ksteps;
@@ -137,9 +138,10 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
       dma16(qb, off, st + (16 * wave + 2 * u) * 512);
     }
   };
-  auto issue_all = [&](int kt, int b) {
+  // loads u0 .. u1 - 1 of step kt
+  auto issue_some = [&](int kt, int b, int u0, int u1) {
 #pragma unroll
-    for (int u = 0; u < 8 + 2 * JM; ++u)
+    for (int u = u0; u < u1; ++u)
       issue(qbase + kt * qstep, pbase + (int64_t)kt * kStep * 2,
             TR ? kt * kStep + kStep - p.KV : 0, b, u);
   };
@@ -180,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
   u32x4 wf[2][4], xf[2][JM];
-  constexpr int kLoads = 8 + 2 * JM;
+  constexpr int kLoads = 8 + 2 * JM, kHalf = kLoads / 2;
   // products among which a substep's reads go
   constexpr int kSpread = JM == 1 ? 3 : 2 * JM + JM / 2;
 
@@ -199,8 +201,9 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
         // every wave holds its last operands of this stage; the next has landed
         mx_wait_loads();
         __syncthreads();
-        if (!STEADY && kt + 2 < kb) issue_all(kt + 2, B);
+        if (!STEADY && kt + 2 < kb) issue_some(kt + 2, B, 0, kHalf);
       }
+      if (!STEADY && s == 0 && kt + 1 < kb) issue_some(kt + 1, B ^ 1, kHalf, kLoads);
       __builtin_amdgcn_sched_barrier(0);
       // one read behind each product, from the first on: a burst of reads fills
       // the LDS queue and holds back the products behind it
@@ -212,8 +215,13 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
           load_frag(st, (s + 1) & 3, i, wf[c ^ 1], xf[c ^ 1]);
         if (STEADY && s == 3) {
 #pragma unroll
-          for (int u = k * kLoads / (4 * JM); u < (k + 1) * kLoads / (4 * JM); ++u)
+          for (int u = k * kHalf / (4 * JM); u < (k + 1) * kHalf / (4 * JM); ++u)
             issue(qb, pb, 0, B, u);
+        }
+        if (STEADY && s == 0) {
+#pragma unroll
+          for (int u = k * kHalf / (4 * JM); u < (k + 1) * kHalf / (4 * JM); ++u)
+            issue(qb - qstep, pb - kStep * 2, 0, B ^ 1, kHalf + u);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -224,10 +232,10 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
   using Yes = std::integral_constant<bool, true>;
   using No = std::integral_constant<bool, false>;
   {
-    issue_all(ka, 0);
+    issue_some(ka, 0, 0, kLoads);
     mx_wait_loads();
     __syncthreads();
-    if (ka + 1 < kb) issue_all(ka + 1, 1);
+    if (ka + 1 < kb) issue_some(ka + 1, 1, 0, kHalf);
 #pragma unroll
     for (int i = 0; i < kReads; ++i) load_frag(sbase, 0, i, wf[0], xf[0]);
     // the last step of W's rows may be short
@@ -248,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
   if (!TR || p.splits > 1) {
     // float32: four consecutive outputs per lane and store
     const int ld = TR ? NI : p.ldz;
-    float* out = p.Z + (TR ? (int64_t)split * M * NI : 0);
+    float* out = p.Z + (int64_t)split * M * ld;
 #pragma unroll
     for (int ms = 0; ms < JM; ++ms) {
       const int m = j0 + 32 * JM * wj + 32 * ms + l32;
@@ -303,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
 // thread; longer rows are read again).
 
 struct RowParams {
-  const float* Z;     // rows x ldz
+  const float* Z;     // splits x rows x ldz
   const int32_t* t;   // rows x kt
   const float* pt;    // rows x kt or NULL
   const float* w;     // rows or NULL
@@ -311,13 +319,14 @@ struct RowParams {
   float* lse;
   uint16_t* D;        // rows x ldd or NULL
   int32_t V, ldz, ldd, kt;
+  int32_t splits;     // Z: so many partial sums, part elements apart
+  int64_t part;
   float scale;
 };
 
-constexpr int kRowThreads = 1024;
 constexpr int kMaxTargets = 128;
 
-template <bool MAX>
+template <bool MAX, int T>
 __device__ __forceinline__ float row_reduce(float v, float* sh) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) {
@@ -329,14 +338,14 @@ __device__ __forceinline__ float row_reduce(float v, float* sh) {
   __syncthreads();
   v = sh[0];
 #pragma unroll
-  for (int i = 1; i < kRowThreads / 64; ++i) v = MAX ? fmaxf(v, sh[i]) : v + sh[i];
+  for (int i = 1; i < T / 64; ++i) v = MAX ? fmaxf(v, sh[i]) : v + sh[i];
   return v;
 }
 
-// Q: groups of four values per thread that stay in registers
-template <int Q>
-__global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
-  __shared__ float sh[kRowThreads / 64];
+// T threads; Q: groups of four values per thread that stay in registers
+template <int T, int Q>
+__global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
+  __shared__ float sh[T / 64];
   __shared__ int tgt[kMaxTargets];
   __shared__ float wgt[kMaxTargets], zt[kMaxTargets];
   const int tid = threadIdx.x, V = p.V;
@@ -347,13 +356,21 @@ __global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
     const bool ok = t >= 0 && t < V;
     tgt[tid] = ok ? t : -1;
     wgt[tid] = ok ? (p.pt ? p.pt[row * p.kt + tid] : 1.0f) : 0.0f;
-    zt[tid] = ok ? z[t] : 0.0f;
+    float v = 0.0f;
+    if (ok)
+      for (int k = 0; k < p.splits; ++k) v += z[k * p.part + t];
+    zt[tid] = v;
   }
   const int groups = (V + 3) / 4;
   const float ninf = -__builtin_inff();
   f32x4 x[Q];
   auto load = [&](int g) {
-    f32x4 v = *reinterpret_cast<const f32x4*>(z + 4 * g);
+    f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(z + 4 * g));
+    for (int i = 1; i < p.splits; ++i) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(z + i * p.part + 4 * g);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += y[k];
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = 4 * g + k < V ? v[k] : ninf;
     return v;
@@ -361,7 +378,7 @@ __global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
   float top = ninf;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    const int g = tid + kRowThreads * i;
+    const int g = tid + T * i;
     x[i] = f32x4{ninf, ninf, ninf, ninf};
     if (g < groups) x[i] = load(g);
   }
@@ -369,12 +386,12 @@ __global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
   for (int i = 0; i < Q; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) top = fmaxf(top, x[i][k]);
-  for (int g = tid + kRowThreads * Q; g < groups; g += kRowThreads) {
+  for (int g = tid + T * Q; g < groups; g += T) {
     const f32x4 v = load(g);
 #pragma unroll
     for (int k = 0; k < 4; ++k) top = fmaxf(top, v[k]);
   }
-  top = row_reduce<true>(top, sh);
+  top = row_reduce<true, T>(top, sh);
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < Q; ++i)
@@ -383,12 +400,12 @@ __global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
       x[i][k] = __expf(x[i][k] - top);
       sum += x[i][k];
     }
-  for (int g = tid + kRowThreads * Q; g < groups; g += kRowThreads) {
+  for (int g = tid + T * Q; g < groups; g += T) {
     const f32x4 v = load(g);
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum += __expf(v[k] - top);
   }
-  sum = row_reduce<false>(sum, sh);
+  sum = row_reduce<false, T>(sum, sh);
   const float lse = top + logf(sum);
   // the targets: every thread adds the few of them in order
   float total = 0.0f, loss = 0.0f;
@@ -414,10 +431,10 @@ __global__ __launch_bounds__(kRowThreads) void head_row_kernel(RowParams p) {
   };
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    const int g = tid + kRowThreads * i;
+    const int g = tid + T * i;
     if (g < p.ldd / 4) store(g, x[i]);
   }
-  for (int g = tid + kRowThreads * Q; g < p.ldd / 4; g += kRowThreads) {
+  for (int g = tid + T * Q; g < p.ldd / 4; g += T) {
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (g < groups) {
       v = load(g);
@@ -464,35 +481,67 @@ size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 constexpr int kCUs = 256;
 
-// 32-row blocks per wave: tiles of 64, 128 or 256 rows
-int tile_jm(int64_t rows) { return rows <= 64 ? 1 : rows <= 128 ? 2 : 4; }
-
 struct Shape {
-  int jm;
+  int jm;  // 32-row blocks per wave: tiles of 64 jm rows
   int64_t ti, tj, splits, ksteps;
 };
 
-Shape z_shape(int64_t rows, int64_t V, int64_t K) {
-  Shape s;
-  s.jm = tile_jm(rows);
-  s.ti = cdiv(V, kTI);
-  s.tj = cdiv(rows, 64 * s.jm);
-  s.splits = 1;
-  s.ksteps = K / kStep;
-  return s;
+// Time of a product's launch in units of a 64-wide step of the 256 x 256 tile
+// (1.45 us), from sweeps at K = 4096, V = 32000 over 1 to 2048 rows: a round of
+// tiles costs 9 such steps outside its loop, a step of the smaller tiles the
+// shares below (64-row tiles fit a compute unit twice, and then take 0.87), and
+// partial sums their way to memory and back.
+double launch_cost(int jm, int64_t rows, int64_t n, int64_t steps, int64_t splits, bool always_part) {
+  const int64_t wgs = cdiv(n, kTI) * cdiv(rows, 64 * jm) * splits;
+  const bool pairs = jm == 1 && wgs > kCUs;
+  const double step = pairs ? 0.87 : jm == 1 ? 0.54 : jm == 2 ? 0.69 : jm == 3 ? 0.84 : 1.0;
+  const double parts = always_part && splits == 1 ? 0.0 : (double)(always_part ? splits : splits - 1);
+  return (double)cdiv(wgs, pairs ? 2 * kCUs : kCUs) * (9.0 + (double)cdiv(steps, splits) * step) +
+         1.2e-6 * parts * (double)rows * (double)n;
 }
 
-// dH: fewer tiles than compute units split the reduction over V
+// The cheapest tile and number of splits.  ``sums``: the splits are added by a
+// launch of their own (dH), not by the softmax (z)
+Shape best_shape(int64_t rows, int64_t n, int64_t steps, int most_splits, bool sums) {
+  Shape best{};
+  double least = 0.0;
+  for (int jm = 1; jm <= 4; ++jm) {
+    const int64_t tiles = cdiv(n, kTI) * cdiv(rows, 64 * jm);
+    for (int fill = 1; fill <= 2; ++fill) {
+      int64_t splits = fill * kCUs / tiles;
+      const int64_t most = cdiv(steps, 8) < most_splits ? cdiv(steps, 8) : most_splits;
+      splits = splits < most ? splits : most;
+      splits = splits < 1 ? 1 : splits;
+      const int64_t ks = cdiv(steps, splits);
+      splits = cdiv(steps, ks);
+      const double cost = launch_cost(jm, rows, n, steps, splits, sums);
+      if (best.jm == 0 || cost < least) {
+        least = cost;
+        best = Shape{jm, cdiv(n, kTI), cdiv(rows, 64 * jm), splits, ks};
+      }
+    }
+  }
+  return best;
+}
+
+Shape z_shape(int64_t rows, int64_t V, int64_t K) {
+  return best_shape(rows, V, K / kStep, 4, false);
+}
 Shape dh_shape(int64_t rows, int64_t V, int64_t K) {
-  Shape s;
-  s.jm = tile_jm(rows);
-  s.ti = cdiv(K, kTI);
-  s.tj = cdiv(rows, 64 * s.jm);
-  const int64_t steps = cdiv(V, kStep), fill = kCUs / (s.ti * s.tj), most = cdiv(steps, 8);
-  s.splits = fill < 1 ? 1 : fill < most ? fill : most;
-  s.ksteps = cdiv(steps, s.splits);
-  s.splits = cdiv(steps, s.ksteps);
-  return s;
+  return best_shape(rows, K, cdiv(V, kStep), 32, true);
+}
+
+// Columns of z that its first launch takes: all, or whole rounds of tiles, where
+// a second launch with smaller tiles is done sooner than a last round of few
+int64_t z_first_columns(const Shape& s, int64_t rows, int64_t V, int64_t K) {
+  const int64_t tiles = s.ti * s.tj, rounds = tiles / kCUs;
+  if (s.splits > 1 || s.jm < 3 || rounds < 1 || tiles % kCUs == 0) return V;
+  const int64_t first = rounds * kCUs / s.tj * kTI;
+  if (first <= 0 || first >= V) return V;
+  const Shape t = best_shape(rows, V - first, K / kStep, 1, false);
+  const double two = launch_cost(s.jm, rows, first, K / kStep, 1, false) + 2.0 +
+                     launch_cost(t.jm, rows, V - first, K / kStep, 1, false);
+  return two < launch_cost(s.jm, rows, V, K / kStep, 1, false) ? first : V;
 }
 
 // Rows of a piece: at most 2^28 logits (1 GiB of float32), whole 256-row tiles
@@ -504,6 +553,13 @@ int64_t piece_rows(int64_t M, int64_t V) {
 
 int64_t ld_of(int64_t V) { return cdiv(V, 64) * 64; }
 
+// the logits of a piece (the last has fewer rows and may have more splits)
+size_t z_bytes(int64_t M, int64_t V, int64_t K) {
+  const int64_t rows = piece_rows(M, V), last = M - (cdiv(M, rows) - 1) * rows;
+  const int64_t a = rows * z_shape(rows, V, K).splits, b = last * z_shape(last, V, K).splits;
+  return (size_t)(a > b ? a : b) * ld_of(V) * 4;
+}
+
 struct Layout {
   size_t z, d, part, end;
 };
@@ -511,7 +567,7 @@ Layout layout(int64_t M, int64_t V, int64_t K, bool need_dh) {
   const int64_t rows = piece_rows(M, V);
   Layout l;
   l.z = 0;
-  l.d = up256((size_t)rows * ld_of(V) * 4);
+  l.d = up256(z_bytes(M, V, K));
   l.part = l.d + (need_dh ? up256((size_t)rows * ld_of(V) * 2) : 0);
   l.end = l.part;
   if (need_dh) {
@@ -533,9 +589,29 @@ int launch_product(const ProdParams& p, int jm, hipStream_t st) {
   const dim3 g((unsigned)(p.ti * p.tj * p.splits)), b(kThreads);
   const auto kernel = jm == 1   ? head_product_kernel<TR, 1>
                       : jm == 2 ? head_product_kernel<TR, 2>
+                      : jm == 3 ? head_product_kernel<TR, 3>
                                 : head_product_kernel<TR, 4>;
   hipLaunchKernelGGL(kernel, g, b, 0, st, p);
   return hip_fail(hipGetLastError(), TR ? "head dH launch" : "head logits launch");
+}
+
+void launch_rows(const RowParams& r, int64_t rows, hipStream_t st) {
+  const int64_t ld = r.ldz;
+  const auto kernel = ld <= 4096 * 4    ? head_row_kernel<1024, 4>
+                      : ld <= 4096 * 8  ? head_row_kernel<1024, 8>
+                      : ld <= 4096 * 13 ? head_row_kernel<1024, 13>
+                                        : head_row_kernel<1024, 16>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(1024), 0, st, r);
+}
+
+// z of columns [first, end), first a multiple of the tile
+int launch_columns(ProdParams p, const Shape& s, int64_t first, int64_t end, hipStream_t st) {
+  p.i_first = (int32_t)first;
+  p.ti = (int32_t)cdiv(end - first, kTI);
+  p.tj = (int32_t)s.tj;
+  p.splits = (int32_t)s.splits;
+  p.ksteps = (int32_t)s.ksteps;
+  return launch_product<false>(p, s.jm, st);
 }
 
 }  // namespace
@@ -566,11 +642,10 @@ int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, con
     p.KV = (int32_t)K;
     p.ldz = (int32_t)ld;
     p.scale = scale;
-    p.ti = (int32_t)z.ti;
-    p.tj = (int32_t)z.tj;
-    p.splits = 1;
-    p.ksteps = (int32_t)z.ksteps;
-    int rc = launch_product<false>(p, z.jm, st);
+    const int64_t first = z_first_columns(z, rows, V, K);
+    int rc = launch_columns(p, z, 0, first, st);
+    if (!rc && first < V)
+      rc = launch_columns(p, best_shape(rows, V - first, K / kStep, 1, false), first, V, st);
     if (rc) return rc;
     RowParams r;
     r.Z = p.Z;
@@ -583,12 +658,10 @@ int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, con
     r.V = (int32_t)V;
     r.ldz = r.ldd = (int32_t)ld;
     r.kt = kt;
+    r.splits = (int32_t)z.splits;
+    r.part = rows * ld;
     r.scale = scale;
-    const auto kernel = ld <= 4096 * 4    ? head_row_kernel<4>
-                        : ld <= 4096 * 8  ? head_row_kernel<8>
-                        : ld <= 4096 * 13 ? head_row_kernel<13>
-                                          : head_row_kernel<16>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(kRowThreads), 0, st, r);
+    launch_rows(r, rows, st);
     if ((rc = hip_fail(hipGetLastError(), "head softmax launch"))) return rc;
     if (!dH) continue;
     const Shape s = dh_shape(rows, V, K);
