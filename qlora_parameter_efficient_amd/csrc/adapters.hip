@@ -35,12 +35,12 @@ struct RowArgs {
   const float* scales;
   // the plan (NULL: M <= kDirect): first sorted position of each place's rows
   // (place ``slots``: rows without an adapter; then M), rows in sorted order,
-  // (place, first position) of each tile, of each segment of the gradients, and
-  // the first segment of each place
+  // (place, first position, rows, rank) of each tile and of each segment of the
+  // gradients, and the first segment of each place
   const int32_t* off;
   const int32_t* perm;
-  const int2* tiles;
-  const int2* segs;
+  const int4* tiles;
+  const int4* segs;
   const int32_t* seg0;
   const int32_t* count;  // tiles, segments
   int32_t M, slots, r;
@@ -50,33 +50,39 @@ __device__ __forceinline__ int place_of(int32_t a, int slots) {
   return a >= 0 && a < slots ? a : slots;
 }
 
-__device__ __forceinline__ int rank_of(const RowArgs& a, int slot) {
-  if (slot >= a.slots) return 0;
-  if (!a.ranks) return a.r;
-  const int k = a.ranks[slot];
-  return k < 0 ? 0 : k > a.r ? a.r : k;
+__device__ __forceinline__ int rank_of(const int32_t* ranks, int slots, int r, int slot) {
+  if (slot >= slots) return 0;
+  if (!ranks) return r;
+  const int k = ranks[slot];
+  return k < 0 ? 0 : k > r ? r : k;
 }
 
-// This workgroup's tile: its place and number of rows (0: none) and their
-// indices in rows_s (ready after the caller's next barrier).
-__device__ __forceinline__ int find_tile(const RowArgs& a, int tile, int32_t* rows_s, int& slot) {
+struct Tile {
+  int slot, n, rank;  // n = 0: none
+};
+
+// This workgroup's tile, and its rows' indices in rows_s (ready after the
+// caller's next barrier).
+__device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* rows_s) {
   const int lane = threadIdx.x & 63;
+  Tile t;
   if (!a.tiles) {
     const int id = lane < a.M ? place_of(a.rows[lane], a.slots) : -1;
-    slot = __builtin_amdgcn_readlane(id, tile);
-    const uint64_t same = __ballot(id == slot);
-    if ((int)__builtin_ctzll(same) != tile) return 0;
-    if (threadIdx.x < 64 && id == slot)
+    t.slot = __builtin_amdgcn_readlane(id, tile);
+    t.rank = rank_of(a.ranks, a.slots, a.r, t.slot);
+    const uint64_t same = __ballot(id == t.slot);
+    t.n = (int)__builtin_ctzll(same) == tile ? __builtin_popcountll(same) : 0;
+    if (threadIdx.x < 64 && id == t.slot)
       rows_s[__builtin_popcountll(same & ((1ull << lane) - 1))] = lane;
-    return __builtin_popcountll(same);
+    return t;
   }
-  if (tile >= a.count[0]) return 0;
-  const int2 t = a.tiles[tile];
-  slot = t.x;
-  const int left = a.off[slot + 1] - t.y;
-  const int n = left < kTM ? left : kTM;
-  if ((int)threadIdx.x < n) rows_s[threadIdx.x] = a.perm[t.y + threadIdx.x];
-  return n;
+  const int4 d = a.tiles[tile];  // (past the last tile: not used)
+  const bool any = tile < a.count[0];
+  t.slot = d.x;
+  t.n = any ? d.z : 0;
+  t.rank = d.w;
+  if ((int)threadIdx.x < t.n) rows_s[threadIdx.x] = a.perm[d.y + threadIdx.x];
+  return t;
 }
 
 // ---------------------------------------------------------------- plan
@@ -88,13 +94,14 @@ __device__ __forceinline__ int find_tile(const RowArgs& a, int tile, int32_t* ro
 // longest part.
 struct PlanArgs {
   const int32_t* rows;
+  const int32_t* ranks;
   int32_t* off;
   int32_t* perm;
-  int2* tiles;
-  int2* segs;
+  int4* tiles;
+  int4* segs;
   int32_t* seg0;
   int32_t* count;
-  int32_t M, slots, waves, bits, seg_rows;
+  int32_t M, slots, r, waves, bits, seg_rows;
 };
 
 // the lanes of the wave whose value equals this lane's
@@ -140,25 +147,32 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   __shared__ int sh[16][3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int S1 = p.slots + 1, W = p.waves;
-  for (int i = tid; i < W * S1; i += 1024) cnt[i] = 0;
-  __syncthreads();
   const int per = (int)cdiv(cdiv(p.M, 64), W) * 64;
   const int64_t lo = (int64_t)wave * per;
   const int64_t end = lo + per;
-  const int hi = wave < W ? (int)(end < p.M ? end : p.M) : 0;
+  const int64_t hi = wave < W ? (end < p.M ? end : p.M) : 0;
   const uint64_t below = (1ull << lane) - 1;
+  int id[8];
+  auto load = [&](int64_t b) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = b + 64 * k + lane;
+      id[k] = i < hi ? p.rows[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) id[k] = place_of(id[k], p.slots);
+  };
+  load(lo);
+  for (int i = tid; i < W * S1; i += 1024) cnt[i] = 0;
+  __syncthreads();
+  // up to 512 rows per wave stay in registers between the walks
   auto walk = [&](bool place) {
     for (int64_t b = lo; b < hi; b += 512) {
-      int id[8];
+      if (per > 512) load(b);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int64_t i = b + 64 * k + lane;
-        id[k] = i < hi ? place_of(p.rows[i], p.slots) : 0;
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t i = b + 64 * k + lane;
         if (b + 64 * k >= hi) break;
+        const int64_t i = b + 64 * k + lane;
         const bool in = i < hi;
         const uint64_t m = lanes_like(id[k], p.bits, in);
         const int first = in ? (int)__builtin_ctzll(m) : lane;
@@ -175,33 +189,44 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   __syncthreads();
   // counts become positions: thread t has places c t .. c t + c - 1
   const int c = (int)cdiv(S1, 1024);
-  int v[3] = {0, 0, 0}, total[3];
-  for (int k = 0; k < c; ++k) {
+  int v[3] = {0, 0, 0}, total[3], n[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {  // S1 <= 4097
     const int s = tid * c + k;
-    if (s >= S1) break;
-    int n = 0;
-    for (int w = 0; w < W; ++w) {
-      const int x = cnt[w * S1 + s];
-      cnt[w * S1 + s] = n;
-      n += x;
-    }
-    v[0] += n;
-    v[1] += (int)cdiv(n, kTM);
-    v[2] += s < p.slots ? (int)cdiv(n, p.seg_rows) : 0;
-    p.off[s + 1] = n;  // the count, until the positions are known
+    n[k] = 0;
+    if (k >= c || s >= S1) continue;
+#pragma unroll
+    for (int w = 0; w < 16; ++w)
+      if (w < W) {
+        const int x = cnt[w * S1 + s];
+        cnt[w * S1 + s] = n[k];
+        n[k] += x;
+      }
+    v[0] += n[k];
+    v[1] += (n[k] + kTM - 1) / kTM;
+    v[2] += s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
   }
   scan3(v, total, sh);
-  for (int k = 0; k < c; ++k) {
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
     const int s = tid * c + k;
-    if (s >= S1) break;
-    const int n = p.off[s + 1];
-    for (int w = 0; w < W; ++w) cnt[w * S1 + s] += v[0];
+    if (k >= c || s >= S1) continue;
+#pragma unroll
+    for (int w = 0; w < 16; ++w)
+      if (w < W) cnt[w * S1 + s] += v[0];
+    const int rank = n[k] ? rank_of(p.ranks, p.slots, p.r, s) : 0;
     if (s < p.slots) {
       p.seg0[s] = v[2];
-      for (int i = 0; i < n; i += p.seg_rows) p.segs[v[2]++] = make_int2(s, v[0] + i);
+      for (int i = 0; i < n[k]; i += p.seg_rows) {
+        const int left = n[k] - i;
+        p.segs[v[2]++] = make_int4(s, v[0] + i, left < p.seg_rows ? left : p.seg_rows, rank);
+      }
     }
-    for (int i = 0; i < n; i += kTM) p.tiles[v[1]++] = make_int2(s, v[0] + i);
-    v[0] += n;
+    for (int i = 0; i < n[k]; i += kTM) {
+      const int left = n[k] - i;
+      p.tiles[v[1]++] = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank);
+    }
+    v[0] += n[k];
     p.off[s + 1] = v[0];
   }
   if (tid == 0) {
@@ -220,14 +245,14 @@ struct ShrinkParams {
   RowArgs a;
   const uint16_t* X;  // M x C
   const uint16_t* A;  // slots x r x C
-  float* Tp;          // splits x M x r
-  int32_t C, steps;   // 64-column steps of the reduction, of one split
+  float* Tp;          // splits x M x rp
+  int32_t C, rp, steps;   // 64-column steps of the reduction, of one split
 };
 
 template <int MB, int JB>
 __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t* rows_s, int n,
                                             const uint16_t* A, int rank, int s0, int s1,
-                                            float* red) {
+                                            f32x4* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const uint16_t* xr[MB];
@@ -278,52 +303,69 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
     }
     if (s < s1) mul(0);
   }
+  // waves 2 and 3 to 0 and 1, then half of the blocks from 0 to 1 and half back
+  constexpr int NB = MB * JB, H0 = (NB + 1) / 2;
+  auto at = [&](int buf, int b) -> f32x4& { return red[(buf * NB + b) * 64 + lane]; };
+  auto add = [&](f32x4& a, const f32x4& b) {
 #pragma unroll
-  for (int m = 0; m < MB; ++m)
+    for (int e = 0; e < 4; ++e) a[e] += b[e];
+  };
+  if (wave >= 2)
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int b = 0; b < NB; ++b) at(wave - 2, b) = acc[b / JB][b % JB];
+  __syncthreads();
+  if (wave < 2)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        red[(wave * kTM + 16 * m + 4 * g + v) * (16 * JB) + 16 * j + i16] = acc[m][j][v];
+    for (int b = 0; b < NB; ++b) add(acc[b / JB][b % JB], at(wave, b));
+  __syncthreads();
+  if (wave < 2)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if ((b < H0) == (wave == 1)) at(wave, b) = acc[b / JB][b % JB];
+  __syncthreads();
+  if (wave >= 2) return;
+  float* out = p.Tp + (int64_t)blockIdx.y * p.a.M * p.rp;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if ((b < H0) != (wave == 0)) continue;
+    add(acc[b / JB][b % JB], at(1 - wave, b));
+    const int j = 16 * (b % JB) + i16;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int i = 16 * (b / JB) + 4 * g + v;
+      if (i < n && j < rank) out[(int64_t)rows_s[i] * p.rp + j] = acc[b / JB][b % JB][v];
+    }
+  }
 }
 
 template <int JB>
 __global__ __launch_bounds__(256) void shrink_tiles_kernel(ShrinkParams p) {
   __shared__ int32_t rows_s[kTM];
-  __shared__ float red[4 * kTM * 16 * JB];
-  int slot;
-  const int n = find_tile(p.a, blockIdx.x, rows_s, slot);
-  if (n == 0) return;
-  const int rank = rank_of(p.a, slot);
-  if (rank == 0) return;
+  __shared__ f32x4 red[2 * 4 * JB * 64];
+  const Tile t = find_tile(p.a, blockIdx.x, rows_s);
+  if (t.n == 0 || t.rank == 0) return;
   __syncthreads();
   const int s0 = blockIdx.y * p.steps, all = p.C / 64;
   const int s1 = s0 + p.steps < all ? s0 + p.steps : all;
-  const uint16_t* A = p.A + (int64_t)slot * p.a.r * p.C;
-  if (n <= 16)
-    shrink_tile<1, JB>(p, rows_s, n, A, rank, s0, s1, red);
+  const uint16_t* A = p.A + (int64_t)t.slot * p.a.r * p.C;
+  if (t.n <= 16)
+    shrink_tile<1, JB>(p, rows_s, t.n, A, t.rank, s0, s1, red);
+  else if (t.n <= 32)
+    shrink_tile<2, JB>(p, rows_s, t.n, A, t.rank, s0, s1, red);
   else
-    shrink_tile<4, JB>(p, rows_s, n, A, rank, s0, s1, red);
-  __syncthreads();
-  float* out = p.Tp + (int64_t)blockIdx.y * p.a.M * p.a.r;
-  for (int e = threadIdx.x; e < n * 16 * JB; e += 256) {
-    const int i = e / (16 * JB), j = e % (16 * JB);
-    if (j < rank)
-      out[(int64_t)rows_s[i] * p.a.r + j] =
-          (red[e] + red[kTM * 16 * JB + e]) + (red[2 * kTM * 16 * JB + e] + red[3 * kTM * 16 * JB + e]);
-  }
+    shrink_tile<4, JB>(p, rows_s, t.n, A, t.rank, s0, s1, red);
 }
 
 // -------------------------------------------------------------- expand
 
 struct ExpandParams {
   RowArgs a;
-  const float* Tp;    // splits x M x r
+  const float* Tp;    // splits x M x rp
   const uint16_t* B;  // slots x N x ldb
   const uint16_t* Yi;
   uint16_t* Yo;
   float* T_out;  // M x r or NULL
-  int32_t splits, N, ldb, passes;
+  int32_t splits, N, ldb, rp, passes;
 };
 
 // B[n][j0 .. j0 + 7], zeros from ``rank``; ld: row stride in elements.  WHOLE:
@@ -355,43 +397,28 @@ __device__ __forceinline__ void split2(float v, uint16_t& hi, uint16_t& lo) {
   lo = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0 : f32_to_bf16(v - h);
 }
 
-// JC: 32-rank chunks
+// JC: 32-rank chunks.  What does not depend on T (B, Y) is loaded before T's
+// partial sums are waited for.
 template <int JC, bool WHOLE>
 __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
   constexpr int LD = 32 * JC + 8;  // LDS row pitch of T in elements
+  constexpr int VT = 2 * JC;       // groups of four values of T per thread
   __shared__ int32_t rows_s[kTM];
   __shared__ __attribute__((aligned(16))) uint16_t t_hi[kTM * LD], t_lo[kTM * LD];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, i16 = lane & 15;
-  int slot;
-  const int n = find_tile(p.a, blockIdx.x, rows_s, slot);
+  const Tile t = find_tile(p.a, blockIdx.x, rows_s);
+  const int n = t.n, rank = t.rank;
   if (n == 0) return;
-  const int rank = rank_of(p.a, slot);
   const bool store_t = p.T_out && blockIdx.y == 0;
   if (rank == 0 && p.Yi == p.Yo && !store_t) return;
-  __syncthreads();
   const int r = p.a.r, M = p.a.M, N = p.N;
-  const float s = rank ? p.a.scales[slot] : 0.0f;
-  for (int e = tid; e < 16 * (int)cdiv(n, 16) * 32 * JC; e += 256) {
-    const int i = e / (32 * JC), j = e % (32 * JC);
-    float v = 0.0f;
-    if (i < n && j < rank) {
-      const float* q = p.Tp + (int64_t)rows_s[i] * r + j;
-      for (int k = 0; k < p.splits; ++k) v += q[(int64_t)k * M * r];
-    }
-    if (store_t && i < n && j < r) p.T_out[(int64_t)rows_s[i] * r + j] = v;
-    uint16_t hi, lo;
-    split2(v * s, hi, lo);
-    t_hi[i * LD + j] = hi;
-    t_lo[i * LD + j] = lo;
-  }
+  const float s = rank ? p.a.scales[t.slot] : 0.0f;
   __syncthreads();
-  if (!p.Yo) return;
-  const uint16_t* B = p.B + (int64_t)slot * N * p.ldb;
-  for (int pass = 0; pass < p.passes; ++pass) {
-    const int n0 = ((int)blockIdx.y * p.passes + pass) * 256 + 64 * wave;
-    if (n0 >= N) return;
-    u32x4 bf[4][JC];
+  const uint16_t* B = p.B + (int64_t)t.slot * N * p.ldb;
+  u32x4 bf[4][JC], y[4][2];
+  int64_t at[4];
+  auto load = [&](int n0) {
     if (rank) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -405,15 +432,78 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
     for (int m = 0; m < 4; ++m) {
       if (16 * m >= n) break;
       const int i = 16 * m + i16;
-      const int64_t at = (int64_t)rows_s[i < n ? i : n - 1] * N + n0 + 16 * g;
-      u32x4 y[2] = {*reinterpret_cast<const u32x4*>(p.Yi + at),
-                    *reinterpret_cast<const u32x4*>(p.Yi + at + 8)};
+      at[m] = (int64_t)rows_s[i < n ? i : n - 1] * N + n0 + 16 * g;
+      y[m][0] = *reinterpret_cast<const u32x4*>(p.Yi + at[m]);
+      y[m][1] = *reinterpret_cast<const u32x4*>(p.Yi + at[m] + 8);
+    }
+  };
+  int n0 = (int)blockIdx.y * p.passes * 256 + 64 * wave;
+  if (p.Yo && n0 < N) load(n0);
+  if (rank || store_t) {
+    f32x4 v[VT];
+    const float* q[VT];
+    bool in[VT];
+#pragma unroll
+    for (int u = 0; u < VT; ++u) {
+      const int e = 256 * u + tid, i = e / (8 * JC), j = 4 * (e % (8 * JC));
+      in[u] = i < n && j < rank;
+      q[u] = p.Tp + (int64_t)rows_s[in[u] ? i : 0] * p.rp + (in[u] ? j : 0);
+      v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    if (rank) {
+      const int64_t part = (int64_t)M * p.rp;
+      int k = 0;
+      for (; k + 4 <= p.splits; k += 4) {
+        f32x4 x[4][VT];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int u = 0; u < VT; ++u) x[d][u] = *reinterpret_cast<const f32x4*>(q[u] + (k + d) * part);
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int u = 0; u < VT; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[u][e] += x[d][u][e];
+      }
+      for (; k < p.splits; ++k)
+#pragma unroll
+        for (int u = 0; u < VT; ++u) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(q[u] + k * part);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[u][e] += x[e];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < VT; ++u) {
+      const int e = 256 * u + tid, i = e / (8 * JC), j = 4 * (e % (8 * JC));
+      uint16_t hi[4], lo[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const float x = in[u] && j + d < rank ? v[u][d] : 0.0f;
+        if (store_t && i < n && j + d < r) p.T_out[(int64_t)rows_s[i] * r + j + d] = x;
+        split2(x * s, hi[d], lo[d]);
+      }
+      *reinterpret_cast<u32x2*>(t_hi + i * LD + j) =
+          u32x2{hi[0] | ((uint32_t)hi[1] << 16), hi[2] | ((uint32_t)hi[3] << 16)};
+      *reinterpret_cast<u32x2*>(t_lo + i * LD + j) =
+          u32x2{lo[0] | ((uint32_t)lo[1] << 16), lo[2] | ((uint32_t)lo[3] << 16)};
+    }
+  }
+  __syncthreads();
+  if (!p.Yo) return;
+  for (int pass = 0; pass < p.passes && n0 < N; ++pass) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (16 * m >= n) break;
+      const int i = 16 * m + i16;
       if (rank) {
         f32x4 acc[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          acc[b] = f32x4{lo_bf16(y[b >> 1][2 * (b & 1)]), hi_bf16(y[b >> 1][2 * (b & 1)]),
-                         lo_bf16(y[b >> 1][2 * (b & 1) + 1]), hi_bf16(y[b >> 1][2 * (b & 1) + 1])};
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t w0 = y[m][b >> 1][2 * (b & 1)], w1 = y[m][b >> 1][2 * (b & 1) + 1];
+          acc[b] = f32x4{lo_bf16(w0), hi_bf16(w0), lo_bf16(w1), hi_bf16(w1)};
+        }
 #pragma unroll
         for (int jc = 0; jc < JC; ++jc) {
           const u32x4 th = *reinterpret_cast<const u32x4*>(t_hi + i * LD + 32 * jc + 8 * g);
@@ -426,15 +516,17 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          y[b >> 1][2 * (b & 1)] = pack_bf16x2(acc[b][0], acc[b][1]);
-          y[b >> 1][2 * (b & 1) + 1] = pack_bf16x2(acc[b][2], acc[b][3]);
+          y[m][b >> 1][2 * (b & 1)] = pack_bf16x2(acc[b][0], acc[b][1]);
+          y[m][b >> 1][2 * (b & 1) + 1] = pack_bf16x2(acc[b][2], acc[b][3]);
         }
       }
       if (i < n) {
-        *reinterpret_cast<u32x4*>(p.Yo + at) = y[0];
-        *reinterpret_cast<u32x4*>(p.Yo + at + 8) = y[1];
+        *reinterpret_cast<u32x4*>(p.Yo + at[m]) = y[m][0];
+        *reinterpret_cast<u32x4*>(p.Yo + at[m] + 8) = y[m][1];
       }
     }
+    n0 += 256;
+    if (pass + 1 < p.passes && n0 < N) load(n0);
   }
 }
 
@@ -490,7 +582,7 @@ struct GradParams {
   float* dA;    // slots x r x K
   float* dB;    // slots x N x r
   float* part;  // segments x (r K + N r)
-  int32_t N, K, seg_rows, accumulate;
+  int32_t N, K, accumulate;
 };
 
 constexpr int kZP = 256 + 16;  // LDS row pitch of a step's columns, in elements
@@ -508,11 +600,8 @@ __device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, 
                                           uint16_t* vs) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, i16 = lane & 15;
-  const int2 sg = p.a.segs[seg];
-  const int slot = sg.x, r = p.a.r, C = DB ? p.N : p.K;
-  const int rank = rank_of(p.a, slot);
-  const int left = p.a.off[slot + 1] - sg.y;
-  const int n = left < p.seg_rows ? left : p.seg_rows;
+  const int4 sg = p.a.segs[seg];
+  const int slot = sg.x, n = sg.z, rank = sg.w, r = p.a.r, C = DB ? p.N : p.K;
   const int32_t* perm = p.a.perm + sg.y;
   const uint16_t* Z = DB ? p.dY : p.X;
   const float* V = DB ? p.T : p.U;
@@ -642,6 +731,9 @@ __global__ __launch_bounds__(256) void grads_finish_kernel(GradParams p) {
 
 // ---------------------------------------------------------------- host
 
+// row pitch of T's partial sums: groups of four
+int t_pitch(int64_t r) { return (int)(r + 3) / 4 * 4; }
+
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 int64_t max_tiles(int64_t M, int32_t slots) {
@@ -679,8 +771,8 @@ PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   l.seg0 = up256((size_t)(slots + 2) * 4);
   l.count = l.seg0 + up256((size_t)(slots + 2) * 4);
   l.tiles = l.count + 256;
-  l.segs = l.tiles + up256((size_t)max_tiles(M > kDirect ? M : kDirect + 1, slots) * 8);
-  l.perm = l.segs + up256((size_t)segs * 8);
+  l.segs = l.tiles + up256((size_t)max_tiles(M > kDirect ? M : kDirect + 1, slots) * 16);
+  l.perm = l.segs + up256((size_t)segs * 16);
   l.end = l.perm + up256((size_t)M * 4);
   return l;
 }
@@ -688,11 +780,13 @@ PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
 int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, hipStream_t st) {
   PlanArgs p;
   p.rows = a.rows;
+  p.ranks = a.ranks;
+  p.r = a.r;
   p.off = (int32_t*)(ws + l.off);
   p.seg0 = (int32_t*)(ws + l.seg0);
   p.count = (int32_t*)(ws + l.count);
-  p.tiles = (int2*)(ws + l.tiles);
-  p.segs = (int2*)(ws + l.segs);
+  p.tiles = (int4*)(ws + l.tiles);
+  p.segs = (int4*)(ws + l.segs);
   p.perm = (int32_t*)(ws + l.perm);
   p.M = a.M;
   p.slots = a.slots;
@@ -718,6 +812,7 @@ int launch_shrink(const RowArgs& a, const void* X, const void* A, int64_t C, flo
   p.A = (const uint16_t*)A;
   p.Tp = Tp;
   p.C = (int32_t)C;
+  p.rp = t_pitch(a.r);
   p.steps = (int32_t)cdiv(C / 64, splits);
   const dim3 g((unsigned)max_tiles(a.M, a.slots), (unsigned)splits), b(256);
   switch ((a.r + 15) / 16) {
@@ -742,10 +837,11 @@ int launch_expand(const RowArgs& a, const float* Tp, int splits, const void* B, 
   p.splits = splits;
   p.N = (int32_t)N;
   p.ldb = ldb;
+  p.rp = t_pitch(a.r);
   // 256 columns per workgroup and pass; more than one pass where full tiles
   // alone are enough workgroups
   const int64_t chunks = Yo ? cdiv(N, 256) : 1, full = cdiv(a.M, kTM);
-  int64_t passes = full * chunks / 1024;
+  int64_t passes = full * chunks / 4096;
   passes = passes < 1 ? 1 : passes > 8 ? 8 : passes;
   p.passes = (int32_t)passes;
   const dim3 g((unsigned)max_tiles(a.M, a.slots), (unsigned)cdiv(chunks, passes)), b(256);
@@ -782,7 +878,7 @@ BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) 
   l.u = l.at + up256((size_t)slots * r8 * K * 2);
   l.t = l.u + up256((size_t)M * r * 4);
   l.tp = l.t + up256((size_t)M * r * 4);
-  l.part = l.tp + up256((size_t)(sn > sk ? sn : sk) * M * r * 4);
+  l.part = l.tp + up256((size_t)(sn > sk ? sn : sk) * M * t_pitch(r) * 4);
   l.end = l.part + up256((size_t)segs * r * (N + K) * 4);
   return l;
 }
@@ -794,7 +890,7 @@ namespace dispatch {
 size_t adapters_fwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
   (void)N;
   const size_t plan = M <= kDirect ? 0 : plan_layout(M, slots, max_segments(M, N, K, slots)).end;
-  return plan + (size_t)shrink_splits(M, K) * M * r * 4;
+  return plan + (size_t)shrink_splits(M, K) * M * t_pitch(r) * 4;
 }
 
 size_t adapters_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
@@ -860,7 +956,6 @@ int adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool
   p.part = (float*)(base + l.part);
   p.N = (int32_t)q.N;
   p.K = (int32_t)q.K;
-  p.seg_rows = (int32_t)segment_rows(M, q.N, q.K);
   p.accumulate = accumulate;
   const dim3 g((unsigned)(cdiv(q.N, 256) + cdiv(q.K, 256)),
                (unsigned)max_segments(M, q.N, q.K, q.slots));
