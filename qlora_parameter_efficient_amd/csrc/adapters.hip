@@ -88,10 +88,10 @@ __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* r
 // ---------------------------------------------------------------- plan
 // Stable counting sort of the rows by place, in one workgroup of 16 waves: each
 // wave counts its own range of rows into counters of its own (rows of a wave
-// that share a place are found with one ballot per bit of the place), the
-// counters become first positions, and a second walk over the rows places them.
-// A wave's range is walked eight loads at a time, since a step's load is its
-// longest part.
+// that share a place are found with one ballot per bit of the place) and notes
+// each row's position among them, the counters become first positions, and the
+// rows are placed.  Rows are loaded eight at a time, since a load is the longest
+// part of a step.
 struct PlanArgs {
   const int32_t* rows;
   const int32_t* ranks;
@@ -114,18 +114,25 @@ __device__ __forceinline__ uint64_t lanes_like(int v, int bits, bool in) {
   return m;
 }
 
+// inclusive sum over the wave's lanes
+__device__ __forceinline__ int wave_scan(int x) {
+#define LQ_SCAN(ctrl, rows) x += __builtin_amdgcn_update_dpp(0, x, ctrl, rows, 0xF, false)
+  LQ_SCAN(0x111, 0xF);  // row_shr 1, 2, 4, 8
+  LQ_SCAN(0x112, 0xF);
+  LQ_SCAN(0x114, 0xF);
+  LQ_SCAN(0x118, 0xF);
+  LQ_SCAN(0x142, 0xA);  // row_bcast 15, 31
+  LQ_SCAN(0x143, 0xC);
+#undef LQ_SCAN
+  return x;
+}
+
 // exclusive sums over the workgroup of three values per thread; the totals
 __device__ __forceinline__ void scan3(int (&v)[3], int (&total)[3], int (*sh)[3]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int x[3];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    x[k] = v[k];
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(x[k], o);
-      if (lane >= o) x[k] += y;
-    }
-  }
+  for (int k = 0; k < 3; ++k) x[k] = wave_scan(v[k]);
   if (lane == 63)
 #pragma unroll
     for (int k = 0; k < 3; ++k) sh[wave][k] = x[k];
@@ -133,7 +140,8 @@ __device__ __forceinline__ void scan3(int (&v)[3], int (&total)[3], int (*sh)[3]
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     int before = 0, all = 0;
-    for (int w = 0; w < nw; ++w) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
       before += w < wave ? sh[w][k] : 0;
       all += sh[w][k];
     }
@@ -141,6 +149,8 @@ __device__ __forceinline__ void scan3(int (&v)[3], int (&total)[3], int (*sh)[3]
     total[k] = all;
   }
 }
+
+constexpr int kPerThread = (LQ_ADAPTERS_MAX_SLOTS + 1024) / 1024;  // places of a thread
 
 __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   __shared__ int32_t cnt[kCnt];
@@ -152,79 +162,81 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   const int64_t end = lo + per;
   const int64_t hi = wave < W ? (end < p.M ? end : p.M) : 0;
   const uint64_t below = (1ull << lane) - 1;
-  int id[8];
+  const int c = (int)cdiv(S1, 1024);  // thread t has places c t .. c t + c - 1
+  int id[8], pos[8], rank[kPerThread];
   auto load = [&](int64_t b) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t i = b + 64 * k + lane;
       id[k] = i < hi ? p.rows[i] : 0;
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) id[k] = place_of(id[k], p.slots);
   };
   load(lo);
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k)
+    rank[k] = k < c && tid * c + k < p.slots ? rank_of(p.ranks, p.slots, p.r, tid * c + k) : 0;
   for (int i = tid; i < W * S1; i += 1024) cnt[i] = 0;
   __syncthreads();
-  // up to 512 rows per wave stay in registers between the walks
-  auto walk = [&](bool place) {
-    for (int64_t b = lo; b < hi; b += 512) {
-      if (per > 512) load(b);
+  // Counts the wave's rows by place; pos: a row's position among those that the
+  // counter has seen.
+  auto count = [&](int64_t b) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (b + 64 * k >= hi) break;
-        const int64_t i = b + 64 * k + lane;
-        const bool in = i < hi;
-        const uint64_t m = lanes_like(id[k], p.bits, in);
-        const int first = in ? (int)__builtin_ctzll(m) : lane;
-        int old = 0;
-        if (in && lane == first) old = atomicAdd(&cnt[wave * S1 + id[k]], __builtin_popcountll(m));
-        if (place) {
-          old = __shfl(old, first);
-          if (in) p.perm[old + __builtin_popcountll(m & below)] = (int32_t)i;
-        }
-      }
+    for (int k = 0; k < 8; ++k) {
+      if (b + 64 * k >= hi) break;
+      const bool in = b + 64 * k + lane < hi;
+      id[k] = place_of(id[k], p.slots);
+      const uint64_t m = lanes_like(id[k], p.bits, in);
+      const int first = in ? (int)__builtin_ctzll(m) : lane;
+      int old = 0;
+      if (in && lane == first) old = atomicAdd(&cnt[wave * S1 + id[k]], __builtin_popcountll(m));
+      pos[k] = __shfl(old, first) + __builtin_popcountll(m & below);
     }
   };
-  walk(false);
+  for (int64_t b = lo; b < hi; b += 512) {
+    if (b > lo) load(b);
+    count(b);
+  }
   __syncthreads();
-  // counts become positions: thread t has places c t .. c t + c - 1
-  const int c = (int)cdiv(S1, 1024);
-  int v[3] = {0, 0, 0}, total[3], n[5];
+  // counts become positions
+  int v[3] = {0, 0, 0}, total[3], n[kPerThread];
 #pragma unroll
-  for (int k = 0; k < 5; ++k) {  // S1 <= 4097
+  for (int k = 0; k < kPerThread; ++k) {
     const int s = tid * c + k;
     n[k] = 0;
     if (k >= c || s >= S1) continue;
+    int x[16];
 #pragma unroll
-    for (int w = 0; w < 16; ++w)
-      if (w < W) {
-        const int x = cnt[w * S1 + s];
-        cnt[w * S1 + s] = n[k];
-        n[k] += x;
-      }
+    for (int w = 0; w < 16; ++w) x[w] = w < W ? cnt[w * S1 + s] : 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      if (w < W) cnt[w * S1 + s] = n[k];
+      n[k] += x[w];
+    }
     v[0] += n[k];
     v[1] += (n[k] + kTM - 1) / kTM;
     v[2] += s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
   }
   scan3(v, total, sh);
 #pragma unroll
-  for (int k = 0; k < 5; ++k) {
+  for (int k = 0; k < kPerThread; ++k) {
     const int s = tid * c + k;
     if (k >= c || s >= S1) continue;
+    int x[16];
+#pragma unroll
+    for (int w = 0; w < 16; ++w) x[w] = w < W ? cnt[w * S1 + s] : 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w)
-      if (w < W) cnt[w * S1 + s] += v[0];
-    const int rank = n[k] ? rank_of(p.ranks, p.slots, p.r, s) : 0;
+      if (w < W) cnt[w * S1 + s] = x[w] + v[0];
     if (s < p.slots) {
       p.seg0[s] = v[2];
       for (int i = 0; i < n[k]; i += p.seg_rows) {
         const int left = n[k] - i;
-        p.segs[v[2]++] = make_int4(s, v[0] + i, left < p.seg_rows ? left : p.seg_rows, rank);
+        p.segs[v[2]++] = make_int4(s, v[0] + i, left < p.seg_rows ? left : p.seg_rows, rank[k]);
       }
     }
     for (int i = 0; i < n[k]; i += kTM) {
       const int left = n[k] - i;
-      p.tiles[v[1]++] = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank);
+      p.tiles[v[1]++] = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank[k]);
     }
     v[0] += n[k];
     p.off[s + 1] = v[0];
@@ -236,7 +248,24 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
     p.count[1] = total[2];
   }
   __syncthreads();
-  walk(true);
+  if (per <= 512) {  // places and positions are still in registers
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = lo + 64 * k + lane;
+      if (i < hi) p.perm[cnt[wave * S1 + id[k]] + pos[k]] = (int32_t)i;
+    }
+    return;
+  }
+  // else the rows are counted again, from their first positions on
+  for (int64_t b = lo; b < hi; b += 512) {
+    load(b);
+    count(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = b + 64 * k + lane;
+      if (i < hi) p.perm[pos[k]] = (int32_t)i;
+    }
+  }
 }
 
 // -------------------------------------------------------------- shrink
@@ -272,7 +301,9 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int j = 0; j < JB; ++j) acc[m][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4 x[2][MB][2], a[2][JB][2];
+  // D steps of a wave in flight
+  constexpr int D = MB == 1 ? 4 : 2;
+  u32x4 x[D][MB][2], a[D][JB][2];
   auto load = [&](int s, int b) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -293,16 +324,16 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
         for (int j = 0; j < JB; ++j) acc[m][j] = mfma16(x[b][m][h], a[b][j][h], acc[m][j]);
   };
   int s = s0 + wave;
-  if (s < s1) {
-    load(s, 0);
-    for (; s + 4 < s1; s += 8) {
-      load(s + 4, 1);
-      mul(0);
-      if (s + 8 < s1) load(s + 8, 0);
-      mul(1);
+#pragma unroll
+  for (int b = 0; b < D; ++b)
+    if (s + 4 * b < s1) load(s + 4 * b, b);
+  for (; s < s1; s += 4 * D)
+#pragma unroll
+    for (int b = 0; b < D; ++b) {
+      if (s + 4 * b >= s1) break;
+      mul(b);
+      if (s + 4 * (b + D) < s1) load(s + 4 * (b + D), b);
     }
-    if (s < s1) mul(0);
-  }
   // waves 2 and 3 to 0 and 1, then half of the blocks from 0 to 1 and half back
   constexpr int NB = MB * JB, H0 = (NB + 1) / 2;
   auto at = [&](int buf, int b) -> f32x4& { return red[(buf * NB + b) * 64 + lane]; };
@@ -368,26 +399,25 @@ struct ExpandParams {
   int32_t splits, N, ldb, rp, passes;
 };
 
-// B[n][j0 .. j0 + 7], zeros from ``rank``; ld: row stride in elements.  WHOLE:
-// ld % 8 == 0, rows 16-byte aligned
+// B[n][j0 .. j0 + 7] of rows of r ranks (zeros past r).  WHOLE: rows 16-byte
+// aligned and padded to eight
 template <bool WHOLE>
-__device__ __forceinline__ u32x4 b_operand(const uint16_t* row, int j0, int rank, int ld) {
-  if (j0 >= rank) return u32x4{0u, 0u, 0u, 0u};
-  if (WHOLE) {
-    u32x4 v = *reinterpret_cast<const u32x4*>(row + j0);
-    const int left = rank - j0;
-    if (left < 8) {
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        v[d] = 2 * d + 1 < left ? v[d] : 2 * d < left ? v[d] & 0xFFFFu : 0u;
-    }
-    return v;
-  }
+__device__ __forceinline__ u32x4 b_load(const uint16_t* row, int j0, int r) {
+  if (j0 >= r) return u32x4{0u, 0u, 0u, 0u};
+  if (WHOLE) return *reinterpret_cast<const u32x4*>(row + j0);
   uint16_t e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = j0 + i < rank ? row[j0 + i] : (uint16_t)0;
+  for (int i = 0; i < 8; ++i) e[i] = j0 + i < r ? row[j0 + i] : (uint16_t)0;
   return u32x4{(uint32_t)e[0] | ((uint32_t)e[1] << 16), (uint32_t)e[2] | ((uint32_t)e[3] << 16),
                (uint32_t)e[4] | ((uint32_t)e[5] << 16), (uint32_t)e[6] | ((uint32_t)e[7] << 16)};
+}
+
+// ... with zeros from ``rank`` on (whatever they were)
+__device__ __forceinline__ void b_mask(u32x4& v, int j0, int rank) {
+  const int left = rank - j0;
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    v[d] = 2 * d + 1 < left ? v[d] : 2 * d < left ? v[d] & 0xFFFFu : 0u;
 }
 
 // v as two bf16 parts: hi + lo is v to 2^-16 of it (lo 0 where hi is not finite)
@@ -411,22 +441,20 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
   const int n = t.n, rank = t.rank;
   if (n == 0) return;
   const bool store_t = p.T_out && blockIdx.y == 0;
-  if (rank == 0 && p.Yi == p.Yo && !store_t) return;
   const int r = p.a.r, M = p.a.M, N = p.N;
-  const float s = rank ? p.a.scales[t.slot] : 0.0f;
+  const float s = t.slot < p.a.slots ? p.a.scales[t.slot] : 0.0f;
   __syncthreads();
   const uint16_t* B = p.B + (int64_t)t.slot * N * p.ldb;
   u32x4 bf[4][JC], y[4][2];
   int64_t at[4];
   auto load = [&](int n0) {
-    if (rank) {
+    if (t.slot < p.a.slots) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
 #pragma unroll
         for (int jc = 0; jc < JC; ++jc)
-          bf[b][jc] = b_operand<WHOLE>(
-              B + (int64_t)(n0 + 16 * (i16 >> 2) + 4 * b + (i16 & 3)) * p.ldb, 32 * jc + 8 * g,
-              rank, p.ldb);
+          bf[b][jc] = b_load<WHOLE>(
+              B + (int64_t)(n0 + 16 * (i16 >> 2) + 4 * b + (i16 & 3)) * p.ldb, 32 * jc + 8 * g, r);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -439,18 +467,18 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
   };
   int n0 = (int)blockIdx.y * p.passes * 256 + 64 * wave;
   if (p.Yo && n0 < N) load(n0);
-  if (rank || store_t) {
+  {
     f32x4 v[VT];
     const float* q[VT];
     bool in[VT];
 #pragma unroll
     for (int u = 0; u < VT; ++u) {
       const int e = 256 * u + tid, i = e / (8 * JC), j = 4 * (e % (8 * JC));
-      in[u] = i < n && j < rank;
+      in[u] = i < n && j < r;
       q[u] = p.Tp + (int64_t)rows_s[in[u] ? i : 0] * p.rp + (in[u] ? j : 0);
       v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (rank) {
+    if (t.slot < p.a.slots) {  // (whatever lies past the rank)
       const int64_t part = (int64_t)M * p.rp;
       int k = 0;
       for (; k + 4 <= p.splits; k += 4) {
@@ -491,8 +519,14 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
     }
   }
   __syncthreads();
-  if (!p.Yo) return;
+  if (!p.Yo || (rank == 0 && p.Yi == p.Yo)) return;
   for (int pass = 0; pass < p.passes && n0 < N; ++pass) {
+    if (rank) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int jc = 0; jc < JC; ++jc) b_mask(bf[b][jc], 32 * jc + 8 * g, rank);
+    }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       if (16 * m >= n) break;
@@ -543,26 +577,52 @@ struct TurnParams {
 };
 
 __global__ __launch_bounds__(256) void turn_kernel(TurnParams p) {
-  __shared__ uint16_t s[64 * 66];
-  const int slot = blockIdx.y, r = p.r;
+  __shared__ uint16_t s[64 * 66];  // [rank][column]
+  const int slot = blockIdx.y, r = p.r, tid = threadIdx.x;
   if (p.off[slot + 1] == p.off[slot]) return;
   const int nb = p.N / 64;
   const bool is_b = (int)blockIdx.x < nb;
   const int c0 = (is_b ? blockIdx.x : blockIdx.x - nb) * 64;
+  // in: 64 columns of r ranks (B) or r ranks of 64 columns (A), eight elements a
+  // thread where rows allow
   if (is_b) {
     const uint16_t* B = p.B + ((int64_t)slot * p.N + c0) * r;
-    for (int e = threadIdx.x; e < 64 * r; e += 256) s[(e % r) * 66 + e / r] = B[e];
+    if (r % 8 == 0) {
+      for (int e = tid; e < 8 * r; e += 256) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(B + 8 * e);
+        const int c = 8 * e / r, j = 8 * e % r;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[(j + k) * 66 + c] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+      }
+    } else {
+      for (int e = tid; e < 64 * r; e += 256) s[(e % r) * 66 + e / r] = B[e];
+    }
     __syncthreads();
-    for (int e = threadIdx.x; e < 64 * r; e += 256)
-      p.Bt[((int64_t)slot * r + e / 64) * p.N + c0 + e % 64] = s[(e / 64) * 66 + e % 64];
+    for (int e = tid; e < 8 * r; e += 256) {
+      const int j = e >> 3, c = 8 * (e & 7);
+      u32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = s[j * 66 + c + 2 * k] | ((uint32_t)s[j * 66 + c + 2 * k + 1] << 16);
+      *reinterpret_cast<u32x4*>(p.Bt + ((int64_t)slot * r + j) * p.N + c0 + c) = v;
+    }
   } else {
-    for (int e = threadIdx.x; e < 64 * r; e += 256)
-      s[(e / 64) * 66 + e % 64] = p.A[((int64_t)slot * r + e / 64) * p.K + c0 + e % 64];
+    for (int e = tid; e < 8 * r; e += 256) {
+      const int j = e >> 3, c = 8 * (e & 7);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p.A + ((int64_t)slot * r + j) * p.K + c0 + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[j * 66 + c + k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    }
     __syncthreads();
-    uint16_t* At = p.At + ((int64_t)slot * p.K + c0) * p.ld;
-    for (int e = threadIdx.x; e < 64 * p.ld; e += 256) {
-      const int j = e % p.ld;
-      At[e] = j < r ? s[j * 66 + e / p.ld] : (uint16_t)0;
+    for (int e = tid; e < 8 * p.ld; e += 256) {  // rows of ld = r rounded up to eight
+      const int c = 8 * e / p.ld, j = 8 * e % p.ld;
+      u32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = j + 2 * k < r ? s[(j + 2 * k) * 66 + c] : 0u;
+        const uint32_t hi = j + 2 * k + 1 < r ? s[(j + 2 * k + 1) * 66 + c] : 0u;
+        v[k] = lo | (hi << 16);
+      }
+      *reinterpret_cast<u32x4*>(p.At + ((int64_t)slot * p.K + c0) * p.ld + 8 * e) = v;
     }
   }
 }
@@ -587,6 +647,7 @@ struct GradParams {
 
 constexpr int kZP = 256 + 16;  // LDS row pitch of a step's columns, in elements
 constexpr int kVP = 32 + 8;    // ... of the parts of U or T
+constexpr int kRowsLds = 512;  // row indices in LDS, two halves
 
 typedef short s16x4g __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x2 read_turned(uint16_t* p) {
@@ -597,7 +658,7 @@ __device__ __forceinline__ u32x2 read_turned(uint16_t* p) {
 
 template <int JB, bool DB>
 __device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, uint16_t* zs,
-                                          uint16_t* vs) {
+                                          uint16_t* vs, int32_t* rows_s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const int4 sg = p.a.segs[seg];
@@ -611,60 +672,77 @@ __device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, 
   for (int c = 0; c < 4; ++c)
 #pragma unroll
     for (int j = 0; j < JB; ++j) acc[c][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4 z[4];
-  float v[VE];
+  u32x4 z[2][4];
+  float v[2][VE];
   // piece k of a thread: row 8 k + tid / 32, columns 8 (tid % 32)
-  auto load = [&](int b) {
+  auto load = [&](int b, int buf) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int i = b + 8 * k + (tid >> 5), c = c0 + 8 * (tid & 31);
-      z[k] = u32x4{0u, 0u, 0u, 0u};
-      if (i < n && c < C) z[k] = *reinterpret_cast<const u32x4*>(Z + (int64_t)perm[i] * C + c);
+      z[buf][k] = u32x4{0u, 0u, 0u, 0u};
+      if (i < n && c < C)
+        z[buf][k] = *reinterpret_cast<const u32x4*>(Z + (int64_t)rows_s[i % kRowsLds] * C + c);
     }
 #pragma unroll
     for (int k = 0; k < VE; ++k) {
       const int e = 256 * k + tid, i = b + e / R, j = e % R;
-      v[k] = 0.0f;
-      if (i < n && j < rank) v[k] = V[(int64_t)perm[i] * r + j];
+      v[buf][k] = 0.0f;
+      if (i < n && j < rank) v[buf][k] = V[(int64_t)rows_s[i % kRowsLds] * r + j];
     }
   };
+  // the indices of rows b0 .. b0 + kRowsLds / 2 - 1 into their half of the list
+  auto rows = [&](int b0) {
+    for (int i = b0 + tid; i < n && i < b0 + kRowsLds / 2; i += 256) rows_s[i % kRowsLds] = perm[i];
+  };
+  auto step = [&](int b, int buf) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<u32x4*>(zs + (8 * k + (tid >> 5)) * kZP + 8 * (tid & 31)) = z[buf][k];
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      const int e = 256 * k + tid, i = e / R, j = e % R;
+      const uint16_t hi = f32_to_bf16(v[buf][k]);
+      const bool fin = (hi & 0x7F80u) != 0x7F80u;
+      const float r1 = fin ? v[buf][k] - bf16_to_f32(hi) : 0.0f;
+      const uint16_t mid = f32_to_bf16(r1);
+      vs[j * kVP + i] = hi;
+      vs[(R + j) * kVP + i] = mid;
+      vs[(2 * R + j) * kVP + i] = f32_to_bf16(r1 - bf16_to_f32(mid));
+    }
+    __syncthreads();
+    if (b + 64 < n) {
+      // (rows of steps b + 64 .. were listed before the barriers above)
+      load(b + 64, buf);
+      if ((b + 128) % (kRowsLds / 2) == 0) rows(b + 128);
+    }
+    u32x4 zf[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint16_t* q = zs + (8 * g + (i16 >> 2)) * kZP + 64 * wave + 16 * c + 4 * (i16 & 3);
+      const u32x2 lo = read_turned(q), hi = read_turned(q + 4 * kZP);
+      zf[c] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+#pragma unroll
+    for (int part = 2; part >= 0; --part)
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        const u32x4 vf =
+            *reinterpret_cast<const u32x4*>(vs + (part * R + 16 * j + i16) * kVP + 8 * g);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[c][j] = DB ? mfma16(vf, zf[c], acc[c][j]) : mfma16(zf[c], vf, acc[c][j]);
+      }
+  };
   if (rank) {
-    load(0);
-    for (int b = 0; b < n; b += 32) {
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<u32x4*>(zs + (8 * k + (tid >> 5)) * kZP + 8 * (tid & 31)) = z[k];
-#pragma unroll
-      for (int k = 0; k < VE; ++k) {
-        const int e = 256 * k + tid, i = e / R, j = e % R;
-        const uint16_t hi = f32_to_bf16(v[k]);
-        const bool fin = (hi & 0x7F80u) != 0x7F80u;
-        const float r1 = fin ? v[k] - bf16_to_f32(hi) : 0.0f;
-        const uint16_t mid = f32_to_bf16(r1);
-        vs[j * kVP + i] = hi;
-        vs[(R + j) * kVP + i] = mid;
-        vs[(2 * R + j) * kVP + i] = f32_to_bf16(r1 - bf16_to_f32(mid));
-      }
-      __syncthreads();
-      if (b + 32 < n) load(b + 32);
-      u32x4 zf[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint16_t* q = zs + (8 * g + (i16 >> 2)) * kZP + 64 * wave + 16 * c + 4 * (i16 & 3);
-        const u32x2 lo = read_turned(q), hi = read_turned(q + 4 * kZP);
-        zf[c] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-      }
-#pragma unroll
-      for (int part = 2; part >= 0; --part)
-#pragma unroll
-        for (int j = 0; j < JB; ++j) {
-          const u32x4 vf =
-              *reinterpret_cast<const u32x4*>(vs + (part * R + 16 * j + i16) * kVP + 8 * g);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            acc[c][j] = DB ? mfma16(vf, zf[c], acc[c][j]) : mfma16(zf[c], vf, acc[c][j]);
-        }
+    rows(0);
+    rows(kRowsLds / 2);
+    __syncthreads();
+    load(0, 0);
+    if (n > 32) load(32, 1);
+    for (int b = 0; b < n; b += 64) {
+      step(b, 0);
+      if (b + 32 < n) step(b + 32, 1);
     }
   }
   const int first = p.a.seg0[slot];
@@ -697,12 +775,13 @@ template <int JB>
 __global__ __launch_bounds__(256) void adapter_grads_kernel(GradParams p) {
   __shared__ __attribute__((aligned(16))) uint16_t zs[32 * kZP];
   __shared__ __attribute__((aligned(16))) uint16_t vs[3 * 16 * JB * kVP];
+  __shared__ int32_t rows_s[kRowsLds];
   if ((int)blockIdx.y >= p.a.count[1]) return;
   const int ca = (p.K + 255) / 256;
   if ((int)blockIdx.x < ca)
-    grad_tile<JB, false>(p, blockIdx.y, 256 * blockIdx.x, zs, vs);
+    grad_tile<JB, false>(p, blockIdx.y, 256 * blockIdx.x, zs, vs, rows_s);
   else
-    grad_tile<JB, true>(p, blockIdx.y, 256 * (blockIdx.x - ca), zs, vs);
+    grad_tile<JB, true>(p, blockIdx.y, 256 * (blockIdx.x - ca), zs, vs, rows_s);
 }
 
 // Places of several segments: their sums in order; places without rows: zeros.
@@ -741,13 +820,20 @@ int64_t max_tiles(int64_t M, int32_t slots) {
   const int64_t t = cdiv(M, kTM) + slots;
   return t < M ? t : M;
 }
+// a multiple of eight, so that a tile's workgroups of both launches run on one
+// XCD and find T's partial sums in its L2
+unsigned tile_grid(const RowArgs& a) {
+  const int64_t t = max_tiles(a.M, a.slots);
+  return (unsigned)(a.tiles ? cdiv(t, 8) * 8 : t);
+}
 
 // Splits of the shrink's reduction over C columns: about 512 workgroups where
-// tiles are full, and no wave without a step
+// tiles are full, each wave with four steps at least, so that they are in flight
+// together
 int shrink_splits(int64_t M, int64_t C) {
-  const int64_t most = cdiv(C / 64, 4), want = cdiv(512, cdiv(M, kTM));
+  const int64_t most = cdiv(C / 64, 16), want = cdiv(512, cdiv(M, kTM));
   const int64_t s = want < most ? want : most;
-  return (int)(s < 32 ? s : 32);
+  return (int)(s < 16 ? s : 16);
 }
 
 // Rows of a segment of the gradients: about 768 workgroups where places have
@@ -771,7 +857,7 @@ PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   l.seg0 = up256((size_t)(slots + 2) * 4);
   l.count = l.seg0 + up256((size_t)(slots + 2) * 4);
   l.tiles = l.count + 256;
-  l.segs = l.tiles + up256((size_t)max_tiles(M > kDirect ? M : kDirect + 1, slots) * 16);
+  l.segs = l.tiles + up256((size_t)(max_tiles(M > kDirect ? M : kDirect + 1, slots) + 7) * 16);
   l.perm = l.segs + up256((size_t)segs * 16);
   l.end = l.perm + up256((size_t)M * 4);
   return l;
@@ -814,7 +900,7 @@ int launch_shrink(const RowArgs& a, const void* X, const void* A, int64_t C, flo
   p.C = (int32_t)C;
   p.rp = t_pitch(a.r);
   p.steps = (int32_t)cdiv(C / 64, splits);
-  const dim3 g((unsigned)max_tiles(a.M, a.slots), (unsigned)splits), b(256);
+  const dim3 g(tile_grid(a), (unsigned)splits), b(256);
   switch ((a.r + 15) / 16) {
     case 1: hipLaunchKernelGGL(shrink_tiles_kernel<1>, g, b, 0, st, p); break;
     case 2: hipLaunchKernelGGL(shrink_tiles_kernel<2>, g, b, 0, st, p); break;
@@ -844,7 +930,7 @@ int launch_expand(const RowArgs& a, const float* Tp, int splits, const void* B, 
   int64_t passes = full * chunks / 4096;
   passes = passes < 1 ? 1 : passes > 8 ? 8 : passes;
   p.passes = (int32_t)passes;
-  const dim3 g((unsigned)max_tiles(a.M, a.slots), (unsigned)cdiv(chunks, passes)), b(256);
+  const dim3 g(tile_grid(a), (unsigned)cdiv(chunks, passes)), b(256);
   const auto kernel = a.r <= 32 ? (ldb % 8 ? expand_tiles_kernel<1, false> : expand_tiles_kernel<1, true>)
                                 : (ldb % 8 ? expand_tiles_kernel<2, false> : expand_tiles_kernel<2, true>);
   hipLaunchKernelGGL(kernel, g, b, 0, st, p);
