@@ -61,6 +61,15 @@ struct Tile {
   int slot, n, rank;  // n = 0: none
 };
 
+// Tile and part (of ``parts``) of workgroup b.  Workgroups of one tile stay on one
+// XCD, b % 8, and the parts run first: rows lie a power of two of bytes apart, so
+// workgroups that read the same columns of many rows meet in few channels of L2.
+__device__ __forceinline__ int tile_of(const RowArgs& a, int b, int parts, int& part) {
+  const int q = a.tiles ? b >> 3 : b;
+  part = q % parts;
+  return a.tiles ? q / parts * 8 + (b & 7) : q / parts;
+}
+
 // This workgroup's tile, and its rows' indices in rows_s (ready after the
 // caller's next barrier).
 __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* rows_s) {
@@ -180,17 +189,25 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   // Counts the wave's rows by place; pos: a row's position among those that the
   // counter has seen.
   auto count = [&](int64_t b) {
+    int old[8], first[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (b + 64 * k >= hi) break;
-      const bool in = b + 64 * k + lane < hi;
+      old[k] = first[k] = 0;
+      pos[k] = lane;
       id[k] = place_of(id[k], p.slots);
-      const uint64_t m = lanes_like(id[k], p.bits, in);
-      const int first = in ? (int)__builtin_ctzll(m) : lane;
-      int old = 0;
-      if (in && lane == first) old = atomicAdd(&cnt[wave * S1 + id[k]], __builtin_popcountll(m));
-      pos[k] = __shfl(old, first) + __builtin_popcountll(m & below);
+      if (b + 64 * k >= hi) continue;
+      const bool in = b + 64 * k + lane < hi;
+      uint64_t m = __ballot(in);
+      // (a request's rows mostly fill the wave)
+      if (__ballot(in && id[k] == __builtin_amdgcn_readfirstlane(id[k])) != m)
+        m = lanes_like(id[k], p.bits, in);
+      first[k] = in ? (int)__builtin_ctzll(m) : lane;
+      pos[k] = __builtin_popcountll(m & below);
+      if (in && lane == first[k])
+        old[k] = atomicAdd(&cnt[wave * S1 + id[k]], __builtin_popcountll(m));
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) pos[k] += __shfl(old[k], first[k]);
   };
   for (int64_t b = lo; b < hi; b += 512) {
     if (b > lo) load(b);
@@ -217,6 +234,11 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
     v[2] += s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
   }
   scan3(v, total, sh);
+  // Workgroup b runs on XCD b % 8: each XCD gets consecutive tiles, so that few of
+  // them read the same factors.
+  const int per_xcd = (total[1] + 7) / 8;
+  auto tile_at = [&](int t) -> int4& { return p.tiles[t % per_xcd * 8 + t / per_xcd]; };
+  if (tid < 8 * per_xcd - total[1]) tile_at(total[1] + tid) = make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int s = tid * c + k;
@@ -236,7 +258,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
     }
     for (int i = 0; i < n[k]; i += kTM) {
       const int left = n[k] - i;
-      p.tiles[v[1]++] = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank[k]);
+      tile_at(v[1]++) = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank[k]);
     }
     v[0] += n[k];
     p.off[s + 1] = v[0];
@@ -244,7 +266,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   if (tid == 0) {
     p.off[0] = 0;
     p.seg0[p.slots] = total[2];
-    p.count[0] = total[1];
+    p.count[0] = 8 * per_xcd;
     p.count[1] = total[2];
   }
   __syncthreads();
@@ -275,13 +297,13 @@ struct ShrinkParams {
   const uint16_t* X;  // M x C
   const uint16_t* A;  // slots x r x C
   float* Tp;          // splits x M x rp
-  int32_t C, rp, steps;   // 64-column steps of the reduction, of one split
+  int32_t C, rp, splits, steps;   // 64-column steps of the reduction, of one split
 };
 
 template <int MB, int JB>
 __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t* rows_s, int n,
-                                            const uint16_t* A, int rank, int s0, int s1,
-                                            f32x4* red) {
+                                            const uint16_t* A, int rank, int s0, int s1, int turn,
+                                            int part, f32x4* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const uint16_t* xr[MB];
@@ -301,38 +323,36 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int j = 0; j < JB; ++j) acc[m][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // D steps of a wave in flight
-  constexpr int D = MB == 1 ? 4 : 2;
-  u32x4 x[D][MB][2], a[D][JB][2];
-  auto load = [&](int s, int b) {
+  // halves of steps in flight, by the registers they take
+  constexpr int D = MB + JB >= 7 ? 2 : MB + JB >= 5 ? 3 : MB + JB == 4 ? 4 : MB + JB == 3 ? 6 : 8;
+  u32x4 x[D][MB], a[D][JB];
+  // the wave's quarter of the steps, from a step on that goes by the tile
+  const int w0 = s0 + (s1 - s0) * wave / 4, nw = s0 + (s1 - s0) * (wave + 1) / 4 - w0;
+  const int off = nw > 0 ? turn % nw : 0;
+  auto load = [&](int i, int b) {
+    int st = (i >> 1) + off;
+    st = w0 + (st < nw ? st : st - nw);
+    const int c = 64 * st + 32 * (i & 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int m = 0; m < MB; ++m) x[b][m] = *reinterpret_cast<const u32x4*>(xr[m] + c);
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
-        x[b][m][h] = *reinterpret_cast<const u32x4*>(xr[m] + 64 * s + 32 * h);
-#pragma unroll
-      for (int j = 0; j < JB; ++j)
-        a[b][j][h] = *reinterpret_cast<const u32x4*>(ar[j] + 64 * s + 32 * h);
-    }
+    for (int j = 0; j < JB; ++j) a[b][j] = *reinterpret_cast<const u32x4*>(ar[j] + c);
   };
   auto mul = [&](int b) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int j = 0; j < JB; ++j) acc[m][j] = mfma16(x[b][m][h], a[b][j][h], acc[m][j]);
+      for (int j = 0; j < JB; ++j) acc[m][j] = mfma16(x[b][m], a[b][j], acc[m][j]);
   };
-  int s = s0 + wave;
 #pragma unroll
   for (int b = 0; b < D; ++b)
-    if (s + 4 * b < s1) load(s + 4 * b, b);
-  for (; s < s1; s += 4 * D)
+    if (b < 2 * nw) load(b, b);
+  for (int i = 0; i < 2 * nw; i += D)
 #pragma unroll
     for (int b = 0; b < D; ++b) {
-      if (s + 4 * b >= s1) break;
+      if (i + b >= 2 * nw) break;
       mul(b);
-      if (s + 4 * (b + D) < s1) load(s + 4 * (b + D), b);
+      if (i + b + D < 2 * nw) load(i + b + D, b);
     }
   // waves 2 and 3 to 0 and 1, then half of the blocks from 0 to 1 and half back
   constexpr int NB = MB * JB, H0 = (NB + 1) / 2;
@@ -355,7 +375,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
       if ((b < H0) == (wave == 1)) at(wave, b) = acc[b / JB][b % JB];
   __syncthreads();
   if (wave >= 2) return;
-  float* out = p.Tp + (int64_t)blockIdx.y * p.a.M * p.rp;
+  float* out = p.Tp + (int64_t)part * p.a.M * p.rp;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     if ((b < H0) != (wave == 0)) continue;
@@ -370,21 +390,23 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
 }
 
 template <int JB>
-__global__ __launch_bounds__(256) void shrink_tiles_kernel(ShrinkParams p) {
+__global__ __launch_bounds__(256, JB <= 2 ? 4 : 3) void shrink_tiles_kernel(ShrinkParams p) {
   __shared__ int32_t rows_s[kTM];
   __shared__ f32x4 red[2 * 4 * JB * 64];
-  const Tile t = find_tile(p.a, blockIdx.x, rows_s);
+  int part;
+  const int tile = tile_of(p.a, blockIdx.x, p.splits, part);
+  const Tile t = find_tile(p.a, tile, rows_s);
   if (t.n == 0 || t.rank == 0) return;
   __syncthreads();
-  const int s0 = blockIdx.y * p.steps, all = p.C / 64;
+  const int s0 = part * p.steps, all = p.C / 64;
   const int s1 = s0 + p.steps < all ? s0 + p.steps : all;
   const uint16_t* A = p.A + (int64_t)t.slot * p.a.r * p.C;
   if (t.n <= 16)
-    shrink_tile<1, JB>(p, rows_s, t.n, A, t.rank, s0, s1, red);
+    shrink_tile<1, JB>(p, rows_s, t.n, A, t.rank, s0, s1, tile, part, red);
   else if (t.n <= 32)
-    shrink_tile<2, JB>(p, rows_s, t.n, A, t.rank, s0, s1, red);
+    shrink_tile<2, JB>(p, rows_s, t.n, A, t.rank, s0, s1, tile, part, red);
   else
-    shrink_tile<4, JB>(p, rows_s, t.n, A, t.rank, s0, s1, red);
+    shrink_tile<4, JB>(p, rows_s, t.n, A, t.rank, s0, s1, tile, part, red);
 }
 
 // -------------------------------------------------------------- expand
@@ -396,7 +418,7 @@ struct ExpandParams {
   const uint16_t* Yi;
   uint16_t* Yo;
   float* T_out;  // M x r or NULL
-  int32_t splits, N, ldb, rp, passes;
+  int32_t splits, N, ldb, rp, parts, passes;
 };
 
 // B[n][j0 .. j0 + 7] of rows of r ranks (zeros past r).  WHOLE: rows 16-byte
@@ -430,23 +452,25 @@ __device__ __forceinline__ void split2(float v, uint16_t& hi, uint16_t& lo) {
 // JC: 32-rank chunks.  What does not depend on T (B, Y) is loaded before T's
 // partial sums are waited for.
 template <int JC, bool WHOLE>
-__global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
+__global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(ExpandParams p) {
   constexpr int LD = 32 * JC + 8;  // LDS row pitch of T in elements
   constexpr int VT = 2 * JC;       // groups of four values of T per thread
   __shared__ int32_t rows_s[kTM];
   __shared__ __attribute__((aligned(16))) uint16_t t_hi[kTM * LD], t_lo[kTM * LD];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, i16 = lane & 15;
-  const Tile t = find_tile(p.a, blockIdx.x, rows_s);
+  int part;
+  const int tile = tile_of(p.a, blockIdx.x, p.parts, part);
+  const Tile t = find_tile(p.a, tile, rows_s);
   const int n = t.n, rank = t.rank;
   if (n == 0) return;
-  const bool store_t = p.T_out && blockIdx.y == 0;
+  const bool store_t = p.T_out && part == 0;
   const int r = p.a.r, M = p.a.M, N = p.N;
   const float s = t.slot < p.a.slots ? p.a.scales[t.slot] : 0.0f;
   __syncthreads();
   const uint16_t* B = p.B + (int64_t)t.slot * N * p.ldb;
   u32x4 bf[4][JC], y[4][2];
-  int64_t at[4];
+  int32_t at[4];  // M N < 2^31
   auto load = [&](int n0) {
     if (t.slot < p.a.slots) {
 #pragma unroll
@@ -460,35 +484,37 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
     for (int m = 0; m < 4; ++m) {
       if (16 * m >= n) break;
       const int i = 16 * m + i16;
-      at[m] = (int64_t)rows_s[i < n ? i : n - 1] * N + n0 + 16 * g;
+      at[m] = rows_s[i < n ? i : n - 1] * N + n0 + 16 * g;
       y[m][0] = *reinterpret_cast<const u32x4*>(p.Yi + at[m]);
       y[m][1] = *reinterpret_cast<const u32x4*>(p.Yi + at[m] + 8);
     }
   };
-  int n0 = (int)blockIdx.y * p.passes * 256 + 64 * wave;
+  int n0 = part * p.passes * 256 + 64 * wave;
   if (p.Yo && n0 < N) load(n0);
   {
     f32x4 v[VT];
-    const float* q[VT];
+    int32_t q[VT];
     bool in[VT];
 #pragma unroll
     for (int u = 0; u < VT; ++u) {
       const int e = 256 * u + tid, i = e / (8 * JC), j = 4 * (e % (8 * JC));
       in[u] = i < n && j < r;
-      q[u] = p.Tp + (int64_t)rows_s[in[u] ? i : 0] * p.rp + (in[u] ? j : 0);
+      q[u] = rows_s[in[u] ? i : 0] * p.rp + (in[u] ? j : 0);
       v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     if (t.slot < p.a.slots) {  // (whatever lies past the rank)
       const int64_t part = (int64_t)M * p.rp;
       int k = 0;
-      for (; k + 4 <= p.splits; k += 4) {
-        f32x4 x[4][VT];
+      constexpr int D = 4 / JC;
+      for (; k + D <= p.splits; k += D) {
+        f32x4 x[D][VT];
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
+        for (int d = 0; d < D; ++d)
 #pragma unroll
-          for (int u = 0; u < VT; ++u) x[d][u] = *reinterpret_cast<const f32x4*>(q[u] + (k + d) * part);
+          for (int u = 0; u < VT; ++u)
+            x[d][u] = *reinterpret_cast<const f32x4*>(p.Tp + (k + d) * part + q[u]);
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
+        for (int d = 0; d < D; ++d)
 #pragma unroll
           for (int u = 0; u < VT; ++u)
 #pragma unroll
@@ -497,7 +523,7 @@ __global__ __launch_bounds__(256) void expand_tiles_kernel(ExpandParams p) {
       for (; k < p.splits; ++k)
 #pragma unroll
         for (int u = 0; u < VT; ++u) {
-          const f32x4 x = *reinterpret_cast<const f32x4*>(q[u] + k * part);
+          const f32x4 x = *reinterpret_cast<const f32x4*>(p.Tp + k * part + q[u]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[u][e] += x[e];
         }
@@ -752,27 +778,35 @@ __device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, 
   float* out = whole ? (DB ? p.dB + (int64_t)slot * p.N * r : p.dA + (int64_t)slot * r * p.K)
                      : p.part + seg * size + (DB ? (int64_t)r * p.K : 0);
   const bool add = whole && p.accumulate;
+  const bool wide = !DB || r % 4 == 0;  // four results of a lane are one aligned group
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int j = 0; j < JB; ++j)
+    for (int j = 0; j < JB; ++j) {
+      const int col = c0 + 64 * wave + 16 * c + (DB ? i16 : 4 * g);
+      const int k = 16 * j + (DB ? 4 * g : i16);
+      if (col >= C || k >= r) continue;
+      float* o = DB ? out + (int64_t)col * r + k : out + (int64_t)k * C + col;
+      f32x4 x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = c0 + 64 * wave + 16 * c + (DB ? i16 : 4 * g + e);
-        const int k = 16 * j + (DB ? 4 * g + e : i16);
-        if (col >= C || k >= r) continue;
-        float* o = DB ? out + (int64_t)col * r + k : out + (int64_t)k * C + col;
-        if (k < rank) {
-          const float x = s * acc[c][j][e];
-          *o = add ? *o + x : x;
-        } else if (!add) {
-          *o = 0.0f;
+      for (int e = 0; e < 4; ++e) x[e] = (DB ? k + e : k) < rank ? s * acc[c][j][e] : 0.0f;
+      if (wide) {
+        if (add) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] += y[e];
         }
+        *reinterpret_cast<f32x4*>(o) = x;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (k + e < r) o[e] = add ? o[e] + x[e] : x[e];
       }
+    }
 }
 
 template <int JB>
-__global__ __launch_bounds__(256) void adapter_grads_kernel(GradParams p) {
+__global__ __launch_bounds__(256, JB <= 2 ? 4 : 3) void adapter_grads_kernel(GradParams p) {
   __shared__ __attribute__((aligned(16))) uint16_t zs[32 * kZP];
   __shared__ __attribute__((aligned(16))) uint16_t vs[3 * 16 * JB * kVP];
   __shared__ int32_t rows_s[kRowsLds];
@@ -899,8 +933,9 @@ int launch_shrink(const RowArgs& a, const void* X, const void* A, int64_t C, flo
   p.Tp = Tp;
   p.C = (int32_t)C;
   p.rp = t_pitch(a.r);
+  p.splits = splits;
   p.steps = (int32_t)cdiv(C / 64, splits);
-  const dim3 g(tile_grid(a), (unsigned)splits), b(256);
+  const dim3 g(tile_grid(a) * (unsigned)splits), b(256);
   switch ((a.r + 15) / 16) {
     case 1: hipLaunchKernelGGL(shrink_tiles_kernel<1>, g, b, 0, st, p); break;
     case 2: hipLaunchKernelGGL(shrink_tiles_kernel<2>, g, b, 0, st, p); break;
@@ -930,7 +965,8 @@ int launch_expand(const RowArgs& a, const float* Tp, int splits, const void* B, 
   int64_t passes = full * chunks / 4096;
   passes = passes < 1 ? 1 : passes > 8 ? 8 : passes;
   p.passes = (int32_t)passes;
-  const dim3 g(tile_grid(a), (unsigned)cdiv(chunks, passes)), b(256);
+  p.parts = (int32_t)cdiv(chunks, passes);
+  const dim3 g(tile_grid(a) * (unsigned)p.parts), b(256);
   const auto kernel = a.r <= 32 ? (ldb % 8 ? expand_tiles_kernel<1, false> : expand_tiles_kernel<1, true>)
                                 : (ldb % 8 ? expand_tiles_kernel<2, false> : expand_tiles_kernel<2, true>);
   hipLaunchKernelGGL(kernel, g, b, 0, st, p);
