@@ -61,9 +61,11 @@ struct Tile {
   int slot, n, rank;  // n = 0: none
 };
 
-// Tile and part (of ``parts``) of workgroup b.  Workgroups of one tile stay on one
-// XCD, b % 8, and the parts run first: rows lie a power of two of bytes apart, so
-// workgroups that read the same columns of many rows meet in few channels of L2.
+// Tile and part (of ``parts``) of workgroup b: workgroups of one tile stay on one
+// XCD, b % 8 (its rows and T's partial sums stay in that L2), and its parts run
+// together.  Tiles go round the XCDs: consecutive ones on one XCD would share its
+// factors, but the short tiles at the end leave the last XCD idle (8192 rows, 16
+// places: 87 us against 78).
 __device__ __forceinline__ int tile_of(const RowArgs& a, int b, int parts, int& part) {
   const int q = a.tiles ? b >> 3 : b;
   part = q % parts;
@@ -234,11 +236,6 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
     v[2] += s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
   }
   scan3(v, total, sh);
-  // Workgroup b runs on XCD b % 8: each XCD gets consecutive tiles, so that few of
-  // them read the same factors.
-  const int per_xcd = (total[1] + 7) / 8;
-  auto tile_at = [&](int t) -> int4& { return p.tiles[t % per_xcd * 8 + t / per_xcd]; };
-  if (tid < 8 * per_xcd - total[1]) tile_at(total[1] + tid) = make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int s = tid * c + k;
@@ -258,7 +255,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
     }
     for (int i = 0; i < n[k]; i += kTM) {
       const int left = n[k] - i;
-      tile_at(v[1]++) = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank[k]);
+      p.tiles[v[1]++] = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank[k]);
     }
     v[0] += n[k];
     p.off[s + 1] = v[0];
@@ -266,7 +263,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
   if (tid == 0) {
     p.off[0] = 0;
     p.seg0[p.slots] = total[2];
-    p.count[0] = 8 * per_xcd;
+    p.count[0] = total[1];
     p.count[1] = total[2];
   }
   __syncthreads();
@@ -302,8 +299,8 @@ struct ShrinkParams {
 
 template <int MB, int JB>
 __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t* rows_s, int n,
-                                            const uint16_t* A, int rank, int s0, int s1, int turn,
-                                            int part, f32x4* red) {
+                                            const uint16_t* A, int rank, int s0, int s1, int part,
+                                            f32x4* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const uint16_t* xr[MB];
@@ -326,13 +323,10 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
   // halves of steps in flight, by the registers they take
   constexpr int D = MB + JB >= 7 ? 2 : MB + JB >= 5 ? 3 : MB + JB == 4 ? 4 : MB + JB == 3 ? 6 : 8;
   u32x4 x[D][MB], a[D][JB];
-  // the wave's quarter of the steps, from a step on that goes by the tile
-  const int w0 = s0 + (s1 - s0) * wave / 4, nw = s0 + (s1 - s0) * (wave + 1) / 4 - w0;
-  const int off = nw > 0 ? turn % nw : 0;
+  // every fourth step: the waves read whole 512-byte pieces of a row between them
+  const int nw = (s1 - s0 - wave + 3) / 4;
   auto load = [&](int i, int b) {
-    int st = (i >> 1) + off;
-    st = w0 + (st < nw ? st : st - nw);
-    const int c = 64 * st + 32 * (i & 1);
+    const int c = 64 * (s0 + wave + 4 * (i >> 1)) + 32 * (i & 1);
 #pragma unroll
     for (int m = 0; m < MB; ++m) x[b][m] = *reinterpret_cast<const u32x4*>(xr[m] + c);
 #pragma unroll
@@ -402,11 +396,11 @@ __global__ __launch_bounds__(256, JB <= 2 ? 4 : 3) void shrink_tiles_kernel(Shri
   const int s1 = s0 + p.steps < all ? s0 + p.steps : all;
   const uint16_t* A = p.A + (int64_t)t.slot * p.a.r * p.C;
   if (t.n <= 16)
-    shrink_tile<1, JB>(p, rows_s, t.n, A, t.rank, s0, s1, tile, part, red);
+    shrink_tile<1, JB>(p, rows_s, t.n, A, t.rank, s0, s1, part, red);
   else if (t.n <= 32)
-    shrink_tile<2, JB>(p, rows_s, t.n, A, t.rank, s0, s1, tile, part, red);
+    shrink_tile<2, JB>(p, rows_s, t.n, A, t.rank, s0, s1, part, red);
   else
-    shrink_tile<4, JB>(p, rows_s, t.n, A, t.rank, s0, s1, tile, part, red);
+    shrink_tile<4, JB>(p, rows_s, t.n, A, t.rank, s0, s1, part, red);
 }
 
 // -------------------------------------------------------------- expand
