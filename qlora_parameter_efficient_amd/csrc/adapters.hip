@@ -10,17 +10,14 @@
 // (one per lane, one ballot) and goes on only if row i is the first with its
 // adapter.  More rows are sorted by one workgroup first (plan_kernel).
 //
-// Shrink (T = X A^T, U = dY B): no LDS in its loop.  The four waves of a
-// workgroup take turns at 64-column steps of the reduction, each with all the
-// tile's rows and ranks, so that an operand line is read once per workgroup,
-// and are added at the end; further workgroups split the reduction, their
-// partial sums are added in order by the expand.
-// Expand (Y += s T B^T, dX += s U A): the output transposed (B's rows = MFMA
-// rows), with B's rows permuted so that a lane holds 16 consecutive outputs of
-// a row and four lanes a whole 128-byte line.
+// Shrink (T = X A^T, U = dY B): workgroups split the reduction, their partial sums
+// are added in order by the expand.
+// Expand (Y += s T B^T, dX += s U A): rows of B in an order (column 4 i + b of a
+// 64-column block is column i of MFMA block b) that gives a lane four consecutive
+// outputs of a row and 16 lanes a whole 128-byte line.
 #include "block.h"
-#include "device_util.h"
 #include "dispatch.h"
+#include "mx_tile.h"
 
 namespace lq {
 namespace {
@@ -80,7 +77,7 @@ __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* r
   if (!a.tiles) {
     const int id = lane < a.M ? place_of(a.rows[lane], a.slots) : -1;
     t.slot = __builtin_amdgcn_readlane(id, tile);
-    t.rank = rank_of(a.ranks, a.slots, a.r, t.slot);
+    t.rank = __builtin_amdgcn_readfirstlane(rank_of(a.ranks, a.slots, a.r, t.slot));
     const uint64_t same = __ballot(id == t.slot);
     t.n = (int)__builtin_ctzll(same) == tile ? __builtin_popcountll(same) : 0;
     if (threadIdx.x < 64 && id == t.slot)
@@ -88,10 +85,10 @@ __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* r
     return t;
   }
   const int4 d = a.tiles[tile];  // (past the last tile: not used)
-  const bool any = tile < a.count[0];
-  t.slot = d.x;
-  t.n = any ? d.z : 0;
-  t.rank = d.w;
+  // (the same for every lane, and known to be)
+  t.slot = __builtin_amdgcn_readfirstlane(d.x);
+  t.n = __builtin_amdgcn_readfirstlane(tile < a.count[0] ? d.z : 0);
+  t.rank = __builtin_amdgcn_readfirstlane(d.w);
   if ((int)threadIdx.x < t.n) rows_s[threadIdx.x] = a.perm[d.y + threadIdx.x];
   return t;
 }
@@ -297,46 +294,51 @@ struct ShrinkParams {
   int32_t C, rp, splits, steps;   // 64-column steps of the reduction, of one split
 };
 
-template <int MB, int JB>
-__device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t* rows_s, int n,
-                                            const uint16_t* A, int rank, int s0, int s1, int part,
-                                            f32x4* red) {
+// p, the same in every lane, in scalar registers
+__device__ __forceinline__ const char* uniform(const void* p) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return (const char*)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
+
+// 16 bytes per lane from base + off to LDS at lds + 16 lane; the kernels wait for
+// these loads themselves
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1"
+      :
+      : "v"(off), "s"(base), "s"(lds)
+      : "memory", "m0");
+}
+
+// At most 16 rows: operands straight into registers, the four waves taking turns
+// at the steps of the split.
+template <int JB>
+__device__ __forceinline__ void shrink_few(const ShrinkParams& p, const int32_t* rows_s, int n,
+                                           const uint16_t* A, int rank, int s0, int s1, float* out,
+                                           f32x4* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
-  const uint16_t* xr[MB];
+  const uint16_t* xr = p.X + (int64_t)rows_s[i16 < n ? i16 : n - 1] * p.C + 8 * g;
   const uint16_t* ar[JB];
-#pragma unroll
-  for (int m = 0; m < MB; ++m) {
-    const int i = 16 * m + i16;
-    xr[m] = p.X + (int64_t)rows_s[i < n ? i : n - 1] * p.C + 8 * g;
-  }
+  f32x4 acc[JB];
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
     const int k = 16 * j + i16;
     ar[j] = A + (int64_t)(k < rank ? k : rank - 1) * p.C + 8 * g;
+    acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  f32x4 acc[MB][JB];
-#pragma unroll
-  for (int m = 0; m < MB; ++m)
-#pragma unroll
-    for (int j = 0; j < JB; ++j) acc[m][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // halves of steps in flight, by the registers they take
-  constexpr int D = MB + JB >= 7 ? 2 : MB + JB >= 5 ? 3 : MB + JB == 4 ? 4 : MB + JB == 3 ? 6 : 8;
-  u32x4 x[D][MB], a[D][JB];
-  // every fourth step: the waves read whole 512-byte pieces of a row between them
+  constexpr int D = JB == 1 ? 8 : JB == 2 ? 6 : 4;  // halves of steps in flight
+  u32x4 x[D], a[D][JB];
   const int nw = (s1 - s0 - wave + 3) / 4;
   auto load = [&](int i, int b) {
     const int c = 64 * (s0 + wave + 4 * (i >> 1)) + 32 * (i & 1);
-#pragma unroll
-    for (int m = 0; m < MB; ++m) x[b][m] = *reinterpret_cast<const u32x4*>(xr[m] + c);
+    x[b] = *reinterpret_cast<const u32x4*>(xr + c);
 #pragma unroll
     for (int j = 0; j < JB; ++j) a[b][j] = *reinterpret_cast<const u32x4*>(ar[j] + c);
-  };
-  auto mul = [&](int b) {
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-      for (int j = 0; j < JB; ++j) acc[m][j] = mfma16(x[b][m], a[b][j], acc[m][j]);
   };
 #pragma unroll
   for (int b = 0; b < D; ++b)
@@ -345,62 +347,118 @@ __device__ __forceinline__ void shrink_tile(const ShrinkParams& p, const int32_t
 #pragma unroll
     for (int b = 0; b < D; ++b) {
       if (i + b >= 2 * nw) break;
-      mul(b);
+#pragma unroll
+      for (int j = 0; j < JB; ++j) acc[j] = mfma16(x[b], a[b][j], acc[j]);
       if (i + b + D < 2 * nw) load(i + b + D, b);
     }
-  // waves 2 and 3 to 0 and 1, then half of the blocks from 0 to 1 and half back
-  constexpr int NB = MB * JB, H0 = (NB + 1) / 2;
-  auto at = [&](int buf, int b) -> f32x4& { return red[(buf * NB + b) * 64 + lane]; };
-  auto add = [&](f32x4& a, const f32x4& b) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] += b[e];
+  for (int j = 0; j < JB; ++j) red[(wave * JB + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  // wave w finishes block w
+  if (wave >= JB) return;
+  f32x4 t = red[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < 4; ++w)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] += red[(w * JB + wave) * 64 + lane][e];
+  const int j = 16 * wave + i16;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (4 * g + v < n && j < rank) out[(int64_t)rows_s[4 * g + v] * p.rp + j] = t[v];
+}
+
+// 17 to 64 rows: steps of X (64 rows of 128 bytes) and of A go straight into one of
+// three LDS stages, chunk c of row x at c ^ mx_swz128(x), by whole lines (read in
+// the operands' layout, where neighbouring lanes have different rows, a load
+// takes the address unit 64 cycles instead of 16); wave w owns rows 16 w .. 16 w +
+// 15, so nothing is left to add.
+constexpr int kStages = 3;
+
+template <int JB>
+__device__ __forceinline__ void shrink_many(const ShrinkParams& p, const int32_t* rows_s, int n,
+                                            const uint16_t* A, int rank, int s0, int s1, float* out,
+                                            char* lds) {
+  constexpr int kX = kTM * 128, kStage = kX + 16 * JB * 128;
+  constexpr int DA = (JB + 1) / 2, DL = 2 + DA;  // loads of a wave and stage: A's, all
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  const uint32_t base = mx_lds_addr(lds);
+  // load u covers rows 8 u .. 8 u + 7; a wave's are wave, wave + 4, ... (past the
+  // end the last again)
+  uint32_t xo[2], ao[DA];
+  int au[DA];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int row = 8 * (wave + 4 * k) + (lane >> 3);
+    xo[k] = ((uint32_t)rows_s[row < n ? row : n - 1] * p.C + 8 * ((lane & 7) ^ mx_swz128(row))) * 2;
+  }
+#pragma unroll
+  for (int k = 0; k < DA; ++k) {
+    au[k] = wave + 4 * k < 2 * JB ? wave + 4 * k : 2 * JB - 1;
+    const int row = 8 * au[k] + (lane >> 3);
+    ao[k] = ((uint32_t)(row < rank ? row : rank - 1) * p.C + 8 * ((lane & 7) ^ mx_swz128(row))) * 2;
+  }
+  auto issue = [&](int s, int b) {
+    const uint32_t st = base + b * kStage;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) dma16(p.X + 64 * s, xo[k], st + (wave + 4 * k) * 1024);
+#pragma unroll
+    for (int k = 0; k < DA; ++k) dma16(A + 64 * s, ao[k], st + kX + au[k] * 1024);
   };
-  if (wave >= 2)
+  f32x4 acc[JB];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) at(wave - 2, b) = acc[b / JB][b % JB];
-  __syncthreads();
-  if (wave < 2)
+  for (int j = 0; j < JB; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const bool mine = 16 * wave < n;
+  const uint32_t row = i16 * 128, sw = mx_swz128(i16);
+  issue(s0, 0);
+  if (s0 + 1 < s1) issue(s0 + 1, 1);
+  int b = 0;
+  for (int s = s0; s < s1; ++s) {
+    // this wave's loads of the stage have landed, then everybody's; all are done
+    // with the stage before it, which the next loads go into
+    mx_wait_loads<DL>(mx_less(s + 1, s1));
+    __syncthreads();
+    if (s + 2 < s1) issue(s + 2, b == 0 ? 2 : b - 1);
+    if (mine) {
+      const uint32_t st = base + b * kStage;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) add(acc[b / JB][b % JB], at(wave, b));
-  __syncthreads();
-  if (wave < 2)
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c = ((4 * h + g) ^ sw) << 4;
+        const u32x4 x = mx_read16(st + wave * 2048 + row + c);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if ((b < H0) == (wave == 1)) at(wave, b) = acc[b / JB][b % JB];
-  __syncthreads();
-  if (wave >= 2) return;
-  float* out = p.Tp + (int64_t)part * p.a.M * p.rp;
+        for (int j = 0; j < JB; ++j)
+          acc[j] = mfma16(x, mx_read16(st + kX + j * 2048 + row + c), acc[j]);
+      }
+    }
+    b = b == 2 ? 0 : b + 1;
+  }
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    if ((b < H0) != (wave == 0)) continue;
-    add(acc[b / JB][b % JB], at(1 - wave, b));
-    const int j = 16 * (b % JB) + i16;
+  for (int j = 0; j < JB; ++j)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int i = 16 * (b / JB) + 4 * g + v;
-      if (i < n && j < rank) out[(int64_t)rows_s[i] * p.rp + j] = acc[b / JB][b % JB][v];
+      const int i = 16 * wave + 4 * g + v, k = 16 * j + i16;
+      if (i < n && k < rank) out[(int64_t)rows_s[i] * p.rp + k] = acc[j][v];
     }
-  }
 }
 
 template <int JB>
-__global__ __launch_bounds__(256, JB <= 2 ? 4 : 3) void shrink_tiles_kernel(ShrinkParams p) {
+__global__ __launch_bounds__(256) void shrink_tiles_kernel(ShrinkParams p) {
   __shared__ int32_t rows_s[kTM];
-  __shared__ f32x4 red[2 * 4 * JB * 64];
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * (kTM + 16 * JB) * 128];
   int part;
   const int tile = tile_of(p.a, blockIdx.x, p.splits, part);
   const Tile t = find_tile(p.a, tile, rows_s);
   if (t.n == 0 || t.rank == 0) return;
   __syncthreads();
-  const int s0 = part * p.steps, all = p.C / 64;
+  const int s0 = __builtin_amdgcn_readfirstlane(part * p.steps), all = p.C / 64;
   const int s1 = s0 + p.steps < all ? s0 + p.steps : all;
-  const uint16_t* A = p.A + (int64_t)t.slot * p.a.r * p.C;
+  const uint16_t* A = (const uint16_t*)uniform(p.A + (int64_t)t.slot * p.a.r * p.C);
+  float* out = p.Tp + (int64_t)part * p.a.M * p.rp;
   if (t.n <= 16)
-    shrink_tile<1, JB>(p, rows_s, t.n, A, t.rank, s0, s1, part, red);
-  else if (t.n <= 32)
-    shrink_tile<2, JB>(p, rows_s, t.n, A, t.rank, s0, s1, part, red);
+    shrink_few<JB>(p, rows_s, t.n, A, t.rank, s0, s1, out, reinterpret_cast<f32x4*>(lds));
   else
-    shrink_tile<4, JB>(p, rows_s, t.n, A, t.rank, s0, s1, part, red);
+    shrink_many<JB>(p, rows_s, t.n, A, t.rank, s0, s1, out, lds);
 }
 
 // -------------------------------------------------------------- expand
@@ -415,17 +473,24 @@ struct ExpandParams {
   int32_t splits, N, ldb, rp, parts, passes;
 };
 
-// B[n][j0 .. j0 + 7] of rows of r ranks (zeros past r).  WHOLE: rows 16-byte
-// aligned and padded to eight
+// chunk c (eight ranks) of row x of a wave's 64 rows of B in LDS sits at c ^
+// b_swz(x), cpr chunks per row
+__device__ __forceinline__ int b_swz(int x, int cpr) {
+  return cpr & (cpr - 1) ? 0 : (x >> 2) & (cpr - 1);
+}
+
+// ranks 8 c .. 8 c + 7 of row x (zeros past r).  WHOLE: rows of whole chunks; else
+// rows of r elements, one after another
 template <bool WHOLE>
-__device__ __forceinline__ u32x4 b_load(const uint16_t* row, int j0, int r) {
-  if (j0 >= r) return u32x4{0u, 0u, 0u, 0u};
-  if (WHOLE) return *reinterpret_cast<const u32x4*>(row + j0);
+__device__ __forceinline__ u32x4 b_read(uint32_t lds, int x, int c, int r, int cpr) {
+  if (8 * c >= r) return u32x4{0u, 0u, 0u, 0u};
+  if (WHOLE) return mx_read16(lds + (x * cpr + (c ^ b_swz(x, cpr))) * 16);
+  typedef __attribute__((address_space(3))) const uint16_t* lds_u16;
   uint16_t e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = j0 + i < r ? row[j0 + i] : (uint16_t)0;
-  return u32x4{(uint32_t)e[0] | ((uint32_t)e[1] << 16), (uint32_t)e[2] | ((uint32_t)e[3] << 16),
-               (uint32_t)e[4] | ((uint32_t)e[5] << 16), (uint32_t)e[6] | ((uint32_t)e[7] << 16)};
+  for (int i = 0; i < 8; ++i)
+    e[i] = 8 * c + i < r ? *(lds_u16)(uintptr_t)(lds + (x * r + 8 * c + i) * 2) : (uint16_t)0;
+  return mx_pack8(e);
 }
 
 // ... with zeros from ``rank`` on (whatever they were)
@@ -449,9 +514,12 @@ template <int JC, bool WHOLE>
 __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(ExpandParams p) {
   constexpr int LD = 32 * JC + 8;  // LDS row pitch of T in elements
   constexpr int VT = 2 * JC;       // groups of four values of T per thread
+  constexpr int kB = 64 * 64 * JC; // bytes of a wave's rows of B
   __shared__ int32_t rows_s[kTM];
   __shared__ __attribute__((aligned(16))) uint16_t t_hi[kTM * LD], t_lo[kTM * LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ __attribute__((aligned(1024))) char bs[4 * kB];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, i16 = lane & 15;
   int part;
   const int tile = tile_of(p.a, blockIdx.x, p.parts, part);
@@ -459,28 +527,43 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
   const int n = t.n, rank = t.rank;
   if (n == 0) return;
   const bool store_t = p.T_out && part == 0;
-  const int r = p.a.r, M = p.a.M, N = p.N;
-  const float s = t.slot < p.a.slots ? p.a.scales[t.slot] : 0.0f;
+  const bool has = t.slot < p.a.slots;
+  const int r = p.a.r, M = p.a.M, N = p.N, ldb = p.ldb, cpr = ldb / 8;
+  const float s = has ? p.a.scales[t.slot] : 0.0f;
   __syncthreads();
-  const uint16_t* B = p.B + (int64_t)t.slot * N * p.ldb;
-  u32x4 bf[4][JC], y[4][2];
-  int32_t at[4];  // M N < 2^31
+  const uint16_t* B = p.B + (int64_t)t.slot * N * ldb;
+  const uint32_t mine = mx_lds_addr(bs) + wave * kB;
+  // 64 rows of B are one run of 128 ldb bytes, 1024 per load (the last load's
+  // lanes past the end: the last 16 bytes again)
+  const int b_loads = (ldb + 7) / 8;
+  u32x2 y[4][4];
+  int32_t at[4][4];  // M N < 2^31
   auto load = [&](int n0) {
-    if (t.slot < p.a.slots) {
+    if (has) {
+      const char* run = uniform(B + (int64_t)n0 * ldb);
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int jc = 0; jc < JC; ++jc)
-          bf[b][jc] = b_load<WHOLE>(
-              B + (int64_t)(n0 + 16 * (i16 >> 2) + 4 * b + (i16 & 3)) * p.ldb, 32 * jc + 8 * g, r);
+      for (int u = 0; u < 4 * JC; ++u) {
+        if (u >= b_loads) break;
+        const int q = 64 * u + lane;
+        uint32_t off;
+        if (WHOLE) {
+          const int x = q / cpr;
+          off = 16 * (x * cpr + ((q - x * cpr) ^ b_swz(x, cpr)));
+        } else {
+          off = 16 * (q < 8 * ldb ? q : 8 * ldb - 1);
+        }
+        dma16(run, off, mine + 1024 * u);
+      }
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       if (16 * m >= n) break;
-      const int i = 16 * m + i16;
-      at[m] = rows_s[i < n ? i : n - 1] * N + n0 + 16 * g;
-      y[m][0] = *reinterpret_cast<const u32x4*>(p.Yi + at[m]);
-      y[m][1] = *reinterpret_cast<const u32x4*>(p.Yi + at[m] + 8);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int i = 16 * m + 4 * g + v;
+        at[m][v] = rows_s[i < n ? i : n - 1] * N + n0 + 4 * i16;
+        y[m][v] = *reinterpret_cast<const u32x2*>(p.Yi + at[m][v]);
+      }
     }
   };
   int n0 = part * p.passes * 256 + 64 * wave;
@@ -496,7 +579,7 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
       q[u] = rows_s[in[u] ? i : 0] * p.rp + (in[u] ? j : 0);
       v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    if (t.slot < p.a.slots) {  // (whatever lies past the rank)
+    if (has) {  // (whatever lies past the rank)
       const int64_t part = (int64_t)M * p.rp;
       int k = 0;
       constexpr int D = 4 / JC;
@@ -541,43 +624,47 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
   __syncthreads();
   if (!p.Yo || (rank == 0 && p.Yi == p.Yo)) return;
   for (int pass = 0; pass < p.passes && n0 < N; ++pass) {
+    u32x4 bf[4][JC];
+    mx_wait_loads();
     if (rank) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
 #pragma unroll
-        for (int jc = 0; jc < JC; ++jc) b_mask(bf[b][jc], 32 * jc + 8 * g, rank);
+        for (int jc = 0; jc < JC; ++jc) {
+          bf[b][jc] = b_read<WHOLE>(mine, 4 * i16 + b, 4 * jc + g, WHOLE ? ldb : r, cpr);
+          b_mask(bf[b][jc], 32 * jc + 8 * g, rank);
+        }
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       if (16 * m >= n) break;
-      const int i = 16 * m + i16;
       if (rank) {
         f32x4 acc[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t w0 = y[m][b >> 1][2 * (b & 1)], w1 = y[m][b >> 1][2 * (b & 1) + 1];
-          acc[b] = f32x4{lo_bf16(w0), hi_bf16(w0), lo_bf16(w1), hi_bf16(w1)};
+        for (int v = 0; v < 4; ++v) {
+          acc[0][v] = lo_bf16(y[m][v][0]);
+          acc[1][v] = hi_bf16(y[m][v][0]);
+          acc[2][v] = lo_bf16(y[m][v][1]);
+          acc[3][v] = hi_bf16(y[m][v][1]);
         }
 #pragma unroll
         for (int jc = 0; jc < JC; ++jc) {
-          const u32x4 th = *reinterpret_cast<const u32x4*>(t_hi + i * LD + 32 * jc + 8 * g);
-          const u32x4 tl = *reinterpret_cast<const u32x4*>(t_lo + i * LD + 32 * jc + 8 * g);
+          const int o = (16 * m + i16) * LD + 32 * jc + 8 * g;
+          const u32x4 th = *reinterpret_cast<const u32x4*>(t_hi + o);
+          const u32x4 tl = *reinterpret_cast<const u32x4*>(t_lo + o);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            acc[b] = mfma16(bf[b][jc], tl, acc[b]);
-            acc[b] = mfma16(bf[b][jc], th, acc[b]);
+            acc[b] = mfma16(tl, bf[b][jc], acc[b]);
+            acc[b] = mfma16(th, bf[b][jc], acc[b]);
           }
         }
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          y[m][b >> 1][2 * (b & 1)] = pack_bf16x2(acc[b][0], acc[b][1]);
-          y[m][b >> 1][2 * (b & 1) + 1] = pack_bf16x2(acc[b][2], acc[b][3]);
-        }
+        for (int v = 0; v < 4; ++v)
+          y[m][v] = u32x2{pack_bf16x2(acc[0][v], acc[1][v]), pack_bf16x2(acc[2][v], acc[3][v])};
       }
-      if (i < n) {
-        *reinterpret_cast<u32x4*>(p.Yo + at[m]) = y[m][0];
-        *reinterpret_cast<u32x4*>(p.Yo + at[m] + 8) = y[m][1];
-      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (16 * m + 4 * g + v < n) *reinterpret_cast<u32x2*>(p.Yo + at[m][v]) = y[m][v];
     }
     n0 += 256;
     if (pass + 1 < p.passes && n0 < N) load(n0);
