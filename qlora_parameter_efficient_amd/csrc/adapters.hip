@@ -562,7 +562,7 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
       for (int v = 0; v < 4; ++v) {
         const int i = 16 * m + 4 * g + v;
         at[m][v] = rows_s[i < n ? i : n - 1] * N + n0 + 4 * i16;
-        y[m][v] = *reinterpret_cast<const u32x2*>(p.Yi + at[m][v]);
+        y[m][v] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p.Yi + at[m][v]));
       }
     }
   };
@@ -664,7 +664,8 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
       }
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        if (16 * m + 4 * g + v < n) *reinterpret_cast<u32x2*>(p.Yo + at[m][v]) = y[m][v];
+        if (16 * m + 4 * g + v < n)
+          __builtin_nontemporal_store(y[m][v], reinterpret_cast<u32x2*>(p.Yo + at[m][v]));
     }
     n0 += 256;
     if (pass + 1 < p.passes && n0 < N) load(n0);

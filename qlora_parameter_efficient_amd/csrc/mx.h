@@ -25,6 +25,21 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+// 16-byte accesses to rows that are aligned to their elements only
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+
+// scale byte of a block from the bits of its amax (sign cleared)
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  constexpr int top = FMT == LQ_MX_FP8 ? 8 : 2;
+  constexpr uint32_t frac = FMT == LQ_MX_FP8 ? 0x600000u : 0x400000u;
+  const int E = (int)(amax >> 23);
+  if (E == 255) return 255u;
+  const int b = E - top + ((amax & 0x7FFFFFu) > frac ? 1 : 0);
+  return (uint32_t)(b > 0 ? b : 0);
+}
+
 __device__ __forceinline__ float mx_scale(uint32_t b) { return __uint_as_float(b << 23); }
 
 // Eight E2M1 codes (element e in bits 4e .. 4e + 3) times 2^(b - 127) as bf16

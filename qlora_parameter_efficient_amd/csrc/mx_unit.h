@@ -1,6 +1,5 @@
-// Sixteen elements of a row on their way into an MX tensor: loads, the block's
-// scale byte, the codes.  Shared by the quantiser and by kernels that quantise
-// what they compute.
+// Sixteen elements of a row on their way into an MX tensor: loads, amax, codes.
+// Shared by the quantiser and by kernels that quantise what they compute.
 #pragma once
 
 #include "mx.h"
@@ -9,24 +8,10 @@ namespace lq {
 
 constexpr int kUnit = 16;  // columns per thread
 
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-
 // max over the lane pair (2 i, 2 i + 1)
 __device__ __forceinline__ uint32_t pair_max(uint32_t v) {
   const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);
   return v > o ? v : o;
-}
-
-// scale byte of a block from the bits of its amax (sign cleared)
-template <int FMT>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-  constexpr int top = FMT == LQ_MX_FP8 ? 8 : 2;
-  constexpr uint32_t frac = FMT == LQ_MX_FP8 ? 0x600000u : 0x400000u;
-  const int E = (int)(amax >> 23);
-  if (E == 255) return 255u;
-  const int b = E - top + ((amax & 0x7FFFFFu) > frac ? 1 : 0);
-  return (uint32_t)(b > 0 ? b : 0);
 }
 
 // a bf16 pair's bits (by value: a vector element must not be bit-cast in place)

@@ -5,10 +5,12 @@
 //   dX = c (g - H c^2 mean(g H)) + dH,  g = dY w;   dW = sum_i dY H c
 //
 // Both are bound by HBM: every element is read once and written once, and a row
-// stays in registers between its sums and its stores.  A thread owns units of 16
-// consecutive columns, so that a lane pair holds one block of an MX output and
-// one DPP move completes the block's amax, as in the quantiser; y is quantised
-// from its float32 value, never stored in between.
+// stays in registers between its sums and its stores (past 16384 columns what does
+// not fit is read again).  A thread owns units of 16 consecutive columns, so that a
+// lane pair holds one block of an MX output and one DPP move completes the block's
+// amax, as in the quantiser; y is quantised from its float32 value, never stored
+// in between.  (Pieces of 16 bytes, consecutive as the threads are, took 61 us
+// against 54 in the backward of 8192 x 4096 and as long in the forward.)
 #include "block.h"
 #include "mx_unit.h"
 
@@ -115,8 +117,8 @@ struct NormParams {
 };
 
 // TPR threads per row (64: four rows per workgroup), U units of 16 columns each:
-// columns 16 (t + TPR u).
-template <bool BF16, int FMT, int TPR, int U>
+// columns 16 (t + TPR u).  KEEP: the gain stays in registers too.
+template <bool BF16, int FMT, int TPR, int U, bool KEEP>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(NormParams p) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
   __shared__ float scratch[16];
@@ -125,18 +127,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(Norm
   const float inv_k = 1.0f / (float)K;
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < p.M;
        row += (int64_t)gridDim.x * RPB) {
-    float h[U][16], w[U][16], s[1] = {0.0f};
+    float h[U][16], w[KEEP ? U : 1][16], s[1] = {0.0f};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = 16 * (t + TPR * u), n = K - c;
       if (n <= 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) h[u][i] = w[u][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) h[u][i] = 0.0f;
         continue;
       }
       const int64_t e = row * K + c;
       load_unit<BF16>(p.X, e, n, h[u]);
-      load_gain(p.W, p.wbf16, c, n, w[u]);
+      if (KEEP) load_gain(p.W, p.wbf16, c, n, w[KEEP ? u : 0]);
       if (p.R) {
         float r[16];
         load_unit<BF16>(p.R, e, n, r);
@@ -158,8 +160,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(Norm
       const int64_t e = row * K + col;
       if (n > 0 && p.H) store_unit<BF16>(p.H, e, n, h[u]);
       float y[16];
+      if (!KEEP && n > 0) load_gain(p.W, p.wbf16, col, n, w[0]);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = h[u][i] * c * w[u][i];
+      for (int i = 0; i < 16; ++i) y[i] = h[u][i] * c * w[KEEP ? u : 0][i];
       if (n > 0 && p.Y) store_unit<BF16>(p.Y, e, n, y);
       if constexpr (FMT != 0) {
         // both units of a block are in one lane pair; one past the row's end is
@@ -187,39 +190,48 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(Norm
 
 // Rows blockIdx, blockIdx + gridDim, ...: each thread adds its columns' shares
 // of dW over the workgroup's rows in registers; the workgroups' sums are added
-// by dw_reduce_kernel.
-template <bool BF16, int TPR, int U>
+// by dw_reduce_kernel.  KEEP: H, dY and the gain stay in registers from the sums
+// on.
+template <bool BF16, int TPR, int U, bool KEEP>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(NormParams p) {
-  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1, UK = KEEP ? U : 1;
   __shared__ float scratch[32];
   const int t = threadIdx.x % TPR, K = p.K;
   const float inv_k = 1.0f / (float)K;
-  float w[U][16], dw[U][16];
+  float w[UK][16], dw[U][16];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = 16 * (t + TPR * u), n = K - c;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[u][i] = dw[u][i] = 0.0f;
-    if (n > 0) load_gain(p.W, p.wbf16, c, n, w[u]);
+    for (int i = 0; i < 16; ++i) dw[u][i] = 0.0f;
+    if (KEEP) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[KEEP ? u : 0][i] = 0.0f;
+      if (n > 0) load_gain(p.W, p.wbf16, c, n, w[KEEP ? u : 0]);
+    }
   }
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < p.M;
        row += (int64_t)gridDim.x * RPB) {
-    float h[U][16], d[U][16], s[2] = {0.0f, 0.0f};
+    float h[UK][16], d[UK][16], s[2] = {0.0f, 0.0f};
+    auto load = [&](int k, int c, int n) {
+      load_unit<BF16>(p.X, row * K + c, n, h[k]);
+      load_unit<BF16>(p.dY, row * K + c, n, d[k]);
+      if (!KEEP) load_gain(p.W, p.wbf16, c, n, w[k]);
+    };
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = 16 * (t + TPR * u), n = K - c;
+      const int c = 16 * (t + TPR * u), n = K - c, k = KEEP ? u : 0;
       if (n <= 0) {
+        if (KEEP)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) h[u][i] = d[u][i] = 0.0f;
+          for (int i = 0; i < 16; ++i) h[k][i] = d[k][i] = 0.0f;
         continue;
       }
-      const int64_t e = row * K + c;
-      load_unit<BF16>(p.X, e, n, h[u]);
-      load_unit<BF16>(p.dY, e, n, d[u]);
+      load(k, c, n);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[0] += d[u][i] * w[u][i] * h[u][i];
-        s[1] += h[u][i] * h[u][i];
+        s[0] += d[k][i] * w[k][i] * h[k][i];
+        s[1] += h[k][i] * h[k][i];
       }
     }
     row_sum<TPR, 2>(s, scratch);
@@ -227,16 +239,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(Norm
     const float m = s[0] * inv_k * c * c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int col = 16 * (t + TPR * u), n = K - col;
+      const int col = 16 * (t + TPR * u), n = K - col, k = KEEP ? u : 0;
       if (n <= 0) continue;
       const int64_t e = row * K + col;
+      if (!KEEP) load(k, col, n);
       if (p.part)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dw[u][i] += d[u][i] * (h[u][i] * c);
+        for (int i = 0; i < 16; ++i) dw[u][i] += d[k][i] * (h[k][i] * c);
       if (p.H) {
         float g[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = c * (d[u][i] * w[u][i] - h[u][i] * m);
+        for (int i = 0; i < 16; ++i) g[i] = c * (d[k][i] * w[k][i] - h[k][i] * m);
         if (p.R) {
           float r[16];
           load_unit<BF16>(p.R, e, n, r);
@@ -257,21 +270,30 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(Norm
   }
 }
 
-// dW[c] (+)= sum of P partial rows, added in order by sixteen waves and then
-// across them
+// dW[c] (+)= sum of P partial rows: 32 columns per workgroup, 32 groups of rows
+// that are added in order, eight loads at a time, and then across the groups
 __global__ __launch_bounds__(1024) void dw_reduce_kernel(const float* part, int P, int K, float* dW,
                                                          int accumulate) {
-  __shared__ float sum[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float sum[32][33];
+  const int l = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + l;
   float s = 0.0f;
-  if (c < K)
-    for (int i = wave; i < P; i += 16) s += part[(int64_t)i * K + c];
-  sum[wave][lane] = s;
-  __syncthreads();
-  if (wave || c >= K) return;
+  if (c < K) {
+    int i = grp;
+    for (; i + 7 * 32 < P; i += 8 * 32) {
+      float x[8];
 #pragma unroll
-  for (int i = 1; i < 16; ++i) s += sum[i][lane];
+      for (int k = 0; k < 8; ++k) x[k] = part[(int64_t)(i + 32 * k) * K + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += x[k];
+    }
+    for (; i < P; i += 32) s += part[(int64_t)i * K + c];
+  }
+  sum[grp][l] = s;
+  __syncthreads();
+  if (grp || c >= K) return;
+#pragma unroll
+  for (int i = 1; i < 32; ++i) s += sum[i][l];
   dW[c] = accumulate ? dW[c] + s : s;
 }
 
@@ -295,11 +317,11 @@ template <bool BF16, int FMT>
 void launch_fwd(const NormParams& p, hipStream_t st) {
   const dim3 g(fwd_grid(p.M, p.K));
   switch (norm_shape(p.K)) {
-    case 0: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 64, 1>), g, dim3(256), 0, st, p); break;
-    case 1: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 256, 1>), g, dim3(256), 0, st, p); break;
-    case 2: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 256, 2>), g, dim3(256), 0, st, p); break;
-    case 3: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 1024, 1>), g, dim3(1024), 0, st, p); break;
-    default: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 1024, 4>), g, dim3(1024), 0, st, p);
+    case 0: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 64, 1, true>), g, dim3(256), 0, st, p); break;
+    case 1: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 256, 1, true>), g, dim3(256), 0, st, p); break;
+    case 2: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 512, 1, true>), g, dim3(512), 0, st, p); break;
+    case 3: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 1024, 1, true>), g, dim3(1024), 0, st, p); break;
+    default: hipLaunchKernelGGL((rmsnorm_fwd_kernel<BF16, FMT, 1024, 4, false>), g, dim3(1024), 0, st, p);
   }
 }
 
@@ -307,11 +329,11 @@ template <bool BF16>
 void launch_bwd(const NormParams& p, hipStream_t st) {
   const dim3 g(bwd_grid(p.M, p.K));
   switch (norm_shape(p.K)) {
-    case 0: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 64, 1>), g, dim3(256), 0, st, p); break;
-    case 1: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 256, 1>), g, dim3(256), 0, st, p); break;
-    case 2: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 256, 2>), g, dim3(256), 0, st, p); break;
-    case 3: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 1024, 1>), g, dim3(1024), 0, st, p); break;
-    default: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 1024, 4>), g, dim3(1024), 0, st, p);
+    case 0: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 64, 1, true>), g, dim3(256), 0, st, p); break;
+    case 1: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 256, 1, true>), g, dim3(256), 0, st, p); break;
+    case 2: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 512, 1, true>), g, dim3(512), 0, st, p); break;
+    case 3: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 1024, 1, true>), g, dim3(1024), 0, st, p); break;
+    default: hipLaunchKernelGGL((rmsnorm_bwd_kernel<BF16, 1024, 4, false>), g, dim3(1024), 0, st, p);
   }
 }
 
@@ -366,7 +388,7 @@ int rmsnorm_bwd(const void* dY, const void* H, int64_t M, int64_t K, lq_dtype dt
   p.eps = eps;
   dt == LQ_BF16 ? launch_bwd<true>(p, st) : launch_bwd<false>(p, st);
   if (dW)
-    hipLaunchKernelGGL(dw_reduce_kernel, dim3((unsigned)cdiv(K, 64)), dim3(1024), 0, st, part,
+    hipLaunchKernelGGL(dw_reduce_kernel, dim3((unsigned)cdiv(K, 32)), dim3(1024), 0, st, part,
                        (int)(bwd_grid(M, K) * rows_per_block(K)), (int)K, dW, accumulate);
   return hip_fail(hipGetLastError(), "rmsnorm_bwd launch");
 }
