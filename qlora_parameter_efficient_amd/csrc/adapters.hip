@@ -158,11 +158,101 @@ __device__ __forceinline__ void scan3(int (&v)[3], int (&total)[3], int (*sh)[3]
   }
 }
 
+// --------------------------------------------- factors turned (backward)
+// Bt[slot][j][n] = B[slot][n][j] and At[slot][k][j] = A[slot][j][k] (rows of ld
+// elements) for the places that have rows: 64 columns n or k per 256 threads.
+struct TurnArgs {
+  const uint16_t* A;
+  const uint16_t* B;
+  uint16_t* At;
+  uint16_t* Bt;
+  int32_t N, K, r, ld;
+  int32_t chunks;  // of 64 columns, of one place
+};
+
+// Whether a row has this place (the workgroup's threads together)
+__device__ __forceinline__ bool any_row(const int32_t* rows, int M, int slot) {
+  for (int64_t b = 0; b < M; b += 8 * (int64_t)blockDim.x) {
+    bool here = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = b + k * (int64_t)blockDim.x + threadIdx.x;
+      here |= i < M && rows[i] == slot;
+    }
+    if (__syncthreads_or(here)) return true;
+  }
+  return false;
+}
+
+// Chunk ``chunk`` of a place by 256 threads (tid) with 64 x 66 elements of LDS;
+// every thread of the workgroup takes part in the barrier
+__device__ __forceinline__ void turn_chunk(const TurnArgs& p, int slot, int chunk, int tid,
+                                           uint16_t* s) {
+  const int r = p.r, nb = p.N / 64;
+  const bool is_b = chunk < nb, in = chunk < p.chunks;
+  const int c0 = (is_b ? chunk : chunk - nb) * 64;
+  // in: 64 columns of r ranks (B) or r ranks of 64 columns (A), eight elements a
+  // thread where rows allow; in LDS as [rank][column]
+  if (in && is_b) {
+    const uint16_t* B = p.B + ((int64_t)slot * p.N + c0) * r;
+    if (r % 8 == 0) {
+      for (int e = tid; e < 8 * r; e += 256) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(B + 8 * e);
+        const int c = 8 * e / r, j = 8 * e % r;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[(j + k) * 66 + c] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+      }
+    } else {
+      for (int e = tid; e < 64 * r; e += 256) s[(e % r) * 66 + e / r] = B[e];
+    }
+  } else if (in) {
+    for (int e = tid; e < 8 * r; e += 256) {
+      const int j = e >> 3, c = 8 * (e & 7);
+      const u32x4 v = *reinterpret_cast<const u32x4*>(p.A + ((int64_t)slot * r + j) * p.K + c0 + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[j * 66 + c + k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+  __syncthreads();
+  if (in && is_b) {
+    for (int e = tid; e < 8 * r; e += 256) {
+      const int j = e >> 3, c = 8 * (e & 7);
+      u32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = s[j * 66 + c + 2 * k] | ((uint32_t)s[j * 66 + c + 2 * k + 1] << 16);
+      *reinterpret_cast<u32x4*>(p.Bt + ((int64_t)slot * r + j) * p.N + c0 + c) = v;
+    }
+  } else if (in) {
+    for (int e = tid; e < 8 * p.ld; e += 256) {  // rows of ld = r rounded up to eight
+      const int c = 8 * e / p.ld, j = 8 * e % p.ld;
+      u32x4 v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = j + 2 * k < r ? s[(j + 2 * k) * 66 + c] : 0u;
+        const uint32_t hi = j + 2 * k + 1 < r ? s[(j + 2 * k + 1) * 66 + c] : 0u;
+        v[k] = lo | (hi << 16);
+      }
+      *reinterpret_cast<u32x4*>(p.At + ((int64_t)slot * p.K + c0) * p.ld + 8 * e) = v;
+    }
+  }
+}
+
 constexpr int kPerThread = (LQ_ADAPTERS_MAX_SLOTS + 1024) / 1024;  // places of a thread
 
-__global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p) {
-  __shared__ int32_t cnt[kCnt];
+// Workgroup 0: the plan.  The others (backward): four chunks each of a place's
+// factors, which wait for nothing of it.
+__global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
+  __shared__ __attribute__((aligned(16))) int32_t cnt[kCnt];
   __shared__ int sh[16][3];
+  if (blockIdx.x > 0) {
+    const int per_place = (q.chunks + 3) / 4, b = blockIdx.x - 1;
+    const int slot = b / per_place, g = threadIdx.x >> 8;
+    if (any_row(p.rows, p.M, slot))
+      turn_chunk(q, slot, 4 * (b % per_place) + g, threadIdx.x & 255,
+                 reinterpret_cast<uint16_t*>(cnt) + g * 64 * 66);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int S1 = p.slots + 1, W = p.waves;
   const int per = (int)cdiv(cdiv(p.M, 64), W) * 64;
@@ -672,69 +762,6 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
   }
 }
 
-// --------------------------------------------- factors turned (backward)
-// Bt[slot][j][n] = B[slot][n][j] and At[slot][k][j] = A[slot][j][k] (rows of ld
-// elements) for the places that have rows: 64 columns n or k per workgroup.
-struct TurnParams {
-  const uint16_t* A;
-  const uint16_t* B;
-  uint16_t* At;
-  uint16_t* Bt;
-  const int32_t* off;
-  int32_t N, K, r, ld;
-};
-
-__global__ __launch_bounds__(256) void turn_kernel(TurnParams p) {
-  __shared__ uint16_t s[64 * 66];  // [rank][column]
-  const int slot = blockIdx.y, r = p.r, tid = threadIdx.x;
-  if (p.off[slot + 1] == p.off[slot]) return;
-  const int nb = p.N / 64;
-  const bool is_b = (int)blockIdx.x < nb;
-  const int c0 = (is_b ? blockIdx.x : blockIdx.x - nb) * 64;
-  // in: 64 columns of r ranks (B) or r ranks of 64 columns (A), eight elements a
-  // thread where rows allow
-  if (is_b) {
-    const uint16_t* B = p.B + ((int64_t)slot * p.N + c0) * r;
-    if (r % 8 == 0) {
-      for (int e = tid; e < 8 * r; e += 256) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(B + 8 * e);
-        const int c = 8 * e / r, j = 8 * e % r;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[(j + k) * 66 + c] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
-      }
-    } else {
-      for (int e = tid; e < 64 * r; e += 256) s[(e % r) * 66 + e / r] = B[e];
-    }
-    __syncthreads();
-    for (int e = tid; e < 8 * r; e += 256) {
-      const int j = e >> 3, c = 8 * (e & 7);
-      u32x4 v;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = s[j * 66 + c + 2 * k] | ((uint32_t)s[j * 66 + c + 2 * k + 1] << 16);
-      *reinterpret_cast<u32x4*>(p.Bt + ((int64_t)slot * r + j) * p.N + c0 + c) = v;
-    }
-  } else {
-    for (int e = tid; e < 8 * r; e += 256) {
-      const int j = e >> 3, c = 8 * (e & 7);
-      const u32x4 v = *reinterpret_cast<const u32x4*>(p.A + ((int64_t)slot * r + j) * p.K + c0 + c);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[j * 66 + c + k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
-    }
-    __syncthreads();
-    for (int e = tid; e < 8 * p.ld; e += 256) {  // rows of ld = r rounded up to eight
-      const int c = 8 * e / p.ld, j = 8 * e % p.ld;
-      u32x4 v;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = j + 2 * k < r ? s[(j + 2 * k) * 66 + c] : 0u;
-        const uint32_t hi = j + 2 * k + 1 < r ? s[(j + 2 * k + 1) * 66 + c] : 0u;
-        v[k] = lo | (hi << 16);
-      }
-      *reinterpret_cast<u32x4*>(p.At + ((int64_t)slot * p.K + c0) * p.ld + 8 * e) = v;
-    }
-  }
-}
-
 // ------------------------------------------------------------- gradients
 // dA_a = s_a sum_i U[i]^T X[i] and dB_a = s_a sum_i dY[i]^T T[i] over one
 // segment of the place's rows, 256 columns of X or dY per workgroup, 64 per
@@ -979,7 +1006,8 @@ PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   return l;
 }
 
-int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, hipStream_t st) {
+int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, const TurnArgs& q,
+                hipStream_t st) {
   PlanArgs p;
   p.rows = a.rows;
   p.ranks = a.ranks;
@@ -1001,7 +1029,8 @@ int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, hip
   a.tiles = p.tiles;
   a.segs = p.segs;
   a.perm = p.perm;
-  hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(1024), 0, st, p);
+  const dim3 g((unsigned)(1 + (int64_t)a.slots * cdiv(q.chunks, 4)));
+  hipLaunchKernelGGL(plan_kernel, g, dim3(1024), 0, st, p, q);
   return hip_fail(hipGetLastError(), "adapters plan launch");
 }
 
@@ -1108,7 +1137,7 @@ int adapters_fwd(const void* X, int64_t M, const lq_adapter_pool& q, const int32
   int rc;
   if (M > kDirect) {
     const PlanLayout l = plan_layout(M, q.slots, max_segments(M, q.N, q.K, q.slots));
-    if ((rc = launch_plan(a, l, base, segment_rows(M, q.N, q.K), st))) return rc;
+    if ((rc = launch_plan(a, l, base, segment_rows(M, q.N, q.K), TurnArgs{}, st))) return rc;
     base += l.end;
   }
   if ((rc = launch_shrink(a, X, q.A, q.K, (float*)base, st))) return rc;
@@ -1122,22 +1151,18 @@ int adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool
   const BwdLayout l = bwd_layout(M, q.N, q.K, q.r, q.slots);
   char* base = (char*)ws;
   RowArgs a = row_args(M, q, rows);
-  int rc = launch_plan(a, l.plan, base, segment_rows(M, q.N, q.K), st);
-  if (rc) return rc;
-  TurnParams t;
+  TurnArgs t;
   t.A = (const uint16_t*)q.A;
   t.B = (const uint16_t*)q.B;
   t.At = (uint16_t*)(base + l.at);
   t.Bt = (uint16_t*)(base + l.bt);
-  t.off = a.off;
   t.N = (int32_t)q.N;
   t.K = (int32_t)q.K;
   t.r = q.r;
   t.ld = (q.r + 7) / 8 * 8;
-  // without dX only B is turned
-  hipLaunchKernelGGL(turn_kernel, dim3((unsigned)(q.N / 64 + (dX_out ? q.K / 64 : 0)), q.slots),
-                     dim3(256), 0, st, t);
-  if ((rc = hip_fail(hipGetLastError(), "adapters turn launch"))) return rc;
+  t.chunks = (int32_t)(q.N / 64 + (dX_out ? q.K / 64 : 0));  // without dX only B is turned
+  int rc = launch_plan(a, l.plan, base, segment_rows(M, q.N, q.K), t, st);
+  if (rc) return rc;
   float *U = (float*)(base + l.u), *Tp = (float*)(base + l.tp), *T = (float*)(base + l.t);
   if ((rc = launch_shrink(a, dY, t.Bt, q.N, Tp, st))) return rc;
   if ((rc = launch_expand(a, Tp, shrink_splits(M, q.N), t.At, q.K, t.ld, dX_in, dX_out,
