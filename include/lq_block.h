@@ -104,7 +104,7 @@ typedef struct lq_adapter_pool {
  *   ws      lq_adapters_workspace_size(LQ_ADAPTERS_OP_FWD, M, N, K, r, slots) bytes
  * Ranks, scales and rows are read on the device: a captured call follows their
  * values at each replay.  T is float32 and enters its product with B in two
- * bf16 parts (2^-16 of its value).
+ * bf16 parts (2^-16 of its value); a row's non-finite elements stay in that row.
  * Requires K % 64 == 0, N % 64 == 0, N, K <= 65536, M K, M N and M r < 2^31,
  * 1 <= r <= 64, 1 <= slots <= 4096; X, A, B, Y_in, Y_out and ws 16-byte
  * aligned.  M = 0 is a no-op.
@@ -126,7 +126,8 @@ int lq_adapters_fwd(const void* X, int64_t M, const lq_adapter_pool* pool, const
  *   T_saved   optional T_out of the forward (NULL: recomputed)
  *   ws        lq_adapters_workspace_size(LQ_ADAPTERS_OP_BWD, ...) bytes
  * dA and dB are float32 sums, in a fixed order, of products with float32 U and
- * T (carried as three bf16 parts, so that nothing of their 24 bits is lost).
+ * T (carried as three bf16 parts, so that nothing of their 24 bits is lost).  A
+ * non-finite element makes the sums that it enters non-finite.
  * Without dA and dB X is not read.  M = 0 writes zeros to dA and dB unless
  * accumulate is set.  Other rules as lq_adapters_fwd (dY, dX: 16-byte aligned).
  */

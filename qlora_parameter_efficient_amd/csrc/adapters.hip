@@ -33,12 +33,14 @@ struct RowArgs {
   // the plan (NULL: M <= kDirect): first sorted position of each place's rows
   // (place ``slots``: rows without an adapter; then M), rows in sorted order,
   // (place, first position, rows, rank) of each tile and of each segment of the
-  // gradients, and the first segment of each place
+  // gradients, the first segment of each place, and its first partial sum (places
+  // of several segments have one a segment)
   const int32_t* off;
   const int32_t* perm;
   const int4* tiles;
   const int4* segs;
   const int32_t* seg0;
+  const int32_t* part0;
   const int32_t* count;  // tiles, segments
   int32_t M, slots, r;
 };
@@ -108,6 +110,7 @@ struct PlanArgs {
   int4* tiles;
   int4* segs;
   int32_t* seg0;
+  int32_t* part0;
   int32_t* count;
   int32_t M, slots, r, waves, bits, seg_rows;
 };
@@ -135,18 +138,19 @@ __device__ __forceinline__ int wave_scan(int x) {
   return x;
 }
 
-// exclusive sums over the workgroup of three values per thread; the totals
-__device__ __forceinline__ void scan3(int (&v)[3], int (&total)[3], int (*sh)[3]) {
+// exclusive sums over the workgroup of NV values per thread; the totals
+template <int NV>
+__device__ __forceinline__ void scan(int (&v)[NV], int (&total)[NV], int (*sh)[NV]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x[3];
+  int x[NV];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) x[k] = wave_scan(v[k]);
+  for (int k = 0; k < NV; ++k) x[k] = wave_scan(v[k]);
   if (lane == 63)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) sh[wave][k] = x[k];
+    for (int k = 0; k < NV; ++k) sh[wave][k] = x[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int k = 0; k < NV; ++k) {
     int before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) {
@@ -244,7 +248,7 @@ constexpr int kPerThread = (LQ_ADAPTERS_MAX_SLOTS + 1024) / 1024;  // places of 
 // factors, which wait for nothing of it.
 __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
   __shared__ __attribute__((aligned(16))) int32_t cnt[kCnt];
-  __shared__ int sh[16][3];
+  __shared__ int sh[16][4];
   if (blockIdx.x > 0) {
     const int per_place = (q.chunks + 3) / 4, b = blockIdx.x - 1;
     const int slot = b / per_place, g = threadIdx.x >> 8;
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
   }
   __syncthreads();
   // counts become positions
-  int v[3] = {0, 0, 0}, total[3], n[kPerThread];
+  int v[4] = {0, 0, 0, 0}, total[4], n[kPerThread];
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int s = tid * c + k;
@@ -320,9 +324,11 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
     }
     v[0] += n[k];
     v[1] += (n[k] + kTM - 1) / kTM;
-    v[2] += s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
+    const int segs = s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
+    v[2] += segs;
+    v[3] += segs > 1 ? segs : 0;
   }
-  scan3(v, total, sh);
+  scan<4>(v, total, sh);
 #pragma unroll
   for (int k = 0; k < kPerThread; ++k) {
     const int s = tid * c + k;
@@ -335,6 +341,8 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
       if (w < W) cnt[w * S1 + s] = x[w] + v[0];
     if (s < p.slots) {
       p.seg0[s] = v[2];
+      p.part0[s] = v[3];
+      v[3] += n[k] > p.seg_rows ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
       for (int i = 0; i < n[k]; i += p.seg_rows) {
         const int left = n[k] - i;
         p.segs[v[2]++] = make_int4(s, v[0] + i, left < p.seg_rows ? left : p.seg_rows, rank[k]);
@@ -776,7 +784,7 @@ struct GradParams {
   const float* T;
   float* dA;    // slots x r x K
   float* dB;    // slots x N x r
-  float* part;  // segments x (r K + N r)
+  float* part;  // partial sums x (r K + N r)
   int32_t N, K, accumulate;
 };
 
@@ -885,7 +893,7 @@ __device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, 
   const float s = p.a.scales[slot];
   const int64_t size = (int64_t)r * p.K + (int64_t)p.N * r;
   float* out = whole ? (DB ? p.dB + (int64_t)slot * p.N * r : p.dA + (int64_t)slot * r * p.K)
-                     : p.part + seg * size + (DB ? (int64_t)r * p.K : 0);
+                     : p.part + (p.a.part0[slot] + seg - first) * size + (DB ? (int64_t)r * p.K : 0);
   const bool add = whole && p.accumulate;
   const bool wide = !DB || r % 4 == 0;  // four results of a lane are one aligned group
 #pragma unroll
@@ -938,8 +946,9 @@ __global__ __launch_bounds__(256) void grads_finish_kernel(GradParams p) {
   f32x4* o = reinterpret_cast<f32x4*>(e < na ? p.dA + slot * na + e
                                              : p.dB + (int64_t)slot * (size - na) + e - na);
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = s0; k < s1; ++k) {
-    const f32x4 x = *reinterpret_cast<const f32x4*>(p.part + k * size + e);
+  const float* part = p.part + p.a.part0[slot] * size + e;
+  for (int k = 0; k < s1 - s0; ++k) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(part + k * size);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += x[i];
   }
@@ -991,14 +1000,22 @@ int64_t max_segments(int64_t M, int64_t N, int64_t K, int32_t slots) {
   return s < M ? s : M;
 }
 
+// Partial sums of the gradients: of places with more rows than a segment, which
+// have at most twice as many segments as their rows fill
+int64_t max_parts(int64_t M, int64_t N, int64_t K, int32_t slots) {
+  const int64_t p = 2 * cdiv(M, segment_rows(M, N, K)), s = max_segments(M, N, K, slots);
+  return p < s ? p : s;
+}
+
 struct PlanLayout {
-  size_t off, seg0, count, tiles, segs, perm, end;
+  size_t off, seg0, part0, count, tiles, segs, perm, end;
 };
 PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   PlanLayout l;
   l.off = 0;
   l.seg0 = up256((size_t)(slots + 2) * 4);
-  l.count = l.seg0 + up256((size_t)(slots + 2) * 4);
+  l.part0 = l.seg0 + up256((size_t)(slots + 2) * 4);
+  l.count = l.part0 + up256((size_t)(slots + 2) * 4);
   l.tiles = l.count + 256;
   l.segs = l.tiles + up256((size_t)(max_tiles(M > kDirect ? M : kDirect + 1, slots) + 7) * 16);
   l.perm = l.segs + up256((size_t)segs * 16);
@@ -1014,6 +1031,7 @@ int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, con
   p.r = a.r;
   p.off = (int32_t*)(ws + l.off);
   p.seg0 = (int32_t*)(ws + l.seg0);
+  p.part0 = (int32_t*)(ws + l.part0);
   p.count = (int32_t*)(ws + l.count);
   p.tiles = (int4*)(ws + l.tiles);
   p.segs = (int4*)(ws + l.segs);
@@ -1025,6 +1043,7 @@ int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, con
   p.seg_rows = (int32_t)seg_rows;
   a.off = p.off;
   a.seg0 = p.seg0;
+  a.part0 = p.part0;
   a.count = p.count;
   a.tiles = p.tiles;
   a.segs = p.segs;
@@ -1112,7 +1131,7 @@ BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) 
   l.t = l.u + up256((size_t)M * r * 4);
   l.tp = l.t + up256((size_t)M * r * 4);
   l.part = l.tp + up256((size_t)(sn > sk ? sn : sk) * M * t_pitch(r) * 4);
-  l.end = l.part + up256((size_t)segs * r * (N + K) * 4);
+  l.end = l.part + up256((size_t)max_parts(M, N, K, slots) * r * (N + K) * 4);
   return l;
 }
 
