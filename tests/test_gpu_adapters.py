@@ -172,3 +172,39 @@ def test_gradients_are_derivatives():
     e[0, 5] = 1e-3
     d = (f(A, B, X + e) - f(A, B, X - e)) / 2e-3
     assert abs(d - float(dX[0, 5])) <= HALF_BF16 * abs(d) + 1e-3
+
+
+@pytest.mark.parametrize("M,N,K,r,slots", [(16000, 4096, 2048, 8, 2), (20011, 64, 192, 16, 1), (9000, 128, 64, 32, 4000)])
+def test_many_rows(M, N, K, r, slots):
+    """More rows than the plan keeps in registers, segments longer than the list of
+    row indices in LDS, nearly as many places as rows; the formulas in float64 on
+    the GPU, one place at a time."""
+    announce(f"adapters M={M} N={N} K={K} r={r} slots={slots}")
+    g = torch.Generator(device=DEV).manual_seed(M)
+    bf = lambda s, *shape: (torch.randn(shape, generator=g, device=DEV) * s).bfloat16()  # noqa: E731
+    X, Y, dY, dX = bf(1.0, M, K), bf(1.3, M, N), bf(1.0, M, N), bf(1.3, M, K)
+    q = block.AdapterPool(bf(K**-0.5, slots, r, K), bf(r**-0.5, slots, N, r), torch.rand(slots, generator=g, device=DEV) + 0.5)
+    rows = torch.randint(-1, slots, (M,), generator=g, device=DEV, dtype=torch.int32)
+    T = torch.empty((M, r), device=DEV)
+    out = block.lq_adapters_fwd(X, q, rows, Y, T_out=T)
+    gx, dA, dB = block.lq_adapters_bwd(dY, X, q, rows, dX, T_saved=T)
+    bare = rows < 0
+    assert torch.equal(out[bare], Y[bare]) and torch.equal(gx[bare], dX[bare]) and (T[bare] == 0).all()
+    for a in range(slots) if slots < 10 else list(range(0, slots, 97)) + [slots - 1]:
+        i = torch.nonzero(rows == a)[:, 0]
+        x, d, A, B, s = X[i].double(), dY[i].double(), q.A[a].double(), q.B[a].double(), float(q.scales[a])
+        t, u = x @ A.t(), d @ B
+        tm, um = x.abs() @ A.t().abs(), d.abs() @ B.abs()
+        small = 2.0**-16 + 2 * r * U32
+
+        def near(got, want, slack, rel=0.0):
+            assert bool(((got.double() - want).abs() <= rel * want.abs() + slack).all())
+
+        near(T[i], t, K * U32 * tm)
+        slack = s * (K * U32 * tm + small * t.abs()) @ B.t().abs() + 2 * U32 * Y[i].double().abs()
+        near(out[i], Y[i].double() + s * t @ B.t(), slack * (1 + HALF_BF16), HALF_BF16)
+        slack = s * (N * U32 * um + small * u.abs()) @ A.abs() + 2 * U32 * dX[i].double().abs()
+        near(gx[i], dX[i].double() + s * u @ A, slack * (1 + HALF_BF16), HALF_BF16)
+        n = len(i)
+        near(dA[a], s * u.t() @ x, s * (N + n + 8) * U32 * (um.t() @ x.abs()))
+        near(dB[a], s * d.t() @ T[i].double(), s * (n + 8) * U32 * (d.abs().t() @ T[i].double().abs()))

@@ -154,3 +154,32 @@ def test_several_pieces():
         assert torch.equal(part[0], loss[rows]) and torch.equal(part[1], lse[rows]) and torch.equal(part[2], dH[rows])
     z = H[[0, 255, 256, 699]].double() @ W.double().t()
     assert torch.allclose(lse[[0, 255, 256, 699]].double(), torch.logsumexp(z, 1), atol=1e-4)
+
+
+@pytest.mark.parametrize("M,V,K", [(1001, 50257, 192), (777, 33000, 320), (2048, 32000, 128), (200, 9999, 1024)])
+def test_larger_shapes(M, V, K):
+    """Several rounds of tiles, a second launch for a short last one, split
+    reductions; the formulas in float64 on the GPU."""
+    announce(f"head M={M} V={V} K={K}")
+    g = torch.Generator(device=DEV).manual_seed(V)
+    H = torch.randn((M, K), generator=g, device=DEV).bfloat16()
+    W = (torch.randn((V, K), generator=g, device=DEV) * 2.0 * K**-0.5).bfloat16()
+    t = torch.randint(0, V, (M,), generator=g, device=DEV, dtype=torch.int32)
+    w = torch.rand(M, generator=g, device=DEV)
+    loss, lse, dH = block.lq_head_loss(H, W, t, w=w)
+    h, e = H.double(), W.double()
+    z = h @ e.t()
+    want = torch.logsumexp(z, 1)
+    e_z = K * U32 * (h.abs() @ e.abs().t()).amax(1)
+    e_lse = e_z + (V / 1024 + 64 + 4 * z.abs().amax(1)) * U32
+    assert bool(((lse.double() - want).abs() <= e_lse + want.abs() * U32).all())
+    zt = z.gather(1, t[:, None].long())[:, 0]
+    assert bool(((loss.double() - (want - zt)).abs() <= e_lse + e_z + 8 * U32 * (want.abs() + zt.abs())).all())
+    soft = torch.exp(z - want[:, None])
+    d = soft.scatter_add(1, t[:, None].long(), -torch.ones_like(zt)[:, None]) * w[:, None].double()
+    off = w[:, None].double() * (2 * e_lse[:, None] + 16 * U32) * (soft + 16 * U32)
+    slack = (d.abs() * (HALF_BF16 + V * U32) + off * (1 + HALF_BF16)) @ e.abs()
+    ref = d @ e
+    assert bool(((dH.double() - ref).abs() <= HALF_BF16 * ref.abs() + slack * (1 + HALF_BF16)).all())
+    # the errors above are worst cases; together the roundings are far smaller
+    assert float((dH.double() - ref).norm() / ref.norm()) < 2 * HALF_BF16
