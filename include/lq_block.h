@@ -102,6 +102,7 @@ typedef struct lq_adapter_pool {
  *   T_out   optional M x r float32: T[i] = X[i] A_a^T, zero past the adapter's
  *           rank and for rows without one (T_saved of lq_adapters_bwd)
  *   ws      lq_adapters_workspace_size(LQ_ADAPTERS_OP_FWD, M, N, K, r, slots) bytes
+ *           (NULL where that is 0)
  * Ranks, scales and rows are read on the device: a captured call follows their
  * values at each replay.  T is float32 and enters its product with B in two
  * bf16 parts (2^-16 of its value); a row's non-finite elements stay in that row.
@@ -139,7 +140,8 @@ int lq_adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_p
 #define LQ_ADAPTERS_MAX_SLOTS 4096
 #define LQ_ADAPTERS_OP_FWD 0
 #define LQ_ADAPTERS_OP_BWD 1
-/* Workspace in bytes; 0 for M = 0 and for sizes that the call refuses. */
+/* Workspace in bytes; 0 for M = 0, for sizes that the call refuses, and for
+ * forwards of few rows that need none. */
 size_t lq_adapters_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r,
                                   int32_t slots);
 

@@ -770,6 +770,155 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
   }
 }
 
+// ------------------------------------------------ few rows in one launch
+// Up to kFew rows: every workgroup forms its tile's T itself, sixteen waves taking
+// turns at the steps of the whole reduction, and then 256 columns of the expand.
+// A is read again for every 256 columns (from L2), but there is one launch, no
+// workspace, and no trip of T through memory.
+constexpr int kFew = 16;
+
+struct FewParams {
+  RowArgs a;
+  const uint16_t* X;
+  const uint16_t* A;
+  const uint16_t* B;
+  const uint16_t* Yi;
+  uint16_t* Yo;
+  float* T_out;
+  int32_t K, N, parts;
+};
+
+template <int JB, bool WHOLE>
+__global__ __launch_bounds__(1024) void few_rows_kernel(FewParams p) {
+  constexpr int JC = (JB + 1) / 2, LD = 32 * JC + 8, kB = 64 * 64 * JC;
+  __shared__ int32_t rows_s[kTM];
+  __shared__ __attribute__((aligned(16))) uint16_t t_hi[16 * LD], t_lo[16 * LD];
+  __shared__ f32x4 red[16 * JB * 64];
+  __shared__ __attribute__((aligned(1024))) char bs[4 * kB];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  int part;
+  const int tile = tile_of(p.a, blockIdx.x, p.parts, part);
+  const Tile t = find_tile(p.a, tile, rows_s);
+  const int n = t.n, rank = t.rank;
+  const bool store_t = p.T_out && part == 0;
+  if (n == 0 || (rank == 0 && p.Yi == p.Yo && !store_t)) return;
+  const int r = p.a.r, N = p.N, K = p.K, cpr = r / 8;
+  const bool has = t.slot < p.a.slots;
+  const float s = has ? p.a.scales[t.slot] : 0.0f;
+  for (int e = threadIdx.x; e < 16 * LD; e += 1024) t_hi[e] = t_lo[e] = 0;
+  __syncthreads();
+  // the expand's operands on their way
+  const int n0 = part * 256 + 64 * wave;
+  const bool mine = wave < 4 && n0 < N;
+  const uint32_t b_lds = mx_lds_addr(bs) + (wave & 3) * kB;
+  u32x2 y[4];
+  int32_t at[4];
+  if (mine) {
+    if (has) {
+      const char* run = uniform(p.B + ((int64_t)t.slot * N + n0) * r);
+#pragma unroll
+      for (int u = 0; u < 4 * JC; ++u) {
+        if (u >= (r + 7) / 8) break;
+        const int q = 64 * u + lane;
+        dma16(run, WHOLE ? 16 * (q / cpr * cpr + ((q % cpr) ^ b_swz(q / cpr, cpr)))
+                         : 16 * (q < 8 * r ? q : 8 * r - 1), b_lds + 1024 * u);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      at[v] = rows_s[4 * g + v < n ? 4 * g + v : n - 1] * N + n0 + 4 * i16;
+      y[v] = *reinterpret_cast<const u32x2*>(p.Yi + at[v]);
+    }
+  }
+  if (rank) {
+    const uint16_t* A = p.A + (int64_t)t.slot * r * K;
+    const uint16_t* xr = p.X + (int64_t)rows_s[i16 < n ? i16 : n - 1] * K + 8 * g;
+    const uint16_t* ar[JB];
+    f32x4 acc[JB];
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      const int k = 16 * j + i16;
+      ar[j] = A + (int64_t)(k < rank ? k : rank - 1) * K + 8 * g;
+      acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    constexpr int D = JB == 1 ? 8 : 4;  // halves of steps in flight
+    u32x4 x[D], a[D][JB];
+    const int nw = (K / 64 - wave + 15) / 16;
+    auto load = [&](int i, int b) {
+      const int c = 64 * (wave + 16 * (i >> 1)) + 32 * (i & 1);
+      x[b] = *reinterpret_cast<const u32x4*>(xr + c);
+#pragma unroll
+      for (int j = 0; j < JB; ++j) a[b][j] = *reinterpret_cast<const u32x4*>(ar[j] + c);
+    };
+#pragma unroll
+    for (int b = 0; b < D; ++b)
+      if (b < 2 * nw) load(b, b);
+    for (int i = 0; i < 2 * nw; i += D)
+#pragma unroll
+      for (int b = 0; b < D; ++b) {
+        if (i + b >= 2 * nw) break;
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[j] = mfma16(x[b], a[b][j], acc[j]);
+        if (i + b + D < 2 * nw) load(i + b + D, b);
+      }
+#pragma unroll
+    for (int j = 0; j < JB; ++j) red[(wave * JB + j) * 64 + lane] = acc[j];
+  }
+  __syncthreads();
+  if (wave < JB) {  // wave w finishes block w
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int j = 16 * wave + i16;
+    if (j < rank) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += red[(w * JB + wave) * 64 + lane][e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 4 * g + e;
+      if (store_t && i < n && j < r) p.T_out[(int64_t)rows_s[i] * r + j] = v[e];
+      uint16_t hi, lo;
+      split2(i < n ? v[e] * s : 0.0f, hi, lo);
+      t_hi[i * LD + j] = hi;
+      t_lo[i * LD + j] = lo;
+    }
+  }
+  __syncthreads();
+  if (!mine || (rank == 0 && p.Yi == p.Yo)) return;
+  mx_wait_loads();
+  if (rank) {
+    f32x4 acc[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      acc[0][v] = lo_bf16(y[v][0]);
+      acc[1][v] = hi_bf16(y[v][0]);
+      acc[2][v] = lo_bf16(y[v][1]);
+      acc[3][v] = hi_bf16(y[v][1]);
+    }
+#pragma unroll
+    for (int jc = 0; jc < JC; ++jc) {
+      const u32x4 th = *reinterpret_cast<const u32x4*>(t_hi + i16 * LD + 32 * jc + 8 * g);
+      const u32x4 tl = *reinterpret_cast<const u32x4*>(t_lo + i16 * LD + 32 * jc + 8 * g);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        u32x4 bf = b_read<WHOLE>(b_lds, 4 * i16 + b, 4 * jc + g, r, cpr);
+        b_mask(bf, 32 * jc + 8 * g, rank);
+        acc[b] = mfma16(tl, bf, acc[b]);
+        acc[b] = mfma16(th, bf, acc[b]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      y[v] = u32x2{pack_bf16x2(acc[0][v], acc[1][v]), pack_bf16x2(acc[2][v], acc[3][v])};
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (4 * g + v < n) *reinterpret_cast<u32x2*>(p.Yo + at[v]) = y[v];
+}
+
 // ------------------------------------------------------------- gradients
 // dA_a = s_a sum_i U[i]^T X[i] and dB_a = s_a sum_i dY[i]^T T[i] over one
 // segment of the place's rows, 256 columns of X or dY per workgroup, 64 per
@@ -786,6 +935,7 @@ struct GradParams {
   float* dB;    // slots x N x r
   float* part;  // partial sums x (r K + N r)
   int32_t N, K, accumulate;
+  int32_t by_place;  // no place has more rows than a segment: blockIdx.y is the place
 };
 
 constexpr int kZP = 256 + 16;  // LDS row pitch of a step's columns, in elements
@@ -800,12 +950,12 @@ __device__ __forceinline__ u32x2 read_turned(uint16_t* p) {
 }
 
 template <int JB, bool DB>
-__device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, uint16_t* zs,
-                                          uint16_t* vs, int32_t* rows_s) {
+__device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int slot, int c0,
+                                          uint16_t* zs, uint16_t* vs, int32_t* rows_s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, i16 = lane & 15;
-  const int4 sg = p.a.segs[seg];
-  const int slot = sg.x, n = sg.z, rank = sg.w, r = p.a.r, C = DB ? p.N : p.K;
+  const int4 sg = seg < 0 ? make_int4(slot, 0, 0, 0) : p.a.segs[seg];
+  const int n = sg.z, rank = sg.w, r = p.a.r, C = DB ? p.N : p.K;
   const int32_t* perm = p.a.perm + sg.y;
   const uint16_t* Z = DB ? p.dY : p.X;
   const float* V = DB ? p.T : p.U;
@@ -889,7 +1039,7 @@ __device__ __forceinline__ void grad_tile(const GradParams& p, int seg, int c0, 
     }
   }
   const int first = p.a.seg0[slot];
-  const bool whole = p.a.seg0[slot + 1] == first + 1;  // the place's only segment
+  const bool whole = p.by_place || p.a.seg0[slot + 1] == first + 1;  // the place's only segment
   const float s = p.a.scales[slot];
   const int64_t size = (int64_t)r * p.K + (int64_t)p.N * r;
   float* out = whole ? (DB ? p.dB + (int64_t)slot * p.N * r : p.dA + (int64_t)slot * r * p.K)
@@ -927,12 +1077,22 @@ __global__ __launch_bounds__(256, JB <= 2 ? 4 : 3) void adapter_grads_kernel(Gra
   __shared__ __attribute__((aligned(16))) uint16_t zs[32 * kZP];
   __shared__ __attribute__((aligned(16))) uint16_t vs[3 * 16 * JB * kVP];
   __shared__ int32_t rows_s[kRowsLds];
-  if ((int)blockIdx.y >= p.a.count[1]) return;
+  int seg = blockIdx.y, slot = blockIdx.y;
+  if (p.by_place) {
+    seg = p.a.seg0[slot];
+    if (p.a.seg0[slot + 1] == seg) {  // no rows: zeros, or nothing to add
+      if (p.accumulate) return;
+      seg = -1;
+    }
+  } else {
+    if (seg >= p.a.count[1]) return;
+    slot = p.a.segs[seg].x;
+  }
   const int ca = (p.K + 255) / 256;
   if ((int)blockIdx.x < ca)
-    grad_tile<JB, false>(p, blockIdx.y, 256 * blockIdx.x, zs, vs, rows_s);
+    grad_tile<JB, false>(p, seg, slot, 256 * blockIdx.x, zs, vs, rows_s);
   else
-    grad_tile<JB, true>(p, blockIdx.y, 256 * (blockIdx.x - ca), zs, vs, rows_s);
+    grad_tile<JB, true>(p, seg, slot, 256 * (blockIdx.x - ca), zs, vs, rows_s);
 }
 
 // Places of several segments: their sums in order; places without rows: zeros.
@@ -1114,6 +1274,36 @@ RowArgs row_args(int64_t M, const lq_adapter_pool& q, const int32_t* rows) {
   return a;
 }
 
+// Whether a forward takes one launch: few rows, and A's rows, which every 256
+// columns read again, within kFewBytes even if each row has an adapter of its own
+constexpr int64_t kFewBytes = (int64_t)32 << 20;
+bool few_rows(int64_t M, int64_t N, int64_t K, int64_t r) {
+  return M <= kFew && M * cdiv(N, 256) * r * K * 2 <= kFewBytes;
+}
+
+int launch_few(const RowArgs& a, const void* X, const lq_adapter_pool& q, const void* Yi, void* Yo,
+               float* T_out, hipStream_t st) {
+  FewParams p;
+  p.a = a;
+  p.X = (const uint16_t*)X;
+  p.A = (const uint16_t*)q.A;
+  p.B = (const uint16_t*)q.B;
+  p.Yi = (const uint16_t*)Yi;
+  p.Yo = (uint16_t*)Yo;
+  p.T_out = T_out;
+  p.K = (int32_t)q.K;
+  p.N = (int32_t)q.N;
+  p.parts = (int32_t)cdiv(q.N, 256);
+  const dim3 g((unsigned)(a.M * p.parts)), b(1024);
+  const bool whole = q.r % 8 == 0;
+  const auto kernel = q.r <= 16   ? (whole ? few_rows_kernel<1, true> : few_rows_kernel<1, false>)
+                      : q.r <= 32 ? (whole ? few_rows_kernel<2, true> : few_rows_kernel<2, false>)
+                      : q.r <= 48 ? (whole ? few_rows_kernel<3, true> : few_rows_kernel<3, false>)
+                                  : (whole ? few_rows_kernel<4, true> : few_rows_kernel<4, false>);
+  hipLaunchKernelGGL(kernel, g, b, 0, st, p);
+  return hip_fail(hipGetLastError(), "adapters few-row launch");
+}
+
 // Workspace of the backward: [plan][B turned][A turned][U][T][partial sums of the
 // shrinks][partial gradients]
 struct BwdLayout {
@@ -1140,7 +1330,7 @@ BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) 
 namespace dispatch {
 
 size_t adapters_fwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
-  (void)N;
+  if (few_rows(M, N, K, r)) return 0;
   const size_t plan = M <= kDirect ? 0 : plan_layout(M, slots, max_segments(M, N, K, slots)).end;
   return plan + (size_t)shrink_splits(M, K) * M * t_pitch(r) * 4;
 }
@@ -1152,6 +1342,7 @@ size_t adapters_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots
 int adapters_fwd(const void* X, int64_t M, const lq_adapter_pool& q, const int32_t* rows,
                  const void* Y_in, void* Y_out, float* T_out, void* ws, hipStream_t st) {
   RowArgs a = row_args(M, q, rows);
+  if (few_rows(M, q.N, q.K, q.r)) return launch_few(a, X, q, Y_in, Y_out, T_out, st);
   char* base = (char*)ws;
   int rc;
   if (M > kDirect) {
@@ -1205,15 +1396,16 @@ int adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool
   p.N = (int32_t)q.N;
   p.K = (int32_t)q.K;
   p.accumulate = accumulate;
+  p.by_place = M <= segment_rows(M, q.N, q.K);
   const dim3 g((unsigned)(cdiv(q.N, 256) + cdiv(q.K, 256)),
-               (unsigned)max_segments(M, q.N, q.K, q.slots));
+               (unsigned)(p.by_place ? q.slots : max_segments(M, q.N, q.K, q.slots)));
   switch ((q.r + 15) / 16) {
     case 1: hipLaunchKernelGGL(adapter_grads_kernel<1>, g, dim3(256), 0, st, p); break;
     case 2: hipLaunchKernelGGL(adapter_grads_kernel<2>, g, dim3(256), 0, st, p); break;
     case 3: hipLaunchKernelGGL(adapter_grads_kernel<3>, g, dim3(256), 0, st, p); break;
     default: hipLaunchKernelGGL(adapter_grads_kernel<4>, g, dim3(256), 0, st, p);
   }
-  if ((rc = hip_fail(hipGetLastError(), "adapters gradient launch"))) return rc;
+  if ((rc = hip_fail(hipGetLastError(), "adapters gradient launch")) || p.by_place) return rc;
   const int64_t size = (int64_t)q.r * (q.N + q.K);
   hipLaunchKernelGGL(grads_finish_kernel, dim3((unsigned)cdiv(size, 1024), q.slots), dim3(256), 0,
                      st, p);

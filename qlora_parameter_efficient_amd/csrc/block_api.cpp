@@ -160,8 +160,8 @@ int lq_adapters_fwd(const void* X, int64_t M, const lq_adapter_pool* pool, const
       (rc = check_to(ws, 16, "ws")))
     return rc;
   const size_t need = dispatch::adapters_fwd_ws(M, pool->N, pool->K, pool->r, pool->slots);
-  REQUIRE(ws != nullptr && ws_bytes >= need, LQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu",
-          ws_bytes, need);
+  REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), LQ_ERR_WORKSPACE,
+          "workspace %zu bytes, need %zu", ws_bytes, need);
   return dispatch::adapters_fwd(X, M, *pool, rows, Y_in, Y_out, T_out, ws, stream);
 }
 

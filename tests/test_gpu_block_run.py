@@ -105,7 +105,7 @@ def test_serving_step_in_a_graph():
         assert torch.equal(got[3][bare], plain[bare]) and not torch.equal(got[3][~bare], plain[~bare])
 
 
-@pytest.mark.parametrize("M", [20, 500])
+@pytest.mark.parametrize("M", [3, 20, 500])
 def test_captured_calls_equal_eager_ones(M):
     """Every call on its own in one graph, replayed with other work between."""
     N, K, V, r = 192, 256, 3000, 12
@@ -160,7 +160,7 @@ def test_calls_on_two_streams():
 
 
 def test_refusals_leave_outputs_alone():
-    c = adapter_case(8, 64, 64, 4, 2)
+    c = adapter_case(20, 64, 64, 4, 2)
     Y = c["Y"].clone()
     with pytest.raises(lq.LqError):
         block.lq_adapters_fwd(c["X"], pool(c), c["rows"], Y, out=Y, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
@@ -177,8 +177,8 @@ def test_refusals_leave_outputs_alone():
     with pytest.raises(lq.LqError):
         block.lq_rmsnorm_fwd(Y, torch.ones(64, device=DEV), float("nan"))
     with pytest.raises(ValueError):
-        block.lq_head_loss(Y, c["X"], torch.zeros(8, device=DEV))
+        block.lq_head_loss(Y, c["X"], torch.zeros(20, device=DEV))
     with pytest.raises(lq.LqError):
-        block.lq_head_loss(Y[:, :32].contiguous(), c["X"][:, :32].contiguous(), torch.zeros(8, dtype=torch.int32, device=DEV))
+        block.lq_head_loss(Y[:, :32].contiguous(), c["X"][:, :32].contiguous(), torch.zeros(20, dtype=torch.int32, device=DEV))
     torch.cuda.synchronize()
     assert torch.equal(Y, c["Y"])
