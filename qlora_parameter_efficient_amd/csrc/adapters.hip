@@ -1274,11 +1274,14 @@ RowArgs row_args(int64_t M, const lq_adapter_pool& q, const int32_t* rows) {
   return a;
 }
 
-// Whether a forward takes one launch: few rows, and A's rows, which every 256
-// columns read again, within kFewBytes even if each row has an adapter of its own
-constexpr int64_t kFewBytes = (int64_t)32 << 20;
+// Whether a forward takes one launch: few rows, one round of workgroups even if
+// each row has an adapter of its own, and a factor A short enough for one
+// workgroup.  In a captured graph, one launch against two: 8.4 us against 8.2 at
+// 4096 x 4096 and rank 16 (1 to 16 rows), 5.0 against 7.7 at 1024 x 1024, but 19.5
+// against 12.2 at rank 64 and 15.3 against 9.0 with 8 rows of 11008 columns; outside
+// a graph it saves 4 us of launch and workspace.
 bool few_rows(int64_t M, int64_t N, int64_t K, int64_t r) {
-  return M <= kFew && M * cdiv(N, 256) * r * K * 2 <= kFewBytes;
+  return M <= kFew && M * cdiv(N, 256) <= 256 && r * K <= 65536;
 }
 
 int launch_few(const RowArgs& a, const void* X, const lq_adapter_pool& q, const void* Yi, void* Yo,

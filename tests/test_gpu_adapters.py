@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 
 SHAPES = [  # M, N, K, r, slots
     (1, 64, 64, 1, 1), (1, 4096, 4096, 16, 8), (2, 64, 128, 64, 3), (16, 320, 192, 7, 16), (17, 256, 576, 33, 4),
-    (3, 11008, 4096, 64, 8), (5, 1000 * 64, 4096, 24, 4), (15, 192, 4096, 48, 3), (48, 1088, 1024, 32, 64), (63, 128, 256, 8, 2), (64, 64, 4160, 17, 70), (65, 64, 4160, 17, 70), (100, 640, 320, 11, 3),
+    (3, 11008, 4096, 16, 8), (5, 1000 * 64, 4096, 24, 4), (15, 192, 960, 48, 3), (12, 4096, 1024, 61, 5), (48, 1088, 1024, 32, 64), (63, 128, 256, 8, 2), (64, 64, 4160, 17, 70), (65, 64, 4160, 17, 70), (100, 640, 320, 11, 3),
     (257, 512, 256, 16, 1), (777, 1024, 512, 48, 6), (2048, 320, 640, 64, 16), (3000, 64, 64, 4, 300)]
 
 
