@@ -5,10 +5,11 @@
 //   dX[i] += s_a U[i] A_a,  U[i] = dY[i] B_a
 //   dA_a = s_a sum_i U[i]^T X[i],  dB_a = s_a sum_i dY[i]^T T[i]
 //
-// Rows are taken in tiles of up to 64 that share one adapter.  Up to 64 rows
-// every workgroup finds its tile by itself: workgroup i looks at the row ids
+// Rows are taken in tiles that share one adapter.  Up to 64 rows every workgroup
+// finds its tile, of up to 16 rows, by itself: workgroup i looks at the row ids
 // (one per lane, one ballot) and goes on only if row i is the first with its
-// adapter.  More rows are sorted by one workgroup first (plan_kernel).
+// adapter, or the 17th, 33rd or 49th.  More rows are sorted by one workgroup
+// first (plan_kernel), into tiles of up to 64.
 //
 // Shrink (T = X A^T, U = dY B): workgroups split the reduction, their partial sums
 // are added in order by the expand.
@@ -23,7 +24,8 @@ namespace lq {
 namespace {
 
 constexpr int kTM = 64;       // rows per tile
-constexpr int kDirect = 64;   // up to so many rows workgroups find their tiles by themselves
+constexpr int kDirect = 64;   // up to so many rows workgroups find their tiles by themselves,
+constexpr int kFew = 16;      // ... of so many rows at most
 constexpr int kCnt = 32768;   // counters of the plan
 
 struct RowArgs {
@@ -81,9 +83,11 @@ __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* r
     t.slot = __builtin_amdgcn_readlane(id, tile);
     t.rank = __builtin_amdgcn_readfirstlane(rank_of(a.ranks, a.slots, a.r, t.slot));
     const uint64_t same = __ballot(id == t.slot);
-    t.n = (int)__builtin_ctzll(same) == tile ? __builtin_popcountll(same) : 0;
-    if (threadIdx.x < 64 && id == t.slot)
-      rows_s[__builtin_popcountll(same & ((1ull << lane) - 1))] = lane;
+    const int before = __builtin_popcountll(same & ((1ull << tile) - 1));
+    const int left = __builtin_popcountll(same) - before;
+    t.n = before % kFew ? 0 : left < kFew ? left : kFew;
+    const int at = __builtin_popcountll(same & ((1ull << lane) - 1)) - before;
+    if (threadIdx.x < 64 && id == t.slot && at >= 0 && at < kFew) rows_s[at] = lane;
     return t;
   }
   const int4 d = a.tiles[tile];  // (past the last tile: not used)
@@ -540,10 +544,11 @@ __device__ __forceinline__ void shrink_many(const ShrinkParams& p, const int32_t
     }
 }
 
-template <int JB>
+// FEW: no tile has more than kFew rows
+template <int JB, bool FEW>
 __global__ __launch_bounds__(256) void shrink_tiles_kernel(ShrinkParams p) {
   __shared__ int32_t rows_s[kTM];
-  __shared__ __attribute__((aligned(1024))) char lds[kStages * (kTM + 16 * JB) * 128];
+  __shared__ __attribute__((aligned(1024))) char lds[FEW ? 4 * JB * 1024 : kStages * (kTM + 16 * JB) * 128];
   int part;
   const int tile = tile_of(p.a, blockIdx.x, p.splits, part);
   const Tile t = find_tile(p.a, tile, rows_s);
@@ -553,7 +558,7 @@ __global__ __launch_bounds__(256) void shrink_tiles_kernel(ShrinkParams p) {
   const int s1 = s0 + p.steps < all ? s0 + p.steps : all;
   const uint16_t* A = (const uint16_t*)uniform(p.A + (int64_t)t.slot * p.a.r * p.C);
   float* out = p.Tp + (int64_t)part * p.a.M * p.rp;
-  if (t.n <= 16)
+  if (FEW || t.n <= kFew)
     shrink_few<JB>(p, rows_s, t.n, A, t.rank, s0, s1, out, reinterpret_cast<f32x4*>(lds));
   else
     shrink_many<JB>(p, rows_s, t.n, A, t.rank, s0, s1, out, lds);
@@ -606,15 +611,15 @@ __device__ __forceinline__ void split2(float v, uint16_t& hi, uint16_t& lo) {
   lo = (hi & 0x7F80u) == 0x7F80u ? (uint16_t)0 : f32_to_bf16(v - h);
 }
 
-// JC: 32-rank chunks.  What does not depend on T (B, Y) is loaded before T's
-// partial sums are waited for.
-template <int JC, bool WHOLE>
-__global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(ExpandParams p) {
+// JC: 32-rank chunks; MB: 16-row blocks of a tile.  What does not depend on T (B,
+// Y) is loaded before T's partial sums are waited for.
+template <int JC, bool WHOLE, int MB>
+__global__ __launch_bounds__(256, MB == 1 ? 6 : JC == 1 ? 4 : 3) void expand_tiles_kernel(ExpandParams p) {
   constexpr int LD = 32 * JC + 8;  // LDS row pitch of T in elements
-  constexpr int VT = 2 * JC;       // groups of four values of T per thread
+  constexpr int VT = MB * JC / 2 > 0 ? MB * JC / 2 : 1;  // groups of four values of T per thread
   constexpr int kB = 64 * 64 * JC; // bytes of a wave's rows of B
   __shared__ int32_t rows_s[kTM];
-  __shared__ __attribute__((aligned(16))) uint16_t t_hi[kTM * LD], t_lo[kTM * LD];
+  __shared__ __attribute__((aligned(16))) uint16_t t_hi[16 * MB * LD], t_lo[16 * MB * LD];
   __shared__ __attribute__((aligned(1024))) char bs[4 * kB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -634,8 +639,8 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
   // 64 rows of B are one run of 128 ldb bytes, 1024 per load (the last load's
   // lanes past the end: the last 16 bytes again)
   const int b_loads = (ldb + 7) / 8;
-  u32x2 y[4][4];
-  int32_t at[4][4];  // M N < 2^31
+  u32x2 y[MB][4];
+  int32_t at[MB][4];  // M N < 2^31
   auto load = [&](int n0) {
     if (has) {
       const char* run = uniform(B + (int64_t)n0 * ldb);
@@ -654,7 +659,7 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
       }
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int m = 0; m < MB; ++m) {
       if (16 * m >= n) break;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
@@ -680,7 +685,7 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
     if (has) {  // (whatever lies past the rank)
       const int64_t part = (int64_t)M * p.rp;
       int k = 0;
-      constexpr int D = 4 / JC;
+      constexpr int D = MB == 1 ? 4 : 4 / JC;
       for (; k + D <= p.splits; k += D) {
         f32x4 x[D][VT];
 #pragma unroll
@@ -706,6 +711,7 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
 #pragma unroll
     for (int u = 0; u < VT; ++u) {
       const int e = 256 * u + tid, i = e / (8 * JC), j = 4 * (e % (8 * JC));
+      if (i >= 16 * MB) break;  // (one block of one chunk: half of the threads)
       uint16_t hi[4], lo[4];
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
@@ -734,7 +740,7 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
         }
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+    for (int m = 0; m < MB; ++m) {
       if (16 * m >= n) break;
       if (rank) {
         f32x4 acc[4];
@@ -775,8 +781,6 @@ __global__ __launch_bounds__(256, JC == 1 ? 4 : 3) void expand_tiles_kernel(Expa
 // turns at the steps of the whole reduction, and then 256 columns of the expand.
 // A is read again for every 256 columns (from L2), but there is one launch, no
 // workspace, and no trip of T through memory.
-constexpr int kFew = 16;
-
 struct FewParams {
   RowArgs a;
   const uint16_t* X;
@@ -1226,12 +1230,15 @@ int launch_shrink(const RowArgs& a, const void* X, const void* A, int64_t C, flo
   p.splits = splits;
   p.steps = (int32_t)cdiv(C / 64, splits);
   const dim3 g(tile_grid(a) * (unsigned)splits), b(256);
-  switch ((a.r + 15) / 16) {
-    case 1: hipLaunchKernelGGL(shrink_tiles_kernel<1>, g, b, 0, st, p); break;
-    case 2: hipLaunchKernelGGL(shrink_tiles_kernel<2>, g, b, 0, st, p); break;
-    case 3: hipLaunchKernelGGL(shrink_tiles_kernel<3>, g, b, 0, st, p); break;
-    default: hipLaunchKernelGGL(shrink_tiles_kernel<4>, g, b, 0, st, p);
-  }
+  const auto kernel = a.tiles ? (a.r <= 16   ? shrink_tiles_kernel<1, false>
+                                 : a.r <= 32 ? shrink_tiles_kernel<2, false>
+                                 : a.r <= 48 ? shrink_tiles_kernel<3, false>
+                                             : shrink_tiles_kernel<4, false>)
+                              : (a.r <= 16   ? shrink_tiles_kernel<1, true>
+                                 : a.r <= 32 ? shrink_tiles_kernel<2, true>
+                                 : a.r <= 48 ? shrink_tiles_kernel<3, true>
+                                             : shrink_tiles_kernel<4, true>);
+  hipLaunchKernelGGL(kernel, g, b, 0, st, p);
   return hip_fail(hipGetLastError(), "adapters shrink launch");
 }
 
@@ -1257,8 +1264,12 @@ int launch_expand(const RowArgs& a, const float* Tp, int splits, const void* B, 
   p.passes = (int32_t)passes;
   p.parts = (int32_t)cdiv(chunks, passes);
   const dim3 g(tile_grid(a) * (unsigned)p.parts), b(256);
-  const auto kernel = a.r <= 32 ? (ldb % 8 ? expand_tiles_kernel<1, false> : expand_tiles_kernel<1, true>)
-                                : (ldb % 8 ? expand_tiles_kernel<2, false> : expand_tiles_kernel<2, true>);
+  const bool whole = ldb % 8 == 0;
+  const auto kernel =
+      a.tiles ? (a.r <= 32 ? (whole ? expand_tiles_kernel<1, true, 4> : expand_tiles_kernel<1, false, 4>)
+                           : (whole ? expand_tiles_kernel<2, true, 4> : expand_tiles_kernel<2, false, 4>))
+              : (a.r <= 32 ? (whole ? expand_tiles_kernel<1, true, 1> : expand_tiles_kernel<1, false, 1>)
+                           : (whole ? expand_tiles_kernel<2, true, 1> : expand_tiles_kernel<2, false, 1>));
   hipLaunchKernelGGL(kernel, g, b, 0, st, p);
   return hip_fail(hipGetLastError(), "adapters expand launch");
 }
