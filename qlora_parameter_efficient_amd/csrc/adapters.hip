@@ -16,6 +16,16 @@
 // Expand (Y += s T B^T, dX += s U A): rows of B in an order (column 4 i + b of a
 // 64-column block is column i of MFMA block b) that gives a lane four consecutive
 // outputs of a row and 16 lanes a whole 128-byte line.
+//
+// Bound by memory: X, Y in and out, the factors once, and for one row by the
+// latency of a chain of dependent loads (rows, place, rank, operands).  Measured
+// (kernels, us): 1 x 4096 x 4096 rank 16 one launch 7.5; 48 x 11008 x 4096, nearly
+// every row its own adapter of rank up to 32, shrink 6 + expand 9.5; 8192 x 4096 x
+// 4096, 16 places of rank up to 64, plan 10 + shrink 18 + expand 42 (2.7 TB/s of
+// the 192 MB of X and Y; without the partial sums of T and without B it would be 31:
+// both come from L2 for every 256 columns).  Backward of 4096 x 4096 x 11008, 8
+// places of rank up to 32: plan and turned factors 10, U 12, dX 45 (4 TB/s),
+// gradients 37 + 7.
 #include "block.h"
 #include "dispatch.h"
 #include "mx_tile.h"
@@ -1143,11 +1153,11 @@ unsigned tile_grid(const RowArgs& a) {
   return (unsigned)(a.tiles ? cdiv(t, 8) * 8 : t);
 }
 
-// Splits of the shrink's reduction over C columns: about 512 workgroups where
+// Splits of the shrink's reduction over C columns: about 256 workgroups where
 // tiles are full, each wave with four steps at least, so that they are in flight
 // together
 int shrink_splits(int64_t M, int64_t C) {
-  const int64_t most = cdiv(C / 64, 16), want = cdiv(512, cdiv(M, kTM));
+  const int64_t most = cdiv(C / 64, 16), want = cdiv(256, cdiv(M, kTM));
   const int64_t s = want < most ? want : most;
   return (int)(s < 16 ? s : 16);
 }
@@ -1181,7 +1191,7 @@ PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   l.part0 = l.seg0 + up256((size_t)(slots + 2) * 4);
   l.count = l.part0 + up256((size_t)(slots + 2) * 4);
   l.tiles = l.count + 256;
-  l.segs = l.tiles + up256((size_t)(max_tiles(M > kDirect ? M : kDirect + 1, slots) + 7) * 16);
+  l.segs = l.tiles + up256((size_t)(cdiv(max_tiles(M, slots), 8) * 8) * 16);  // tile_grid's
   l.perm = l.segs + up256((size_t)segs * 16);
   l.end = l.perm + up256((size_t)M * 4);
   return l;

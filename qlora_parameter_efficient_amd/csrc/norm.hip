@@ -9,7 +9,9 @@
 // not fit is read again).  A thread owns units of 16 consecutive columns, so that a
 // lane pair holds one block of an MX output and one DPP move completes the block's
 // amax, as in the quantiser; y is quantised from its float32 value, never stored
-// in between.  (Pieces of 16 bytes, consecutive as the threads are, took 61 us
+// in between.  Measured: 2048 x 4096 bf16 with residual, y and MXFP8 out 15.5 us (4.8
+// TB/s), backward of 8192 x 4096 with dW 50 + 5 us (5.3 TB/s in the first), 777 x
+// 4095 float32 to y and MXFP4 11 us, one row of 4096 2.6 us.  (Pieces of 16 bytes, consecutive as the threads are, took 61 us
 // against 54 in the backward of 8192 x 4096 and as long in the forward.)
 #include "block.h"
 #include "mx_unit.h"
