@@ -640,6 +640,8 @@ __global__ __launch_bounds__(256, MB == 1 ? 6 : JC == 1 ? 4 : 3) void expand_til
   const int n = t.n, rank = t.rank;
   if (n == 0) return;
   const bool store_t = p.T_out && part == 0;
+  const bool same = !p.Yo || (rank == 0 && p.Yi == p.Yo);  // Y stays as it is
+  if (same && !store_t) return;
   const bool has = t.slot < p.a.slots;
   const int r = p.a.r, M = p.a.M, N = p.N, ldb = p.ldb, cpr = ldb / 8;
   const float s = has ? p.a.scales[t.slot] : 0.0f;
@@ -680,7 +682,7 @@ __global__ __launch_bounds__(256, MB == 1 ? 6 : JC == 1 ? 4 : 3) void expand_til
     }
   };
   int n0 = part * p.passes * 256 + 64 * wave;
-  if (p.Yo && n0 < N) load(n0);
+  if (!same && n0 < N) load(n0);
   {
     f32x4 v[VT];
     int32_t q[VT];
@@ -736,7 +738,7 @@ __global__ __launch_bounds__(256, MB == 1 ? 6 : JC == 1 ? 4 : 3) void expand_til
     }
   }
   __syncthreads();
-  if (!p.Yo || (rank == 0 && p.Yi == p.Yo)) return;
+  if (same) return;
   for (int pass = 0; pass < p.passes && n0 < N; ++pass) {
     u32x4 bf[4][JC];
     mx_wait_loads();

@@ -30,11 +30,11 @@
 // next behind the products of two substeps, half behind the barrier and half in the
 // next step (766; all behind the barrier, or over three substeps, 4 to 6% more).
 //
-// Measured at 4096 x 32000 x 4096: logits 868 us (1.24 PFLOP/s; 150 of it go to
-// their stores, which come in bursts of 64 MB as all tiles of a round end), softmax
-// 191 (4.1 TB/s), dH 788 (1.36 PFLOP/s; the matrix units are then busy about 60% of
-// the cycles at 2.0 GHz).  130 rows: logits 68 to 81 us (W once, 3.2 to 3.9 TB/s),
-// dH 66 + 8.
+// Measured at 4096 x 32000 x 4096: logits 860 us (1.25 PFLOP/s; of a tile's 102 us 2 to
+// 3 go to its first loads, 6 to the stores of its logits, the rest to 64 steps of
+// 1.45 us), softmax 191 (4.1 TB/s), dH 785 (1.37 PFLOP/s).  Over both products the
+// matrix units are busy 70% of the cycles and waves wait 17% of theirs.  130 rows:
+// logits 68 to 81 us (W once, 3.2 to 3.9 TB/s), dH 66 + 8.
 #include <type_traits>
 
 #include "block.h"
