@@ -21,11 +21,11 @@
 // latency of a chain of dependent loads (rows, place, rank, operands).  Measured
 // (kernels, us): 1 x 4096 x 4096 rank 16 one launch 7.5; 48 x 11008 x 4096, nearly
 // every row its own adapter of rank up to 32, shrink 6 + expand 9.5; 8192 x 4096 x
-// 4096, 16 places of rank up to 64, plan 10 + shrink 18 + expand 42 (2.7 TB/s of
-// the 192 MB of X and Y; without the partial sums of T and without B it would be 31:
-// both come from L2 for every 256 columns).  Backward of 4096 x 4096 x 11008, 8
-// places of rank up to 32: plan and turned factors 10, U 12, dX 45 (4 TB/s),
-// gradients 37 + 7.
+// 4096, 16 places of rank up to 64, plan 7 + shrink 18 + expand 40 (65 in all, 3.1
+// TB/s of the 201 MB of X and Y; without the partial sums of T and without B the
+// expand would take 31: both come from L2 for every 256 columns).  Backward of 4096 x
+// 4096 x 11008, 8 places of rank up to 32: plan and turned factors 9.5, U 12, dX 44
+// (4.1 TB/s), gradients 37 + 7.
 #include "block.h"
 #include "dispatch.h"
 #include "mx_tile.h"
@@ -36,18 +36,17 @@ namespace {
 constexpr int kTM = 64;       // rows per tile
 constexpr int kDirect = 64;   // up to so many rows workgroups find their tiles by themselves,
 constexpr int kFew = 16;      // ... of so many rows at most
-constexpr int kCnt = 32768;   // counters of the plan
+constexpr int kCnt = 36880;   // LDS words of the plan's workgroup: larger pools, ...
+constexpr int kCntOne = 19 * 1024;  // ... and up to 1023 places (two workgroups fit a CU)
 
 struct RowArgs {
   const int32_t* rows;
   const int32_t* ranks;
   const float* scales;
-  // the plan (NULL: M <= kDirect): first sorted position of each place's rows
-  // (place ``slots``: rows without an adapter; then M), rows in sorted order,
-  // (place, first position, rows, rank) of each tile and of each segment of the
-  // gradients, the first segment of each place, and its first partial sum (places
-  // of several segments have one a segment)
-  const int32_t* off;
+  // the plan (NULL: M <= kDirect): rows sorted by place (place ``slots``: rows
+  // without an adapter), (place, first position, rows, rank) of each tile and of
+  // each segment of the gradients, the first segment of each place, and its first
+  // partial sum (places of several segments have one a segment)
   const int32_t* perm;
   const int4* tiles;
   const int4* segs;
@@ -113,13 +112,15 @@ __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* r
 // Stable counting sort of the rows by place, in one workgroup of 16 waves: each
 // wave counts its own range of rows into counters of its own (rows of a wave
 // that share a place are found with one ballot per bit of the place) and notes
-// each row's position among them, the counters become first positions, and the
-// rows are placed.  Rows are loaded eight at a time, since a load is the longest
-// part of a step.
+// each row's position among them, the counters become the waves' first positions
+// within the place, and the rows are placed; the row that begins a tile or a
+// segment lists it (from the counting threads, one place after another, the lists
+// took 2 to 3 us).  Rows are loaded eight at a time, since a load is the longest
+// part of a step.  Of 6.2 us for 8192 rows in 16 places, 2.4 go until the rows are
+// there, 1 to counting, 1 to the sums and 1.9 to the stores.
 struct PlanArgs {
   const int32_t* rows;
   const int32_t* ranks;
-  int32_t* off;
   int32_t* perm;
   int4* tiles;
   int4* segs;
@@ -129,50 +130,52 @@ struct PlanArgs {
   int32_t M, slots, r, waves, bits, seg_rows;
 };
 
-// the lanes of the wave whose value equals this lane's
-__device__ __forceinline__ uint64_t lanes_like(int v, int bits, bool in) {
-  uint64_t m = __ballot(in);
+// the lanes of m whose value equals this lane's
+__device__ __forceinline__ uint64_t lanes_like(int v, int bits, uint64_t m) {
+  uint32_t lo = (uint32_t)m, hi = (uint32_t)(m >> 32);
   for (int b = 0; b < bits; ++b) {
-    const uint64_t k = __ballot((v >> b) & 1);
-    m &= (v >> b) & 1 ? k : ~k;
+    const uint32_t bit = __builtin_amdgcn_sbfe(v, b, 1);  // 0 or all ones
+    const uint64_t set = __ballot(bit != 0);
+    lo &= ~((uint32_t)set ^ bit);
+    hi &= ~((uint32_t)(set >> 32) ^ bit);
   }
-  return m;
+  return (uint64_t)hi << 32 | lo;
 }
 
-// inclusive sum over the wave's lanes
-__device__ __forceinline__ int wave_scan(int x) {
+// inclusive sums over rows of 16 lanes, and over the wave's lanes
 #define LQ_SCAN(ctrl, rows) x += __builtin_amdgcn_update_dpp(0, x, ctrl, rows, 0xF, false)
+__device__ __forceinline__ int row_scan(int x) {
   LQ_SCAN(0x111, 0xF);  // row_shr 1, 2, 4, 8
   LQ_SCAN(0x112, 0xF);
   LQ_SCAN(0x114, 0xF);
   LQ_SCAN(0x118, 0xF);
-  LQ_SCAN(0x142, 0xA);  // row_bcast 15, 31
-  LQ_SCAN(0x143, 0xC);
-#undef LQ_SCAN
   return x;
 }
+__device__ __forceinline__ int wave_scan(int x) {
+  x = row_scan(x);
+  LQ_SCAN(0x142, 0xA);  // row_bcast 15, 31
+  LQ_SCAN(0x143, 0xC);
+  return x;
+}
+#undef LQ_SCAN
 
-// exclusive sums over the workgroup of NV values per thread; the totals
-template <int NV>
-__device__ __forceinline__ void scan(int (&v)[NV], int (&total)[NV], int (*sh)[NV]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x[NV];
+// exclusive sums over the workgroup's 16 waves of four values per thread; the totals
+__device__ __forceinline__ void scan(int (&v)[4], int (&total)[4], int4* sh) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int x[4];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) x[k] = wave_scan(v[k]);
-  if (lane == 63)
-#pragma unroll
-    for (int k = 0; k < NV; ++k) sh[wave][k] = x[k];
+  for (int k = 0; k < 4; ++k) x[k] = wave_scan(v[k]);
+  if (lane == 63) sh[wave] = make_int4(x[0], x[1], x[2], x[3]);
   __syncthreads();
+  // the waves' sums, one per lane of a row of 16
+  const int4 q = sh[lane & 15];
+  const int w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? sh[w][k] : 0;
-      all += sh[w][k];
-    }
-    v[k] = before + x[k] - v[k];
-    total[k] = all;
+  for (int k = 0; k < 4; ++k) {
+    const int all = row_scan(w[k]);
+    v[k] = x[k] - v[k] + (wave ? __builtin_amdgcn_readlane(all, wave - 1) : 0);
+    total[k] = __builtin_amdgcn_readlane(all, 15);
   }
 }
 
@@ -186,6 +189,7 @@ struct TurnArgs {
   uint16_t* Bt;
   int32_t N, K, r, ld;
   int32_t chunks;  // of 64 columns, of one place
+  uint32_t inv;    // 2^16 / (ld / 8), rounded up: e * inv >> 16 is e / (ld / 8), e < 512
 };
 
 // Whether a row has this place (the workgroup's threads together)
@@ -216,7 +220,7 @@ __device__ __forceinline__ void turn_chunk(const TurnArgs& p, int slot, int chun
     if (r % 8 == 0) {
       for (int e = tid; e < 8 * r; e += 256) {
         const u32x4 v = *reinterpret_cast<const u32x4*>(B + 8 * e);
-        const int c = 8 * e / r, j = 8 * e % r;
+        const int c = e * p.inv >> 16, j = 8 * (e - c * (r / 8));
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[(j + k) * 66 + c] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
       }
@@ -243,7 +247,7 @@ __device__ __forceinline__ void turn_chunk(const TurnArgs& p, int slot, int chun
     }
   } else if (in) {
     for (int e = tid; e < 8 * p.ld; e += 256) {  // rows of ld = r rounded up to eight
-      const int c = 8 * e / p.ld, j = 8 * e % p.ld;
+      const int c = e * p.inv >> 16, j = 8 * (e - c * (p.ld / 8));
       u32x4 v;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -256,13 +260,15 @@ __device__ __forceinline__ void turn_chunk(const TurnArgs& p, int slot, int chun
   }
 }
 
-constexpr int kPerThread = (LQ_ADAPTERS_MAX_SLOTS + 1024) / 1024;  // places of a thread
+constexpr int kPerThread = (LQ_ADAPTERS_MAX_SLOTS + 1024) / 1024;  // most places of a thread
 
 // Workgroup 0: the plan.  The others (backward): four chunks each of a place's
-// factors, which wait for nothing of it.
+// factors, which wait for nothing of it.  PT: places per thread; one in pools of
+// up to 1023 places, where all 16 waves have counters too.
+template <int PT>
 __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
-  __shared__ __attribute__((aligned(16))) int32_t cnt[kCnt];
-  __shared__ int sh[16][4];
+  __shared__ __attribute__((aligned(16))) int32_t cnt[PT == 1 ? kCntOne : kCnt];
+  __shared__ int4 sh[16];
   if (blockIdx.x > 0) {
     const int per_place = (q.chunks + 3) / 4, b = blockIdx.x - 1;
     const int slot = b / per_place, g = threadIdx.x >> 8;
@@ -272,14 +278,16 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int S1 = p.slots + 1, W = p.waves;
+  const int S1 = p.slots + 1, W = PT == 1 ? 16 : p.waves;
+  // of each place: its first position, its first tile and rank, its first segment
+  int32_t *first_s = cnt + W * S1, *tile_s = first_s + S1, *seg_s = tile_s + S1;
   const int per = (int)cdiv(cdiv(p.M, 64), W) * 64;
   const int64_t lo = (int64_t)wave * per;
   const int64_t end = lo + per;
   const int64_t hi = wave < W ? (end < p.M ? end : p.M) : 0;
   const uint64_t below = (1ull << lane) - 1;
   const int c = (int)cdiv(S1, 1024);  // thread t has places c t .. c t + c - 1
-  int id[8], pos[8], rank[kPerThread];
+  int id[8], pos[8], rank[PT];
   auto load = [&](int64_t b) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -289,7 +297,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
   };
   load(lo);
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k)
+  for (int k = 0; k < PT; ++k)
     rank[k] = k < c && tid * c + k < p.slots ? rank_of(p.ranks, p.slots, p.r, tid * c + k) : 0;
   for (int i = tid; i < W * S1; i += 1024) cnt[i] = 0;
   __syncthreads();
@@ -306,8 +314,8 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
       const bool in = b + 64 * k + lane < hi;
       uint64_t m = __ballot(in);
       // (a request's rows mostly fill the wave)
-      if (__ballot(in && id[k] == __builtin_amdgcn_readfirstlane(id[k])) != m)
-        m = lanes_like(id[k], p.bits, in);
+      if (__ballot(in && id[k] != __builtin_amdgcn_readfirstlane(id[k])))
+        m = lanes_like(id[k], p.bits, m);
       first[k] = in ? (int)__builtin_ctzll(m) : lane;
       pos[k] = __builtin_popcountll(m & below);
       if (in && lane == first[k])
@@ -322,9 +330,9 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
   }
   __syncthreads();
   // counts become positions
-  int v[4] = {0, 0, 0, 0}, total[4], n[kPerThread];
+  int v[4] = {0, 0, 0, 0}, total[4], n[PT];
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
+  for (int k = 0; k < PT; ++k) {
     const int s = tid * c + k;
     n[k] = 0;
     if (k >= c || s >= S1) continue;
@@ -342,56 +350,57 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {
     v[2] += segs;
     v[3] += segs > 1 ? segs : 0;
   }
-  scan<4>(v, total, sh);
+  scan(v, total, sh);
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
+  for (int k = 0; k < PT; ++k) {
     const int s = tid * c + k;
     if (k >= c || s >= S1) continue;
-    int x[16];
-#pragma unroll
-    for (int w = 0; w < 16; ++w) x[w] = w < W ? cnt[w * S1 + s] : 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w)
-      if (w < W) cnt[w * S1 + s] = x[w] + v[0];
-    if (s < p.slots) {
-      p.seg0[s] = v[2];
-      p.part0[s] = v[3];
-      v[3] += n[k] > p.seg_rows ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
-      for (int i = 0; i < n[k]; i += p.seg_rows) {
-        const int left = n[k] - i;
-        p.segs[v[2]++] = make_int4(s, v[0] + i, left < p.seg_rows ? left : p.seg_rows, rank[k]);
-      }
-    }
-    for (int i = 0; i < n[k]; i += kTM) {
-      const int left = n[k] - i;
-      p.tiles[v[1]++] = make_int4(s, v[0] + i, left < kTM ? left : kTM, rank[k]);
-    }
+    first_s[s] = v[0];
+    tile_s[s] = v[1] << 7 | rank[k];  // (fewer than 2^20 tiles, ranks up to 64)
+    seg_s[s] = v[2];
+    p.seg0[s] = v[2];
+    if (s < p.slots) p.part0[s] = v[3];
     v[0] += n[k];
-    p.off[s + 1] = v[0];
+    v[1] += (n[k] + kTM - 1) / kTM;
+    const int segs = s < p.slots ? (n[k] + p.seg_rows - 1) / p.seg_rows : 0;
+    v[2] += segs;
+    v[3] += segs > 1 ? segs : 0;
   }
   if (tid == 0) {
-    p.off[0] = 0;
-    p.seg0[p.slots] = total[2];
     p.count[0] = total[1];
     p.count[1] = total[2];
   }
   __syncthreads();
+  // row i of place s, the d-th of its place; the first of a tile or segment lists it
+  auto put = [&](int64_t i, int s, int d) {
+    const int first = first_s[s];
+    p.perm[first + d] = (int32_t)i;
+    if (d % 32) return;
+    const int left = (s < p.slots ? first_s[s + 1] : p.M) - first - d;
+    const int tile = tile_s[s], rank = tile & 127;
+    if (d % kTM == 0)
+      p.tiles[(tile >> 7) + d / kTM] = make_int4(s, first + d, left < kTM ? left : kTM, rank);
+    if (!p.segs || s >= p.slots) return;
+    const int q = d / p.seg_rows;  // (a multiple of 32)
+    if (q * p.seg_rows == d)
+      p.segs[seg_s[s] + q] = make_int4(s, first + d, left < p.seg_rows ? left : p.seg_rows, rank);
+  };
   if (per <= 512) {  // places and positions are still in registers
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t i = lo + 64 * k + lane;
-      if (i < hi) p.perm[cnt[wave * S1 + id[k]] + pos[k]] = (int32_t)i;
+      if (i < hi) put(i, id[k], cnt[wave * S1 + id[k]] + pos[k]);
     }
     return;
   }
-  // else the rows are counted again, from their first positions on
+  // else the rows are counted again, from the wave's first positions on
   for (int64_t b = lo; b < hi; b += 512) {
     load(b);
     count(b);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int64_t i = b + 64 * k + lane;
-      if (i < hi) p.perm[pos[k]] = (int32_t)i;
+      if (i < hi) put(i, id[k], pos[k]);
     }
   }
 }
@@ -1184,12 +1193,11 @@ int64_t max_parts(int64_t M, int64_t N, int64_t K, int32_t slots) {
 }
 
 struct PlanLayout {
-  size_t off, seg0, part0, count, tiles, segs, perm, end;
+  size_t seg0, part0, count, tiles, segs, perm, end;
 };
 PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   PlanLayout l;
-  l.off = 0;
-  l.seg0 = up256((size_t)(slots + 2) * 4);
+  l.seg0 = 0;
   l.part0 = l.seg0 + up256((size_t)(slots + 2) * 4);
   l.count = l.part0 + up256((size_t)(slots + 2) * 4);
   l.tiles = l.count + 256;
@@ -1199,25 +1207,25 @@ PlanLayout plan_layout(int64_t M, int32_t slots, int64_t segs) {
   return l;
 }
 
+// seg_rows 0: without segments (forward)
 int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, const TurnArgs& q,
                 hipStream_t st) {
   PlanArgs p;
   p.rows = a.rows;
   p.ranks = a.ranks;
   p.r = a.r;
-  p.off = (int32_t*)(ws + l.off);
   p.seg0 = (int32_t*)(ws + l.seg0);
   p.part0 = (int32_t*)(ws + l.part0);
   p.count = (int32_t*)(ws + l.count);
   p.tiles = (int4*)(ws + l.tiles);
-  p.segs = (int4*)(ws + l.segs);
+  p.segs = seg_rows ? (int4*)(ws + l.segs) : nullptr;
   p.perm = (int32_t*)(ws + l.perm);
   p.M = a.M;
   p.slots = a.slots;
-  p.waves = kCnt / (a.slots + 1) < 16 ? kCnt / (a.slots + 1) : 16;
+  const int waves = kCnt / (a.slots + 1) - 3;
+  p.waves = waves < 16 ? waves : 16;
   p.bits = 32 - __builtin_clz(a.slots);
-  p.seg_rows = (int32_t)seg_rows;
-  a.off = p.off;
+  p.seg_rows = seg_rows ? (int32_t)seg_rows : kTM;
   a.seg0 = p.seg0;
   a.part0 = p.part0;
   a.count = p.count;
@@ -1225,7 +1233,8 @@ int launch_plan(RowArgs& a, const PlanLayout& l, char* ws, int64_t seg_rows, con
   a.segs = p.segs;
   a.perm = p.perm;
   const dim3 g((unsigned)(1 + (int64_t)a.slots * cdiv(q.chunks, 4)));
-  hipLaunchKernelGGL(plan_kernel, g, dim3(1024), 0, st, p, q);
+  const auto kernel = a.slots < 1024 ? plan_kernel<1> : plan_kernel<kPerThread>;
+  hipLaunchKernelGGL(kernel, g, dim3(1024), 0, st, p, q);
   return hip_fail(hipGetLastError(), "adapters plan launch");
 }
 
@@ -1373,7 +1382,7 @@ int adapters_fwd(const void* X, int64_t M, const lq_adapter_pool& q, const int32
   int rc;
   if (M > kDirect) {
     const PlanLayout l = plan_layout(M, q.slots, max_segments(M, q.N, q.K, q.slots));
-    if ((rc = launch_plan(a, l, base, segment_rows(M, q.N, q.K), TurnArgs{}, st))) return rc;
+    if ((rc = launch_plan(a, l, base, 0, TurnArgs{}, st))) return rc;
     base += l.end;
   }
   if ((rc = launch_shrink(a, X, q.A, q.K, (float*)base, st))) return rc;
@@ -1396,6 +1405,7 @@ int adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool
   t.K = (int32_t)q.K;
   t.r = q.r;
   t.ld = (q.r + 7) / 8 * 8;
+  t.inv = (uint32_t)cdiv(65536, t.ld / 8);
   t.chunks = (int32_t)(q.N / 64 + (dX_out ? q.K / 64 : 0));  // without dX only B is turned
   int rc = launch_plan(a, l.plan, base, segment_rows(M, q.N, q.K), t, st);
   if (rc) return rc;
