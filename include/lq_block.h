@@ -168,7 +168,7 @@ size_t lq_adapters_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, i
  *   ws       lq_head_loss_workspace(M, V, K, kt, dH != NULL) bytes (more is not used)
  * One of loss, lse and dH at least.  The logits of one piece of rows at a time
  * are held in ws as float32; the gradient with respect to them enters its
- * product with W0 as bf16.
+ * product with W0 as bf16, over the row's largest entry (which is then exact).
  * Requires K % 64 == 0, 64 <= K <= 16384, 1 <= V <= 2^20, 1 <= kt <= 128,
  * M K < 2^31 and V K < 2^31; H, W0, dH and ws 16-byte aligned.  M = 0 is a no-op.
  */

@@ -2,12 +2,13 @@
 // (lq_head_loss).
 //
 //   z = c H W^T,  lse_i = log sum_v exp z_iv,  loss_i = sum_j p_ij (lse_i - z_i,t_ij)
-//   D = w_i c (P_i softmax(z_i) - sum_j p_ij e(t_ij)),  P_i = sum_j p_ij,   dH = D W
+//   g_i D = w_i c (P_i softmax(z_i) - sum_j p_ij e(t_ij)),  P_i = sum_j p_ij
+//   dH_i = g_i (D W)_i,  g_i such that D's largest entry is 1
 //
 // Two products of 2 M V K operations bound it; the softmax between them costs
 // memory traffic only.  A piece of rows at a time: its logits as float32 (a bf16
 // logit of 16 would be off by 0.03, three percent of its probability) and then D as
-// bf16 (2^-8 of each entry, as the outputs are) lie in the workspace.  Kept
+// bf16 (2^-8 of each entry but the largest) lie in the workspace.  Kept
 // logits are cheaper than formed ones: 12 bytes of traffic per logit against 2 K
 // operations.
 //
@@ -53,6 +54,7 @@ struct ProdParams {
   const uint16_t* Q;  // z: W, NI x KR.  dH: W, KV x NI (KV <= KR rows)
   float* Z;           // z: splits x rows x ldz; dH, split: splits x rows x NI
   uint16_t* Y;        // dH, not split: rows x NI
+  const float* g;     // ... each row times g
   int32_t M, NI, KR, KV, ldz;
   float scale;
   int32_t ti, tj, splits, ksteps;
@@ -304,10 +306,17 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
   }
   // bf16: the tile through LDS (row j of 512 bytes, chunk c at c ^ (j & 15)), whole
   // output lines from there
+  float gain[JM];
+#pragma unroll
+  for (int ms = 0; ms < JM; ++ms) {
+    const int m = j0 + 32 * JM * wj + 32 * ms + l32;
+    gain[ms] = p.g[m < M ? m : M - 1];
+  }
   __syncthreads();
 #pragma unroll
   for (int ms = 0; ms < JM; ++ms) {
     const int j = 32 * JM * wj + 32 * ms + l32;
+    const float gm = gain[ms];
 #pragma unroll
     for (int ns = 0; ns < 4; ++ns)
 #pragma unroll
@@ -316,7 +325,8 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
         const f32x16& x = acc[ns][ms];
         typedef __attribute__((address_space(3))) u32x2* lds_ptr;
         *(lds_ptr)(uintptr_t)(sbase + (uint32_t)(j * 512 + (((i >> 3) ^ (j & 15)) * 16) + (i & 7) * 2)) =
-            u32x2{pack_bf16x2(x[4 * q], x[4 * q + 1]), pack_bf16x2(x[4 * q + 2], x[4 * q + 3])};
+            u32x2{pack_bf16x2(gm * x[4 * q], gm * x[4 * q + 1]),
+                  pack_bf16x2(gm * x[4 * q + 2], gm * x[4 * q + 3])};
       }
   }
   __syncthreads();
@@ -343,6 +353,7 @@ struct RowParams {
   float* loss;
   float* lse;
   uint16_t* D;        // rows x ldd or NULL
+  float* g;           // rows: the gradient of the logits is g D
   int32_t V, ldz, ldd, kt;
   int32_t splits;     // Z: so many partial sums, part elements apart
   int64_t part;
@@ -372,7 +383,7 @@ template <int T, int Q>
 __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
   __shared__ float sh[T / 64];
   __shared__ int tgt[kMaxTargets];
-  __shared__ float wgt[kMaxTargets], zt[kMaxTargets];
+  __shared__ float wgt[kMaxTargets], zt[kMaxTargets], dt[kMaxTargets];
   const int tid = threadIdx.x, V = p.V;
   const int64_t row = blockIdx.x;
   const float* z = p.Z + row * p.ldz;
@@ -417,6 +428,15 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     for (int k = 0; k < 4; ++k) top = fmaxf(top, v[k]);
   }
   top = row_reduce<true, T>(top, sh);
+  // the weight of a target, at the first of several with one index
+  bool first = tid < p.kt && tgt[tid] >= 0;
+  float q = 0.0f;
+  if (first && p.D)
+    for (int j = 0; j < p.kt; ++j) {
+      if (tgt[j] != tgt[tid]) continue;
+      if (j < tid) first = false;
+      q += wgt[j];
+    }
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < Q; ++i)
@@ -446,9 +466,18 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     if (p.lse) p.lse[row] = lse;
   }
   if (!p.D) return;
+  // the targets' entries of the gradient, but for the row's share
+  if (tid < p.kt) dt[tid] = first ? total * (__expf(zt[tid] - top) / sum) - q : 0.0f;
+  __syncthreads();
+  // D is the gradient over its largest entry, which is then exact in bf16.  That
+  // entry is most of dH, and the same error of it in every row (w and 1 - p are often
+  // the same in all) would be dH's error: up to 2^-8, where the others' errors, half
+  // of that and of either sign, are mostly lost in dH's own rounding.
+  float most = fmaxf(fabsf(total / sum), 1e-37f);
+  for (int j = 0; j < p.kt; ++j) most = fmaxf(most, fabsf(dt[j]));
   uint16_t* d = p.D + row * p.ldd;
-  const float share = any ? (p.w ? p.w[row] : 1.0f) * p.scale : 0.0f;
-  const float f = share * total / sum;
+  const float inv = 1.0f / most, f = total / sum * inv;
+  if (tid == 0) p.g[row] = any ? (p.w ? p.w[row] : 1.0f) * p.scale * most : 0.0f;
   auto store = [&](int g, f32x4 e) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) e[k] = any ? e[k] * f : 0.0f;
@@ -468,23 +497,13 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     }
     store(g, v);
   }
-  // the targets' entries, from float32: by the first of several with one index
-  __syncthreads();
-  if (tid < p.kt && tgt[tid] >= 0) {
-    float q = 0.0f;
-    bool first = true;
-    for (int j = 0; j < p.kt; ++j) {
-      if (tgt[j] != tgt[tid]) continue;
-      if (j < tid) first = false;
-      q += wgt[j];
-    }
-    if (first) d[tgt[tid]] = f32_to_bf16(share * (total * (__expf(zt[tid] - top) / sum) - q));
-  }
+  __syncthreads();  // the targets' entries over what is stored for them
+  if (first) d[tgt[tid]] = f32_to_bf16(dt[tid] * inv);
 }
 
-// out (bf16) = the splits' sums in order; n % 8 == 0
-__global__ __launch_bounds__(256) void head_sum_kernel(const float* part, uint16_t* out, int64_t n,
-                                                       int splits) {
+// out (bf16) = the splits' sums in order, row i of K times g[i]; K % 8 == 0, n < 2^31
+__global__ __launch_bounds__(256) void head_sum_kernel(const float* part, uint16_t* out, const float* g,
+                                                       int64_t n, int K, int splits) {
   const int64_t e = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (e >= n) return;
   f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
@@ -496,8 +515,10 @@ __global__ __launch_bounds__(256) void head_sum_kernel(const float* part, uint16
       b[i] += q[1][i];
     }
   }
-  *reinterpret_cast<u32x4*>(out + e) = u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                                             pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])};
+  const float gm = g[(uint32_t)e / (uint32_t)K];
+  *reinterpret_cast<u32x4*>(out + e) =
+      u32x4{pack_bf16x2(gm * a[0], gm * a[1]), pack_bf16x2(gm * a[2], gm * a[3]),
+            pack_bf16x2(gm * b[0], gm * b[1]), pack_bf16x2(gm * b[2], gm * b[3])};
 }
 
 // ---------------------------------------------------------------- host
@@ -586,14 +607,15 @@ size_t z_bytes(int64_t M, int64_t V, int64_t K) {
 }
 
 struct Layout {
-  size_t z, d, part, end;
+  size_t z, d, g, part, end;
 };
 Layout layout(int64_t M, int64_t V, int64_t K, bool need_dh) {
   const int64_t rows = piece_rows(M, V);
   Layout l;
   l.z = 0;
   l.d = up256(z_bytes(M, V, K));
-  l.part = l.d + (need_dh ? up256((size_t)rows * ld_of(V) * 2) : 0);
+  l.g = l.d + (need_dh ? up256((size_t)rows * ld_of(V) * 2) : 0);
+  l.part = l.g + (need_dh ? up256((size_t)rows * 4) : 0);
   l.end = l.part;
   if (need_dh) {
     // the last piece may have fewer rows and more splits
@@ -680,6 +702,7 @@ int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, con
     r.loss = loss ? loss + m0 : nullptr;
     r.lse = lse ? lse + m0 : nullptr;
     r.D = dH ? (uint16_t*)(base + l.d) : nullptr;
+    r.g = (float*)(base + l.g);
     r.V = (int32_t)V;
     r.ldz = r.ldd = (int32_t)ld;
     r.kt = kt;
@@ -695,6 +718,7 @@ int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, con
     q.Q = (const uint16_t*)W;
     q.Z = (float*)(base + l.part);
     q.Y = (uint16_t*)dH + m0 * K;
+    q.g = r.g;
     q.M = (int32_t)rows;
     q.NI = (int32_t)K;
     q.KR = (int32_t)ld;
@@ -707,7 +731,7 @@ int head_loss(const void* H, int64_t M, int64_t V, int64_t K, const void* W, con
     if (s.splits > 1) {
       const int64_t n = rows * K;
       hipLaunchKernelGGL(head_sum_kernel, dim3((unsigned)cdiv(n, 2048)), dim3(256), 0, st,
-                         (const float*)q.Z, q.Y, n, (int)s.splits);
+                         (const float*)q.Z, q.Y, r.g, n, (int)K, (int)s.splits);
       if ((rc = hip_fail(hipGetLastError(), "head sums launch"))) return rc;
     }
   }

@@ -183,3 +183,21 @@ def test_larger_shapes(M, V, K):
     assert bool(((dH.double() - ref).abs() <= HALF_BF16 * ref.abs() + slack * (1 + HALF_BF16)).all())
     # the errors above are worst cases; together the roundings are far smaller
     assert float((dH.double() - ref).norm() / ref.norm()) < 2 * HALF_BF16
+
+
+@pytest.mark.parametrize("M,V", [(1, 256), (300, 256), (3, 2048), (130, 4096)])
+def test_a_rows_largest_entry_is_not_rounded(M, V):
+    """All logits 0 and one row of W not zero: dH = w (1 / V - 1) W_t, whose factor lies
+    half a bf16 step off that type's values.  With the factor in bf16 dH would be
+    off by up to two half steps; here it is rounded once, plus the float32
+    factors' roundings."""
+    g = torch.Generator(device=DEV).manual_seed(V)
+    K = 256
+    H = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    W = torch.zeros((V, K), dtype=torch.bfloat16, device=DEV)
+    W[5] = torch.randn(K, generator=g, device=DEV).bfloat16()
+    w = torch.full((M,), (1.0 + 2.0**-8 + 2.0**-13) * V / (V - 1), device=DEV)
+    t = torch.full((M,), 5, dtype=torch.int32, device=DEV)
+    _, _, dH = block.lq_head_loss(H, W, t, w=w)
+    ref = w.double()[:, None] * (1.0 / V - 1.0) * W[5].double()
+    assert bool(((dH.double() - ref).abs() <= (HALF_BF16 + (V + 32) * U32) * ref.abs()).all())
