@@ -208,3 +208,28 @@ def test_many_rows(M, N, K, r, slots):
         n = len(i)
         near(dA[a], s * u.t() @ x, s * (N + n + 8) * U32 * (um.t() @ x.abs()))
         near(dB[a], s * d.t() @ T[i].double(), s * (n + 8) * U32 * (d.abs().t() @ T[i].double().abs()))
+
+
+@pytest.mark.parametrize("M", [70, 600, 9000])
+@pytest.mark.parametrize("slots", [1022, 1023, 1024, 2047, 4096])
+def test_results_do_not_depend_on_the_places(slots, M):
+    """Six adapters at the ends and in the middle of a large pool: the bits that a
+    pool of six gives, zeros in the gradients of all other places."""
+    announce(f"adapters slots={slots} M={M}")
+    c = adapter_case(M, 64, 128, 8, 6, rows="random")
+    at = torch.tensor([0, 1, slots // 2, slots - 3, slots - 2, slots - 1], device=DEV)
+    A = torch.full((slots, 8, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    B = torch.full((slots, 64, 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    scales, ranks = torch.full((slots,), float("nan"), device=DEV), torch.full((slots,), 8, dtype=torch.int32, device=DEV)
+    A[at], B[at], scales[at], ranks[at] = c["A"], c["B"], c["scales"], c["ranks"]
+    inside = (c["rows"] >= 0) & (c["rows"] < 6)
+    rows = torch.where(inside, at[c["rows"].clamp(0, 5).long()].int(), slots + 5)
+    big, small = block.AdapterPool(A, B, scales, ranks), pool(c)
+    want = block.lq_adapters_fwd(c["X"], small, c["rows"], c["Y"])
+    assert torch.equal(block.lq_adapters_fwd(c["X"], big, rows, c["Y"]), want)
+    gx, dA, dB = block.lq_adapters_bwd(c["dY"], c["X"], small, c["rows"], c["dX"])
+    gx2, dA2, dB2 = block.lq_adapters_bwd(c["dY"], c["X"], big, rows, c["dX"])
+    assert torch.equal(gx2, gx) and torch.equal(dA2[at], dA) and torch.equal(dB2[at], dB)
+    rest = torch.ones(slots, dtype=torch.bool, device=DEV)
+    rest[at] = False
+    assert (dA2[rest] == 0).all() and (dB2[rest] == 0).all()
