@@ -6,23 +6,41 @@
 //
 // Both are bound by HBM: every element is read once and written once, and a row
 // stays in registers between its sums and its stores (past 16384 columns what does
-// not fit is read again).  A thread owns units of 16 consecutive columns, so that a
-// lane pair holds one block of an MX output and one DPP move completes the block's
-// amax, as in the quantiser; y is quantised from its float32 value, never stored
-// in between.  Measured: 2048 x 4096 bf16 with residual, y and MXFP8 out 15.5 us (4.8
-// TB/s), backward of 8192 x 4096 with dW 50 + 5 us (5.3 TB/s in the first), 777 x
-// 4095 float32 to y and MXFP4 11 us, one row of 4096 2.6 us.  (Pieces of 16 bytes, consecutive as the threads are, took 61 us
-// against 54 in the backward of 8192 x 4096 and as long in the forward.)
+// not fit is read again).  A thread owns 16 columns of a row at a time, so that a lane
+// pair, or eight lanes, hold one block of an MX output and a few DPP moves complete
+// the block's amax; y is quantised from its float32 value, never stored in between.
+// Measured: 2048 x 4096 bf16 with residual, y and MXFP8 out 15.8 us (4.7 TB/s),
+// backward of 8192 x 4096 with dW 50 + 5 us (5.3 TB/s in the first), 777 x 4095
+// float32 to y and MXFP4 8.4 us, one row of 4096 2.6 us.
+#include <type_traits>
+
 #include "block.h"
 #include "mx_unit.h"
 
 namespace lq {
 namespace {
 
-// a thread's 16 values of type BF16 ? bf16 : float32 as floats; n < 16: the
-// row's last unit, the rest is 0
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+
+// Which columns a thread's unit u is.  LONG (bf16 rows, and rows that are read
+// twice): 16 in a run.  Else (float32 rows up to 16384): four runs of 4, consecutive
+// as the threads are, since runs of 64 bytes make each of their four loads touch
+// every line that the wave has (us, long runs / short: float32 forward 2048 x 4096
+// 32 / 21, 4096 x 11008 161 / 132, 777 x 4095 16.2 / 10.4, backward 2048 x 4096 29 /
+// 24, but 1000 x 30000 forward 140 / 167 and backward 146 / 173; bf16 in runs of 4:
+// forward 2048 x 4096 with MX output 15.8 / 18.7, backward 8192 x 4096 50 / 78).
+template <bool LONG, int TPR>
+struct Cols {
+  static constexpr int kRun = LONG ? 16 : 4, kRuns = 16 / kRun;
+  // first column of run k
+  static __device__ __forceinline__ int at(int t, int u, int k = 0) {
+    return kRun * (t + TPR * (kRuns * u + k));
+  }
+};
+
+// n (some: 1 to 15) of 16 consecutive values at e as floats, zeros past them
 template <bool BF16>
-__device__ __forceinline__ void load_unit(const void* p, int64_t e, int n, float (&x)[16]) {
+__device__ __forceinline__ void load_run(const void* p, int64_t e, int n, float* x, std::integral_constant<int, 16>) {
   Unit<BF16> u;
   if (n >= 16)
     u.load(p, e);
@@ -38,11 +56,47 @@ __device__ __forceinline__ void load_unit(const void* p, int64_t e, int n, float
     }
   }
 }
-
+// ... of four
 template <bool BF16>
-__device__ __forceinline__ void store_unit(void* p, int64_t e, int n, const float (&x)[16]) {
-  if constexpr (BF16) {
-    uint16_t* d = (uint16_t*)p + e;
+__device__ __forceinline__ void load_run(const void* p, int64_t e, int n, float* x, std::integral_constant<int, 4>) {
+  if (n >= 4) {
+    if constexpr (BF16) {
+      const u32x2 w = *reinterpret_cast<const u32x2_a2*>((const uint16_t*)p + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = i & 1 ? hi_bf16(w[i >> 1]) : lo_bf16(w[i >> 1]);
+    } else {
+      const f32x4 v = *reinterpret_cast<const f32x4_a4*>((const float*)p + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = v[i];
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = 0.0f;
+    if (i < n)
+      x[i] = BF16 ? bf16_to_f32(((const uint16_t*)p)[e + i]) : ((const float*)p)[e + i];
+  }
+}
+
+// a thread's unit u of the row of K values of type EB ? bf16 : float32 at e
+template <bool EB, bool LONG, int TPR>
+__device__ __forceinline__ void load_unit(const void* p, int64_t e, int K, int t, int u, float (&x)[16]) {
+  using C = Cols<LONG, TPR>;
+#pragma unroll
+  for (int k = 0; k < C::kRuns; ++k) {
+    const int c = C::at(t, u, k);
+    load_run<EB>(p, e + c, K - c, x + C::kRun * k, std::integral_constant<int, C::kRun>{});
+  }
+}
+
+template <bool EB, bool LONG, int TPR>
+__device__ __forceinline__ void store_unit(void* p, int64_t row, int K, int t, int u, const float (&x)[16]) {
+  using C = Cols<LONG, TPR>;
+  if constexpr (EB) {
+    static_assert(LONG, "bf16 rows are stored in long runs");
+    const int c = C::at(t, u), n = K - c;
+    uint16_t* d = (uint16_t*)p + row + c;
     u32x4 v[2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
@@ -55,25 +109,100 @@ __device__ __forceinline__ void store_unit(void* p, int64_t e, int n, const floa
         if (i < n) d[i] = (uint16_t)(v[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
     }
   } else {
-    float* d = (float*)p + e;
-    if (n >= 16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<f32x4_a4*>(d)[i] =
-            f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-    } else {
+    for (int k = 0; k < C::kRuns; ++k) {
+      const int c = C::at(t, u, k), n = K - c;
+      float* d = (float*)p + row + c;
+      const float* v = x + C::kRun * k;
+      if (n >= C::kRun) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) d[i] = x[i];
+        for (int i = 0; i < C::kRun / 4; ++i)
+          reinterpret_cast<f32x4_a4*>(d)[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kRun; ++i)
+          if (i < n) d[i] = v[i];
+      }
     }
   }
 }
 
-__device__ __forceinline__ void load_gain(const void* W, bool bf16, int c, int n, float (&w)[16]) {
-  if (bf16)
-    load_unit<true>(W, c, n, w);
+template <bool LONG, int TPR>
+__device__ __forceinline__ void load_gain(const void* W, bool wbf16, int K, int t, int u, float (&w)[16]) {
+  if (wbf16)
+    load_unit<true, LONG, TPR>(W, 0, K, t, u, w);
   else
-    load_unit<false>(W, c, n, w);
+    load_unit<false, LONG, TPR>(W, 0, K, t, u, w);
+}
+
+// max over eight lanes 8 i .. 8 i + 7
+__device__ __forceinline__ uint32_t max8(uint32_t v) {
+#define LQ_MAX(ctrl)                                                                       \
+  {                                                                                        \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xF, 0xF, false);  \
+    v = v > o ? v : o;                                                                     \
+  }
+  LQ_MAX(0xB1)   // lane ^ 1
+  LQ_MAX(0x4E)   // lane ^ 2
+  LQ_MAX(0x141)  // mirrored within eight
+#undef LQ_MAX
+  return v;
+}
+
+// codes and scales of a unit; row: its first block's place in elements, kp: the
+// row's columns with padding (a lane pair or eight lanes hold one block)
+template <int FMT, bool LONG, int TPR>
+__device__ __forceinline__ void quantise(const float (&y)[16], int64_t row, int K, int kp, int t, int u,
+                                         uint8_t* codes, uint8_t* scales) {
+  using C = Cols<LONG, TPR>;
+  if constexpr (LONG) {
+    // one past the row's end is padding (a short row's second unit: zeros)
+    const int col = C::at(t, u), n = K - col;
+    if (col >= kp) return;
+    Unit<false> q;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q.v[i >> 2][i & 3] = i < n ? y[i] : 0.0f;
+    const uint32_t b = scale_byte<FMT>(pair_max(q.amax()));
+    const float sc = mx_scale(b);
+    const int64_t un = (row + col) >> 4;
+    if constexpr (FMT == LQ_MX_FP8) {
+      *reinterpret_cast<u32x4*>(codes + 16 * un) = sel4(b != 255u, q.fp8(sc));
+    } else {
+      u32x2 o = q.fp4(sc);
+      if (b == 255u) o = u32x2{0u, 0u};
+      *reinterpret_cast<u32x2*>(codes + 8 * un) = o;
+    }
+    if (!(un & 1)) scales[un >> 1] = (uint8_t)b;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int col = C::at(t, u, k), n = K - col;
+      if (col >= kp) return;
+      float v[4];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = i < n ? y[4 * k + i] : 0.0f;
+        const uint32_t a = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+        m = m > a ? m : a;
+      }
+      const uint32_t b = scale_byte<FMT>(max8(m));
+      const float sc = mx_scale(b);
+      const int64_t at = row + col;
+      if constexpr (FMT == LQ_MX_FP8) {
+        s16x2 c = {0, 0};
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[0], v[1], sc, false);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, v[2], v[3], sc, true);
+        *reinterpret_cast<uint32_t*>(codes + at) = b != 255u ? __builtin_bit_cast(uint32_t, c) : 0u;
+      } else {
+        uint32_t c = 0;
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], sc, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], sc, 1);
+        *reinterpret_cast<uint16_t*>(codes + (at >> 1)) = b != 255u ? (uint16_t)c : (uint16_t)0;
+      }
+      if (!(at & 31)) scales[at >> 5] = (uint8_t)b;
+    }
+  }
 }
 
 // Sum over the TPR threads of a row; scratch: one float per wave of the
@@ -123,27 +252,27 @@ struct NormParams {
 template <bool BF16, int FMT, int TPR, int U, bool KEEP>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(NormParams p) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  constexpr bool LONG = BF16 || !KEEP;
+  using C = Cols<LONG, TPR>;
   __shared__ float scratch[16];
   const int t = threadIdx.x % TPR, K = p.K;
-  const int64_t kp = mx_spitch(K) * kMxB;
+  const int kp = (int)(mx_spitch(K) * kMxB);
   const float inv_k = 1.0f / (float)K;
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < p.M;
        row += (int64_t)gridDim.x * RPB) {
     float h[U][16], w[KEEP ? U : 1][16], s[1] = {0.0f};
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = 16 * (t + TPR * u), n = K - c;
-      if (n <= 0) {
+      if (C::at(t, u) >= K) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) h[u][i] = 0.0f;
         continue;
       }
-      const int64_t e = row * K + c;
-      load_unit<BF16>(p.X, e, n, h[u]);
-      if (KEEP) load_gain(p.W, p.wbf16, c, n, w[KEEP ? u : 0]);
+      load_unit<BF16, LONG, TPR>(p.X, row * K, K, t, u, h[u]);
+      if (KEEP) load_gain<LONG, TPR>(p.W, p.wbf16, K, t, u, w[KEEP ? u : 0]);
       if (p.R) {
         float r[16];
-        load_unit<BF16>(p.R, e, n, r);
+        load_unit<BF16, LONG, TPR>(p.R, row * K, K, t, u, r);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           h[u][i] += r[i];
@@ -158,34 +287,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(Norm
     if (p.rstd && t == 0) p.rstd[row] = c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int col = 16 * (t + TPR * u), n = K - col;
-      const int64_t e = row * K + col;
-      if (n > 0 && p.H) store_unit<BF16>(p.H, e, n, h[u]);
+      const bool in = C::at(t, u) < K;
+      if (in && p.H) store_unit<BF16, LONG, TPR>(p.H, row * K, K, t, u, h[u]);
       float y[16];
-      if (!KEEP && n > 0) load_gain(p.W, p.wbf16, col, n, w[0]);
+      if (!KEEP && in) load_gain<LONG, TPR>(p.W, p.wbf16, K, t, u, w[0]);
 #pragma unroll
       for (int i = 0; i < 16; ++i) y[i] = h[u][i] * c * w[KEEP ? u : 0][i];
-      if (n > 0 && p.Y) store_unit<BF16>(p.Y, e, n, y);
-      if constexpr (FMT != 0) {
-        // both units of a block are in one lane pair; one past the row's end is
-        // padding (a short row's second unit: zeros)
-        if (col < kp) {
-          Unit<false> q;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) q.v[i >> 2][i & 3] = i < n ? y[i] : 0.0f;
-          const uint32_t b = scale_byte<FMT>(pair_max(q.amax()));
-          const float sc = mx_scale(b);
-          const int64_t un = (row * kp + col) >> 4;
-          if constexpr (FMT == LQ_MX_FP8) {
-            *reinterpret_cast<u32x4*>(p.codes + 16 * un) = sel4(b != 255u, q.fp8(sc));
-          } else {
-            u32x2 o = q.fp4(sc);
-            if (b == 255u) o = u32x2{0u, 0u};
-            *reinterpret_cast<u32x2*>(p.codes + 8 * un) = o;
-          }
-          if (!(un & 1)) p.scales[un >> 1] = (uint8_t)b;
-        }
-      }
+      if (in && p.Y) store_unit<BF16, LONG, TPR>(p.Y, row * K, K, t, u, y);
+      if constexpr (FMT != 0) quantise<FMT, LONG, TPR>(y, row * kp, K, kp, t, u, p.codes, p.scales);
     }
   }
 }
@@ -197,39 +306,42 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(Norm
 template <bool BF16, int TPR, int U, bool KEEP>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(NormParams p) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1, UK = KEEP ? U : 1;
+  constexpr bool LONG = BF16 || !KEEP;
+  using C = Cols<LONG, TPR>;
   __shared__ float scratch[32];
   const int t = threadIdx.x % TPR, K = p.K;
   const float inv_k = 1.0f / (float)K;
   float w[UK][16], dw[U][16];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = 16 * (t + TPR * u), n = K - c;
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[u][i] = 0.0f;
     if (KEEP) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) w[KEEP ? u : 0][i] = 0.0f;
-      if (n > 0) load_gain(p.W, p.wbf16, c, n, w[KEEP ? u : 0]);
+      if (C::at(t, u) < K) load_gain<LONG, TPR>(p.W, p.wbf16, K, t, u, w[KEEP ? u : 0]);
     }
   }
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < p.M;
        row += (int64_t)gridDim.x * RPB) {
     float h[UK][16], d[UK][16], s[2] = {0.0f, 0.0f};
-    auto load = [&](int k, int c, int n) {
-      load_unit<BF16>(p.X, row * K + c, n, h[k]);
-      load_unit<BF16>(p.dY, row * K + c, n, d[k]);
-      if (!KEEP) load_gain(p.W, p.wbf16, c, n, w[k]);
+    auto load = [&](int k, int u) {
+      load_unit<BF16, LONG, TPR>(p.X, row * K, K, t, u, h[k]);
+      load_unit<BF16, LONG, TPR>(p.dY, row * K, K, t, u, d[k]);
+      if (!KEEP) load_gain<LONG, TPR>(p.W, p.wbf16, K, t, u, w[k]);
     };
-#pragma unroll
+    // (bf16 rows in turn where they do not fit: the loads of four units at once spill,
+    // 1000 x 30000 100 us against 86)
+#pragma unroll(BF16 && !KEEP ? 1 : U)
     for (int u = 0; u < U; ++u) {
-      const int c = 16 * (t + TPR * u), n = K - c, k = KEEP ? u : 0;
-      if (n <= 0) {
+      const int k = KEEP ? u : 0;
+      if (C::at(t, u) >= K) {
         if (KEEP)
 #pragma unroll
           for (int i = 0; i < 16; ++i) h[k][i] = d[k][i] = 0.0f;
         continue;
       }
-      load(k, c, n);
+      load(k, u);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[0] += d[k][i] * w[k][i] * h[k][i];
@@ -241,10 +353,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(Norm
     const float m = s[0] * inv_k * c * c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int col = 16 * (t + TPR * u), n = K - col, k = KEEP ? u : 0;
-      if (n <= 0) continue;
-      const int64_t e = row * K + col;
-      if (!KEEP) load(k, col, n);
+      const int k = KEEP ? u : 0;
+      if (C::at(t, u) >= K) continue;
+      if (!KEEP) load(k, u);
       if (p.part)
 #pragma unroll
         for (int i = 0; i < 16; ++i) dw[u][i] += d[k][i] * (h[k][i] * c);
@@ -254,11 +365,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(Norm
         for (int i = 0; i < 16; ++i) g[i] = c * (d[k][i] * w[k][i] - h[k][i] * m);
         if (p.R) {
           float r[16];
-          load_unit<BF16>(p.R, e, n, r);
+          load_unit<BF16, LONG, TPR>(p.R, row * K, K, t, u, r);
 #pragma unroll
           for (int i = 0; i < 16; ++i) g[i] += r[i];
         }
-        store_unit<BF16>(p.H, e, n, g);
+        store_unit<BF16, LONG, TPR>(p.H, row * K, K, t, u, g);
       }
     }
   }
@@ -267,8 +378,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(Norm
   float* out = p.part + ((int64_t)blockIdx.x * RPB + threadIdx.x / TPR) * K;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int c = 16 * (t + TPR * u), n = K - c;
-    if (n > 0) store_unit<false>(out, c, n, dw[u]);
+    if (C::at(t, u) < K) store_unit<false, LONG, TPR>(out, 0, K, t, u, dw[u]);
   }
 }
 

@@ -70,14 +70,18 @@ def test_forward_arguments(dt, residual, gain):
 @pytest.mark.parametrize("M,K", SHAPES)
 def test_mx_output_is_the_quantisers_of_float32_y(M, K, fmt):
     """float32 in and out: y as it was quantised is there to compare with, bit for
-    bit; bf16 inputs of the same values give the same codes."""
+    bit; of bf16 inputs it is formed here, from the row's factor, in the same two
+    float32 products (the factor itself comes from sums in another order than the
+    float32 rows', so the codes of both need not be the same)."""
     announce(f"rmsnorm fwd {M}x{K} {fmt}")
     t, w = inputs(M, K, torch.bfloat16)
     X, W = t(2.0), w.to(DEV)
     _, Y, q = block.lq_rmsnorm_fwd(X.float(), W, 1e-5, format=fmt)
     want = mx.lq_mx_quantize(Y, fmt)
     assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
-    _, Y, q = block.lq_rmsnorm_fwd(X, W, 1e-5, format=fmt, need_y=False)
+    c = torch.empty(M, device=DEV)
+    _, Y, q = block.lq_rmsnorm_fwd(X, W, 1e-5, format=fmt, need_y=False, rstd_out=c)
+    want = mx.lq_mx_quantize(X.float() * c[:, None] * W.float(), fmt)
     assert Y is None and torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
 
 
