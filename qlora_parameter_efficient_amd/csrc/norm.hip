@@ -419,11 +419,12 @@ unsigned fwd_grid(int64_t M, int64_t K) {
   return (unsigned)(b < (1 << 20) ? b : 1 << 20);
 }
 
-// Backward: about what the chip holds at once, so that dW's partial sums, one
-// row of them for each row at work, stay few (us, 1024 workgroups / so many: 8192 x 1024 27 /
-// 21, 8192 x 4096 56.4 / 54.8, 8192 x 8192 111 / 105, 1024 x 8192 30 / 21; halves of
-// these 22, 72 and 116); a number that leaves a second row to a few is evened out (777
-// x 4095 float32 18.8 / 16.7), of many rows not (8192 x 4096 54.8 / 56.9)
+// Backward: about what the chip holds at once, so that dW's partial sums, one row of
+// them for each row at work, stay few (us, 1024 workgroups / so many: 8192 x 1024 27 /
+// 21, 8192 x 4096 56.4 / 54.8, 8192 x 8192 111 / 105, 1024 x 8192 30 / 21; with half
+// as many 22, 72, 116 for the first three); a number that leaves a second row to a few
+// is evened out (777 x 4095 float32 18.8 / 16.7), of many rows not (8192 x 4096 54.8 /
+// 56.9)
 unsigned bwd_grid(int64_t M, int64_t K) {
   const int shape = norm_shape(K);
   const int64_t b = cdiv(M, rows_per_block(K)), most = shape == 1 ? 768 : shape >= 3 ? 256 : 512;
