@@ -590,14 +590,17 @@ int64_t z_first_columns(const Shape& s, int64_t rows, int64_t V, int64_t K) {
   return two < launch_cost(s.jm, rows, V, K / kStep, 1, false) ? first : V;
 }
 
-// Rows of a piece: at most 2^28 logits (1 GiB of float32), whole 256-row tiles
-int64_t piece_rows(int64_t M, int64_t V) {
-  const int64_t most = ((int64_t)1 << 28) / V / 256 * 256;
-  const int64_t rows = most < 256 ? 256 : most;
-  return M < rows ? M : rows;
-}
-
 int64_t ld_of(int64_t V) { return cdiv(V, 64) * 64; }
+
+// Rows of a piece: at most 2^28 logits with their padding (1 GiB of float32), whole
+// 256-row tiles; at most 2^21, since a launch's first dimension holds fewer than 2^32
+// threads and the softmax has 1024 a row
+int64_t piece_rows(int64_t M, int64_t V) {
+  constexpr int64_t kMost = (int64_t)1 << 21;
+  int64_t most = ((int64_t)1 << 28) / ld_of(V) / 256 * 256;
+  most = most < 256 ? 256 : most > kMost ? kMost : most;
+  return M < most ? M : most;
+}
 
 // the logits of a piece (the last has fewer rows and may have more splits)
 size_t z_bytes(int64_t M, int64_t V, int64_t K) {
