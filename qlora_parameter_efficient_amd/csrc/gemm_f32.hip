@@ -106,15 +106,19 @@ int gemm(const Acc& P, const Acc& Q, float* C, int64_t ldc, int64_t I, int64_t J
 }
 
 __global__ void zero_f32_kernel(float* p, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) p[i] = 0.0f;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x)
+    p[i] = 0.0f;
 }
 
 }  // namespace
 
 int launch_zero_f32(float* p, int64_t n, hipStream_t stream) {
   if (n == 0) return LQ_OK;
-  hipLaunchKernelGGL(zero_f32_kernel, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, stream, p, n);
+  // (a launch's first dimension holds fewer than 2^32 threads)
+  const int64_t b = cdiv(n, 256);
+  hipLaunchKernelGGL(zero_f32_kernel, dim3((unsigned)(b < (1 << 20) ? b : 1 << 20)), dim3(256), 0,
+                     stream, p, n);
   return hip_fail(hipGetLastError(), "zero launch");
 }
 
