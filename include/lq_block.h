@@ -166,6 +166,8 @@ size_t lq_adapters_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, i
  *            a mean); NULL: 1.  Read for dH only
  *   loss, lse  optional device float[M];  dH  optional M x K bf16
  *   ws       lq_head_loss_workspace(M, V, K, kt, dH != NULL) bytes (more is not used)
+ * Infinite logits: lse is +inf with a logit of +inf, -inf where all are -inf, NaN
+ * with a NaN; loss follows from it, and dH of such a row is NaN.
  * One of loss, lse and dH at least.  The logits of one piece of rows at a time
  * are held in ws as float32; the gradient with respect to them enters its
  * product with W0 as bf16, over the row's largest entry (which is then exact).

@@ -428,6 +428,9 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     for (int k = 0; k < 4; ++k) top = fmaxf(top, v[k]);
   }
   top = row_reduce<true, T>(top, sh);
+  // What the exponentials are taken from: an infinite maximum would make inf - inf of
+  // itself (from 0 a sum with +inf in it is +inf, of all -inf it is 0, and a NaN stays)
+  const float base = fabsf(top) < __builtin_inff() ? top : 0.0f;
   // the weight of a target, at the first of several with one index
   bool first = tid < p.kt && tgt[tid] >= 0;
   float q = 0.0f;
@@ -442,16 +445,16 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
   for (int i = 0; i < Q; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      x[i][k] = __expf(x[i][k] - top);
+      x[i][k] = __expf(x[i][k] - base);
       sum += x[i][k];
     }
   for (int g = tid + T * Q; g < groups; g += T) {
     const f32x4 v = load(g);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum += __expf(v[k] - top);
+    for (int k = 0; k < 4; ++k) sum += __expf(v[k] - base);
   }
   sum = row_reduce<false, T>(sum, sh);
-  const float lse = top + logf(sum);
+  const float lse = base + logf(sum);
   // the targets: every thread adds the few of them in order
   float total = 0.0f, loss = 0.0f;
   bool any = false;
@@ -467,7 +470,7 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
   }
   if (!p.D) return;
   // the targets' entries of the gradient, but for the row's share
-  if (tid < p.kt) dt[tid] = first ? total * (__expf(zt[tid] - top) / sum) - q : 0.0f;
+  if (tid < p.kt) dt[tid] = first ? total * (__expf(zt[tid] - base) / sum) - q : 0.0f;
   __syncthreads();
   // D is the gradient over its largest entry, which is then exact in bf16.  That
   // entry is most of dH, and the same error of it in every row (w and 1 - p are often
@@ -493,7 +496,7 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     if (g < groups) {
       v = load(g);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __expf(v[k] - top);
+      for (int k = 0; k < 4; ++k) v[k] = __expf(v[k] - base);
     }
     store(g, v);
   }
