@@ -383,10 +383,17 @@ template <int T, int Q>
 __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
   __shared__ float sh[T / 64];
   __shared__ int tgt[kMaxTargets];
-  __shared__ float wgt[kMaxTargets], zt[kMaxTargets], dt[kMaxTargets];
+  __shared__ float wgt[kMaxTargets], zt[kMaxTargets], et[kMaxTargets], dt[kMaxTargets];
+  // bit 4 i + k: value x[i][k] of a thread is a target's; and whether one is among those
+  // that it reads again
+  __shared__ unsigned long long own[T];
+  __shared__ uint8_t beyond[T];
   const int tid = threadIdx.x, V = p.V;
   const int64_t row = blockIdx.x;
   const float* z = p.Z + row * p.ldz;
+  own[tid] = 0;
+  beyond[tid] = 0;
+  __syncthreads();
   if (tid < p.kt) {
     const int t = p.t[row * p.kt + tid];
     const bool ok = t >= 0 && t < V;
@@ -396,6 +403,10 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     if (ok)
       for (int k = 0; k < p.splits; ++k) v += z[k * p.part + t];
     zt[tid] = v;
+    if (ok && (t >> 2) < T * Q)
+      atomicOr(&own[(t >> 2) % T], 1ull << (4 * ((t >> 2) / T) + (t & 3)));
+    else if (ok)
+      beyond[(t >> 2) % T] = 1;
   }
   const int groups = (V + 3) / 4;
   const float ninf = -__builtin_inff();
@@ -431,52 +442,95 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
   // What the exponentials are taken from: an infinite maximum would make inf - inf of
   // itself (from 0 a sum with +inf in it is +inf, of all -inf it is 0, and a NaN stays)
   const float base = fabsf(top) < __builtin_inff() ? top : 0.0f;
-  // the weight of a target, at the first of several with one index
+  // the weight of a target, at the first of several with one index, and the others'
   bool first = tid < p.kt && tgt[tid] >= 0;
-  float q = 0.0f;
-  if (first && p.D)
+  float q = 0.0f, rest_q = 0.0f;
+  if (first)
     for (int j = 0; j < p.kt; ++j) {
-      if (tgt[j] != tgt[tid]) continue;
+      if (tgt[j] != tgt[tid]) {
+        rest_q += wgt[j];
+        continue;
+      }
       if (j < tid) first = false;
       q += wgt[j];
     }
-  float sum = 0.0f;
+  if (tid < p.kt) et[tid] = first ? __expf(zt[tid] - base) : 0.0f;
+  // The exponentials but for the targets' (0 in their places): of a row whose label is
+  // the largest logit, 1 - p is their sum over all, not what 1 / sum - 1 leaves of it.
+  const unsigned long long mine = own[tid];
+  float sum = 0.0f, big = 0.0f;
 #pragma unroll
   for (int i = 0; i < Q; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[i][k] = __expf(x[i][k] - base);
-      sum += x[i][k];
-    }
+    for (int k = 0; k < 4; ++k) x[i][k] = __expf(x[i][k] - base);
+  if (mine)
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] = mine >> (4 * i + k) & 1 ? 0.0f : x[i][k];
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum += x[i][k];
   for (int g = tid + T * Q; g < groups; g += T) {
     const f32x4 v = load(g);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum += __expf(v[k] - base);
+    for (int k = 0; k < 4; ++k) {
+      float e = __expf(v[k] - base);
+      if (beyond[tid])
+        for (int j = 0; j < p.kt; ++j) e = tgt[j] == 4 * g + k ? 0.0f : e;
+      sum += e;
+      big = fmaxf(big, e);
+    }
   }
   sum = row_reduce<false, T>(sum, sh);
-  const float lse = base + logf(sum);
-  // the targets: every thread adds the few of them in order
-  float total = 0.0f, loss = 0.0f;
-  bool any = false;
+  // The targets: every thread adds the few of them in order.  less: the sum without one
+  // largest exponential (1) where a target's is that
+  float total = 0.0f, less = sum;
+  bool any = false, top_in = false;
   for (int j = 0; j < p.kt; ++j) {
     const bool ok = tgt[j] >= 0;
     any |= ok;
     total += wgt[j];
-    loss += ok ? wgt[j] * (lse - zt[j]) : 0.0f;
+    if (ok && !top_in && zt[j] == top && base == top)
+      top_in = true;
+    else
+      less += et[j];
   }
+  sum = top_in ? 1.0f + less : less;
+  const float lse = base + logf(sum);
+  float loss = 0.0f;
+  for (int j = 0; j < p.kt; ++j) loss += tgt[j] >= 0 ? wgt[j] * (lse - zt[j]) : 0.0f;
   if (tid == 0) {
     if (p.loss) p.loss[row] = loss;
     if (p.lse) p.lse[row] = lse;
   }
   if (!p.D) return;
   // the targets' entries of the gradient, but for the row's share
-  if (tid < p.kt) dt[tid] = first ? total * (__expf(zt[tid] - base) / sum) - q : 0.0f;
+  if (tid < p.kt) {
+    float v = 0.0f;
+    if (first && zt[tid] == top && base == top)
+      v = rest_q - total * (less / sum);  // total p - q with p = 1 - less / sum
+    else if (first)
+      v = total * (et[tid] / sum) - q;
+    dt[tid] = v;
+  }
+  // The largest exponential that stays: 1, but where a target's is that, the largest of
+  // the others (no matter with one target, whose entry is all of theirs together)
+  float others = top_in ? 0.0f : 1.0f;
+  if (top_in && p.kt > 1) {
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) big = fmaxf(big, x[i][k]);
+    others = row_reduce<true, T>(big, sh);
+  }
   __syncthreads();
   // D is the gradient over its largest entry, which is then exact in bf16.  That
   // entry is most of dH, and the same error of it in every row (w and 1 - p are often
   // the same in all) would be dH's error: up to 2^-8, where the others' errors, half
   // of that and of either sign, are mostly lost in dH's own rounding.
-  float most = fmaxf(fabsf(total / sum), 1e-37f);
+  float most = fmaxf(others * fabsf(total / sum), 1e-37f);
   for (int j = 0; j < p.kt; ++j) most = fmaxf(most, fabsf(dt[j]));
   uint16_t* d = p.D + row * p.ldd;
   const float inv = 1.0f / most, f = total / sum * inv;
