@@ -362,54 +362,74 @@ struct RowParams {
 
 constexpr int kMaxTargets = 128;
 
-template <bool MAX, int T>
-__device__ __forceinline__ float row_reduce(float v, float* sh) {
+// The sum, or the largest, over the N (16 or 64) lanes that share lane / N, in every one:
+// 16 lanes by moves within the row (lane ^ 1, ^ 2, mirrored within eight and sixteen)
+template <bool MAX, int N>
+__device__ __forceinline__ float lanes(float v) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#define LQ_JOIN(ctrl) \
+  v = join(v, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), ctrl, 0xF, 0xF, false)))
+  LQ_JOIN(0xB1);
+  LQ_JOIN(0x4E);
+  LQ_JOIN(0x141);
+  LQ_JOIN(0x140);
+#undef LQ_JOIN
 #pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const float y = __shfl_xor(v, o);
-    v = MAX ? fmaxf(v, y) : v + y;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = sh[0];
-#pragma unroll
-  for (int i = 1; i < T / 64; ++i) v = MAX ? fmaxf(v, sh[i]) : v + sh[i];
+  for (int o = 16; o < N; o *= 2) v = join(v, __shfl_xor(v, o));
   return v;
 }
+template <int N = 64>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes<false, N>(v);
+}
+template <int N = 64>
+__device__ __forceinline__ float lanes_max(float v) {
+  return lanes<true, N>(v);
+}
 
-// T threads; Q: groups of four values per thread that stay in registers
+// T threads; Q: groups of four values per thread that stay in registers.  Wave 0 has the
+// targets, two a lane at most (lane and lane + 64): in every wave, what there is to do
+// for 16 of them costs as much as the row.  Scalar registers: with more than 80 (it
+// would take 97) a compute unit holds one workgroup instead of two (rows of 1000: 30 us
+// against 20 for 2048 of them).
 template <int T, int Q>
-__global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
-  __shared__ float sh[T / 64];
+__global__ __launch_bounds__(T) __attribute__((amdgpu_num_sgpr(80))) void head_row_kernel(RowParams p) {
+  constexpr int W = T / 64;
+  __shared__ float waves[3][W];  // of each wave: its maximum, its sum, its largest that stays
+  __shared__ float top_target, factor, has_target;
+  __shared__ int n_ones;
   __shared__ int tgt[kMaxTargets];
-  __shared__ float wgt[kMaxTargets], zt[kMaxTargets], et[kMaxTargets], dt[kMaxTargets];
-  // bit 4 i + k: value x[i][k] of a thread is a target's; and whether one is among those
-  // that it reads again
+  __shared__ float wgt[kMaxTargets];
+  // several targets.  Bit 4 i + k: value x[i][k] of a thread is a target's; and whether
+  // one is among those that it reads again
   __shared__ unsigned long long own[T];
   __shared__ uint8_t beyond[T];
-  const int tid = threadIdx.x, V = p.V;
+  const int tid = threadIdx.x, V = p.V, kt = p.kt;
   const int64_t row = blockIdx.x;
   const float* z = p.Z + row * p.ldz;
-  own[tid] = 0;
-  beyond[tid] = 0;
-  __syncthreads();
-  if (tid < p.kt) {
-    const int t = p.t[row * p.kt + tid];
-    const bool ok = t >= 0 && t < V;
-    tgt[tid] = ok ? t : -1;
-    wgt[tid] = ok ? (p.pt ? p.pt[row * p.kt + tid] : 1.0f) : 0.0f;
-    float v = 0.0f;
-    if (ok)
-      for (int k = 0; k < p.splits; ++k) v += z[k * p.part + t];
-    zt[tid] = v;
-    if (ok && (t >> 2) < T * Q)
-      atomicOr(&own[(t >> 2) % T], 1ull << (4 * ((t >> 2) / T) + (t & 3)));
-    else if (ok)
-      beyond[(t >> 2) % T] = 1;
-  }
-  const int groups = (V + 3) / 4;
   const float ninf = -__builtin_inff();
+  int tj[2] = {-1, -1};
+  float wj[2] = {0.0f, 0.0f}, zj[2] = {0.0f, 0.0f};
+  const float w_row = tid == 0 && p.w ? p.w[row] : 1.0f;
+  if (tid == 0) n_ones = 0;
+  if (kt > 1) {
+    own[tid] = 0;
+    beyond[tid] = 0;
+  }
+  if (tid < 64)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = tid + 64 * u;
+      if (j >= kt) continue;
+      const int t = p.t[row * kt + j];
+      if (t >= 0 && t < V) {
+        tj[u] = t;
+        wj[u] = p.pt ? p.pt[row * kt + j] : 1.0f;
+      }
+      tgt[j] = tj[u];
+      wgt[j] = wj[u];
+    }
+  const int groups = (V + 3) / 4;
   f32x4 x[Q];
   auto load = [&](int g) {
     f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(z + 4 * g));
@@ -422,119 +442,189 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     for (int k = 0; k < 4; ++k) v[k] = 4 * g + k < V ? v[k] : ninf;
     return v;
   };
-  float top = ninf;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     const int g = tid + T * i;
     x[i] = f32x4{ninf, ninf, ninf, ninf};
     if (g < groups) x[i] = load(g);
   }
+  // a target's logit, its weight at the first of several with one index, the others'
+  // weights
+  bool first[2] = {tj[0] >= 0, tj[1] >= 0};
+  float same_w[2] = {wj[0], wj[1]}, other_w[2] = {0.0f, 0.0f};
+  if (tid < 64) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (tj[u] >= 0)
+        for (int k = 0; k < p.splits; ++k) zj[u] += z[k * p.part + tj[u]];
+    if (kt > 1) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (64 * u >= kt) break;
+        same_w[u] = 0.0f;
+        for (int j = 0; j < kt; ++j) {
+          const bool same = tgt[j] == tj[u];
+          const float w = wgt[j];
+          same_w[u] += same ? w : 0.0f;
+          other_w[u] += same ? 0.0f : w;
+          first[u] &= !same || j >= tid + 64 * u;
+        }
+      }
+    }
+  }
+  float own_top = ninf;
 #pragma unroll
   for (int i = 0; i < Q; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, x[i][k]);
+    for (int k = 0; k < 4; ++k) own_top = fmaxf(own_top, x[i][k]);
   for (int g = tid + T * Q; g < groups; g += T) {
     const f32x4 v = load(g);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, v[k]);
+    for (int k = 0; k < 4; ++k) own_top = fmaxf(own_top, v[k]);
   }
-  top = row_reduce<true, T>(top, sh);
+  float top = lanes_max(own_top);
+  if ((tid & 63) == 0) waves[0][tid >> 6] = top;
+  if (tid < 64) {
+    float best = fmaxf(tj[0] >= 0 ? zj[0] : ninf, tj[1] >= 0 ? zj[1] : ninf);
+    if (kt > 1) best = lanes_max(best);
+    if (tid == 0) top_target = best;
+  }
+  __syncthreads();
+  if (kt > 1 && tid < 64)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (!first[u]) continue;
+      const int g = tj[u] >> 2;
+      if (g < T * Q)
+        atomicOr(&own[g % T], 1ull << (4 * (g / T) + (tj[u] & 3)));
+      else
+        beyond[g % T] = 1;
+    }
+#pragma unroll
+  for (int i = 0; i < W; ++i) top = fmaxf(top, waves[0][i]);
   // What the exponentials are taken from: an infinite maximum would make inf - inf of
   // itself (from 0 a sum with +inf in it is +inf, of all -inf it is 0, and a NaN stays)
-  const float base = fabsf(top) < __builtin_inff() ? top : 0.0f;
-  // the weight of a target, at the first of several with one index, and the others'
-  bool first = tid < p.kt && tgt[tid] >= 0;
-  float q = 0.0f, rest_q = 0.0f;
-  if (first)
-    for (int j = 0; j < p.kt; ++j) {
-      if (tgt[j] != tgt[tid]) {
-        rest_q += wgt[j];
-        continue;
-      }
-      if (j < tid) first = false;
-      q += wgt[j];
-    }
-  if (tid < p.kt) et[tid] = first ? __expf(zt[tid] - base) : 0.0f;
-  // The exponentials but for the targets' (0 in their places): of a row whose label is
-  // the largest logit, 1 - p is their sum over all, not what 1 / sum - 1 leaves of it.
-  const unsigned long long mine = own[tid];
+  const bool finite = fabsf(top) < __builtin_inff();
+  const float base = finite ? top : 0.0f;
+  const bool top_in = finite && top_target == top;  // a target is the largest logit
+  // The sum of the exponentials without the first 1 of each thread that has the largest
+  // logit (n_ones of them, mostly one): where a target is that logit, 1 - p is the rest
+  // over all, not what 1 / sum - 1 leaves of it.
   float sum = 0.0f, big = 0.0f;
 #pragma unroll
   for (int i = 0; i < Q; ++i)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[i][k] = __expf(x[i][k] - base);
-  if (mine)
+    for (int k = 0; k < 4; ++k) {
+      x[i][k] = __expf(x[i][k] - base);
+      sum += x[i][k];
+    }
+  bool one = finite && own_top == top;  // still to leave out
+  if (one) {
+    atomicAdd(&n_ones, 1);
+    sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < Q; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[i][k] = mine >> (4 * i + k) & 1 ? 0.0f : x[i][k];
-#pragma unroll
-  for (int i = 0; i < Q; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum += x[i][k];
+      for (int k = 0; k < 4; ++k) {
+        const bool skip = one && x[i][k] == 1.0f;
+        sum += skip ? 0.0f : x[i][k];
+        one &= !skip;
+      }
+  }
   for (int g = tid + T * Q; g < groups; g += T) {
     const f32x4 v = load(g);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float e = __expf(v[k] - base);
-      if (beyond[tid])
-        for (int j = 0; j < p.kt; ++j) e = tgt[j] == 4 * g + k ? 0.0f : e;
-      sum += e;
-      big = fmaxf(big, e);
+      const float e = __expf(v[k] - base);
+      const bool skip = one && e == 1.0f;
+      sum += skip ? 0.0f : e;
+      one &= !skip;
     }
   }
-  sum = row_reduce<false, T>(sum, sh);
-  // The targets: every thread adds the few of them in order.  less: the sum without one
-  // largest exponential (1) where a target's is that
-  float total = 0.0f, less = sum;
-  bool any = false, top_in = false;
-  for (int j = 0; j < p.kt; ++j) {
-    const bool ok = tgt[j] >= 0;
-    any |= ok;
-    total += wgt[j];
-    if (ok && !top_in && zt[j] == top && base == top)
-      top_in = true;
-    else
-      less += et[j];
-  }
-  sum = top_in ? 1.0f + less : less;
-  const float lse = base + logf(sum);
-  float loss = 0.0f;
-  for (int j = 0; j < p.kt; ++j) loss += tgt[j] >= 0 ? wgt[j] * (lse - zt[j]) : 0.0f;
-  if (tid == 0) {
-    if (p.loss) p.loss[row] = loss;
-    if (p.lse) p.lse[row] = lse;
-  }
-  if (!p.D) return;
-  // the targets' entries of the gradient, but for the row's share
-  if (tid < p.kt) {
-    float v = 0.0f;
-    if (first && zt[tid] == top && base == top)
-      v = rest_q - total * (less / sum);  // total p - q with p = 1 - less / sum
-    else if (first)
-      v = total * (et[tid] / sum) - q;
-    dt[tid] = v;
-  }
-  // The largest exponential that stays: 1, but where a target's is that, the largest of
-  // the others (no matter with one target, whose entry is all of theirs together)
-  float others = top_in ? 0.0f : 1.0f;
-  if (top_in && p.kt > 1) {
+  // The largest exponential that stays in D: 1, or beside such a target the largest of
+  // no target's (with one target its entry, all of the others' together, is larger)
+  const bool look = kt > 1 && top_in && p.D;
+  if (look) {
+    __syncthreads();
+    const unsigned long long mine = own[tid];
 #pragma unroll
     for (int i = 0; i < Q; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) big = fmaxf(big, x[i][k]);
-    others = row_reduce<true, T>(big, sh);
+      for (int k = 0; k < 4; ++k)
+        big = fmaxf(big, mine >> (4 * i + k) & 1 ? 0.0f : x[i][k]);
+    for (int g = tid + T * Q; g < groups; g += T) {
+      const f32x4 v = load(g);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float e = __expf(v[k] - base);
+        if (beyond[tid])
+          for (int j = 0; j < kt; ++j) e = tgt[j] == 4 * g + k ? 0.0f : e;
+        big = fmaxf(big, e);
+      }
+    }
+    big = lanes_max(big);
+  }
+  sum = lanes_sum(sum);
+  if ((tid & 63) == 0) {
+    waves[1][tid >> 6] = sum;
+    waves[2][tid >> 6] = big;
   }
   __syncthreads();
-  // D is the gradient over its largest entry, which is then exact in bf16.  That
-  // entry is most of dH, and the same error of it in every row (w and 1 - p are often
-  // the same in all) would be dH's error: up to 2^-8, where the others' errors, half
-  // of that and of either sign, are mostly lost in dH's own rounding.
-  float most = fmaxf(others * fabsf(total / sum), 1e-37f);
-  for (int j = 0; j < p.kt; ++j) most = fmaxf(most, fabsf(dt[j]));
+  float out[3] = {0.0f, 0.0f, 0.0f};  // loss, lse, g
+  float dj[2] = {0.0f, 0.0f};         // the targets' entries of D
+  if (tid < 64) {
+    const float less = lanes_sum<W>(waves[1][tid % W]) + (finite ? (float)(n_ones - 1) : 0.0f);
+    sum = finite ? 1.0f + less : less;
+    const float lse = base + (finite ? log1pf(less) : logf(sum));
+    const bool any = (__ballot(tj[0] >= 0) | __ballot(tj[1] >= 0)) != 0;
+    float total = wj[0] + wj[1], loss = 0.0f, most = 0.0f;
+    if (kt > 1) total = lanes_sum(total);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (tj[u] < 0) continue;
+      loss += wj[u] * (lse - zj[u]);
+      // (total p - weight; of the largest logit with p = 1 - less / sum)
+      dj[u] = finite && zj[u] == top ? other_w[u] - total * (less / sum)
+                                     : total * (__expf(zj[u] - base) / sum) - same_w[u];
+      most = fmaxf(most, fabsf(dj[u]));
+    }
+    if (kt > 1) {
+      loss = lanes_sum(loss);
+      most = lanes_max(most);
+    }
+    // D is the gradient over its largest entry, which is then exact in bf16.  That
+    // entry is most of dH, and the same error of it in every row (w and 1 - p are often
+    // the same in all) would be dH's error: up to 2^-8, where the others' errors, half
+    // of that and of either sign, are mostly lost in dH's own rounding.
+    const float stays = look ? lanes_max<W>(waves[2][tid % W]) : top_in ? 0.0f : 1.0f;
+    most = fmaxf(fmaxf(most, 1e-37f), stays * fabsf(total / sum));
+    most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
+    const float inv = 1.0f / most;
+    out[0] = loss;
+    out[1] = lse;
+    out[2] = any ? w_row * p.scale * most : 0.0f;
+    if (tid == 0) {
+      // (a NaN in a row without a target must not reach D)
+      has_target = any ? 1.0f : 0.0f;
+      factor = total / sum * inv;
+    }
+    dj[0] *= inv;
+    dj[1] *= inv;
+  }
+  auto store_row = [&] {
+    if (tid) return;
+    if (p.loss) p.loss[row] = out[0];
+    if (p.lse) p.lse[row] = out[1];
+    if (p.D) p.g[row] = out[2];
+  };
+  if (!p.D) return store_row();
+  __syncthreads();
+  store_row();
+  const float f = factor;
+  const bool any = has_target != 0.0f;
   uint16_t* d = p.D + row * p.ldd;
-  const float inv = 1.0f / most, f = total / sum * inv;
-  if (tid == 0) p.g[row] = any ? (p.w ? p.w[row] : 1.0f) * p.scale * most : 0.0f;
   auto store = [&](int g, f32x4 e) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) e[k] = any ? e[k] * f : 0.0f;
@@ -555,7 +645,9 @@ __global__ __launch_bounds__(T) void head_row_kernel(RowParams p) {
     store(g, v);
   }
   __syncthreads();  // the targets' entries over what is stored for them
-  if (first) d[tgt[tid]] = f32_to_bf16(dt[tid] * inv);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (first[u]) d[tj[u]] = f32_to_bf16(dj[u]);
 }
 
 // out (bf16) = the splits' sums in order, row i of K times g[i]; K % 8 == 0, n < 2^31

@@ -38,3 +38,16 @@ def test_more_short_rows_than_a_launch_takes(M, V):
         slack = (d.abs() * (HALF_BF16 + V * U32) + (2 * e[:, None] + 16 * U32) * (soft + 16 * U32) * (1 + HALF_BF16)) @ w.abs()
         ref = d @ w
         assert bool(((dH[i].double() - ref).abs() <= HALF_BF16 * ref.abs() + slack * (1 + HALF_BF16)).all()), int(i[0])
+
+
+@pytest.mark.parametrize("V", [300, 5000, 70001])
+def test_lse_does_not_depend_on_the_targets(V):
+    """The same bits with any target, among the largest logits or not, or several."""
+    announce(f"lse of any target V={V}")
+    g = torch.Generator(device=DEV).manual_seed(V)
+    H = torch.randn((9, 64), generator=g, device=DEV).bfloat16()
+    W = (torch.randn((V, 64), generator=g, device=DEV) * 0.5).bfloat16()
+    top = (H.float() @ W.float().t()).topk(8, 1).indices.int()
+    want = block.lq_head_loss(H, W, torch.full((9,), -1, dtype=torch.int32, device=DEV))[1]
+    for t in (top[:, 0].contiguous(), top[:, 7].contiguous(), top.contiguous(), torch.full_like(top[:, 0], V - 1)):
+        assert torch.equal(block.lq_head_loss(H, W, t)[1], want)
