@@ -577,14 +577,16 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_num_sgpr(80))) void head_r
   if (tid < 64) {
     const float less = lanes_sum<W>(waves[1][tid % W]) + (finite ? (float)(n_ones - 1) : 0.0f);
     sum = finite ? 1.0f + less : less;
-    const float lse = base + (finite ? log1pf(less) : logf(sum));
+    // (lse - z of a target from the differences to the largest logit, which are small
+    // where the loss is: lse itself is rounded beside that logit)
+    const float log_sum = finite ? log1pf(less) : logf(sum);
     const bool any = (__ballot(tj[0] >= 0) | __ballot(tj[1] >= 0)) != 0;
     float total = wj[0] + wj[1], loss = 0.0f, most = 0.0f;
     if (kt > 1) total = lanes_sum(total);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (tj[u] < 0) continue;
-      loss += wj[u] * (lse - zj[u]);
+      loss += wj[u] * (log_sum + (base - zj[u]));
       // (total p - weight; of the largest logit with p = 1 - less / sum)
       dj[u] = finite && zj[u] == top ? other_w[u] - total * (less / sum)
                                      : total * (__expf(zj[u] - base) / sum) - same_w[u];
@@ -603,7 +605,7 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_num_sgpr(80))) void head_r
     most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
     const float inv = 1.0f / most;
     out[0] = loss;
-    out[1] = lse;
+    out[1] = base + log_sum;
     out[2] = any ? w_row * p.scale * most : 0.0f;
     if (tid == 0) {
       // (a NaN in a row without a target must not reach D)

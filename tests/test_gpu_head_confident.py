@@ -117,3 +117,22 @@ def test_a_row_that_is_all_but_certain():
         tiny = 2.0**-126  # float32's and bf16's smallest normal value
         e = HALF_BF16 + (1 + HALF_BF16) * (rel(V, h) + 8 * U32)
         assert bool(((dH[:, 1:].double() - ref).abs() <= e * ref.abs() + 4 * tiny).all()), h
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.75])
+@pytest.mark.parametrize("V", [300, 70001])
+def test_loss_of_large_confident_logits(V, scale):
+    """Logits in the hundreds, the label's largest by a little or by much: the loss is
+    log(1 + the others' sum), as exact as that sum; and (top - z_t) + log(sum) otherwise."""
+    announce(f"loss of large logits V={V} scale={scale}")
+    for near in (284.0, 288.0, 296.0, 300.0):
+        z, H, W = case(7, V, 4.0, {5: 75.0, 9: near / 4.0}, 11)
+        z = z * scale
+        for t in (5, 9):
+            loss, lse, _ = block.lq_head_loss(H, W, torch.full((7,), t, dtype=torch.int32, device=DEV), logit_scale=scale)
+            d = z - z.max()
+            e = torch.exp(d)
+            top = int(z.argmax())
+            want = float((z.max() - z[t]) + torch.log1p(e[torch.arange(V) != top].sum()))
+            assert bool(((loss.double() - want).abs() <= rel(V, float(z.max() - z[9]) + 1.0) * want).all()), (near, t)
+            assert abs(float(lse[0]) - float(torch.logsumexp(z, 0))) <= U32 * float(lse[0]) + rel(V, 0.0)
