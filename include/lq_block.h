@@ -63,7 +63,8 @@ int lq_rmsnorm_bwd(const void* dY, const void* H, int64_t M, int64_t K, lq_dtype
                    void* dX, float* dW, int32_t accumulate, void* ws, size_t ws_bytes,
                    hipStream_t stream);
 
-/* Workspace of lq_rmsnorm_bwd with dW, in bytes; 0 for sizes that it refuses. */
+/* Workspace of lq_rmsnorm_bwd with dW, in bytes; 0 for sizes that it refuses.  The
+ * workspace of M rows is enough for fewer. */
 size_t lq_rmsnorm_bwd_workspace(int64_t M, int64_t K);
 
 /* -------------------------------- adapters of many requests, one projection */

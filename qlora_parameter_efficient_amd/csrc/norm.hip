@@ -425,9 +425,12 @@ unsigned fwd_grid(int64_t M, int64_t K) {
 // as many 22, 72, 116 for the first three); a number that leaves a second row to a few
 // is evened out (777 x 4095 float32 18.8 / 16.7), of many rows not (8192 x 4096 54.8 /
 // 56.9)
-unsigned bwd_grid(int64_t M, int64_t K) {
+int64_t bwd_most(int64_t K) {
   const int shape = norm_shape(K);
-  const int64_t b = cdiv(M, rows_per_block(K)), most = shape == 1 ? 768 : shape >= 3 ? 256 : 512;
+  return shape == 1 ? 768 : shape >= 3 ? 256 : 512;
+}
+unsigned bwd_grid(int64_t M, int64_t K) {
+  const int64_t b = cdiv(M, rows_per_block(K)), most = bwd_most(K);
   return (unsigned)(b < 2 * most ? cdiv(b, cdiv(b, most)) : most);
 }
 
@@ -459,8 +462,10 @@ void launch_bwd(const NormParams& p, hipStream_t st) {
 
 namespace dispatch {
 
+// (for M rows or fewer: an evened-out grid may be smaller than that of fewer rows)
 size_t rmsnorm_part_bytes(int64_t M, int64_t K) {
-  return (size_t)bwd_grid(M, K) * rows_per_block(K) * (size_t)K * 4;
+  const int64_t b = cdiv(M, rows_per_block(K)), most = bwd_most(K);
+  return (size_t)(b < most ? b : most) * rows_per_block(K) * (size_t)K * 4;
 }
 
 int rmsnorm_fwd(const void* X, const void* R, int64_t M, int64_t K, lq_dtype dt, const void* W,

@@ -21,3 +21,23 @@ def test_head_holds_one_piece_of_logits(V):
     logits = min(max(1 << 28, 256 * ld), (1 << 21) * ld)
     assert 0 < size(M, V, K, 1, 0) <= 4 * logits + 4096
     assert size(M, V, K, 1, 1) <= 6 * logits + 4 * (1 << 21) + 4 * (1 << 20) * K + 4096
+
+
+def rows_up_to(most):
+    """Row counts whose neighbours have other tiles, splits and pieces."""
+    edges = [1, 16, 17, 63, 64, 65, 128, 129, 256, 511, 767, 768, 769, 1024, 1025, 1535, 1536, 1537, 4096, 4097, 8128,
+             8129, 8192, 8193, 16384, 16385, 65536, 65537, 262143]
+    return sorted({m for m in edges + list(range(1, 9000, 37)) if m <= most})
+
+
+def grows(size, most=1 << 20):
+    last = 0
+    for M in rows_up_to(most):
+        now = size(M)
+        assert now >= last, (M, now, last)
+        last = now
+
+
+@pytest.mark.parametrize("K", [64, 1024, 1025, 4096, 5000, 8192, 16384, 30000, 65536])
+def test_norm_workspace_is_enough_for_fewer_rows(K):
+    grows(lambda M: block.lib().lq_rmsnorm_bwd_workspace(M, K))
