@@ -142,7 +142,8 @@ int lq_adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_p
 #define LQ_ADAPTERS_OP_FWD 0
 #define LQ_ADAPTERS_OP_BWD 1
 /* Workspace in bytes; 0 for M = 0, for sizes that the call refuses, and for
- * forwards of few rows that need none. */
+ * forwards of few rows that need none.  The workspace of M rows is enough for
+ * fewer. */
 size_t lq_adapters_workspace_size(int32_t op, int64_t M, int64_t N, int64_t K, int64_t r,
                                   int32_t slots);
 

@@ -1152,16 +1152,15 @@ int t_pitch(int64_t r) { return (int)(r + 3) / 4 * 4; }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// Tiles of a plan: every place may have one that is not full
 int64_t max_tiles(int64_t M, int32_t slots) {
-  if (M <= kDirect) return M;
   const int64_t t = cdiv(M, kTM) + slots;
   return t < M ? t : M;
 }
 // a multiple of eight, so that a tile's workgroups of both launches run on one
 // XCD and find T's partial sums in its L2
 unsigned tile_grid(const RowArgs& a) {
-  const int64_t t = max_tiles(a.M, a.slots);
-  return (unsigned)(a.tiles ? cdiv(t, 8) * 8 : t);
+  return (unsigned)(a.tiles ? cdiv(max_tiles(a.M, a.slots), 8) * 8 : a.M);
 }
 
 // Splits of the shrink's reduction over C columns: about 256 workgroups where
@@ -1171,6 +1170,16 @@ int shrink_splits(int64_t M, int64_t C) {
   const int64_t most = cdiv(C / 64, 16), want = cdiv(256, cdiv(M, kTM));
   const int64_t s = want < most ? want : most;
   return (int)(s < 16 ? s : 16);
+}
+// Rows of all splits of T's partial sums, of M rows or fewer: s splits need 256 / (s -
+// 1) or more tiles to be too many
+int64_t split_rows(int64_t M, int64_t C) {
+  int64_t rows = M;
+  for (int64_t s = shrink_splits(1, C); s > 1; --s) {
+    const int64_t m = (cdiv(256, s - 1) - 1) * kTM;
+    if (s * (m < M ? m : M) > rows) rows = s * (m < M ? m : M);
+  }
+  return rows;
 }
 
 // Rows of a segment of the gradients: about 768 workgroups where places have
@@ -1185,10 +1194,21 @@ int64_t max_segments(int64_t M, int64_t N, int64_t K, int32_t slots) {
   return s < M ? s : M;
 }
 
-// Partial sums of the gradients: of places with more rows than a segment, which
-// have at most twice as many segments as their rows fill
-int64_t max_parts(int64_t M, int64_t N, int64_t K, int32_t slots) {
-  const int64_t p = 2 * cdiv(M, segment_rows(M, N, K)), s = max_segments(M, N, K, slots);
+// The same for M rows or fewer: full segments are cdiv(M, 128) at most, and as many as
+// segment_rows wants
+int64_t most_full(int64_t M, int64_t N, int64_t K) {
+  const int64_t want = cdiv(768, cdiv(N, 256) + cdiv(K, 256)), s = cdiv(M, 128);
+  return s < want ? s : want;
+}
+int64_t most_segments(int64_t M, int64_t N, int64_t K, int32_t slots) {
+  const int64_t s = most_full(M, N, K) + slots;
+  return s < M ? s : M;
+}
+
+// Partial sums of the gradients, of M rows or fewer: of places with more rows than a
+// segment, which have at most twice as many segments as their rows fill
+int64_t most_parts(int64_t M, int64_t N, int64_t K, int32_t slots) {
+  const int64_t p = 2 * most_full(M, N, K), s = most_segments(M, N, K, slots);
   return p < s ? p : s;
 }
 
@@ -1347,16 +1367,15 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
   BwdLayout l;
-  const int64_t segs = max_segments(M, N, K, slots), r8 = cdiv(r, 8) * 8;
-  const int64_t sn = shrink_splits(M, N), sk = shrink_splits(M, K);
-  l.plan = plan_layout(M, slots, segs);
+  const int64_t r8 = cdiv(r, 8) * 8, sn = split_rows(M, N), sk = split_rows(M, K);
+  l.plan = plan_layout(M, slots, most_segments(M, N, K, slots));
   l.bt = l.plan.end;
   l.at = l.bt + up256((size_t)slots * r * N * 2);
   l.u = l.at + up256((size_t)slots * r8 * K * 2);
   l.t = l.u + up256((size_t)M * r * 4);
   l.tp = l.t + up256((size_t)M * r * 4);
-  l.part = l.tp + up256((size_t)(sn > sk ? sn : sk) * M * t_pitch(r) * 4);
-  l.end = l.part + up256((size_t)max_parts(M, N, K, slots) * r * (N + K) * 4);
+  l.part = l.tp + up256((size_t)(sn > sk ? sn : sk) * t_pitch(r) * 4);
+  l.end = l.part + up256((size_t)most_parts(M, N, K, slots) * r * (N + K) * 4);
   return l;
 }
 
@@ -1366,8 +1385,8 @@ namespace dispatch {
 
 size_t adapters_fwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
   if (few_rows(M, N, K, r)) return 0;
-  const size_t plan = M <= kDirect ? 0 : plan_layout(M, slots, max_segments(M, N, K, slots)).end;
-  return plan + (size_t)shrink_splits(M, K) * M * t_pitch(r) * 4;
+  const size_t plan = M <= kDirect ? 0 : plan_layout(M, slots, 0).end;
+  return plan + (size_t)split_rows(M, K) * t_pitch(r) * 4;
 }
 
 size_t adapters_bwd_ws(int64_t M, int64_t N, int64_t K, int64_t r, int32_t slots) {
@@ -1381,7 +1400,7 @@ int adapters_fwd(const void* X, int64_t M, const lq_adapter_pool& q, const int32
   char* base = (char*)ws;
   int rc;
   if (M > kDirect) {
-    const PlanLayout l = plan_layout(M, q.slots, max_segments(M, q.N, q.K, q.slots));
+    const PlanLayout l = plan_layout(M, q.slots, 0);  // (no segments)
     if ((rc = launch_plan(a, l, base, 0, TurnArgs{}, st))) return rc;
     base += l.end;
   }

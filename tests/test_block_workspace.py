@@ -41,3 +41,10 @@ def grows(size, most=1 << 20):
 @pytest.mark.parametrize("K", [64, 1024, 1025, 4096, 5000, 8192, 16384, 30000, 65536])
 def test_norm_workspace_is_enough_for_fewer_rows(K):
     grows(lambda M: block.lib().lq_rmsnorm_bwd_workspace(M, K))
+
+
+@pytest.mark.parametrize("op", [block.LQ_ADAPTERS_OP_FWD, block.LQ_ADAPTERS_OP_BWD])
+@pytest.mark.parametrize("N,K,r,slots", [(4096, 4096, 64, 16), (11008, 4096, 32, 64), (4096, 11008, 11, 1), (64, 8128, 16, 300),
+                                         (64, 64, 1, 4096), (1024, 1024, 7, 8)])
+def test_adapter_workspace_is_enough_for_fewer_rows(op, N, K, r, slots):
+    grows(lambda M: block.lib().lq_adapters_workspace_size(op, M, N, K, r, slots), ((1 << 31) - 1) // max(N, K))
