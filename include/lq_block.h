@@ -180,7 +180,8 @@ int lq_head_loss(const void* H, int64_t M, const lq_weight* W0, const int32_t* t
                  const float* p, int32_t kt, const float* w, float logit_scale, float* loss,
                  float* lse, void* dH, void* ws, size_t ws_bytes, hipStream_t stream);
 
-/* Workspace in bytes; 0 for M = 0 and for sizes that the call refuses. */
+/* Workspace in bytes; 0 for M = 0 and for sizes that the call refuses.  The
+ * workspace of M rows is enough for fewer. */
 size_t lq_head_loss_workspace(int64_t M, int64_t V, int64_t K, int32_t kt, int32_t need_dh);
 
 #ifdef __cplusplus

@@ -697,6 +697,12 @@ double launch_cost(int jm, int64_t rows, int64_t n, int64_t steps, int64_t split
          1.2e-6 * parts * (double)rows * (double)n;
 }
 
+// Splits of eight steps at least
+int64_t split_limit(int64_t steps, int most_splits) {
+  const int64_t s = cdiv(steps, 8);
+  return s < most_splits ? s : most_splits;
+}
+
 // The cheapest tile and number of splits.  ``sums``: the splits are added by a
 // launch of their own (dH), not by the softmax (z)
 Shape best_shape(int64_t rows, int64_t n, int64_t steps, int most_splits, bool sums) {
@@ -706,7 +712,7 @@ Shape best_shape(int64_t rows, int64_t n, int64_t steps, int most_splits, bool s
     const int64_t tiles = cdiv(n, kTI) * cdiv(rows, 64 * jm);
     for (int fill = 1; fill <= 2; ++fill) {
       int64_t splits = fill * kCUs / tiles;
-      const int64_t most = cdiv(steps, 8) < most_splits ? cdiv(steps, 8) : most_splits;
+      const int64_t most = split_limit(steps, most_splits);
       splits = splits < most ? splits : most;
       splits = splits < 1 ? 1 : splits;
       const int64_t ks = cdiv(steps, splits);
@@ -721,11 +727,19 @@ Shape best_shape(int64_t rows, int64_t n, int64_t steps, int most_splits, bool s
   return best;
 }
 
+// Rows of all splits together, of so many rows or fewer, where there are splits: two
+// rounds of tiles of up to 256 rows at most
+int64_t most_split_rows(int64_t rows, int64_t n, int64_t steps, int most_splits) {
+  const int64_t a = split_limit(steps, most_splits) * rows, b = 2 * kCUs / cdiv(n, kTI) * 256;
+  return split_limit(steps, most_splits) < 2 ? 0 : a < b ? a : b;
+}
+
+constexpr int kZSplits = 4, kDhSplits = 32;
 Shape z_shape(int64_t rows, int64_t V, int64_t K) {
-  return best_shape(rows, V, K / kStep, 4, false);
+  return best_shape(rows, V, K / kStep, kZSplits, false);
 }
 Shape dh_shape(int64_t rows, int64_t V, int64_t K) {
-  return best_shape(rows, K, cdiv(V, kStep), 32, true);
+  return best_shape(rows, K, cdiv(V, kStep), kDhSplits, true);
 }
 
 // Columns of z that its first launch takes: all, or whole rounds of tiles, where
@@ -753,35 +767,21 @@ int64_t piece_rows(int64_t M, int64_t V) {
   return M < most ? M : most;
 }
 
-// the logits of a piece (the last has fewer rows and may have more splits)
-size_t z_bytes(int64_t M, int64_t V, int64_t K) {
-  const int64_t rows = piece_rows(M, V), last = M - (cdiv(M, rows) - 1) * rows;
-  const int64_t a = rows * z_shape(rows, V, K).splits, b = last * z_shape(last, V, K).splits;
-  return (size_t)(a > b ? a : b) * ld_of(V) * 4;
-}
-
+// The workspace of M rows is enough for fewer, those of the last piece among them:
+// fewer rows may have more splits.
 struct Layout {
   size_t z, d, g, part, end;
 };
 Layout layout(int64_t M, int64_t V, int64_t K, bool need_dh) {
-  const int64_t rows = piece_rows(M, V);
+  const int64_t rows = piece_rows(M, V), split = most_split_rows(rows, V, K / kStep, kZSplits);
   Layout l;
   l.z = 0;
-  l.d = up256(z_bytes(M, V, K));
+  l.d = up256((size_t)(split > rows ? split : rows) * ld_of(V) * 4);
   l.g = l.d + (need_dh ? up256((size_t)rows * ld_of(V) * 2) : 0);
   l.part = l.g + (need_dh ? up256((size_t)rows * 4) : 0);
   l.end = l.part;
-  if (need_dh) {
-    // the last piece may have fewer rows and more splits
-    const int64_t last = M - (cdiv(M, rows) - 1) * rows;
-    size_t most = 0;
-    for (int64_t n : {rows, last}) {
-      const Shape s = dh_shape(n, V, K);
-      const size_t b = s.splits > 1 ? (size_t)s.splits * n * K * 4 : 0;
-      if (b > most) most = b;
-    }
-    l.end += up256(most);
-  }
+  if (need_dh)
+    l.end += up256((size_t)most_split_rows(rows, K, cdiv(V, kStep), kDhSplits) * K * 4);
   return l;
 }
 

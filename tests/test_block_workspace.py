@@ -48,3 +48,9 @@ def test_norm_workspace_is_enough_for_fewer_rows(K):
                                          (64, 64, 1, 4096), (1024, 1024, 7, 8)])
 def test_adapter_workspace_is_enough_for_fewer_rows(op, N, K, r, slots):
     grows(lambda M: block.lib().lq_adapters_workspace_size(op, M, N, K, r, slots), ((1 << 31) - 1) // max(N, K))
+
+
+@pytest.mark.parametrize("need_dh", [0, 1])
+@pytest.mark.parametrize("V,K", [(32000, 4096), (50257, 2048), (128256, 4096), (1000, 512), (3, 64), (1 << 20, 1024), (9999, 16384)])
+def test_head_workspace_is_enough_for_fewer_rows(V, K, need_dh):
+    grows(lambda M: block.lib().lq_head_loss_workspace(M, V, K, 1, need_dh), ((1 << 31) - 1) // K)
