@@ -31,6 +31,7 @@ extern "C" {
  *            LQ_MX_FP4), quantised from float32 y by lq_mx_quantize's rule;
  *            codes NULL: none (scales and format are then not read)
  *   rstd_out optional M float32: 1 / sqrt(mean(H^2) + eps), for lq_rmsnorm_bwd
+ * Rows whose H^2 leave float32's range are off as that sum is (|H| past 1e19: y is 0).
  * One of Y and codes at least.  H_out and Y may be X or R (the same pointer;
  * not both the same buffer); any other overlap of outputs with inputs or each
  * other is outside the contract.
@@ -79,6 +80,10 @@ size_t lq_rmsnorm_bwd_workspace(int64_t M, int64_t K);
  *           (NULL: r everywhere).  A's rows and B's columns past it are not
  *           part of the adapter: they may hold anything, NaN included
  *   scales  device float[slots]: each adapter's alpha / rank
+ * Beside lq_lora_fwd_multi_ranks: that call forms the shared product too and rounds the
+ * sum once, for segments given by the host and ranks of 64 together.  Here the rows
+ * come in any order, places are loaded while serving, there is a backward, and the
+ * base is any call's output, rounded before the adapters are added.
  */
 typedef struct lq_adapter_pool {
   int32_t slots;
@@ -130,7 +135,8 @@ int lq_adapters_fwd(const void* X, int64_t M, const lq_adapter_pool* pool, const
  * dA and dB are float32 sums, in a fixed order, of products with float32 U and
  * T (carried as three bf16 parts, so that nothing of their 24 bits is lost).  A
  * non-finite element makes the sums that it enters non-finite.
- * Without dA and dB X is not read.  M = 0 writes zeros to dA and dB unless
+ * Without dA and dB X is not read.  The workspace and the time of the first launch grow
+ * with slots, since factors are turned by place.  M = 0 writes zeros to dA and dB unless
  * accumulate is set.  Other rules as lq_adapters_fwd (dY, dX: 16-byte aligned).
  */
 int lq_adapters_bwd(const void* dY, const void* X, int64_t M, const lq_adapter_pool* pool,

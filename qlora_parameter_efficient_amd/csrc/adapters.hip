@@ -24,8 +24,8 @@
 // 4096, 16 places of rank up to 64, plan 7 + shrink 18 + expand 40 (65 in all, 3.1
 // TB/s of the 201 MB of X and Y; without the partial sums of T and without B the
 // expand would take 31: both come from L2 for every 256 columns).  Backward of 4096 x
-// 4096 x 11008, 8 places of rank up to 32: plan and turned factors 9.5, U 12, dX 44
-// (4.1 TB/s), gradients 37 + 7.
+// 4096 x 11008, 8 places of rank up to 32: plan and turned factors 9.5, U 12, dX 45
+// (4.0 TB/s), gradients 37 + 8.
 #include "block.h"
 #include "dispatch.h"
 #include "mx_tile.h"
@@ -116,8 +116,9 @@ __device__ __forceinline__ Tile find_tile(const RowArgs& a, int tile, int32_t* r
 // within the place, and the rows are placed; the row that begins a tile or a
 // segment lists it (from the counting threads, one place after another, the lists
 // took 2 to 3 us).  Rows are loaded eight at a time, since a load is the longest
-// part of a step.  Of 6.2 us for 8192 rows in 16 places, 2.4 go until the rows are
-// there, 1 to counting, 1 to the sums and 1.9 to the stores.
+// part of a step.  Of 6.2 us for 8192 rows in 16 places (without the launch, 7.3
+// with it), 2.4 go until the rows are there, 1 to counting, 1 to the sums and 1.9 to
+// the stores.
 struct PlanArgs {
   const int32_t* rows;
   const int32_t* ranks;
@@ -263,7 +264,10 @@ __device__ __forceinline__ void turn_chunk(const TurnArgs& p, int slot, int chun
 constexpr int kPerThread = (LQ_ADAPTERS_MAX_SLOTS + 1024) / 1024;  // most places of a thread
 
 // Workgroup 0: the plan.  The others (backward): four chunks each of a place's
-// factors, which wait for nothing of it.  PT: places per thread; one in pools of
+// factors, which wait for nothing of it, but look for the place among all rows, so
+// the launch takes as long as the pool is large: dX of 64 rows beside 4096 x 4096
+// rank 16, six places in use, 15 us with 8 places, 23 with 64, 167 with 1024, 639 with
+// 4096.  PT: places per thread; one in pools of
 // up to 1023 places, where all 16 waves have counters too.
 template <int PT>
 __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs p, TurnArgs q) {

@@ -8,7 +8,7 @@
 // Two products of 2 M V K operations bound it; the softmax between them costs
 // memory traffic only.  A piece of rows at a time: its logits as float32 (a bf16
 // logit of 16 would be off by 0.03, three percent of its probability) and then D as
-// bf16 (2^-8 of each entry but the largest) lie in the workspace.  Kept
+// bf16 (half a step, 2^-8, of each entry but the largest) lie in the workspace.  Kept
 // logits are cheaper than formed ones: 12 bytes of traffic per logit against 2 K
 // operations.
 //
@@ -31,11 +31,11 @@
 // next behind the products of two substeps, half behind the barrier and half in the
 // next step (766; all behind the barrier, or over three substeps, 4 to 6% more).
 //
-// Measured at 4096 x 32000 x 4096: logits 860 us (1.25 PFLOP/s; of a tile's 102 us 2 to
+// Measured at 4096 x 32000 x 4096: logits 871 us (1.23 PFLOP/s; of a tile's 102 us 2 to
 // 3 go to its first loads, 6 to the stores of its logits, the rest to 64 steps of
-// 1.45 us), softmax 191 (4.1 TB/s), dH 785 (1.37 PFLOP/s).  Over both products the
-// matrix units are busy 70% of the cycles and waves wait 17% of theirs.  130 rows:
-// logits 68 to 81 us (W once, 3.2 to 3.9 TB/s), dH 66 + 8.
+// 1.45 us), softmax 195 (4.0 TB/s), dH 779 (1.38 PFLOP/s).  Over both products the
+// matrix units are busy 72% of the cycles and waves wait 16% of theirs.  130 rows:
+// logits 69 to 81 us (W once, 3.2 to 3.8 TB/s), dH 66 + 9.
 #include <type_traits>
 
 #include "block.h"
@@ -342,8 +342,8 @@ __global__ __launch_bounds__(kThreads) void head_product_kernel(ProdParams p) {
 
 // ---------------------------------------------------------------- softmax
 // One workgroup per row: its maximum, its sum of exponentials, the loss, and D.
-// The row stays in registers from its one read to D's store (kKeep values per
-// thread; longer rows are read again).
+// The row stays in registers from its one read to D's store; what does not fit
+// (past 65536 columns) is read three times.
 
 struct RowParams {
   const float* Z;     // splits x rows x ldz
@@ -796,6 +796,9 @@ int launch_product(const ProdParams& p, int jm, hipStream_t st) {
   return hip_fail(hipGetLastError(), TR ? "head dH launch" : "head logits launch");
 }
 
+// The fewest values per thread that hold the row, since those past its end cost as much
+// (us of the whole call with 4, 8 or 13 groups / with 16: 4096 x 16000 x 64 173 / 250,
+// 4096 x 32000 x 64 373 / 401, 4000 x 53000 x 64 602 / 613, 2048 x 33000 x 256 264 / 269)
 void launch_rows(const RowParams& r, int64_t rows, hipStream_t st) {
   const int64_t ld = r.ldz;
   const auto kernel = ld <= 4096 * 4    ? head_row_kernel<1024, 4>
