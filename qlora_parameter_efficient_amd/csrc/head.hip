@@ -601,7 +601,9 @@ __global__ __launch_bounds__(T) __attribute__((amdgpu_num_sgpr(80))) void head_r
     // the same in all) would be dH's error: up to 2^-8, where the others' errors, half
     // of that and of either sign, are mostly lost in dH's own rounding.
     const float stays = look ? lanes_max<W>(waves[2][tid % W]) : top_in ? 0.0f : 1.0f;
-    most = fmaxf(fmaxf(most, 1e-37f), stays * fabsf(total / sum));
+    // (at least so much that 1 / most and factor are finite: D's zeros must stay that)
+    const float share = fabsf(total / sum);
+    most = fmaxf(fmaxf(most, stays * share), 1e-37f * fmaxf(share, 1.0f));
     most = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most)));
     const float inv = 1.0f / most;
     out[0] = loss;

@@ -136,3 +136,22 @@ def test_loss_of_large_confident_logits(V, scale):
             want = float((z.max() - z[t]) + torch.log1p(e[torch.arange(V) != top].sum()))
             assert bool(((loss.double() - want).abs() <= rel(V, float(z.max() - z[9]) + 1.0) * want).all()), (near, t)
             assert abs(float(lse[0]) - float(torch.logsumexp(z, 0))) <= U32 * float(lse[0]) + rel(V, 0.0)
+
+
+@pytest.mark.parametrize("V", [1, 60, 1000, 70001])
+@pytest.mark.parametrize("h", [40.0, 120.0, 200.0])
+def test_heavy_weights_on_a_certain_row(V, h):
+    """All of 100 targets are the largest logit, with weights of 50 together: the gradient is
+    50 (1 - p), down to nothing, and never 0 times an overflow."""
+    announce(f"heavy weights V={V} h={h}")
+    t = V // 2
+    z, H, W = case(3, V, h, {t: 1.0}, t)
+    ids = torch.full((3, 100), t, dtype=torch.int32, device=DEV)
+    loss, _, dH = block.lq_head_loss(H, W, ids, p=torch.full((3, 100), 0.5, device=DEV))
+    rest = (V - 1) * math.exp(-h)
+    ref = -50.0 * rest / (1.0 + rest) * W[t, 1:].double()
+    tiny = 2.0**-126
+    e = HALF_BF16 + (1 + HALF_BF16) * (rel(V, h) + 108 * U32)
+    assert bool(((dH[:, 1:].double() - ref).abs() <= e * ref.abs() + 4 * tiny).all())
+    want = 50.0 * math.log1p(rest)
+    assert bool(((loss.double() - want).abs() <= (rel(V, h) + 108 * U32) * want + 200 * tiny).all())
